@@ -1,7 +1,7 @@
 /*
  * pkv.h -- C ABI of the paged KV-cache kernels for NVIDIA GB300 (sm_103a).
  *
- * Three operations make up the path:
+ * These operations make up the path:
  *   - kv_append: scatter new K/V rows into a paged block pool through a
  *     slot_mapping, optionally quantising them to fp8 e4m3 (per-kv-head
  *     fp32 scales) or to 3-bit affine codes packed 8 values per 3 bytes;
@@ -9,6 +9,9 @@
  *     block tables, with grouped-query heads, online softmax, a split over
  *     the context merged by log-sum-exp rescaling, and the fp8 / int8 /
  *     3-bit dequantisation done in registers;
+ *   - paged_prefill: causal attention of packed prompts, or chunks of them,
+ *     over the same pool;
+ *   - kv_gather: the read back of cached rows, dequantised;
  *   - pack3 / unpack3: the bit-exact 3-bit packing on its own.
  *
  * Conventions shared by every call
@@ -75,7 +78,8 @@ enum {
     PKV_DEVERR_BLOCK_RANGE = 2,   /* decode: block id outside [0, num_blocks) */
     PKV_DEVERR_CONTEXT_RANGE = 4, /* decode: context_len < 0 or > table capacity */
     PKV_DEVERR_POS_RANGE = 8,     /* slot_mapping: position outside the table */
-    PKV_DEVERR_TIMEOUT = 16       /* a bounded in-kernel wait gave up */
+    PKV_DEVERR_TIMEOUT = 16,      /* a bounded in-kernel wait gave up */
+    PKV_DEVERR_QSTART_RANGE = 32  /* prefill: q_starts decreasing or outside [0, num_tokens] */
 };
 
 /* A strided view of device memory (up to 4 dimensions). */
@@ -244,6 +248,94 @@ int pkv_kv_append_scaled(const pkv_tensor *k_new, const pkv_tensor *v_new,
                          const pkv_tensor *k_new_scale, const pkv_tensor *v_new_scale,
                          const pkv_tensor *slot_mapping, const pkv_cache *cache, int32_t *err_flag,
                          void *stream);
+
+/*
+ * pkv_kv_append_dynamic -- pkv_kv_append_scaled that computes the scales
+ * itself, for caches with per-token scales: per (token, kv head) row of K
+ * and of V, all in fp32 with IEEE rounding,
+ *   a = max |x_d| over the row's finite elements (0 when there is none),
+ *   s = max(a / qmax, 2^-126), qmax = 448 (E4M3), 57344 (E5M2), 127 (I8),
+ *   code_d = the cast of x_d / s that pkv_kv_append describes (infinities
+ *            saturate, NaN stores 0x7F or, for I8, 0),
+ * and s is stored at the token's slot in cache->k_scales / v_scales.  Every
+ * stored scale is a positive normal number.  An addition of this library.
+ *   k_new, v_new, slot_mapping, err_flag, stream: as pkv_kv_append.
+ *   cache : E4M3, E5M2 or I8 with scale_mode PKV_SCALE_PER_TOKEN, head_dim
+ *           64 or 128 (PKV_ERR_UNSUPPORTED otherwise); any block size.
+ */
+int pkv_kv_append_dynamic(const pkv_tensor *k_new, const pkv_tensor *v_new,
+                          const pkv_tensor *slot_mapping, const pkv_cache *cache, int32_t *err_flag,
+                          void *stream);
+
+/*
+ * pkv_kv_gather -- read cached rows back: the inverse of the appends.
+ *   cache        : every dtype, layout and scale granularity (pkv_cache),
+ *                  head_dim a multiple of 8; U3 head_dim 64 or 128; any
+ *                  block size.
+ *   slot_mapping : I64 [num_tokens], any stride; slot as in pkv_kv_append.
+ *                  The same slot may appear more than once.
+ *   k_out, v_out : F16 or BF16 (both the same), [num_tokens, num_kv_heads,
+ *                  head_dim], head_dim contiguous, any token and head
+ *                  strides.  Row i receives the row at slot_mapping[i]:
+ *                  16-bit elements of the cache's own dtype as they are;
+ *                  otherwise the value the stored code or element stands
+ *                  for, formed in fp32 (one rounding: code * scale) and
+ *                  rounded once to nearest even.  A finite value beyond the
+ *                  output type's range becomes an infinity.
+ *   A slot < 0 leaves its output rows as they were; one >= num_blocks *
+ *   block_size does too and raises PKV_DEVERR_SLOT_RANGE.  An addition of
+ *   this library.
+ */
+int pkv_kv_gather(const pkv_cache *cache, const pkv_tensor *slot_mapping, const pkv_tensor *k_out,
+                  const pkv_tensor *v_out, int32_t *err_flag, void *stream);
+
+/*
+ * pkv_paged_prefill -- causal attention of packed new tokens over the paged
+ * cache: whole prompts, chunks of prompts, or a few tokens per sequence.
+ * The new tokens' K/V rows are in the cache already (pkv_kv_append*).
+ *
+ *   q            : F16 or BF16 [num_tokens, num_heads, head_dim], head_dim
+ *                  contiguous, 16-byte aligned rows: the new tokens of all
+ *                  sequences one sequence after another.
+ *   cache, block_tables, context_lens, sm_scale : as pkv_paged_decode
+ *                  (context_lens counts the new tokens in).
+ *   q_starts     : I32 [batch + 1], non-decreasing: sequence b owns rows
+ *                  q_starts[b] .. q_starts[b + 1] - 1, n_b of them, which
+ *                  are the last n_b of its context_lens[b] cached tokens.
+ *   out          : as q's shape and dtype, head_dim contiguous.  Row i of
+ *                  sequence b (i = 0 .. n_b - 1) is
+ *                  softmax(sm_scale * q . K^T) V over the cached tokens
+ *                  0 .. context_lens[b] - n_b + i, accumulated in fp32 and
+ *                  rounded once; a row that sees no token (context_lens[b] <
+ *                  n_b) is zero.  Rows of q / out that no sequence owns are
+ *                  neither read nor written.
+ *   workspace    : as pkv_paged_decode, of pkv_paged_prefill_workspace's size.
+ *                  Calls whose kernels may overlap must not share one.
+ *
+ *   Cache contents that a row does not see never affect it, whatever they
+ *   hold.  Supported: every cache dtype, layout and scale granularity;
+ *   head_dim 64 or 128; block_size a power of two from 8 to 256; num_heads a
+ *   multiple of num_kv_heads; num_tokens * (num_heads / num_kv_heads) <
+ *   2^30; batch < 2^20.  Dequantised F16 / BF16 products take the codes
+ *   exactly; scales are applied in fp32.
+ *   Bad data never faults: a block id outside [0, num_blocks) is left out
+ *   (PKV_DEVERR_BLOCK_RANGE); a context length below 0 counts as 0 and one
+ *   above the table's capacity as that capacity
+ *   (PKV_DEVERR_CONTEXT_RANGE); a sequence whose q_starts decrease or leave
+ *   [0, num_tokens] is left out (PKV_DEVERR_QSTART_RANGE).  The rows of such
+ *   sequences are then not meaningful.  An addition of this library.
+ */
+int pkv_paged_prefill_workspace(const pkv_tensor *q, const pkv_cache *cache,
+                                const pkv_tensor *block_tables, size_t *bytes);
+
+/* Kernel launches a pkv_paged_prefill call with these arguments makes. */
+int pkv_paged_prefill_launches(const pkv_tensor *q, const pkv_cache *cache,
+                               const pkv_tensor *block_tables, int32_t *launches);
+
+int pkv_paged_prefill(const pkv_tensor *q, const pkv_cache *cache, const pkv_tensor *block_tables,
+                      const pkv_tensor *q_starts, const pkv_tensor *context_lens, float sm_scale,
+                      const pkv_tensor *out, void *workspace, size_t workspace_bytes, int32_t *err_flag,
+                      void *stream);
 
 /*
  * pkv_paged_decode -- paged attention for one query token per sequence

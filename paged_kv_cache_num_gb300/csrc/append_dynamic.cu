@@ -1,0 +1,112 @@
+// append_dynamic.cu -- the append that computes its per-token scales.
+//
+// Per (token, kv head) row of K and of V: a = max |x_d| over the finite
+// elements, s = max(a / qmax, 2^-126), code_d = cast(x_d / s), all in fp32
+// with IEEE rounding; the scale goes to the token's slot.
+//
+// A row is read once: head_dim / 16 lanes hold 16 elements each in
+// registers (two 16-byte loads), the maximum is a shuffle reduction among
+// them, and each lane stores its 16 codes as one 16-byte piece, which is
+// also a piece of the x-vectorised layout.
+#include <type_traits>
+
+#include "append_common.cuh"
+
+namespace pkv {
+namespace {
+
+template <int Q8> __device__ __forceinline__ float q8_max()
+{
+    return Q8 == kE4M3 ? 448.0f : Q8 == kE5M2 ? 57344.0f : 127.0f;
+}
+
+template <int SRC, bool VEC, int Q8, int LPR>
+__global__ void __launch_bounds__(kAppendThreads) append_dynamic_kernel(AppendParams p)
+{
+    griddep_wait();
+    griddep_launch_dependents();
+    constexpr int RPW = 32 / LPR;                   // rows per warp
+    const int lane = threadIdx.x & 31;
+    const int sub = lane % LPR;
+    const int64_t warp = (blockIdx.x * int64_t(blockDim.x) + threadIdx.x) >> 5;
+    const int64_t warps = (int64_t(gridDim.x) * blockDim.x) >> 5;
+    // items: (token, K|V and kv head)
+    Walk2 w(warp * RPW + lane / LPR, warps * RPW, 2 * p.num_kv_heads);
+    while (__any_sync(0xffffffffu, w.major < p.num_tokens)) {
+        const int64_t t = w.major;
+        const int kv = w.minor >= p.num_kv_heads;
+        const int h = w.minor - (kv ? p.num_kv_heads : 0);
+        int64_t blk = 0, off = 0;
+        const bool live = t < p.num_tokens && resolve_slot(p, t, blk, off);
+        uint32_t e[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e[j] = 0u;
+        if (live) {
+            const char *src = kv ? p.v_new + t * p.v_src_tok + h * p.v_src_head
+                                 : p.k_new + t * p.k_src_tok + h * p.k_src_head;
+            if constexpr (VEC) {
+                const uint4 *s4 = reinterpret_cast<const uint4 *>(src) + 2 * sub;
+                const uint4 a = __ldg(s4), b = __ldg(s4 + 1);
+                e[0] = a.x; e[1] = a.y; e[2] = a.z; e[3] = a.w;
+                e[4] = b.x; e[5] = b.y; e[6] = b.z; e[7] = b.w;
+            } else {
+                const uint16_t *s2 = reinterpret_cast<const uint16_t *>(src) + 16 * sub;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) e[j] = uint32_t(s2[2 * j]) | (uint32_t(s2[2 * j + 1]) << 16);
+            }
+        }
+        float a = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float lo = fabsf(h2f<SRC>(uint16_t(e[j]))), hi = fabsf(h2f<SRC>(uint16_t(e[j] >> 16)));
+            // NaN fails the comparison too
+            if (lo < __int_as_float(0x7f800000)) a = fmaxf(a, lo);
+            if (hi < __int_as_float(0x7f800000)) a = fmaxf(a, hi);
+        }
+#pragma unroll
+        for (int o = 1; o < LPR; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+        const float s = fmaxf(__fdiv_rn(a, q8_max<Q8>()), 1.17549435e-38f);
+        if (live) {
+            uint32_t c[4];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float2 x;
+                x.x = __fdiv_rn(h2f<SRC>(uint16_t(e[j])), s);
+                x.y = __fdiv_rn(h2f<SRC>(uint16_t(e[j] >> 16)), s);
+                const uint32_t two = q8x2_encode<Q8>(x);
+                if (j & 1) c[j >> 1] |= two << 16; else c[j >> 1] = two;
+            }
+            char *dst = (kv ? p.v_cache : p.k_cache) + blk * p.c_blk + off * p.c_slot + h * p.c_head + sub * p.c_chunk;
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(c[0], c[1], c[2], c[3]);
+            if (sub == 0) (kv ? p.v_gs : p.k_gs)[blk * p.gs_blk + off * p.gs_slot + h * p.gs_head] = s;
+        }
+        w.next();
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_append_dynamic(const AppendParams &p, int cache_kind, bool vec16, cudaStream_t s)
+{
+    if (p.num_tokens == 0 || p.num_kv_heads == 0) return cudaSuccess;
+    const int lpr = p.head_dim / 16;
+    const int g = grid_for(p.num_tokens * 2 * p.num_kv_heads * lpr, kAppendThreads);
+    auto kind = [&](auto src_c, auto vec_c, auto lpr_c) -> cudaError_t {
+        constexpr int S = decltype(src_c)::value;
+        constexpr bool V = decltype(vec_c)::value;
+        constexpr int L = decltype(lpr_c)::value;
+        if (cache_kind == kE4M3) return launch_pdl(append_dynamic_kernel<S, V, kE4M3, L>, g, kAppendThreads, 0, s, p);
+        if (cache_kind == kE5M2) return launch_pdl(append_dynamic_kernel<S, V, kE5M2, L>, g, kAppendThreads, 0, s, p);
+        return launch_pdl(append_dynamic_kernel<S, V, kI8, L>, g, kAppendThreads, 0, s, p);
+    };
+    auto lanes = [&](auto src_c, auto vec_c) -> cudaError_t {
+        return lpr == 8 ? kind(src_c, vec_c, std::integral_constant<int, 8>{})
+                        : kind(src_c, vec_c, std::integral_constant<int, 4>{});
+    };
+    auto vec = [&](auto src_c) -> cudaError_t {
+        return vec16 ? lanes(src_c, std::true_type{}) : lanes(src_c, std::false_type{});
+    };
+    return p.src_kind == kBF16 ? vec(std::integral_constant<int, kBF16>{}) : vec(std::integral_constant<int, kF16>{});
+}
+
+}  // namespace pkv

@@ -260,7 +260,7 @@ int pkv_slot_mapping(const pkv_tensor *block_tables, const pkv_tensor *req, cons
 static int prep_kv_append(const pkv_tensor *k_new, const pkv_tensor *v_new, const pkv_tensor *slot_mapping,
                           const pkv_cache *cache, int32_t *err_flag, pkv::AppendParams &p, int &kind,
                           bool &vec16, const pkv_tensor *k_new_scale = nullptr,
-                          const pkv_tensor *v_new_scale = nullptr)
+                          const pkv_tensor *v_new_scale = nullptr, bool dynamic = false)
 {
     TRY(check_tensor(k_new, "k_new", 3));
     TRY(check_tensor(v_new, "v_new", 3));
@@ -318,9 +318,11 @@ static int prep_kv_append(const pkv_tensor *k_new, const pkv_tensor *v_new, cons
         p.gs_slot = ci.gs_slot;
         p.gs_head = ci.gs_head;
     }
-    if (ci.scale_mode == PKV_SCALE_PER_TOKEN) {
+    if (dynamic) {
+        // the kernel computes the scales
+    } else if (ci.scale_mode == PKV_SCALE_PER_TOKEN) {
         if (!k_new_scale || !v_new_scale)
-            return fail(PKV_ERR_UNSUPPORTED, "a per-token-scale cache is appended with pkv_kv_append_scaled");
+            return fail(PKV_ERR_UNSUPPORTED, "a per-token-scale cache is appended with pkv_kv_append_scaled or pkv_kv_append_dynamic");
         TRY(check_tensor(k_new_scale, "k_new_scale", 2));
         TRY(check_tensor(v_new_scale, "v_new_scale", 2));
         if (k_new_scale->dtype != PKV_DTYPE_F32 || v_new_scale->dtype != PKV_DTYPE_F32)
@@ -387,6 +389,45 @@ int pkv_kv_append_scaled(const pkv_tensor *k_new, const pkv_tensor *v_new, const
 
 namespace {
 
+// the fields of the decode and prefill parameters that describe the cache
+void fill_cache_params(const pkv_cache *cache, const CacheInfo &ci, pkv::DecodeParams &p)
+{
+    p.k_cache = static_cast<const char *>(cache->k_cache.data);
+    p.v_cache = static_cast<const char *>(cache->v_cache.data);
+    const int ces = elem_size(ci.kind);
+    p.c_blk = cache->k_cache.stride[0] * ces;
+    p.c_slot = cache->k_cache.stride[1] * ces;
+    p.c_head = cache->k_cache.stride[2] * ces;
+    p.c_chunk = ci.c_chunk;
+    p.k_scale = cache->k_scale;
+    p.v_scale = cache->v_scale;
+    p.scale_mode = ci.scale_mode;
+    if (ci.scale_mode != PKV_SCALE_PER_HEAD) {
+        p.k_gs = static_cast<const float *>(cache->k_scales.data);
+        p.v_gs = static_cast<const float *>(cache->v_scales.data);
+        p.gs_blk = ci.gs_blk;
+        p.gs_slot = ci.gs_slot;
+        p.gs_head = ci.gs_head;
+    }
+    if (ci.kind == PKV_DTYPE_U3) {
+        p.k_qs = static_cast<const uint16_t *>(cache->k_qscale.data);
+        p.v_qs = static_cast<const uint16_t *>(cache->v_qscale.data);
+        p.k_qz = static_cast<const uint8_t *>(cache->k_qzero.data);
+        p.v_qz = static_cast<const uint8_t *>(cache->v_qzero.data);
+        p.m_blk = cache->k_qscale.stride[0];
+        p.m_slot = cache->k_qscale.stride[1];
+        p.m_head = cache->k_qscale.stride[2];
+        p.z_blk = cache->k_qzero.stride[0];
+        p.z_slot = cache->k_qzero.stride[1];
+        p.z_head = cache->k_qzero.stride[2];
+    }
+    p.num_kv_heads = int(ci.num_kv_heads);
+    p.head_dim = int(ci.head_dim);
+    p.block_size = int(ci.block_size);
+    p.block_shift = is_pow2(ci.block_size) ? log2i(ci.block_size) : -1;
+    p.num_blocks = int(ci.num_blocks);
+}
+
 struct DecodeCheck {
     CacheInfo ci;
     int64_t batch, num_heads, max_blocks;
@@ -429,47 +470,14 @@ int check_decode_common(const pkv_tensor *q, const pkv_cache *cache, const pkv_t
     p.q = static_cast<const char *>(q->data);
     p.q_b = q->stride[0] * 2;
     p.q_h = q->stride[1] * 2;
-    p.k_cache = static_cast<const char *>(cache->k_cache.data);
-    p.v_cache = static_cast<const char *>(cache->v_cache.data);
-    const int ces = elem_size(ci.kind);
-    p.c_blk = cache->k_cache.stride[0] * ces;
-    p.c_slot = cache->k_cache.stride[1] * ces;
-    p.c_head = cache->k_cache.stride[2] * ces;
-    p.c_chunk = ci.c_chunk;
-    p.k_scale = cache->k_scale;
-    p.v_scale = cache->v_scale;
-    p.scale_mode = ci.scale_mode;
-    if (ci.scale_mode != PKV_SCALE_PER_HEAD) {
-        p.k_gs = static_cast<const float *>(cache->k_scales.data);
-        p.v_gs = static_cast<const float *>(cache->v_scales.data);
-        p.gs_blk = ci.gs_blk;
-        p.gs_slot = ci.gs_slot;
-        p.gs_head = ci.gs_head;
-    }
-    if (ci.kind == PKV_DTYPE_U3) {
-        p.k_qs = static_cast<const uint16_t *>(cache->k_qscale.data);
-        p.v_qs = static_cast<const uint16_t *>(cache->v_qscale.data);
-        p.k_qz = static_cast<const uint8_t *>(cache->k_qzero.data);
-        p.v_qz = static_cast<const uint8_t *>(cache->v_qzero.data);
-        p.m_blk = cache->k_qscale.stride[0];
-        p.m_slot = cache->k_qscale.stride[1];
-        p.m_head = cache->k_qscale.stride[2];
-        p.z_blk = cache->k_qzero.stride[0];
-        p.z_slot = cache->k_qzero.stride[1];
-        p.z_head = cache->k_qzero.stride[2];
-    }
+    fill_cache_params(cache, ci, p);
     p.block_tables = static_cast<const int32_t *>(block_tables->data);
     p.bt_b = block_tables->stride[0];
     p.bt_j = block_tables->stride[1];
     p.batch = int(dc.batch);
     p.num_heads = int(dc.num_heads);
-    p.num_kv_heads = int(ci.num_kv_heads);
     p.group = int(dc.num_heads / ci.num_kv_heads);
-    p.head_dim = int(ci.head_dim);
-    p.block_size = int(ci.block_size);
-    p.block_shift = log2i(ci.block_size);
     p.max_blocks = int(dc.max_blocks);
-    p.num_blocks = int(ci.num_blocks);
     p.q_is_bf16 = q->dtype == PKV_DTYPE_BF16;
 
     const int sm = pkv::sm_count_current_device();
@@ -649,6 +657,180 @@ int pkv_decode_step(const pkv_tensor *k_new, const pkv_tensor *v_new, const pkv_
     dc.p.early_inputs = ap.num_tokens > 0 ? 1 : 0;
     TRY(launch_status(pkv::launch_append(ap, kind, vec16, as_stream(stream)), "kv_append kernel"));
     return launch_paged_decode(dc, q->dtype, workspace, workspace_bytes, stream);
+}
+
+int pkv_kv_append_dynamic(const pkv_tensor *k_new, const pkv_tensor *v_new, const pkv_tensor *slot_mapping,
+                          const pkv_cache *cache, int32_t *err_flag, void *stream)
+{
+    if (!cache) return fail(PKV_ERR_NULL, "cache: descriptor is NULL");
+    if (cache->scale_mode != PKV_SCALE_PER_TOKEN)
+        return fail(PKV_ERR_VALUE, "pkv_kv_append_dynamic needs a cache with scale_mode PKV_SCALE_PER_TOKEN");
+    pkv::AppendParams p;
+    int kind = 0;
+    bool vec16 = false;
+    TRY(prep_kv_append(k_new, v_new, slot_mapping, cache, err_flag, p, kind, vec16, nullptr, nullptr, true));
+    if (p.head_dim != 64 && p.head_dim != 128)
+        return fail(PKV_ERR_UNSUPPORTED, "pkv_kv_append_dynamic supports head_dim 64 and 128");
+    return launch_status(pkv::launch_append_dynamic(p, kind, vec16, as_stream(stream)), "kv_append_dynamic kernel");
+}
+
+int pkv_kv_gather(const pkv_cache *cache, const pkv_tensor *slot_mapping, const pkv_tensor *k_out,
+                  const pkv_tensor *v_out, int32_t *err_flag, void *stream)
+{
+    CacheInfo ci{};
+    TRY(check_cache(cache, ci, true));
+    TRY(check_tensor(slot_mapping, "slot_mapping", 1));
+    TRY(check_tensor(k_out, "k_out", 3));
+    TRY(check_tensor(v_out, "v_out", 3));
+    if (slot_mapping->dtype != PKV_DTYPE_I64) return fail(PKV_ERR_DTYPE, "slot_mapping must be I64");
+    if (k_out->dtype != v_out->dtype) return fail(PKV_ERR_DTYPE, "k_out and v_out dtypes differ");
+    if (k_out->dtype != PKV_DTYPE_F16 && k_out->dtype != PKV_DTYPE_BF16)
+        return fail(PKV_ERR_DTYPE, "k_out must be F16 or BF16");
+    const int64_t want[3] = {slot_mapping->shape[0], ci.num_kv_heads, ci.head_dim};
+    for (int i = 0; i < 3; ++i)
+        if (k_out->shape[i] != want[i] || v_out->shape[i] != want[i])
+            return fail(PKV_ERR_SHAPE, "k_out and v_out must be [num_tokens, num_kv_heads, head_dim]");
+    if (k_out->stride[2] != 1 || v_out->stride[2] != 1)
+        return fail(PKV_ERR_LAYOUT, "head_dim of k_out / v_out must be contiguous");
+    if (ci.head_dim % 8 != 0) return fail(PKV_ERR_UNSUPPORTED, "gather needs head_dim % 8 == 0");
+    if (ci.kind == PKV_DTYPE_U3 && ci.head_dim != 64 && ci.head_dim != 128)
+        return fail(PKV_ERR_UNSUPPORTED, "U3 gather supports head_dim 64 and 128");
+    pkv::GatherParams p{};
+    fill_cache_params(cache, ci, p.c);
+    p.num_slots = ci.num_blocks * ci.block_size;
+    p.slot_mapping = static_cast<const int64_t *>(slot_mapping->data);
+    p.slot_stride = slot_mapping->stride[0];
+    p.num_tokens = slot_mapping->shape[0];
+    p.k_out = static_cast<char *>(k_out->data);
+    p.v_out = static_cast<char *>(v_out->data);
+    p.k_tok = k_out->stride[0] * 2;
+    p.k_head = k_out->stride[1] * 2;
+    p.v_tok = v_out->stride[0] * 2;
+    p.v_head = v_out->stride[1] * 2;
+    p.vec16 = aligned(k_out->data, 16) && aligned(v_out->data, 16) && p.k_tok % 16 == 0 && p.k_head % 16 == 0 &&
+              p.v_tok % 16 == 0 && p.v_head % 16 == 0;
+    p.err_flag = err_flag;
+    return launch_status(pkv::launch_gather(p, ci.kind, k_out->dtype, as_stream(stream)), "kv_gather kernel");
+}
+
+namespace {
+
+struct PrefillCheck {
+    CacheInfo ci;
+    pkv::PrefillParams p;      // every field known before q_starts / context_lens / out / workspace
+    pkv::PrefillPlan plan;
+};
+
+// What the workspace query and the prefill share: validation, the launch
+// parameters that follow, and the plan.
+int check_prefill_common(const pkv_tensor *q, const pkv_cache *cache, const pkv_tensor *block_tables, PrefillCheck &pc)
+{
+    TRY(check_tensor(q, "q", 3));
+    TRY(check_cache(cache, pc.ci));
+    TRY(check_tensor(block_tables, "block_tables", 2));
+    const CacheInfo &ci = pc.ci;
+    if (q->dtype != PKV_DTYPE_F16 && q->dtype != PKV_DTYPE_BF16) return fail(PKV_ERR_DTYPE, "q must be F16 or BF16");
+    if ((ci.kind == PKV_DTYPE_F16 || ci.kind == PKV_DTYPE_BF16) && ci.kind != q->dtype)
+        return fail(PKV_ERR_DTYPE, "16-bit cache dtype must equal q's dtype");
+    if (block_tables->dtype != PKV_DTYPE_I32) return fail(PKV_ERR_DTYPE, "block_tables must be I32");
+    const int64_t T = q->shape[0], heads = q->shape[1], batch = block_tables->shape[0];
+    if (q->shape[2] != ci.head_dim) return fail(PKV_ERR_SHAPE, "q head_dim %lld, cache %lld", (long long)q->shape[2],
+                                                (long long)ci.head_dim);
+    if (ci.head_dim != 64 && ci.head_dim != 128) return fail(PKV_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+    if (ci.block_size < 8) return fail(PKV_ERR_UNSUPPORTED, "prefill needs a block_size of 8 or more");
+    if (q->stride[2] != 1) return fail(PKV_ERR_LAYOUT, "q head_dim must be contiguous");
+    if (ci.num_kv_heads <= 0 || heads <= 0 || heads % ci.num_kv_heads != 0)
+        return fail(PKV_ERR_SHAPE, "num_heads %lld not a multiple of num_kv_heads %lld", (long long)heads,
+                    (long long)ci.num_kv_heads);
+    if (T * (heads / ci.num_kv_heads) >= (int64_t(1) << 30))
+        return fail(PKV_ERR_UNSUPPORTED, "num_tokens * group must be below 2^30");
+    if (batch >= (1 << 20)) return fail(PKV_ERR_UNSUPPORTED, "batch must be below 2^20");
+    if (block_tables->shape[1] * ci.block_size >= (int64_t(1) << 31))
+        return fail(PKV_ERR_UNSUPPORTED, "block table rows must cover fewer than 2^31 tokens");
+    pkv::PrefillParams &p = pc.p;
+    p = pkv::PrefillParams{};
+    pkv::DecodeParams &d = p.d;
+    d.q = static_cast<const char *>(q->data);
+    d.q_b = q->stride[0] * 2;
+    d.q_h = q->stride[1] * 2;
+    if (T > 0 && (!aligned(q->data, 16) || d.q_b % 16 != 0 || d.q_h % 16 != 0))
+        return fail(PKV_ERR_LAYOUT, "q rows must be 16-byte aligned");
+    fill_cache_params(cache, ci, d);
+    d.block_tables = static_cast<const int32_t *>(block_tables->data);
+    d.bt_b = block_tables->stride[0];
+    d.bt_j = block_tables->stride[1];
+    d.batch = int(batch);
+    d.num_heads = int(heads);
+    d.group = int(heads / ci.num_kv_heads);
+    d.max_blocks = int(block_tables->shape[1]);
+    d.q_is_bf16 = q->dtype == PKV_DTYPE_BF16;
+    p.num_tokens = int(T);
+    pc.plan = pkv::plan_prefill(p, ci.kind, pkv::sm_count_current_device());
+    return PKV_OK;
+}
+
+}  // namespace
+
+int pkv_paged_prefill_workspace(const pkv_tensor *q, const pkv_cache *cache, const pkv_tensor *block_tables,
+                                size_t *bytes)
+{
+    if (!bytes) return fail(PKV_ERR_NULL, "bytes is NULL");
+    PrefillCheck pc{};
+    TRY(check_prefill_common(q, cache, block_tables, pc));
+    *bytes = pc.plan.workspace_bytes;
+    return ok();
+}
+
+int pkv_paged_prefill_launches(const pkv_tensor *q, const pkv_cache *cache, const pkv_tensor *block_tables,
+                               int32_t *launches)
+{
+    if (!launches) return fail(PKV_ERR_NULL, "launches is NULL");
+    PrefillCheck pc{};
+    TRY(check_prefill_common(q, cache, block_tables, pc));
+    *launches = pc.plan.launches;
+    return ok();
+}
+
+int pkv_paged_prefill(const pkv_tensor *q, const pkv_cache *cache, const pkv_tensor *block_tables,
+                      const pkv_tensor *q_starts, const pkv_tensor *context_lens, float sm_scale,
+                      const pkv_tensor *out, void *workspace, size_t workspace_bytes, int32_t *err_flag, void *stream)
+{
+    PrefillCheck pc{};
+    TRY(check_prefill_common(q, cache, block_tables, pc));
+    TRY(check_tensor(q_starts, "q_starts", 1));
+    TRY(check_tensor(context_lens, "context_lens", 1));
+    TRY(check_tensor(out, "out", 3));
+    pkv::PrefillParams &p = pc.p;
+    if (q_starts->dtype != PKV_DTYPE_I32 || context_lens->dtype != PKV_DTYPE_I32)
+        return fail(PKV_ERR_DTYPE, "q_starts and context_lens must be I32");
+    if (q_starts->shape[0] != int64_t(p.d.batch) + 1)
+        return fail(PKV_ERR_SHAPE, "q_starts must have batch + 1 entries");
+    if (context_lens->shape[0] != p.d.batch) return fail(PKV_ERR_SHAPE, "context_lens length differs from batch");
+    if (out->dtype != q->dtype) return fail(PKV_ERR_DTYPE, "out dtype must equal q dtype");
+    for (int i = 0; i < 3; ++i)
+        if (out->shape[i] != q->shape[i]) return fail(PKV_ERR_SHAPE, "out shape must equal q shape");
+    if (out->stride[2] != 1) return fail(PKV_ERR_LAYOUT, "out head_dim must be contiguous");
+    if (!std::isfinite(sm_scale)) return fail(PKV_ERR_VALUE, "sm_scale must be finite");
+    if (pc.plan.workspace_bytes > 0) {
+        if (!workspace) return fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes required", pc.plan.workspace_bytes);
+        if (workspace_bytes < pc.plan.workspace_bytes)
+            return fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes given, %zu required", workspace_bytes,
+                        pc.plan.workspace_bytes);
+        if (!aligned(workspace, 16)) return fail(PKV_ERR_LAYOUT, "workspace must be 16-byte aligned");
+    }
+    p.q_starts = static_cast<const int32_t *>(q_starts->data);
+    p.qs_stride = q_starts->stride[0];
+    p.d.context_lens = static_cast<const int32_t *>(context_lens->data);
+    p.d.cl_stride = context_lens->stride[0];
+    p.d.out = static_cast<char *>(out->data);
+    p.d.o_b = out->stride[0] * 2;
+    p.d.o_h = out->stride[1] * 2;
+    p.d.out_vec_ok = aligned(out->data, 16) && p.d.o_b % 16 == 0 && p.d.o_h % 16 == 0;
+    p.d.scale_log2 = sm_scale * 1.4426950408889634f;
+    p.d.err_flag = err_flag;
+    if (p.num_tokens == 0 || p.d.batch == 0) return ok();
+    return launch_status(pkv::launch_prefill(p, pc.plan, pc.ci.kind, workspace, as_stream(stream)),
+                         "paged_prefill kernels");
 }
 
 int pkv_pack3(const uint8_t *values, uint8_t *packed, int64_t n_octets, void *stream)

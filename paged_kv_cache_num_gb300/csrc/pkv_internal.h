@@ -173,6 +173,41 @@ cudaError_t launch_decode(const DecodeParams &p, int cache_kind, int q_kind, cud
 cudaError_t launch_decode_fast(const DecodeParams &p, FastParams f, int cache_kind, void *ws,
                                size_t ws_bytes, cudaStream_t s);
 
+// ---------------------------------------------------------------- append with computed scales, gather
+cudaError_t launch_append_dynamic(const AppendParams &p, int cache_kind, bool vec16, cudaStream_t s);
+
+struct GatherParams {
+    DecodeParams c;             // the cache fields (fill_cache_params)
+    int64_t num_slots;          // num_blocks * block_size
+    const int64_t *slot_mapping;
+    int64_t slot_stride;        // elements
+    int64_t num_tokens;
+    char *k_out;
+    char *v_out;
+    int64_t k_tok, k_head;      // byte strides
+    int64_t v_tok, v_head;
+    int vec16;                  // output rows 16-byte aligned
+    int32_t *err_flag;
+};
+
+cudaError_t launch_gather(const GatherParams &p, int cache_kind, int out_kind, cudaStream_t s);
+
+// ---------------------------------------------------------------- prefill
+struct PrefillParams {
+    DecodeParams d;             // q / out: [num_tokens, num_heads, head_dim], q_b / o_b the token strides
+    const int32_t *q_starts;    // [batch + 1]
+    int64_t qs_stride;
+    int num_tokens;
+};
+
+struct PrefillPlan {
+    int launches;
+    size_t workspace_bytes;
+};
+
+PrefillPlan plan_prefill(const PrefillParams &p, int cache_kind, int sm_count);
+cudaError_t launch_prefill(const PrefillParams &p, const PrefillPlan &plan, int cache_kind, void *ws, cudaStream_t s);
+
 // ---------------------------------------------------------------- pack3 / copy
 cudaError_t launch_pack3(const uint8_t *values, uint8_t *packed, int64_t n, cudaStream_t s);
 cudaError_t launch_unpack3(const uint8_t *packed, uint8_t *values, int64_t n, cudaStream_t s);

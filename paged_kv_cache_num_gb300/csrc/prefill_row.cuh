@@ -1,0 +1,94 @@
+// prefill_row.cuh -- one output row of the prefill attention by one warp,
+// straight from the definition: each lane owns head_dim / 32 elements, the
+// keys are taken one at a time, fp32 throughout.
+#pragma once
+
+#include "pkv_device.cuh"
+
+namespace pkv {
+namespace {
+
+// This lane's EPL elements (e0 .. e0 + EPL - 1) of one cached row, dequantised.
+template <int CK, int EPL>
+__device__ __forceinline__ void cached_elems(const DecodeParams &p, bool v, int64_t blk, int off, int h, int e0,
+                                             float (&x)[EPL])
+{
+    const char *row = (v ? p.v_cache : p.k_cache) + blk * p.c_blk + off * p.c_slot + h * p.c_head;
+    if constexpr (CK == kU3) {
+        const float s = __half2float(__ushort_as_half((v ? p.v_qs : p.k_qs)[blk * p.m_blk + off * p.m_slot + h * p.m_head]));
+        const float z = float((v ? p.v_qz : p.k_qz)[blk * p.z_blk + off * p.z_slot + h * p.z_head]);
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) {
+            const int bit = 3 * (e0 + e);
+            uint32_t w = uint8_t(row[bit >> 3]);
+            if ((bit & 7) > 5) w |= uint32_t(uint8_t(row[(bit >> 3) + 1])) << 8;
+            x[e] = (float((w >> (bit & 7)) & 7u) - z) * s;
+        }
+    } else {
+        constexpr int es = is_q8(CK) ? 1 : 2;
+        const char *piece = row + (e0 * es >> 4) * p.c_chunk + (e0 * es & 15);
+        float s = 1.0f;
+        if constexpr (is_q8(CK))
+            s = p.scale_mode == 0 ? (v ? p.v_scale : p.k_scale)[h]
+                                  : (v ? p.v_gs : p.k_gs)[blk * p.gs_blk + off * p.gs_slot + h * p.gs_head];
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) {
+            if constexpr (CK == kI8)
+                x[e] = float(reinterpret_cast<const int8_t *>(piece)[e]) * s;
+            else if constexpr (is_q8(CK))
+                x[e] = fp8x2_to_float2<CK, 0>(uint32_t(reinterpret_cast<const uint8_t *>(piece)[e])).x * s;
+            else
+                x[e] = h2f<CK>(reinterpret_cast<const uint16_t *>(piece)[e]);
+        }
+    }
+}
+
+// out = softmax(sm_scale q . K^T) V over the first `limit` tokens of the
+// sequence whose block-table row is `table`.  The whole warp calls it.
+template <int QK, int CK, int D>
+__device__ void prefill_row(const DecodeParams &p, const int32_t *table, int64_t tok, int head, int limit)
+{
+    constexpr int EPL = D / 32;
+    const int lane = threadIdx.x & 31;
+    const int h = head / p.group;
+    const uint16_t *qr = reinterpret_cast<const uint16_t *>(p.q + tok * p.q_b + head * p.q_h) + EPL * lane;
+    float q[EPL], acc[EPL];
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) {
+        q[e] = h2f<QK>(qr[e]);
+        acc[e] = 0.0f;
+    }
+    const float ninf = -__int_as_float(0x7f800000);
+    float m = ninf, l = 0.0f;
+    for (int t = 0; t < limit; ++t) {
+        const int64_t blk = table[(t >> p.block_shift) * p.bt_j];
+        if (blk < 0 || blk >= p.num_blocks) {
+            if (lane == 0) raise_err(p.err_flag, PKV_DEVERR_BLOCK_RANGE);
+            continue;
+        }
+        const int off = t & (p.block_size - 1);
+        float x[EPL], s = 0.0f;
+        cached_elems<CK, EPL>(p, false, blk, off, h, EPL * lane, x);
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) s = fmaf(q[e], x[e], s);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        s *= p.scale_log2;
+        // a NaN score makes m and every later weight NaN, as the formula does
+        const float mn = s > m || isnan(s) ? s : m;
+        const float old = m == ninf ? 0.0f : exp2f(m - mn);
+        const float w = s == ninf ? 0.0f : exp2f(s - mn);
+        m = mn;
+        l = l * old + w;
+        cached_elems<CK, EPL>(p, true, blk, off, h, EPL * lane, x);
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) acc[e] = fmaf(w, x[e], acc[e] * old);
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint16_t *o = reinterpret_cast<uint16_t *>(p.out + tok * p.o_b + head * p.o_h) + EPL * lane;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) o[e] = f2h<QK>(acc[e] * inv);
+}
+
+}  // namespace
+}  // namespace pkv

@@ -22,6 +22,7 @@ F16, BF16, E4M3, U3, U8, I32, I64, F32, E5M2, I8 = 1, 2, 3, 4, 5, 6, 7, 8, 9, 10
 # device error bits
 DEVERR_SLOT_RANGE, DEVERR_BLOCK_RANGE, DEVERR_CONTEXT_RANGE, DEVERR_POS_RANGE, DEVERR_TIMEOUT = (
     1, 2, 4, 8, 16)
+DEVERR_QSTART_RANGE = 32
 
 _TORCH_CODES = {torch.float16: F16, torch.bfloat16: BF16, torch.float8_e4m3fn: E4M3,
                 torch.float8_e5m2: E5M2, torch.int8: I8,
@@ -86,6 +87,12 @@ def lib():
                                                    ctypes.c_int, P, P]
             L.pkv_decode_step.argtypes = [TP, TP, TP, TP, TP, TP, CP, TP, TP, ctypes.c_float, TP,
                                           ctypes.c_int, P, ctypes.c_size_t, P, P]
+            L.pkv_kv_append_dynamic.argtypes = [TP, TP, TP, CP, P, P]
+            L.pkv_kv_gather.argtypes = [CP, TP, TP, TP, P, P]
+            L.pkv_paged_prefill_workspace.argtypes = [TP, CP, TP, ctypes.POINTER(ctypes.c_size_t)]
+            L.pkv_paged_prefill_launches.argtypes = [TP, CP, TP, ctypes.POINTER(ctypes.c_int32)]
+            L.pkv_paged_prefill.argtypes = [TP, CP, TP, TP, TP, ctypes.c_float, TP, P,
+                                            ctypes.c_size_t, P, P]
             L.pkv_noalloc_scratch_bytes.restype = ctypes.c_size_t
             L.pkv_pack3.argtypes = [P, P, ctypes.c_int64, P]
             L.pkv_unpack3.argtypes = [P, P, ctypes.c_int64, P]
@@ -94,7 +101,8 @@ def lib():
             for fn in ("pkv_slot_mapping", "pkv_kv_append", "pkv_kv_append_scaled",
                        "pkv_paged_decode_workspace", "pkv_paged_decode_launches",
                        "pkv_paged_decode", "pkv_paged_decode_noalloc", "pkv_decode_step", "pkv_pack3",
-                       "pkv_unpack3", "pkv_unpack3_words", "pkv_copy_peak"):
+                       "pkv_kv_append_dynamic", "pkv_kv_gather", "pkv_paged_prefill_workspace",
+                       "pkv_paged_prefill_launches", "pkv_paged_prefill", "pkv_unpack3", "pkv_unpack3_words", "pkv_copy_peak"):
                 getattr(L, fn).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -148,6 +156,37 @@ def _need_cuda(*ts):
     for t in ts:
         if t is not None and not t.is_cuda:
             raise ValueError("all tensors must be CUDA tensors")
+
+
+class _on_device:
+    """Checks that every tensor is on one CUDA device, makes that device and
+    `stream` (or the device's current stream) current inside the block -- so
+    that what the call allocates belongs to the stream that uses it -- and
+    gives the stream's handle."""
+
+    def __init__(self, stream, *ts):
+        _need_cuda(*ts)
+        devices = {t.device for t in ts if t is not None}
+        if len(devices) > 1:
+            raise ValueError("all tensors must be on one device, got %s" % sorted(map(str, devices)))
+        self.device = devices.pop()
+        if stream is not None and stream.device != self.device:
+            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, self.device))
+        self.given = stream
+
+    def __enter__(self):
+        if self.given is None and torch.cuda.current_device() == self.device.index:
+            self.guard = None
+            return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        stream = self.given if self.given is not None else torch.cuda.current_stream(self.device)
+        self.guard = torch.cuda.stream(stream)
+        self.guard.__enter__()
+        return ctypes.c_void_p(stream.cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
 
 
 @dataclass
@@ -340,6 +379,78 @@ def kv_append_scaled(k_new, v_new, k_new_scale, v_new_scale, slot_mapping, cache
                                       ctypes.byref(_desc(k_new_scale)), ctypes.byref(_desc(v_new_scale)),
                                       ctypes.byref(_desc(slot_mapping)), ctypes.byref(cache._struct()),
                                       _ptr(err_flag), _stream(stream)))
+
+
+def kv_append_dynamic(k_new, v_new, slot_mapping, cache: KVCache, err_flag=None, stream=None):
+    """kv_append for a cache with per-token scales that computes each row's
+    scales, amax / (the format's largest value), and stores them with it."""
+    with _on_device(stream, k_new, v_new, slot_mapping, err_flag, *cache.tensors()) as s:
+        _check(lib().pkv_kv_append_dynamic(ctypes.byref(_desc(k_new)), ctypes.byref(_desc(v_new)),
+                                           ctypes.byref(_desc(slot_mapping)),
+                                           ctypes.byref(cache._struct()), _ptr(err_flag), s))
+
+
+def kv_gather(cache: KVCache, slot_mapping, dtype: Optional[torch.dtype] = None, k_out=None, v_out=None,
+              err_flag=None, stream=None):
+    """The cached rows at slot_mapping, dequantised: (k_out, v_out), each
+    [num_tokens, Hkv, D].  Without k_out / v_out they are allocated in `dtype`
+    (the cache's own for 16-bit caches, else bfloat16), zero where
+    slot_mapping < 0; given buffers keep those rows as they were."""
+    with _on_device(stream, slot_mapping, k_out, v_out, err_flag, *cache.tensors()) as s:
+        if dtype is None:
+            given = k_out if k_out is not None else v_out
+            dtype = given.dtype if given is not None else \
+                cache.k_cache.dtype if cache.kind in ("f16", "bf16") else torch.bfloat16
+        shape = (slot_mapping.shape[0], cache.num_kv_heads, cache.head_dim)
+        if k_out is None:
+            k_out = torch.zeros(shape, dtype=dtype, device=slot_mapping.device)
+        if v_out is None:
+            v_out = torch.zeros(shape, dtype=dtype, device=slot_mapping.device)
+        _check(lib().pkv_kv_gather(ctypes.byref(cache._struct()), ctypes.byref(_desc(slot_mapping)),
+                                   ctypes.byref(_desc(k_out)), ctypes.byref(_desc(v_out)),
+                                   _ptr(err_flag), s))
+    return k_out, v_out
+
+
+def prefill_workspace_bytes(q, cache: KVCache, block_tables) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().pkv_paged_prefill_workspace(ctypes.byref(_desc(q)), ctypes.byref(cache._struct()),
+                                             ctypes.byref(_desc(block_tables)), ctypes.byref(n)))
+    return int(n.value)
+
+
+def prefill_launches(q, cache: KVCache, block_tables) -> int:
+    """Kernel launches one paged_prefill call with these arguments makes."""
+    n = ctypes.c_int32(0)
+    _check(lib().pkv_paged_prefill_launches(ctypes.byref(_desc(q)), ctypes.byref(cache._struct()),
+                                            ctypes.byref(_desc(block_tables)), ctypes.byref(n)))
+    return int(n.value)
+
+
+def paged_prefill(q, cache: KVCache, block_tables, q_starts, context_lens,
+                  sm_scale: Optional[float] = None, out=None, workspace=None, err_flag=None, stream=None):
+    """Causal attention of packed new tokens q [T, Hq, D] over the cache:
+    sequence b owns rows q_starts[b] .. q_starts[b + 1] - 1, the last tokens of
+    its context_lens[b] cached ones (their K/V are appended before).  Without
+    `out` one is allocated, zero in the rows that no sequence owns."""
+    with _on_device(stream, q, block_tables, q_starts, context_lens, out, workspace, err_flag,
+                    *cache.tensors()) as s:
+        if sm_scale is None:
+            sm_scale = 1.0 / math.sqrt(q.shape[-1])
+        if out is None:
+            out = torch.zeros_like(q, memory_format=torch.contiguous_format)
+        if workspace is None:
+            need = prefill_workspace_bytes(q, cache, block_tables)
+            if need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        ws_n = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        _check(lib().pkv_paged_prefill(ctypes.byref(_desc(q)), ctypes.byref(cache._struct()),
+                                       ctypes.byref(_desc(block_tables)),
+                                       ctypes.byref(_desc(q_starts)),
+                                       ctypes.byref(_desc(context_lens)), float(sm_scale),
+                                       ctypes.byref(_desc(out)), _ptr(workspace), ws_n,
+                                       _ptr(err_flag), s))
+    return out
 
 
 def decode_workspace_bytes(q, cache: KVCache, block_tables, num_splits: int = 0) -> int:
