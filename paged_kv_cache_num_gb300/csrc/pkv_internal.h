@@ -202,6 +202,8 @@ struct PrefillParams {
 
 struct PrefillPlan {
     int launches;
+    int grid;                   // persistent CTAs
+    int join;                   // whether row tiles may be split between CTAs
     size_t workspace_bytes;
 };
 

@@ -1,81 +1,101 @@
-// prefill.cu -- causal attention of packed new tokens over the paged cache.
+// prefill.cu -- host side of the prefill attention: plan, tensor maps, and
+// the choice of the kernel instance (built in prefill_*.cu).
 //
 // Sequence b owns rows q_starts[b] .. q_starts[b+1]-1 of q, the last n_b of
 // its ctx_b cached tokens; row i sees tokens 0 .. ctx_b - n_b + i:
 //   out_i = sum_t exp(s_it - m_i) v_t / sum_t exp(s_it - m_i), s_it = sm_scale q_i . k_t,
 // with q head h reading kv head h / group.
-//
-// One warp per (token, q head) row: the plainest form.
-#include <type_traits>
+#include <cudaTypedefs.h>
 
-#include "prefill_row.cuh"
+#include <algorithm>
+#include <mutex>
+
+#include "prefill_launch.h"
 
 namespace pkv {
 namespace {
 
-template <int QK, int CK, int D>
-__global__ void __launch_bounds__(128) prefill_rows_kernel(PrefillParams p)
+PFN_cuTensorMapEncodeTiled_v12000 encoder()
 {
-    griddep_wait();
-    griddep_launch_dependents();
-    const DecodeParams &d = p.d;
-    const int lane = threadIdx.x & 31;
-    const int64_t rows = int64_t(p.num_tokens) * d.num_heads;
-    const int64_t step = (int64_t(gridDim.x) * blockDim.x) >> 5;
-    for (int b = blockIdx.x * blockDim.x + threadIdx.x; b < d.batch; b += gridDim.x * blockDim.x) {
-        const int a = p.q_starts[b * p.qs_stride], e = p.q_starts[(b + 1) * p.qs_stride];
-        if (a < 0 || e < a || e > p.num_tokens) raise_err(d.err_flag, PKV_DEVERR_QSTART_RANGE);
-    }
-    for (int64_t r = (blockIdx.x * int64_t(blockDim.x) + threadIdx.x) >> 5; r < rows; r += step) {
-        const int tok = int(r / d.num_heads), head = int(r - int64_t(tok) * d.num_heads);
-        int lo = 0, hi = d.batch;                   // the last sequence that starts at or before tok
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (p.q_starts[mid * p.qs_stride] <= tok) lo = mid; else hi = mid;
-        }
-        const int s0 = p.q_starts[lo * p.qs_stride], s1 = p.q_starts[(lo + 1) * p.qs_stride];
-        if (tok < s0 || tok >= s1) continue;
-        if (s0 < 0 || s1 > p.num_tokens) continue;
-        int ctx = d.context_lens[lo * d.cl_stride];
-        const int cap = d.max_blocks << d.block_shift;
-        if (ctx < 0 || ctx > cap) {
-            if (lane == 0) raise_err(d.err_flag, PKV_DEVERR_CONTEXT_RANGE);
-            ctx = ctx < 0 ? 0 : cap;
-        }
-        prefill_row<QK, CK, D>(d, d.block_tables + lo * d.bt_b, tok, head, max(0, ctx - (s1 - s0) + (tok - s0) + 1));
-    }
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    });
+    return fn;
 }
+
+// (element, slot, kv head, block) of a 16-bit cache; a box is 64 elements
+// (one 128-byte swizzled row) of a block's slots, at most 128
+bool cache_map(CUtensorMap *m, const char *base, const DecodeParams &d, bool bf16)
+{
+    auto enc = encoder();
+    if (!enc || d.num_blocks == 0) return false;
+    cuuint64_t dims[4] = {cuuint64_t(d.head_dim), cuuint64_t(d.block_size), cuuint64_t(d.num_kv_heads),
+                          cuuint64_t(d.num_blocks)};
+    cuuint64_t strides[3] = {cuuint64_t(d.c_slot), cuuint64_t(d.c_head), cuuint64_t(d.c_blk)};
+    cuuint32_t box[4] = {64, cuuint32_t(std::min(d.block_size, 128)), 1, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<char *>(base),
+               dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
-PrefillPlan plan_prefill(const PrefillParams &, int, int)
+PrefillPlan plan_prefill(const PrefillParams &p, int, int sm_count)
 {
     PrefillPlan pl{};
-    pl.launches = 1;
+    const DecodeParams &d = p.d;
+    // an upper bound of the units, from the shapes alone: every sequence's
+    // rows end in a row tile of their own, every tile sees the whole table
+    const int64_t tiles = int64_t(p.num_tokens) * d.group / 256 + d.batch;
+    const int64_t keys = (int64_t(d.max_blocks) * d.block_size + 127) / 128;
+    const int64_t units = tiles * d.num_kv_heads * std::max<int64_t>(keys, 1);
+    pl.grid = int(std::max<int64_t>(1, std::min<int64_t>(units, sm_count)));
+    pl.join = keys > 1 && pl.grid > 1;
+    pl.launches = pl.join ? 2 : 1;
+    pl.workspace_bytes = round256(size_t(pl.grid) * sizeof(int4));
+    if (pl.join) pl.workspace_bytes += size_t(pl.grid) * 2 * 256 * (2 + size_t(d.head_dim)) * sizeof(float);
     return pl;
 }
 
-cudaError_t launch_prefill(const PrefillParams &p, const PrefillPlan &, int cache_kind, void *, cudaStream_t s)
+cudaError_t launch_prefill(const PrefillParams &p, const PrefillPlan &pl, int cache_kind, void *ws, cudaStream_t s)
 {
-    const int64_t rows = int64_t(p.num_tokens) * p.d.num_heads;
-    const int g = int(rows / 4 + 1 < 152 * 64 ? rows / 4 + 1 : 152 * 64);
-    auto go = [&](auto qk_c, auto ck_c) -> cudaError_t {
-        constexpr int QK = decltype(qk_c)::value;
-        constexpr int CK = decltype(ck_c)::value;
-        return p.d.head_dim == 128 ? launch_pdl(prefill_rows_kernel<QK, CK, 128>, g, 128, 0, s, p)
-                                   : launch_pdl(prefill_rows_kernel<QK, CK, 64>, g, 128, 0, s, p);
-    };
-    auto q8 = [&](auto qk_c) -> cudaError_t {
-        if (cache_kind == kE4M3) return go(qk_c, std::integral_constant<int, kE4M3>{});
-        if (cache_kind == kE5M2) return go(qk_c, std::integral_constant<int, kE5M2>{});
-        if (cache_kind == kI8) return go(qk_c, std::integral_constant<int, kI8>{});
-        return go(qk_c, std::integral_constant<int, kU3>{});
-    };
-    using HF = std::integral_constant<int, kF16>;
-    using BF = std::integral_constant<int, kBF16>;
-    if (cache_kind == kF16) return go(HF{}, HF{});
-    if (cache_kind == kBF16) return go(BF{}, BF{});
-    return p.d.q_is_bf16 ? q8(BF{}) : q8(HF{});
+    PrefillLaunch a{};
+    a.p = &p;
+    a.grid = pl.grid;
+    a.join = pl.join;
+    a.stream = s;
+    char *w = static_cast<char *>(ws);
+    a.desc = w;
+    w += round256(size_t(pl.grid) * sizeof(int4));
+    a.part_ml = w;
+    a.part_acc = w + size_t(pl.grid) * 2 * 256 * 2 * sizeof(float);
+    const DecodeParams &d = p.d;
+    switch (cache_kind) {
+    case kF16:
+    case kBF16:
+        // whole pieces of blocks by TMA where the rows are contiguous and a
+        // map of the cache can be made; else (x-vectorised rows) 16-byte copies
+        a.tma = d.c_chunk == 16 && cache_map(&a.tmk, d.k_cache, d, cache_kind == kBF16) &&
+                cache_map(&a.tmv, d.v_cache, d, cache_kind == kBF16);
+        return launch_prefill_16(a);
+    case kE4M3: return launch_prefill_e4m3(a);
+    case kE5M2: return launch_prefill_e5m2(a);
+    case kI8: return launch_prefill_i8(a);
+    default:
+        a.rows_aligned = (reinterpret_cast<uintptr_t>(d.k_cache) | reinterpret_cast<uintptr_t>(d.v_cache) |
+                          uintptr_t(d.c_blk) | uintptr_t(d.c_slot) | uintptr_t(d.c_head)) % 4 == 0;
+        return launch_prefill_u3(a);
+    }
 }
 
 }  // namespace pkv

@@ -1,0 +1,11 @@
+// prefill_16.cu -- prefill kernel instances for 16-bit caches.
+#include "prefill_instance.cuh"
+
+namespace pkv {
+cudaError_t launch_prefill_16(const PrefillLaunch &a)
+{
+    if (a.p->d.q_is_bf16)
+        return a.tma ? launch_dim<kBF16, kBF16, true, false>(a) : launch_dim<kBF16, kBF16, false, false>(a);
+    return a.tma ? launch_dim<kF16, kF16, true, false>(a) : launch_dim<kF16, kF16, false, false>(a);
+}
+}  // namespace pkv

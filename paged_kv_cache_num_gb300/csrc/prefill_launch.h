@@ -1,0 +1,27 @@
+// prefill_launch.h -- what prefill.cu hands to the instances of the kernel.
+#pragma once
+
+#include <cuda.h>
+
+#include "pkv_internal.h"
+
+namespace pkv {
+
+struct PrefillLaunch {
+    const PrefillParams *p;
+    int grid;
+    bool join;                  // launch the join kernel too
+    bool tma;                   // K/V by TMA (tmk, tmv)
+    int rows_aligned;           // 3-bit rows at multiples of 4 bytes
+    void *desc, *part_ml, *part_acc;
+    CUtensorMap tmk, tmv;
+    cudaStream_t stream;
+};
+
+cudaError_t launch_prefill_16(const PrefillLaunch &a);
+cudaError_t launch_prefill_e4m3(const PrefillLaunch &a);
+cudaError_t launch_prefill_e5m2(const PrefillLaunch &a);
+cudaError_t launch_prefill_i8(const PrefillLaunch &a);
+cudaError_t launch_prefill_u3(const PrefillLaunch &a);
+
+}  // namespace pkv

@@ -43,12 +43,14 @@ __device__ __forceinline__ void cached_elems(const DecodeParams &p, bool v, int6
     }
 }
 
-// out = softmax(sm_scale q . K^T) V over the first `limit` tokens of the
-// sequence whose block-table row is `table`.  The whole warp calls it.
+// out[d0 .. d1) = (softmax(sm_scale q . K^T) V)[d0 .. d1) over the first
+// `limit` tokens of the sequence whose block-table row is `table`.  The
+// whole warp calls it.
 template <int QK, int CK, int D>
-__device__ void prefill_row(const DecodeParams &p, const int32_t *table, int64_t tok, int head, int limit)
+__device__ void prefill_row(const DecodeParams &p, const int32_t *table, int64_t tok, int head, int limit, int d0, int d1)
 {
     constexpr int EPL = D / 32;
+    constexpr int U = 4;                            // keys in flight
     const int lane = threadIdx.x & 31;
     const int h = head / p.group;
     const uint16_t *qr = reinterpret_cast<const uint16_t *>(p.q + tok * p.q_b + head * p.q_h) + EPL * lane;
@@ -60,34 +62,70 @@ __device__ void prefill_row(const DecodeParams &p, const int32_t *table, int64_t
     }
     const float ninf = -__int_as_float(0x7f800000);
     float m = ninf, l = 0.0f;
-    for (int t = 0; t < limit; ++t) {
-        const int64_t blk = table[(t >> p.block_shift) * p.bt_j];
-        if (blk < 0 || blk >= p.num_blocks) {
-            if (lane == 0) raise_err(p.err_flag, PKV_DEVERR_BLOCK_RANGE);
-            continue;
+    for (int t0 = 0; t0 < limit; t0 += U) {
+        float s[U], v[U][EPL];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int t = t0 + u;
+            int64_t blk = -1;
+            if (t < limit) blk = table[int64_t(t >> p.block_shift) * p.bt_j];
+            float x[EPL];
+#pragma unroll
+            for (int e = 0; e < EPL; ++e) x[e] = v[u][e] = 0.0f;
+            const bool in = blk >= 0 && blk < p.num_blocks;
+            if (in) {
+                cached_elems<CK, EPL>(p, false, blk, t & (p.block_size - 1), h, EPL * lane, x);
+                cached_elems<CK, EPL>(p, true, blk, t & (p.block_size - 1), h, EPL * lane, v[u]);
+            }
+            s[u] = 0.0f;
+#pragma unroll
+            for (int e = 0; e < EPL; ++e) s[u] = fmaf(q[e], x[e], s[u]);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
+            s[u] = in ? s[u] * p.scale_log2 : ninf;
         }
-        const int off = t & (p.block_size - 1);
-        float x[EPL], s = 0.0f;
-        cached_elems<CK, EPL>(p, false, blk, off, h, EPL * lane, x);
 #pragma unroll
-        for (int e = 0; e < EPL; ++e) s = fmaf(q[e], x[e], s);
+        for (int u = 0; u < U; ++u) {
+            if (s[u] == ninf) continue;
+            // a NaN score makes m and every later weight NaN, as the formula does
+            const float mn = s[u] > m || isnan(s[u]) ? s[u] : m;
+            const float old = m == ninf ? 0.0f : exp2f(m - mn);
+            const float w = exp2f(s[u] - mn);
+            m = mn;
+            l = l * old + w;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        s *= p.scale_log2;
-        // a NaN score makes m and every later weight NaN, as the formula does
-        const float mn = s > m || isnan(s) ? s : m;
-        const float old = m == ninf ? 0.0f : exp2f(m - mn);
-        const float w = s == ninf ? 0.0f : exp2f(s - mn);
-        m = mn;
-        l = l * old + w;
-        cached_elems<CK, EPL>(p, true, blk, off, h, EPL * lane, x);
-#pragma unroll
-        for (int e = 0; e < EPL; ++e) acc[e] = fmaf(w, x[e], acc[e] * old);
+            for (int e = 0; e < EPL; ++e) acc[e] = fmaf(w, v[u][e], acc[e] * old);
+        }
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     uint16_t *o = reinterpret_cast<uint16_t *>(p.out + tok * p.o_b + head * p.o_h) + EPL * lane;
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) o[e] = f2h<QK>(acc[e] * inv);
+    for (int e = 0; e < EPL; ++e)
+        if (EPL * lane + e >= d0 && EPL * lane + e < d1) o[e] = f2h<QK>(acc[e] * inv);
+}
+
+// A row whose result is not finite.  It is right when what made it so lies
+// among the tokens that the row sees.  When V holds such values in the
+// tokens behind the row's limit that its tile worked on (limit .. hi), zero
+// weights may have met them: then the row is done again from its own tokens.
+template <int QK, int CK, int D>
+__device__ __noinline__ void redo_row(const DecodeParams &p, const int32_t *table, int64_t tok, int head, int limit,
+                                      int hi, int d0, int d1)
+{
+    constexpr int EPL = D / 32;
+    const int lane = threadIdx.x & 31;
+    bool found = false;
+    for (int t = limit; t < hi && !found; ++t) {
+        const int64_t blk = table[int64_t(t >> p.block_shift) * p.bt_j];
+        if (blk < 0 || blk >= p.num_blocks) continue;
+        float x[EPL];
+        cached_elems<CK, EPL>(p, true, blk, t & (p.block_size - 1), head / p.group, EPL * lane, x);
+        bool bad = false;
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) bad |= !isfinite(x[e]);
+        found = __any_sync(0xffffffffu, bad);
+    }
+    if (found) prefill_row<QK, CK, D>(p, table, tok, head, limit, d0, d1);
 }
 
 }  // namespace

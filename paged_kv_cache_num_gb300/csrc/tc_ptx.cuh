@@ -1,0 +1,159 @@
+// tc_ptx.cuh -- inline-PTX wrappers of the tensor-core (tcgen05) instructions,
+// tensor memory and the asynchronous copies used by the prefill kernel.
+#pragma once
+
+#include <stdint.h>
+
+#include "pkv_internal.h"
+#include "pkv_ptx.cuh"
+
+namespace pkv {
+namespace tc {
+
+// ---------------------------------------------------------------- tensor memory
+__device__ __forceinline__ void tmem_alloc(uint32_t smem_dst, uint32_t cols)
+{
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols)
+{
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+#define PKV_R32(r, o)                                                                                              \
+    "r"((r)[(o) + 0]), "r"((r)[(o) + 1]), "r"((r)[(o) + 2]), "r"((r)[(o) + 3]), "r"((r)[(o) + 4]),                 \
+        "r"((r)[(o) + 5]), "r"((r)[(o) + 6]), "r"((r)[(o) + 7]), "r"((r)[(o) + 8]), "r"((r)[(o) + 9]),             \
+        "r"((r)[(o) + 10]), "r"((r)[(o) + 11]), "r"((r)[(o) + 12]), "r"((r)[(o) + 13]), "r"((r)[(o) + 14]),        \
+        "r"((r)[(o) + 15]), "r"((r)[(o) + 16]), "r"((r)[(o) + 17]), "r"((r)[(o) + 18]), "r"((r)[(o) + 19]),        \
+        "r"((r)[(o) + 20]), "r"((r)[(o) + 21]), "r"((r)[(o) + 22]), "r"((r)[(o) + 23]), "r"((r)[(o) + 24]),        \
+        "r"((r)[(o) + 25]), "r"((r)[(o) + 26]), "r"((r)[(o) + 27]), "r"((r)[(o) + 28]), "r"((r)[(o) + 29]),        \
+        "r"((r)[(o) + 30]), "r"((r)[(o) + 31])
+#define PKV_W32(c, r, o)                                                                                           \
+    c((r)[(o) + 0]), c((r)[(o) + 1]), c((r)[(o) + 2]), c((r)[(o) + 3]), c((r)[(o) + 4]), c((r)[(o) + 5]),          \
+        c((r)[(o) + 6]), c((r)[(o) + 7]), c((r)[(o) + 8]), c((r)[(o) + 9]), c((r)[(o) + 10]), c((r)[(o) + 11]),    \
+        c((r)[(o) + 12]), c((r)[(o) + 13]), c((r)[(o) + 14]), c((r)[(o) + 15]), c((r)[(o) + 16]),                  \
+        c((r)[(o) + 17]), c((r)[(o) + 18]), c((r)[(o) + 19]), c((r)[(o) + 20]), c((r)[(o) + 21]),                  \
+        c((r)[(o) + 22]), c((r)[(o) + 23]), c((r)[(o) + 24]), c((r)[(o) + 25]), c((r)[(o) + 26]),                  \
+        c((r)[(o) + 27]), c((r)[(o) + 28]), c((r)[(o) + 29]), c((r)[(o) + 30]), c((r)[(o) + 31])
+
+// 32 columns of the warp's 32 lanes: thread = lane (row), register = column.
+// The registers hold the data only after tmem_ld_wait32 on them.
+template <int N>
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[N], int o)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : PKV_W32("=r", r, o)
+        : "r"(addr));
+}
+
+// wait for this thread's tensor-memory loads; names the registers so that
+// nothing reads them before it
+template <int N>
+__device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[N], int o)
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : PKV_W32("+r", r, o)::"memory");
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[N], int o)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+        PKV_R32(r, o)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// ---------------------------------------------------------------- matrix descriptors
+// Shared-memory operand in 128-byte-swizzled rows: `lbo` the byte stride
+// between 64-element chunks of the contiguous dimension (operands whose
+// contiguous dimension is M or N), `sbo` between groups of 8 rows.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo)
+{
+    return uint64_t((addr & 0x3ffffu) >> 4) | (uint64_t(lbo >> 4) << 16) | (uint64_t(sbo >> 4) << 32) |
+           (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+// Instruction descriptor: 16-bit operands of one type, fp32 accumulator.
+template <bool BF16, bool B_MN_MAJOR, int M, int N>
+__device__ __forceinline__ constexpr uint32_t instr_desc()
+{
+    return (1u << 4) | ((BF16 ? 1u : 0u) << 7) | ((BF16 ? 1u : 0u) << 10) | ((B_MN_MAJOR ? 1u : 0u) << 16) |
+           (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
+}
+
+// D[tmem] (+)= A[smem] * B[smem]
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc)
+{
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(acc))
+        : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc)
+{
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(acc))
+        : "memory");
+}
+
+// arrive on `bar` once every earlier tcgen05 operation of this thread is done
+__device__ __forceinline__ void commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// ---------------------------------------------------------------- copies
+// 16 bytes global -> shared, zeros when !ok
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool ok)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16u : 0u) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint4 v)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+
+template <int N> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// two floats -> packed 16-bit pair (lo in the low half), nearest even
+template <int KIND>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi)
+{
+    uint32_t r;
+    if constexpr (KIND == kBF16)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+}  // namespace tc
+}  // namespace pkv
