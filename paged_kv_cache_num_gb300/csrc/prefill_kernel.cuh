@@ -238,7 +238,7 @@ struct Smem {
     static constexpr int cols = ring + kStages * kTile;         // kColSlots x ColSlot
     static constexpr int kColBytes = 2 * kKeyTile * 4 + 32;
     static constexpr int bars = cols + kColSlots * kColBytes;
-    static constexpr int n_bars = 2 * kStages + 2 + 2 + 2 + 2 + 1;
+    static constexpr int n_bars = 2 * kStages + 2 + 4 * 2 + 1;
     static constexpr int misc = bars + 8 * n_bars;
     static constexpr int total = misc + 128;
     static constexpr int alloc = total + 1024;                  // the base is rounded up to 1024
@@ -269,7 +269,8 @@ struct Bars {
     __device__ __forceinline__ uint32_t s_full(int i) const { return base + 8 * (2 * stages + 2 + i); }
     __device__ __forceinline__ uint32_t p_full(int i) const { return base + 8 * (2 * stages + 4 + i); }
     __device__ __forceinline__ uint32_t o_full(int i) const { return base + 8 * (2 * stages + 6 + i); }
-    __device__ __forceinline__ uint32_t tail() const { return base + 8 * (2 * stages + 8); }
+    __device__ __forceinline__ uint32_t p_half(int i) const { return base + 8 * (2 * stages + 8 + i); }
+    __device__ __forceinline__ uint32_t tail() const { return base + 8 * (2 * stages + 10); }
 };
 
 // Wait for a phase, giving up when it takes too long or another warp gave up.
@@ -287,11 +288,22 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
     return true;
 }
 
+// the same for a whole warp: every lane gives up or none
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *gone)
+{
+    return __all_sync(0xffffffffu, bar_wait(bar, parity, gone));
+}
+
 // byte offset of 16-byte piece `c` of row `r` in a tile of 128-byte swizzled
 // rows, [64-element chunk][128 rows][128 bytes]
 __device__ __forceinline__ uint32_t piece_at(int r, int c)
 {
     return uint32_t((c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+template <int N> __device__ __forceinline__ float2 f2(const uint32_t (&x)[N], int j)
+{
+    return make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1]));
 }
 
 // ---------------------------------------------------------------- codes -> 16 bits
@@ -439,7 +451,7 @@ __device__ __forceinline__ void load_rows(const PrefillParams &p, const PrefillF
         return true;
     };
     auto room = [&]() -> bool {
-        return __all_sync(0xffffffffu, pos < ST || bar_wait(bars.empty(pos % ST), (pos / ST - 1) & 1, gone));
+        return pos < ST || warp_wait(bars.empty(pos % ST), (pos / ST - 1) & 1, gone);
     };
     auto arrive = [&](uint32_t stage) {
         ptx::fence_proxy_async_smem();
@@ -500,10 +512,10 @@ __device__ __forceinline__ void load_rows(const PrefillParams &p, const PrefillF
                 const bool ok = __shfl_sync(0xffffffffu, int(in), r);
 #pragma unroll
                 for (int j = 0; j < kWords; ++j) x[i][j] = 0u;
-                if (!ok) continue;
                 if constexpr (CK == kU3) {
                     const char *src = cache + o + 12 * c;
-                    if (f.rows_aligned) {
+                    if (!ok) {
+                    } else if (f.rows_aligned) {
 #pragma unroll
                         for (int j = 0; j < 3; ++j) x[i][j] = __ldg(reinterpret_cast<const uint32_t *>(src) + j);
                     } else {
@@ -512,7 +524,8 @@ __device__ __forceinline__ void load_rows(const PrefillParams &p, const PrefillF
                             x[i][j >> 2] |= uint32_t(__ldg(reinterpret_cast<const uint8_t *>(src) + j)) << (8 * (j & 3));
                     }
                 } else {
-                    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(cache + o + c * d.c_chunk));
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (ok) v = __ldg(reinterpret_cast<const uint4 *>(cache + o + c * d.c_chunk));
                     x[i][0] = v.x;
                     x[i][1] = v.y;
                     x[i][2] = v.z;
@@ -569,7 +582,7 @@ __device__ __forceinline__ void load_rows(const PrefillParams &p, const PrefillF
 }
 
 // ---------------------------------------------------------------- the kernel
-template <bool TMA> constexpr int prefill_threads() { return TMA ? 384 : 512; }
+template <bool TMA> constexpr int prefill_threads() { return TMA ? 384 : 448; }
 
 template <int QK, int CK, int D, bool TMA, bool GS>
 __global__ void __launch_bounds__(prefill_threads<TMA>(), 1)
@@ -580,7 +593,8 @@ __global__ void __launch_bounds__(prefill_threads<TMA>(), 1)
     constexpr int ST = L::kStages;
     constexpr bool BF = QK == kBF16;
     constexpr int kMmaWarp = TMA ? 8 : 12;
-    constexpr int kQWarp = TMA ? 10 : 14;                       // two of them
+    constexpr int kQWarp = TMA ? 10 : 13;
+    constexpr int kQWarps = TMA ? 2 : 1;
     constexpr bool kVRef = GS && QK == kF16;                    // V scales are taken relative to a power of two
     const DecodeParams &d = p.d;
     extern __shared__ unsigned char smem_raw[];
@@ -599,11 +613,12 @@ __global__ void __launch_bounds__(prefill_threads<TMA>(), 1)
             ptx::mbar_init(bars.full(i), TMA ? 1 : 4);
             ptx::mbar_init(bars.empty(i), 1);
         }
-        ptx::mbar_init(bars.q_full(), 2);
+        ptx::mbar_init(bars.q_full(), kQWarps);
         ptx::mbar_init(bars.q_empty(), 1);
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(bars.s_full(i), 1);
             ptx::mbar_init(bars.p_full(i), 4);
+            ptx::mbar_init(bars.p_half(i), 4);
             ptx::mbar_init(bars.o_full(i), 1);
         }
         ptx::mbar_init(bars.tail(), 1);
@@ -621,7 +636,6 @@ __global__ void __launch_bounds__(prefill_threads<TMA>(), 1)
 
     if (warp < 8) {
         // ------------------------------------------------ softmax, a thread per row
-        if constexpr (TMA) tc::regs_inc<216>(); else tc::regs_inc<184>();
         const int sub = warp >> 2, row = threadIdx.x & 127;
         const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + sub * 128, to = tmem + lanes + 256 + sub * 128;
@@ -643,47 +657,63 @@ __global__ void __launch_bounds__(prefill_threads<TMA>(), 1)
                 float m = ninf, l = 0.0f, vref = 0.0f;
                 bool ok = true;
                 for (int k = w.k0; k < w.k1; ++k, ++tile_n, ++mine_n) {
-                    ok = bar_wait(bars.s_full(sub), mine_n & 1, gone);
+                    ok = warp_wait(bars.s_full(sub), mine_n & 1, gone);
                     if (!ok) break;
                     tc::fence_after();
                     const ColSlot &cs = cols[tile_n % L::kColSlots];
-                    uint32_t s[128];
-#pragma unroll
-                    for (int o = 0; o < 128; o += 32) tc::tmem_ld32(ts + o, s, o);
-#pragma unroll
-                    for (int o = 0; o < 128; o += 32) tc::tmem_ld_wait32(s, o);
-                    if constexpr (GS) {
-#pragma unroll
-                        for (int j = 0; j < 128; j += 4) {
-                            const float4 ks = *reinterpret_cast<const float4 *>(cs.k + j);
-                            s[j] = __float_as_uint(__uint_as_float(s[j]) * ks.x);
-                            s[j + 1] = __float_as_uint(__uint_as_float(s[j + 1]) * ks.y);
-                            s[j + 2] = __float_as_uint(__uint_as_float(s[j + 2]) * ks.z);
-                            s[j + 3] = __float_as_uint(__uint_as_float(s[j + 3]) * ks.w);
-                        }
-                    }
+                    // the tile's columns in four chunks of 32.  Three stay in registers from
+                    // the maximum on; chunk 2 is read twice, which costs less than the
+                    // registers would.
+                    uint32_t a[32], b[32], t[32];
+                    tc::tmem_ld32(ts, a, 0);
+                    tc::tmem_ld32(ts + 64, t, 0);
+                    tc::tmem_ld32(ts + 32, b, 0);
                     // keys behind the row's limit, and blocks that are not there
                     uint32_t there = cs.mask[0];
                     if constexpr (!TMA) there |= cs.mask[1] | cs.mask[2] | cs.mask[3];
                     const int rel = lim - k * kKeyTile;
                     const bool masked = __any_sync(0xffffffffu, rel < kKeyTile || there != 0xffffu);
-                    if (masked) {
+                    // scales and mask of a chunk
+                    auto prepare = [&](uint32_t (&x)[32], int ch) {
+                        if constexpr (GS) {
 #pragma unroll
-                        for (int j = 0; j < 128; ++j)
-                            if (j >= rel || !((there >> (j >> 3)) & 1u)) s[j] = 0xff800000u;
-                    }
-                    float mx[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(s[i]);
-#pragma unroll
-                    for (int j = 4; j < 128; j += 8) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float a = __uint_as_float(s[j + i]);
-                            mx[i] = j + 4 + i < 128 ? fmaxf(fmaxf(mx[i], a), __uint_as_float(s[(j + 4 + i) & 127]))
-                                                    : fmaxf(mx[i], a);
+                            for (int j = 0; j < 32; j += 4) {
+                                const float4 ks = *reinterpret_cast<const float4 *>(cs.k + 32 * ch + j);
+                                const float2 u = tc::mul2(f2(x, j), make_float2(ks.x, ks.y));
+                                const float2 v = tc::mul2(f2(x, j + 2), make_float2(ks.z, ks.w));
+                                x[j] = __float_as_uint(u.x);
+                                x[j + 1] = __float_as_uint(u.y);
+                                x[j + 2] = __float_as_uint(v.x);
+                                x[j + 3] = __float_as_uint(v.y);
+                            }
                         }
-                    }
+                        if (masked) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (32 * ch + j >= rel || !((there >> (4 * ch + (j >> 3))) & 1u)) x[j] = 0xff800000u;
+                        }
+                    };
+                    float mx[4] = {ninf, ninf, ninf, ninf};
+                    auto largest = [&](const uint32_t (&x)[32]) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(x[j + i])), __uint_as_float(x[j + 4 + i]));
+                    };
+                    tc::tmem_ld_wait32(a, 0);
+                    tc::tmem_ld_wait32(t, 0);
+                    tc::tmem_ld_wait32(b, 0);
+                    prepare(t, 2);
+                    largest(t);
+                    tc::tmem_ld32(ts + 96, t, 0);
+                    prepare(a, 0);
+                    largest(a);
+                    prepare(b, 1);
+                    largest(b);
+                    tc::tmem_ld_wait32(t, 0);
+                    prepare(t, 3);
+                    largest(t);
                     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     float grow = 1.0f;                          // what O and l shrink by
                     if (top > m && (m == ninf || (top - m) * c > 8.0f)) {
@@ -703,50 +733,57 @@ __global__ void __launch_bounds__(prefill_threads<TMA>(), 1)
                         vinv = 1.0f / vref;
                     }
                     if (k > w.k0 && __any_sync(0xffffffffu, grow != 1.0f)) {
+                        // seldom: a rolled loop keeps its registers out of the way
+#pragma unroll 1
+                        for (int o = 0; o < D; o += 16) {
+                            uint32_t x[16];
+                            tc::tmem_ld16_wait(to + o, x);
 #pragma unroll
-                        for (int o = 0; o < D; o += 32) {
-                            uint32_t a[32];
-                            tc::tmem_ld32(to + o, a, 0);
-                            tc::tmem_ld_wait32(a, 0);
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) a[j] = __float_as_uint(__uint_as_float(a[j]) * grow);
-                            tc::tmem_st32(to + o, a, 0);
+                            for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * grow);
+                            tc::tmem_st16(to + o, x);
                         }
                     }
                     const float off = m == ninf ? 0.0f : m * c;
-                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    const float2 c2 = make_float2(c, c), off2 = make_float2(-off, -off);
+                    float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+                    auto weights = [&](const uint32_t (&x)[32], int ch) {
+                        uint32_t pk[16];
 #pragma unroll
-                    for (int o = 0; o < 2; ++o) {
-                        uint32_t pk[32];
-#pragma unroll
-                        for (int j = 0; j < 64; j += 4) {
-                            float e[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                e[i] = exp2_approx(fmaf(__uint_as_float(s[64 * o + j + i]), c, -off));
-                                sum[i] += e[i];
-                            }
+                        for (int j = 0; j < 32; j += 2) {
+                            const float2 y = tc::fma2(f2(x, j), c2, off2);
+                            float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+                            sum[(j >> 1) & 1] = tc::add2(sum[(j >> 1) & 1], e);
                             if constexpr (GS) {
-                                const float4 vs = *reinterpret_cast<const float4 *>(cs.v + 64 * o + j);
-                                const float sc[4] = {vs.x, vs.y, vs.z, vs.w};
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const float y = e[i] * (kVRef ? sc[i] * vinv : sc[i]);
-                                    e[i] = masked && e[i] == 0.0f ? 0.0f : y;
-                                }
+                                float2 vs = *reinterpret_cast<const float2 *>(cs.v + 32 * ch + j);
+                                if constexpr (kVRef) vs = tc::mul2(vs, make_float2(vinv, vinv));
+                                const float2 z = tc::mul2(e, vs);
+                                e.x = masked && e.x == 0.0f ? 0.0f : z.x;
+                                e.y = masked && e.y == 0.0f ? 0.0f : z.y;
                             }
-                            pk[j / 2] = tc::pack16<QK>(e[0], e[1]);
-                            pk[j / 2 + 1] = tc::pack16<QK>(e[2], e[3]);
+                            pk[j >> 1] = tc::pack16<QK>(e.x, e.y);
                         }
-                        tc::tmem_st32(ts + 32 * o, pk, 0);
-                    }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                    tc::tmem_st_wait();
-                    tc::fence_before();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(bars.p_full(sub));
+                        tc::tmem_st16(ts + 16 * ch, pk);
+                    };
+                    auto hand = [&](uint32_t bar) {
+                        tc::tmem_st_wait();
+                        tc::fence_before();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(bar);
+                    };
+                    // P overwrites chunks 0 and 1, which are in registers by now
+                    weights(a, 0);
+                    tc::tmem_ld32(ts + 64, a, 0);
+                    weights(b, 1);
+                    tc::tmem_ld_wait32(a, 0);
+                    hand(bars.p_half(sub));
+                    prepare(a, 2);
+                    weights(a, 2);
+                    weights(t, 3);
+                    hand(bars.p_full(sub));
+                    sum[0] = tc::add2(sum[0], sum[1]);
+                    l += sum[0].x + sum[0].y;
                 }
-                if (!ok || !bar_wait(bars.o_full(sub), item_n & 1, gone)) break;
+                if (!ok || !warp_wait(bars.o_full(sub), item_n & 1, gone)) break;
                 ++item_n;
                 tc::fence_after();
                 const bool whole = w.k0 == 0 && w.k1 == w.units;
@@ -821,11 +858,6 @@ __global__ void __launch_bounds__(prefill_threads<TMA>(), 1)
             } while (w.next(p));
         }
     } else {
-        if constexpr (TMA) {
-            tc::regs_dec<72>();
-        } else {
-            if (warp < 12) tc::regs_dec<104>(); else tc::regs_dec<40>();
-        }
         if (warp == kMmaWarp) {
             // -------------------------------------------- the products
             if (work && lane == 0) {
@@ -855,16 +887,24 @@ __global__ void __launch_bounds__(prefill_threads<TMA>(), 1)
                     for (int j = 0; j < nk && ok; ++j) {
                         const uint32_t vpos = pos + 1, kpos = pos + 2;
                         for (int i = 0; i < ns; ++i) {
-                            ok = bar_wait(bars.p_full(i), n_p[i] & 1, gone);
+                            ok = bar_wait(bars.p_half(i), n_p[i] & 1, gone);
                             if (ok && i == 0) ok = bar_wait(bars.full(vpos % ST), (vpos / ST) & 1, gone);
+                            if (!ok) break;
+                            tc::fence_after();
+                            // P in two halves: the first keys' products run while the others' weights are made
+                            auto pv = [&](int ks) {
+                                tc::mma_ts(tmem + 256 + i * 128, tmem + i * 128 + ks * 8,
+                                           tc::smem_desc(sm32 + L::ring + (vpos % ST) * L::kTile + ks * 2048, 16384, 1024),
+                                           id_pv, j > 0 || ks > 0);
+                            };
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks) pv(ks);
+                            ok = bar_wait(bars.p_full(i), n_p[i] & 1, gone);
                             if (!ok) break;
                             ++n_p[i];
                             tc::fence_after();
 #pragma unroll
-                            for (int ks = 0; ks < kKeyTile / 16; ++ks)
-                                tc::mma_ts(tmem + 256 + i * 128, tmem + i * 128 + ks * 8,
-                                           tc::smem_desc(sm32 + L::ring + (vpos % ST) * L::kTile + ks * 2048, 16384, 1024),
-                                           id_pv, j > 0 || ks > 0);
+                            for (int ks = 4; ks < 8; ++ks) pv(ks);
                             if (j + 1 < nk) {
                                 if (i == 0) {
                                     ok = bar_wait(bars.full(kpos % ST), (kpos / ST) & 1, gone);
@@ -888,9 +928,9 @@ __global__ void __launch_bounds__(prefill_threads<TMA>(), 1)
                 } while (ok && w.next(p));
             }
             __syncwarp();
-        } else if (warp >= kQWarp && warp < kQWarp + 2) {
-            // -------------------------------------------- Q, a warp per subtile
-            const int sub = warp - kQWarp;
+        } else if (warp >= kQWarp && warp < kQWarp + kQWarps) {
+            // -------------------------------------------- Q, a warp per subtile or one for both
+            const int first = warp - kQWarp;
             const bool negate = d.scale_log2 < 0.0f;
             constexpr int PPR = D / 8;                          // pieces per row
             constexpr int RPI = 32 / PPR;                       // rows per instruction
@@ -899,8 +939,8 @@ __global__ void __launch_bounds__(prefill_threads<TMA>(), 1)
             bool have = work;
             if (work) w = walk_from(p, st);
             while (have) {
-                if (item > 0 && !bar_wait(bars.q_empty(), (item - 1) & 1, gone)) break;
-                if (sub < w.subtiles()) {
+                if (item > 0 && !warp_wait(bars.q_empty(), (item - 1) & 1, gone)) break;
+                for (int sub = first; sub < w.subtiles(); sub += kQWarps) {
                     const int c = lane % PPR;
                     int r = w.tile * kRowTile + sub * 128 + lane / PPR;
                     int tok = r / d.group, g = r - tok * d.group;
@@ -916,25 +956,27 @@ __global__ void __launch_bounds__(prefill_threads<TMA>(), 1)
                             ++tok;
                         }
                     }
-                    tc::cp_async_wait_all();
-                    if (negate) {
-                        for (int i = lane / PPR; i < 128; i += RPI) {
-                            uint4 v = tc::ld_shared16(dst + piece_at(i, c));
-                            v.x ^= 0x80008000u;
-                            v.y ^= 0x80008000u;
-                            v.z ^= 0x80008000u;
-                            v.w ^= 0x80008000u;
-                            tc::st_shared16(dst + piece_at(i, c), v);
-                        }
-                    }
-                    ptx::fence_proxy_async_smem();
                 }
+                tc::cp_async_wait_all();
+                for (int sub = first; negate && sub < w.subtiles(); sub += kQWarps) {
+                    const uint32_t dst = sm32 + L::q + sub * L::kTile;
+                    const int c = lane % PPR;
+                    for (int i = lane / PPR; i < 128; i += RPI) {
+                        uint4 v = tc::ld_shared16(dst + piece_at(i, c));
+                        v.x ^= 0x80008000u;
+                        v.y ^= 0x80008000u;
+                        v.z ^= 0x80008000u;
+                        v.w ^= 0x80008000u;
+                        tc::st_shared16(dst + piece_at(i, c), v);
+                    }
+                }
+                ptx::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(bars.q_full());
                 ++item;
                 have = w.next(p);
             }
-            if (sub == 0 && lane == 0) {
+            if (first == 0 && lane == 0) {
                 // the row tile that this CTA begins and does not end
                 int4 ds = make_int4(0, 0, 0, -1);
                 if (work && !have && w.k0 == 0 && w.k1 < w.units) {
@@ -975,8 +1017,7 @@ __global__ void __launch_bounds__(prefill_threads<TMA>(), 1)
 #pragma unroll
                         for (int kv = 0; kv < 2; ++kv, ++pos) {
                             const uint32_t stage = pos % ST;
-                            if (pos >= ST) ok = bar_wait(bars.empty(stage), (pos / ST - 1) & 1, gone);
-                            ok = __all_sync(0xffffffffu, ok);
+                            if (pos >= ST) ok = warp_wait(bars.empty(stage), (pos / ST - 1) & 1, gone);
                             if (!ok) break;
                             // V rows that nothing loads, or that no row sees, are zeroed: a weight of zero
                             // must not meet what lies there
@@ -999,9 +1040,8 @@ __global__ void __launch_bounds__(prefill_threads<TMA>(), 1)
                                                      w.h, blk);
                             }
                             if (fix) {
-                                ok = bar_wait(bar, fixes & 1, gone);
+                                ok = warp_wait(bar, fixes & 1, gone);
                                 ++fixes;
-                                ok = __all_sync(0xffffffffu, ok);
                                 if (!ok) break;
                                 for (int i = lane; i < kKeyTile * (D / 8); i += 32) {
                                     const int rr = i / (D / 8);
