@@ -30,20 +30,36 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder()
     return fn;
 }
 
-// (element, slot, kv head, block) of a 16-bit cache; a box is 64 elements
-// (one 128-byte swizzled row) of a block's slots, at most 128
-bool cache_map(CUtensorMap *m, const char *base, const DecodeParams &d, bool bf16)
+// A box is one block's slots (at most 128) of one kv head.  16-bit caches:
+// (element, slot, kv head, block), 64 elements (one 128-byte swizzled row).
+// Codes: the whole rows as bytes, (byte, slot, kv head, block), or
+// x-vectorised (byte of a piece, slot, piece, kv head, block).
+bool cache_map(CUtensorMap *m, const char *base, const DecodeParams &d, int kind)
 {
     auto enc = encoder();
     if (!enc || d.num_blocks == 0) return false;
-    cuuint64_t dims[4] = {cuuint64_t(d.head_dim), cuuint64_t(d.block_size), cuuint64_t(d.num_kv_heads),
-                          cuuint64_t(d.num_blocks)};
+    const bool coded = kind != kF16 && kind != kBF16;
+    const int row = kind == kU3 ? 3 * d.head_dim / 8 : d.head_dim;
+    const cuuint32_t slots = cuuint32_t(std::min(d.block_size, 128));
+    cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    if (coded && d.c_chunk != 16) {
+        cuuint64_t dims[5] = {16, cuuint64_t(d.block_size), cuuint64_t(row / 16), cuuint64_t(d.num_kv_heads),
+                              cuuint64_t(d.num_blocks)};
+        cuuint64_t strides[4] = {cuuint64_t(d.c_slot), cuuint64_t(d.c_chunk), cuuint64_t(d.c_head), cuuint64_t(d.c_blk)};
+        cuuint32_t box[5] = {16, slots, cuuint32_t(row / 16), 1, 1};
+        return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<char *>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    }
+    cuuint64_t dims[4] = {cuuint64_t(row), cuuint64_t(d.block_size), cuuint64_t(d.num_kv_heads), cuuint64_t(d.num_blocks)};
     cuuint64_t strides[3] = {cuuint64_t(d.c_slot), cuuint64_t(d.c_head), cuuint64_t(d.c_blk)};
-    cuuint32_t box[4] = {64, cuuint32_t(std::min(d.block_size, 128)), 1, 1};
-    cuuint32_t estr[4] = {1, 1, 1, 1};
-    return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<char *>(base),
-               dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    cuuint32_t box[4] = {cuuint32_t(coded ? row : 64), slots, 1, 1};
+    const CUtensorMapDataType type = coded ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : kind == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                     : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    return enc(m, type, 4, const_cast<char *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               coded ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
@@ -80,21 +96,21 @@ cudaError_t launch_prefill(const PrefillParams &p, const PrefillPlan &pl, int ca
     a.part_ml = w;
     a.part_acc = w + size_t(pl.grid) * 2 * 256 * 2 * sizeof(float);
     const DecodeParams &d = p.d;
+    a.out32 = (reinterpret_cast<uintptr_t>(d.out) | uintptr_t(d.o_b) | uintptr_t(d.o_h)) % 32 == 0;
+    // by TMA where a map of the cache can be made (and, for 16-bit caches, the
+    // rows are contiguous: x-vectorised ones take 16-byte copies)
+    const bool coded = cache_kind != kF16 && cache_kind != kBF16;
+    a.tma = (coded || d.c_chunk == 16) && cache_map(&a.tmk, d.k_cache, d, cache_kind) &&
+            cache_map(&a.tmv, d.v_cache, d, cache_kind);
+    a.raw_unit = (reinterpret_cast<uintptr_t>(d.k_cache) | reinterpret_cast<uintptr_t>(d.v_cache) | uintptr_t(d.c_blk) |
+                  uintptr_t(d.c_slot) | uintptr_t(d.c_head)) % 4 == 0 ? 4 : 1;
     switch (cache_kind) {
     case kF16:
-    case kBF16:
-        // whole pieces of blocks by TMA where the rows are contiguous and a
-        // map of the cache can be made; else (x-vectorised rows) 16-byte copies
-        a.tma = d.c_chunk == 16 && cache_map(&a.tmk, d.k_cache, d, cache_kind == kBF16) &&
-                cache_map(&a.tmv, d.v_cache, d, cache_kind == kBF16);
-        return launch_prefill_16(a);
+    case kBF16: return launch_prefill_16(a);
     case kE4M3: return launch_prefill_e4m3(a);
     case kE5M2: return launch_prefill_e5m2(a);
     case kI8: return launch_prefill_i8(a);
-    default:
-        a.rows_aligned = (reinterpret_cast<uintptr_t>(d.k_cache) | reinterpret_cast<uintptr_t>(d.v_cache) |
-                          uintptr_t(d.c_blk) | uintptr_t(d.c_slot) | uintptr_t(d.c_head)) % 4 == 0;
-        return launch_prefill_u3(a);
+    default: return launch_prefill_u3(a);
     }
 }
 

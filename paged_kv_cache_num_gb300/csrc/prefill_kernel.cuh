@@ -23,12 +23,15 @@
 //
 // CTA.  Two softmax warpgroups (one per subtile, a thread per row), one warp
 // that issues the products (tcgen05.mma, accumulators and P in tensor
-// memory), two warps that load Q, and the K/V producer: TMA copies of whole
-// block pieces for 16-bit caches in the flash layout (one warp), or four
-// warps that load, convert and store codes (one-byte and 3-bit caches) or
-// copy 16-byte pieces (other layouts).  While one subtile's softmax runs the
-// tensor core works on the other's products.
+// memory), warps that load Q, and the K/V producers.  While one subtile's
+// softmax runs the tensor core works on the other's products.  A row tile of
+// at most 128 rows has one subtile: then the warpgroups take its key tiles in
+// turn, with states of their own that are joined at the end.
 //
+// K/V.  16-bit caches in the flash layout: one warp issues TMA copies of
+// whole block pieces into the operand ring; x-vectorised 16-bit caches: four
+// warps copy 16-byte pieces.  One-byte and 3-bit caches: one warp issues TMA
+// copies of the raw codes, four warps convert them into the operand ring.
 // Codes are converted exactly (every code of every kind is a number of both
 // 16-bit types); their scales are applied in fp32: per-head scales to c and
 // to the result, per-row scales to the columns of S and of P.
@@ -45,7 +48,9 @@ struct PrefillFast {
     int4 *desc;                 // [grid] (sequence, kv head, row tile, last CTA) of the row tile split at a CTA's end
     float *part_ml;             // [2 grid][2][256]
     float *part_acc;            // [2 grid][D / 4][256][4]
-    int rows_aligned;           // 3-bit rows at multiples of 4 bytes
+    int out32;                  // output rows at multiples of 32 bytes
+    int raw_tma;                // raw codes by TMA (else by loads of the producer warp)
+    int raw_unit;               // ... of 4 bytes or 1
 };
 
 namespace {
@@ -228,30 +233,43 @@ __device__ __forceinline__ void find_start(const PrefillParams &p, int64_t *bins
 }
 
 // ---------------------------------------------------------------- shared memory
-template <int D>
+template <int CK> constexpr bool is_coded() { return CK != kF16 && CK != kBF16; }
+template <int CK, int D> constexpr int raw_row() { return CK == kU3 ? 3 * D / 8 : D; }
+
+template <int CK, int D>
 struct Smem {
-    static constexpr int kTile = 128 * D * 2;                   // bytes of 128 rows
-    static constexpr int kStages = D == 128 ? 4 : 8;
-    static constexpr int kColSlots = kStages;                    // see ColSlot
+    static constexpr bool kCoded = is_coded<CK>();
+    static constexpr int kTile = 128 * D * 2;                   // bytes of 128 operand rows
+    static constexpr int kStages = (kCoded ? 3 : 4) * (D == 128 ? 1 : 2);
+    static constexpr int kRaw = kCoded ? kStages : 0;           // stages of raw codes
+    static constexpr int kRawTile = kCoded ? 128 * raw_row<CK, D>() : 0;
+    static constexpr int kColSlots = D == 128 ? 4 : 8;          // see ColSlot
     static constexpr int q = 0;
     static constexpr int ring = 2 * kTile;
-    static constexpr int cols = ring + kStages * kTile;         // kColSlots x ColSlot
+    static constexpr int raw = ring + kStages * kTile;
+    static constexpr int cols = raw + kRaw * kRawTile;
     static constexpr int kColBytes = 2 * kKeyTile * 4 + 32;
-    static constexpr int bars = cols + kColSlots * kColBytes;
-    static constexpr int n_bars = 2 * kStages + 2 + 4 * 2 + 1;
-    static constexpr int misc = bars + 8 * n_bars;
+    static constexpr int ones = cols + kColSlots * kColBytes;   // 128 ones
+    static constexpr int state = ones + 512;                    // warpgroup 1's (m, l) for the join
+    static constexpr int bars = state + 1024;
+    static constexpr int n_bars = 2 * kStages + 2 * kRaw + 2 + 4 * 2 + 1 + 2;
+    static constexpr int info = bars + 8 * n_bars;              // per raw stage: which blocks are there
+    static constexpr int misc = (info + 4 * 8 + 15) / 16 * 16;
     static constexpr int total = misc + 128;
     static constexpr int alloc = total + 1024;                  // the base is rounded up to 1024
     static_assert(kStages * kTile >= (kBins + 1) * 8, "bins lie in the ring");
+    static_assert(kRaw <= 8, "info");
     static_assert(alloc <= 232448, "shared memory of a CTA");
     static_assert(sizeof(Start) <= 96, "misc");
 };
 
 // Column data of a key tile: scales of its 128 K and V rows, the largest V
 // scale of each 32 rows, and which groups of 8 rows are there.  Tile T's is
-// written once K's stage of tile T - kStages / 2 is free: its products are
-// done then, and both subtiles' softmax of the tiles before it, so a ring of
-// kStages / 2 + 1 slots or more is never written while it is read.
+// written once the ring has room for K of tile T.  With 2 R stages that is
+// when the scores of tile T - R are done, and so the softmax of tile
+// T - R - 2 at the latest (scores run at most two tiles ahead of a softmax):
+// R + 2 slots are enough (R = 2 or 4).  With three (six) stages it is when
+// P V of tile T - 2 (the scores of tile T - 3) are done: 2 (5) slots.
 struct ColSlot {
     float k[kKeyTile];
     float v[kKeyTile];
@@ -261,7 +279,7 @@ struct ColSlot {
 
 struct Bars {
     uint32_t base;
-    int stages;
+    int stages, raws;
     __device__ __forceinline__ uint32_t full(int s) const { return base + 8 * s; }
     __device__ __forceinline__ uint32_t empty(int s) const { return base + 8 * (stages + s); }
     __device__ __forceinline__ uint32_t q_full() const { return base + 8 * (2 * stages); }
@@ -271,6 +289,11 @@ struct Bars {
     __device__ __forceinline__ uint32_t o_full(int i) const { return base + 8 * (2 * stages + 6 + i); }
     __device__ __forceinline__ uint32_t p_half(int i) const { return base + 8 * (2 * stages + 8 + i); }
     __device__ __forceinline__ uint32_t tail() const { return base + 8 * (2 * stages + 10); }
+    // the join of two warpgroups' states: warpgroup 1's is there, and has been read
+    __device__ __forceinline__ uint32_t j_full() const { return base + 8 * (2 * stages + 11); }
+    __device__ __forceinline__ uint32_t j_empty() const { return base + 8 * (2 * stages + 12); }
+    __device__ __forceinline__ uint32_t raw_full(int s) const { return base + 8 * (2 * stages + 13 + s); }
+    __device__ __forceinline__ uint32_t raw_empty(int s) const { return base + 8 * (2 * stages + 13 + raws + s); }
 };
 
 // Wait for a phase, giving up when it takes too long or another warp gave up.
@@ -369,233 +392,322 @@ __device__ __forceinline__ uint4 u3x8_to_16(uint32_t w, uint32_t zero2)
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// ---------------------------------------------------------------- K/V by loads
-// Rows 32 lw .. 32 lw + 31 of every key tile, by one warp (lane = row for
-// the lookups): codes are loaded, converted to the 16-bit operand type and
-// stored swizzled; 16-bit pieces are copied.  A stage's loads are issued
-// before the stage before it is converted.
-template <int QK, int CK, int D, bool GS>
-__device__ __forceinline__ void load_rows(const PrefillParams &p, const PrefillFast &f, const Start &st, bool work,
-                                          uint32_t ring, ColSlot *cols, const Bars &bars, volatile int *gone, int lw,
-                                          int lane)
+// ---------------------------------------------------------------- K/V producers
+// Where a producer stands: the key tiles of the CTA's segments in order.
+struct TileWalk {
+    Walk w;
+    int k;
+    __device__ __forceinline__ bool next(const PrefillParams &p)
+    {
+        if (++k < w.k1) return true;
+        if (!w.next(p)) return false;
+        k = w.k0;
+        return true;
+    }
+};
+
+// 16-bit rows by 16-byte copies, rows 32 lw .. 32 lw + 31 of every tile by
+// one warp: a lane copies its row's pieces (neighbouring slots are neighbours
+// in the x-vectorised layout).  A stage is handed over once the next one's
+// copies are under way.
+template <int CK, int D>
+__device__ __forceinline__ void copy_rows(const PrefillParams &p, const Start &st, uint32_t ring, ColSlot *cols,
+                                          const Bars &bars, volatile int *gone, int lw, int lane)
 {
-    using L = Smem<D>;
+    using L = Smem<CK, D>;
     constexpr int ST = L::kStages;
-    constexpr bool kCopy = CK == kF16 || CK == kBF16;
-    constexpr int kLoads = CK == kU3 ? D / 32 : D / 16;         // per lane and stage (codes)
-    constexpr int kWords = CK == kU3 ? 3 : 4;
-    if (!work) return;
     const DecodeParams &d = p.d;
     const int row = 32 * lw + lane;
-    Walk w = walk_from(p, st);
+    TileWalk tw{walk_from(p, st), 0};
+    tw.k = tw.w.k0;
     uint32_t pos = 0, tile_n = 0;
-    int k = w.k0;
-    // this lane's row of the current tile
-    int64_t at = 0;
-    bool in = false;
-    float ks = 0.0f, vs = 0.0f, kz = 0.0f, vz = 0.0f;
-    auto lookup = [&]() {
-        const int t = k * kKeyTile + row;
-        in = t < w.limit;
+    int pending = -1;
+    auto flush = [&](bool all) {
+        if (pending < 0) return;
+        if (all) tc::cp_async_wait<0>(); else tc::cp_async_wait<1>();
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bars.full(pending));
+        pending = -1;
+    };
+    do {
+        const int t = tw.k * kKeyTile + row;
+        bool in = t < tw.w.limit;
         int64_t blk = 0;
         if (in) {
-            blk = d.block_tables[w.b * d.bt_b + int64_t(t >> d.block_shift) * d.bt_j];
+            blk = d.block_tables[tw.w.b * d.bt_b + int64_t(t >> d.block_shift) * d.bt_j];
             if (blk < 0 || blk >= d.num_blocks) {
                 raise_err(d.err_flag, PKV_DEVERR_BLOCK_RANGE);
                 in = false;
             }
         }
-        const int64_t slot = t & (d.block_size - 1);
-        at = in ? blk * d.c_blk + slot * d.c_slot + w.h * d.c_head : 0;
-        if constexpr (GS) {
-            ks = vs = kz = vz = 0.0f;
-            if (in) {
-                if constexpr (CK == kU3) {
-                    const int64_t m = blk * d.m_blk + slot * d.m_slot + w.h * d.m_head;
-                    const int64_t z = blk * d.z_blk + slot * d.z_slot + w.h * d.z_head;
-                    ks = __half2float(__ushort_as_half(__ldg(d.k_qs + m)));
-                    vs = __half2float(__ushort_as_half(__ldg(d.v_qs + m)));
-                    kz = float(__ldg(d.k_qz + z));
-                    vz = float(__ldg(d.v_qz + z));
-                } else {
-                    const int64_t m = blk * d.gs_blk + slot * d.gs_slot + w.h * d.gs_head;
-                    ks = __ldg(d.k_gs + m);
-                    vs = __ldg(d.v_gs + m);
-                }
-            }
-        }
-    };
-    auto columns = [&]() {                                      // before K's arrival
-        ColSlot &cs = cols[tile_n % L::kColSlots];
+        const int64_t at = in ? blk * d.c_blk + int64_t(t & (d.block_size - 1)) * d.c_slot + tw.w.h * d.c_head : 0;
         const unsigned got = __ballot_sync(0xffffffffu, in);
-        if constexpr (GS) {
-            cs.k[row] = ks;
-            cs.v[row] = vs;
-            float mx = vs;
+        for (int kv = 0; kv < 2; ++kv, ++pos) {
+            // never wait for room with a stage in hand
+            if (!__all_sync(0xffffffffu, pos < ST || ptx::mbar_try_wait(bars.empty(pos % ST), (pos / ST - 1) & 1)))
+                flush(true);
+            if (pos >= ST && !warp_wait(bars.empty(pos % ST), (pos / ST - 1) & 1, gone)) return;
+            if (kv == 0 && lane == 0) {
+                uint32_t there = 0;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            if (lane == 0) cs.vmax[lw] = mx;
-        }
-        if (lane == 0) {
-            uint32_t there = 0;
+                for (int i = 0; i < 4; ++i) there |= ((got >> (8 * i)) & 0xffu ? 1u : 0u) << (4 * lw + i);
+                cols[tile_n % L::kColSlots].mask[lw] = there;
+            }
+            const char *src = (kv ? d.v_cache : d.k_cache) + at;
+            const uint32_t dst = ring + (pos % ST) * L::kTile;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) there |= ((got >> (8 * i)) & 0xffu ? 1u : 0u) << (4 * lw + i);
-            cs.mask[lw] = there;
+            for (int c = 0; c < D / 8; ++c) tc::cp_async16(dst + piece_at(row, c), src + (in ? c * d.c_chunk : 0), in);
+            tc::cp_async_commit();
+            flush(false);
+            pending = int(pos % ST);
         }
-    };
-    auto step = [&]() -> bool {                                 // to the next tile
         ++tile_n;
-        if (++k < w.k1) return true;
-        if (!w.next(p)) return false;
-        k = w.k0;
-        return true;
+    } while (tw.next(p));
+    flush(true);
+}
+
+// Raw codes of every tile into the raw ring, by one warp: one TMA copy per
+// block, [rows][row bytes], or [16-byte piece][rows][16] of an x-vectorised
+// cache; or by loads where no tensor map can be made.
+template <int CK, int D>
+__device__ __forceinline__ void raw_codes(const PrefillParams &p, const PrefillFast &f, const Start &st, unsigned char *sm,
+                                          uint32_t sm32, const Bars &bars, const CUtensorMap *tmk, const CUtensorMap *tmv,
+                                          volatile int *gone, int lane)
+{
+    using L = Smem<CK, D>;
+    constexpr int RB = raw_row<CK, D>();
+    const DecodeParams &d = p.d;
+    const int shift = min(d.block_shift, 7), rows = 1 << shift, nblk = kKeyTile >> shift;
+    uint32_t *info = reinterpret_cast<uint32_t *>(sm + L::info);
+    TileWalk tw{walk_from(p, st), 0};
+    tw.k = tw.w.k0;
+    if (lane == 0) {
+        ptx::prefetch_tmap(tmk);
+        ptx::prefetch_tmap(tmv);
+    }
+    // this lane's block of the tile, -1 where it wants none
+    auto lookup = [&]() -> int {
+        const int t = tw.k * kKeyTile + lane * rows;
+        return lane < nblk && t < tw.w.limit
+                   ? d.block_tables[tw.w.b * d.bt_b + int64_t(t >> d.block_shift) * d.bt_j] : -1;
     };
-    auto room = [&]() -> bool {
-        return pos < ST || warp_wait(bars.empty(pos % ST), (pos / ST - 1) & 1, gone);
-    };
-    auto arrive = [&](uint32_t stage) {
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bars.full(stage));
-    };
-    if constexpr (kCopy) {
-        // a lane copies its row's 16-byte pieces (neighbouring slots are
-        // neighbours in the x-vectorised layout); a stage is handed over
-        // once the next one's copies are under way
-        int pending = -1;
-        auto flush = [&](bool all) {
-            if (pending < 0) return;
-            if (all) tc::cp_async_wait<0>(); else tc::cp_async_wait<1>();
-            arrive(pending);
-            pending = -1;
-        };
-        bool more = true;
-        while (more) {
-            lookup();
-            for (int kv = 0; kv < 2; ++kv, ++pos) {
-                // never wait for room with a stage in hand
-                if (!__all_sync(0xffffffffu, pos < ST || ptx::mbar_try_wait(bars.empty(pos % ST), (pos / ST - 1) & 1)))
-                    flush(true);
-                if (!room()) return;
-                if (kv == 0) columns();
-                const char *src = (kv ? d.v_cache : d.k_cache) + at;
-                const uint32_t dst = ring + (pos % ST) * L::kTile;
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c) tc::cp_async16(dst + piece_at(row, c), src + (in ? c * d.c_chunk : 0), in);
-                tc::cp_async_commit();
-                flush(false);
-                pending = int(pos % ST);
-            }
-            more = step();
-        }
-        flush(true);
-    } else {
-        uint32_t kr[kLoads][kWords], vr[kLoads][kWords];
-        // lane -> (row of 32, piece): 16 codes of a one-byte row, 32 codes
-        // (12 bytes) of a 3-bit row; the 8 lanes of a store phase hit
-        // 8 different 16-byte columns of the banks
-        auto place = [&](int i, int &r, int &c) {
-            if constexpr (CK == kU3) {
-                r = (lane >> 1) + 16 * (i & 1);
-                c = (lane & 1) + 2 * (i >> 1);
+    uint32_t pos = 0;
+    int blk = lookup();
+    bool more = true;
+    while (more) {
+        const int t = tw.k * kKeyTile + lane * rows, h = tw.w.h;
+        const bool want = lane < nblk && t < tw.w.limit;
+        const bool in = want && blk >= 0 && blk < d.num_blocks;
+        if (want && !in) raise_err(d.err_flag, PKV_DEVERR_BLOCK_RANGE);
+        const unsigned got = __ballot_sync(0xffffffffu, in);
+        const int now = blk, slot0 = t & (d.block_size - 1);
+        more = tw.next(p);
+        if (more) blk = lookup();
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv, ++pos) {
+            const uint32_t s = pos % L::kRaw;
+            if (pos >= L::kRaw && !warp_wait(bars.raw_empty(s), (pos / L::kRaw - 1) & 1, gone)) return;
+            if (lane == 0) info[s] = got;
+            const uint32_t dst = sm32 + L::raw + s * L::kRawTile;
+            if (f.raw_tma) {
+                if (lane == 0) ptx::mbar_arrive_expect_tx(bars.raw_full(s), uint32_t(__popc(got) * rows * RB));
+                __syncwarp();
+                if (in) {
+                    const CUtensorMap *m = kv ? tmv : tmk;
+                    if (d.c_chunk == 16 || CK == kU3)
+                        ptx::tma_load_4d(dst + lane * rows * RB, m, bars.raw_full(s), 0, slot0, h, now);
+                    else
+                        ptx::tma_load_5d(dst + lane * rows * RB, m, bars.raw_full(s), 0, slot0, 0, h, now);
+                }
             } else {
-                r = i * (32 / kLoads) + lane / kLoads;
-                c = lane % kLoads;
-            }
-        };
-        auto load = [&](const char *cache, uint32_t (&x)[kLoads][kWords]) {
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                int r, c;
-                place(i, r, c);
-                const int64_t o = __shfl_sync(0xffffffffu, at, r);
-                const bool ok = __shfl_sync(0xffffffffu, int(in), r);
-#pragma unroll
-                for (int j = 0; j < kWords; ++j) x[i][j] = 0u;
-                if constexpr (CK == kU3) {
-                    const char *src = cache + o + 12 * c;
-                    if (!ok) {
-                    } else if (f.rows_aligned) {
-#pragma unroll
-                        for (int j = 0; j < 3; ++j) x[i][j] = __ldg(reinterpret_cast<const uint32_t *>(src) + j);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 12; ++j)
-                            x[i][j >> 2] |= uint32_t(__ldg(reinterpret_cast<const uint8_t *>(src) + j)) << (8 * (j & 3));
+                const char *cache = kv ? d.v_cache : d.k_cache;
+                unsigned char *to = sm + L::raw + s * L::kRawTile;
+                for (int i = 0; i < kKeyTile; ++i) {
+                    const int b = __shfl_sync(0xffffffffu, now, i >> shift);
+                    const int o = __shfl_sync(0xffffffffu, slot0, i >> shift) + (i & (rows - 1));
+                    if (!((got >> (i >> shift)) & 1u)) continue;
+                    const char *src = cache + b * d.c_blk + o * d.c_slot + h * d.c_head;
+                    for (int j = lane * f.raw_unit; j < RB; j += 32 * f.raw_unit) {
+                        const bool xv = d.c_chunk != 16 && CK != kU3;
+                        const char *from = xv ? src + (j >> 4) * d.c_chunk + (j & 15) : src + j;
+                        unsigned char *at = to + (i >> shift) * rows * RB +
+                                            (xv ? (j >> 4) * rows * 16 + (i & (rows - 1)) * 16 + (j & 15)
+                                                : (i & (rows - 1)) * RB + j);
+                        if (f.raw_unit == 4)
+                            *reinterpret_cast<uint32_t *>(at) = __ldg(reinterpret_cast<const uint32_t *>(from));
+                        else
+                            *at = __ldg(reinterpret_cast<const unsigned char *>(from));
                     }
-                } else {
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (ok) v = __ldg(reinterpret_cast<const uint4 *>(cache + o + c * d.c_chunk));
-                    x[i][0] = v.x;
-                    x[i][1] = v.y;
-                    x[i][2] = v.z;
-                    x[i][kWords - 1] = v.w;
                 }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bars.raw_full(s));
             }
-        };
-        auto store = [&](uint32_t dst, const uint32_t (&x)[kLoads][kWords], float zero) {
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                int r, c;
-                place(i, r, c);
-                const int rr = 32 * lw + r;
-                if constexpr (CK == kU3) {
-                    const float z = __shfl_sync(0xffffffffu, zero, r);
-                    const uint32_t z2 = QK == kBF16 ? tc::pack16<QK>(z, z) : tc::pack16<QK>(1024.0f + z, 1024.0f + z);
-                    const uint32_t w0 = x[i][0], w1 = x[i][1], w2 = x[i][2];
-                    const uint32_t fl[4] = {w0, __funnelshift_r(w0, w1, 24), __funnelshift_r(w1, w2, 16), w2 >> 8};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) tc::st_shared16(dst + piece_at(rr, 4 * c + j), u3x8_to_16<QK>(fl[j], z2));
-                } else {
-                    uint4 o[2];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint2 a = q8x4_to_16<QK, CK>(x[i][2 * j]), b = q8x4_to_16<QK, CK>(x[i][2 * j + 1]);
-                        o[j] = make_uint4(a.x, a.y, b.x, b.y);
-                    }
-                    const int a = D == 128 ? c >> 2 : 0;
-                    tc::st_shared16(dst + piece_at(rr, 2 * c + a), a ? o[1] : o[0]);
-                    tc::st_shared16(dst + piece_at(rr, 2 * c + 1 - a), a ? o[0] : o[1]);
-                }
-            }
-        };
-        lookup();
-        load(d.k_cache, kr);
-        bool more = true;
-        while (more) {
-            load(d.v_cache, vr);
-            const float kz_now = kz, vz_now = vz;
-            if (!room()) return;
-            columns();
-            more = step();
-            if (more) lookup();
-            store(ring + (pos % ST) * L::kTile, kr, kz_now);
-            arrive(pos % ST);
-            ++pos;
-            if (more) load(d.k_cache, kr);
-            if (!room()) return;
-            store(ring + (pos % ST) * L::kTile, vr, vz_now);
-            arrive(pos % ST);
-            ++pos;
         }
     }
 }
 
-// ---------------------------------------------------------------- the kernel
-template <bool TMA> constexpr int prefill_threads() { return TMA ? 384 : 448; }
+// Raw codes -> operand ring, rows 32 lw .. 32 lw + 31 of every tile by one
+// warp (lane = row for the scales).  The loop over a row's pieces is rolled:
+// four roles share the SM's instruction cache.
+template <int QK, int CK, int D, bool GS>
+__device__ __forceinline__ void convert_rows(const PrefillParams &p, const Start &st, unsigned char *sm, uint32_t sm32,
+                                             const Bars &bars, volatile int *gone, int lw, int lane)
+{
+    using L = Smem<CK, D>;
+    constexpr int ST = L::kStages, RB = raw_row<CK, D>();
+    constexpr int kPieces = CK == kU3 ? D / 32 : D / 16;        // per row and per lane: 16 one-byte codes, or 32
+                                                                // 3-bit ones (12 bytes)
+    const DecodeParams &d = p.d;
+    const uint32_t *info = reinterpret_cast<const uint32_t *>(sm + L::info);
+    ColSlot *cols = reinterpret_cast<ColSlot *>(sm + L::cols);
+    const int row = 32 * lw + lane;
+    const int shift = min(d.block_shift, 7), rows = 1 << shift;
+    const bool xv = d.c_chunk != 16 && CK != kU3;
+    TileWalk tw{walk_from(p, st), 0};
+    tw.k = tw.w.k0;
+    uint32_t pos = 0, tile_n = 0;
+    // scales of this lane's row: a tile ahead, its table entry two ahead
+    int64_t entry = -1;
+    float ks = 0.0f, vs = 0.0f, kz = 0.0f, vz = 0.0f;
+    TileWalk ahead = tw;
+    bool ahead_more = GS;
+    auto fetch = [&]() {
+        const int t = ahead.k * kKeyTile + row;
+        entry = t < ahead.w.limit
+                    ? d.block_tables[ahead.w.b * d.bt_b + int64_t(t >> d.block_shift) * d.bt_j] : -1;
+    };
+    auto scales = [&](const TileWalk &x) {
+        ks = vs = kz = vz = 0.0f;
+        if (entry < 0 || entry >= d.num_blocks) return;
+        const int64_t slot = (x.k * kKeyTile + row) & (d.block_size - 1);
+        if constexpr (CK == kU3) {
+            const int64_t m = entry * d.m_blk + slot * d.m_slot + x.w.h * d.m_head;
+            const int64_t z = entry * d.z_blk + slot * d.z_slot + x.w.h * d.z_head;
+            ks = __half2float(__ushort_as_half(__ldg(d.k_qs + m)));
+            vs = __half2float(__ushort_as_half(__ldg(d.v_qs + m)));
+            kz = float(__ldg(d.k_qz + z));
+            vz = float(__ldg(d.v_qz + z));
+        } else {
+            const int64_t m = entry * d.gs_blk + slot * d.gs_slot + x.w.h * d.gs_head;
+            ks = __ldg(d.k_gs + m);
+            vs = __ldg(d.v_gs + m);
+        }
+    };
+    if constexpr (GS) {
+        fetch();
+        scales(tw);
+        ahead_more = ahead.next(p);
+        if (ahead_more) fetch();
+    }
+    bool more = true;
+    while (more) {
+        const int limit = tw.w.limit - tw.k * kKeyTile;         // rows of the tile that are wanted
+        const float zero[2] = {kz, vz};
+        unsigned ok = 0;
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv, ++pos) {
+            const uint32_t rs = pos % L::kRaw, s = pos % ST;
+            if (!warp_wait(bars.raw_full(rs), (pos / L::kRaw) & 1, gone)) return;
+            if (pos >= ST && !warp_wait(bars.empty(s), (pos / ST - 1) & 1, gone)) return;
+            if (kv == 0) {
+                const unsigned got = info[rs];
+                ok = __ballot_sync(0xffffffffu, row < limit && ((got >> (row >> shift)) & 1u));
+                ColSlot &cs = cols[tile_n % L::kColSlots];
+                if constexpr (GS) {
+                    cs.k[row] = ks;
+                    cs.v[row] = vs;
+                    float mx = vs;
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    if (lane == 0) cs.vmax[lw] = mx;
+                }
+                if (lane == 0) {
+                    uint32_t there = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) there |= ((ok >> (8 * i)) & 0xffu ? 1u : 0u) << (4 * lw + i);
+                    cs.mask[lw] = there;
+                }
+                if constexpr (GS) {                             // the next tile's scales, the one after's entry
+                    if (ahead_more) {
+                        scales(ahead);
+                        ahead_more = ahead.next(p);
+                        if (ahead_more) fetch();
+                    }
+                }
+            }
+            const unsigned char *from = sm + L::raw + rs * L::kRawTile;
+            const uint32_t dst = sm32 + L::ring + s * L::kTile;
+#pragma unroll 2
+            for (int i = 0; i < kPieces; ++i) {
+                // lane -> (row, piece) so that the 8 lanes of a load or store phase
+                // hit different banks
+                int r, c;
+                if constexpr (CK == kU3) {
+                    r = (lane >> 1) + 16 * (i & 1);
+                    c = (lane & 1) + 2 * (i >> 1);
+                } else if (xv) {
+                    r = lane;
+                    c = i;
+                } else {
+                    r = i * (32 / kPieces) + lane / kPieces;
+                    c = lane % kPieces;
+                }
+                const int rr = 32 * lw + r;
+                const bool there = (ok >> r) & 1u;
+                if constexpr (CK == kU3) {
+                    const uint32_t *src = reinterpret_cast<const uint32_t *>(from + rr * RB + 12 * c);
+                    const uint32_t w0 = there ? src[0] : 0u, w1 = there ? src[1] : 0u, w2 = there ? src[2] : 0u;
+                    const float z = __shfl_sync(0xffffffffu, zero[kv], r);
+                    const uint32_t z2 = QK == kBF16 ? tc::pack16<QK>(z, z) : tc::pack16<QK>(1024.0f + z, 1024.0f + z);
+                    const uint32_t fl[4] = {w0, __funnelshift_r(w0, w1, 24), __funnelshift_r(w1, w2, 16), w2 >> 8};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) tc::st_shared16(dst + piece_at(rr, 4 * c + j), u3x8_to_16<QK>(fl[j], z2));
+                } else {
+                    const unsigned char *src =
+                        xv ? from + (rr >> shift) * rows * RB + c * rows * 16 + (rr & (rows - 1)) * 16 : from + rr * RB + 16 * c;
+                    uint4 v = *reinterpret_cast<const uint4 *>(src);
+                    if (!there) v = make_uint4(0, 0, 0, 0);
+                    const uint2 a = q8x4_to_16<QK, CK>(v.x), b = q8x4_to_16<QK, CK>(v.y);
+                    const uint2 e = q8x4_to_16<QK, CK>(v.z), g = q8x4_to_16<QK, CK>(v.w);
+                    const uint4 o0 = make_uint4(a.x, a.y, b.x, b.y), o1 = make_uint4(e.x, e.y, g.x, g.y);
+                    const bool swap = D == 128 && !xv && (c >> 2);
+                    tc::st_shared16(dst + piece_at(rr, 2 * c + swap), swap ? o1 : o0);
+                    tc::st_shared16(dst + piece_at(rr, 2 * c + 1 - swap), swap ? o0 : o1);
+                }
+            }
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                ptx::mbar_arrive(bars.full(s));
+                ptx::mbar_arrive(bars.raw_empty(rs));
+            }
+        }
+        ++tile_n;
+        more = tw.next(p);
+    }
+}
 
-template <int QK, int CK, int D, bool TMA, bool GS>
-__global__ void __launch_bounds__(prefill_threads<TMA>(), 1)
+// ---------------------------------------------------------------- the kernel
+// Warps 0-7 softmax, 8-11 producers; 16-bit caches by TMA have the products
+// among the latter, the others in a fourth warpgroup.  Registers: the pool is
+// what the block was launched with.
+enum Feed : int { kFeedTma, kFeedCopy, kFeedCodes };
+template <int CK> constexpr int feed_of(bool tma) { return is_coded<CK>() ? kFeedCodes : tma ? kFeedTma : kFeedCopy; }
+template <int FEED> constexpr int prefill_threads() { return FEED == kFeedTma ? 384 : 512; }
+
+template <int QK, int CK, int D, int FEED, bool GS>
+__global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
     prefill_kernel(PrefillParams p, PrefillFast f, const __grid_constant__ CUtensorMap tmk,
                    const __grid_constant__ CUtensorMap tmv)
 {
-    using L = Smem<D>;
+    using L = Smem<CK, D>;
     constexpr int ST = L::kStages;
+    constexpr bool TMA = FEED == kFeedTma;
     constexpr bool BF = QK == kBF16;
     constexpr int kMmaWarp = TMA ? 8 : 12;
-    constexpr int kQWarp = TMA ? 10 : 13;
-    constexpr int kQWarps = TMA ? 2 : 1;
-    constexpr bool kVRef = GS && QK == kF16;                    // V scales are taken relative to a power of two
+    constexpr int kQWarp = TMA ? 10 : 14;                       // two of them
+    constexpr bool kVRef = GS && QK == kF16;                    // P relative to the V scales' magnitude
     const DecodeParams &d = p.d;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *sm = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -605,7 +717,7 @@ __global__ void __launch_bounds__(prefill_threads<TMA>(), 1)
     uint32_t *tmem_at = reinterpret_cast<uint32_t *>(sm + L::misc + 104);
     ColSlot *cols = reinterpret_cast<ColSlot *>(sm + L::cols);
     static_assert(sizeof(ColSlot) == L::kColBytes, "column slots");
-    const Bars bars{sm32 + L::bars, ST};
+    const Bars bars{sm32 + L::bars, ST, L::kRaw};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -613,7 +725,11 @@ __global__ void __launch_bounds__(prefill_threads<TMA>(), 1)
             ptx::mbar_init(bars.full(i), TMA ? 1 : 4);
             ptx::mbar_init(bars.empty(i), 1);
         }
-        ptx::mbar_init(bars.q_full(), kQWarps);
+        for (int i = 0; i < L::kRaw; ++i) {
+            ptx::mbar_init(bars.raw_full(i), 1);
+            ptx::mbar_init(bars.raw_empty(i), 4);
+        }
+        ptx::mbar_init(bars.q_full(), 2);
         ptx::mbar_init(bars.q_empty(), 1);
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(bars.s_full(i), 1);
@@ -622,9 +738,12 @@ __global__ void __launch_bounds__(prefill_threads<TMA>(), 1)
             ptx::mbar_init(bars.o_full(i), 1);
         }
         ptx::mbar_init(bars.tail(), 1);
+        ptx::mbar_init(bars.j_full(), 4);
+        ptx::mbar_init(bars.j_empty(), 4);
         ptx::fence_mbar_init();
         *gone = 0;
     }
+    if (threadIdx.x < 128) reinterpret_cast<float *>(sm + L::ones)[threadIdx.x] = 1.0f;
     if (warp == kMmaWarp) tc::tmem_alloc(ptx::smem_u32(tmem_at), 512);
     griddep_wait();
     griddep_launch_dependents();
@@ -636,131 +755,154 @@ __global__ void __launch_bounds__(prefill_threads<TMA>(), 1)
 
     if (warp < 8) {
         // ------------------------------------------------ softmax, a thread per row
+        if constexpr (!TMA) tc::regs_inc<152>();
         const int sub = warp >> 2, row = threadIdx.x & 127;
         const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + sub * 128, to = tmem + lanes + 256 + sub * 128;
-        uint32_t tile_n = 0, mine_n = 0, item_n = 0;            // key tiles of the CTA, of this subtile, segments
+        float *state = reinterpret_cast<float *>(sm + L::state) + row;      // m, l of warpgroup 1
+        uint32_t tile_n = 0, mine_n = 0, joins = 0;             // key tiles of the CTA, of this warpgroup; joins
+        uint32_t outs[2] = {0, 0};                              // accumulators completed so far
         if (work) {
             Walk w = walk_from(p, st);
             do {
-                if (sub >= w.subtiles()) {
-                    tile_n += w.k1 - w.k0;
-                    continue;
-                }
-                const int r = w.tile * kRowTile + sub * 128 + row;
+                const int nk = w.k1 - w.k0;
+                const bool split = w.subtiles() == 1;           // both warpgroups on one subtile
+                const int r = w.tile * kRowTile + (split ? 0 : sub * 128) + row;
                 const bool live = r < w.s.rows;
+                const bool idle = !__any_sync(0xffffffffu, live);
                 const int lim = live ? row_limit(p, w.s, r) : 0;
                 float c = fabsf(d.scale_log2);
                 if constexpr (is_q8(CK) && !GS) c *= fabsf(d.k_scale[w.h]);
                 c = fmaxf(c, 1e-30f);                           // keeps 0 * -inf out: masked weights stay zero
                 const float ninf = -__int_as_float(0x7f800000);
-                float m = ninf, l = 0.0f, vref = 0.0f;
+                float m = ninf, l = 0.0f, vexp = -1000.0f;
                 bool ok = true;
-                for (int k = w.k0; k < w.k1; ++k, ++tile_n, ++mine_n) {
+                const int step = split ? 2 : 1, j0 = split ? sub : 0;
+                for (int j = j0; j < nk; j += step, ++mine_n) {
                     ok = warp_wait(bars.s_full(sub), mine_n & 1, gone);
                     if (!ok) break;
                     tc::fence_after();
-                    const ColSlot &cs = cols[tile_n % L::kColSlots];
-                    // the tile's columns in four chunks of 32.  Three stay in registers from
-                    // the maximum on; chunk 2 is read twice, which costs less than the
-                    // registers would.
-                    uint32_t a[32], b[32], t[32];
-                    tc::tmem_ld32(ts, a, 0);
-                    tc::tmem_ld32(ts + 64, t, 0);
-                    tc::tmem_ld32(ts + 32, b, 0);
+                    if (idle) {                                 // no row of the warp is there
+                        tc::fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            ptx::mbar_arrive(bars.p_half(sub));
+                            ptx::mbar_arrive(bars.p_full(sub));
+                        }
+                        continue;
+                    }
+                    const ColSlot &cs = cols[(tile_n + j) % L::kColSlots];
+                    const float *kcol = cs.k;
                     // keys behind the row's limit, and blocks that are not there
                     uint32_t there = cs.mask[0];
                     if constexpr (!TMA) there |= cs.mask[1] | cs.mask[2] | cs.mask[3];
-                    const int rel = lim - k * kKeyTile;
-                    const bool masked = __any_sync(0xffffffffu, rel < kKeyTile || there != 0xffffu);
-                    // scales and mask of a chunk
-                    auto prepare = [&](uint32_t (&x)[32], int ch) {
+                    const int rel = lim - (w.k0 + j) * kKeyTile;
+                    if (__any_sync(0xffffffffu, rel < kKeyTile || there != 0xffffu)) {
+                        // few tiles: masked in place, in a rolled loop, before the others' path
+#pragma unroll 1
+                        for (int o = 0; o < kKeyTile; o += 16) {
+                            uint32_t x[16];
+                            tc::tmem_ld16_wait(ts + o, x);
+                            const uint32_t g = there >> (o >> 3);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                if constexpr (GS) x[i] = __float_as_uint(__uint_as_float(x[i]) * cs.k[o + i]);
+                                if (o + i >= rel || !((g >> (i >> 3)) & 1u)) x[i] = 0xff800000u;
+                            }
+                            tc::tmem_st16(ts + o, x);
+                        }
+                        tc::tmem_st_wait();
+                        kcol = reinterpret_cast<const float *>(sm + L::ones);
+                    }
+                    // the tile's columns in four chunks of 32.  The first two stay in registers
+                    // from the maximum on; the others are read twice, which costs less
+                    // than the registers would.
+                    uint32_t a[32], b[32];
+                    tc::tmem_ld32(ts + 64, a, 0);
+                    tc::tmem_ld32(ts + 96, b, 0);
+                    auto scaled = [&](uint32_t (&x)[32], int ch) {
                         if constexpr (GS) {
 #pragma unroll
-                            for (int j = 0; j < 32; j += 4) {
-                                const float4 ks = *reinterpret_cast<const float4 *>(cs.k + 32 * ch + j);
-                                const float2 u = tc::mul2(f2(x, j), make_float2(ks.x, ks.y));
-                                const float2 v = tc::mul2(f2(x, j + 2), make_float2(ks.z, ks.w));
-                                x[j] = __float_as_uint(u.x);
-                                x[j + 1] = __float_as_uint(u.y);
-                                x[j + 2] = __float_as_uint(v.x);
-                                x[j + 3] = __float_as_uint(v.y);
+                            for (int i = 0; i < 32; i += 4) {
+                                const float4 k4 = *reinterpret_cast<const float4 *>(kcol + 32 * ch + i);
+                                const float2 u = tc::mul2(f2(x, i), make_float2(k4.x, k4.y));
+                                const float2 v = tc::mul2(f2(x, i + 2), make_float2(k4.z, k4.w));
+                                x[i] = __float_as_uint(u.x);
+                                x[i + 1] = __float_as_uint(u.y);
+                                x[i + 2] = __float_as_uint(v.x);
+                                x[i + 3] = __float_as_uint(v.y);
                             }
-                        }
-                        if (masked) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (32 * ch + j >= rel || !((there >> (4 * ch + (j >> 3))) & 1u)) x[j] = 0xff800000u;
                         }
                     };
                     float mx[4] = {ninf, ninf, ninf, ninf};
                     auto largest = [&](const uint32_t (&x)[32]) {
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8)
+                        for (int u = 0; u < 32; u += 8)
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(x[j + i])), __uint_as_float(x[j + 4 + i]));
+                                mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(x[u + i])), __uint_as_float(x[u + 4 + i]));
                     };
                     tc::tmem_ld_wait32(a, 0);
-                    tc::tmem_ld_wait32(t, 0);
                     tc::tmem_ld_wait32(b, 0);
-                    prepare(t, 2);
-                    largest(t);
-                    tc::tmem_ld32(ts + 96, t, 0);
-                    prepare(a, 0);
+                    scaled(a, 2);
                     largest(a);
-                    prepare(b, 1);
+                    tc::tmem_ld32(ts, a, 0);
+                    scaled(b, 3);
                     largest(b);
-                    tc::tmem_ld_wait32(t, 0);
-                    prepare(t, 3);
-                    largest(t);
+                    tc::tmem_ld32(ts + 32, b, 0);
+                    tc::tmem_ld_wait32(a, 0);
+                    tc::tmem_ld_wait32(b, 0);
+                    scaled(a, 0);
+                    largest(a);
+                    scaled(b, 1);
+                    largest(b);
                     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     float grow = 1.0f;                          // what O and l shrink by
                     if (top > m && (m == ninf || (top - m) * c > 8.0f)) {
                         grow = m == ninf ? 0.0f : exp2_approx((m - top) * c);
-                        l *= grow;
                         m = top;
                     }
-                    float vinv = 1.0f;
                     if constexpr (kVRef) {
-                        // a power of two at or above the tile's V scales
+                        // 2^vexp at or above the V scales so far: P times a scale stays in f16's range
                         const float vm = fmaxf(fmaxf(cs.vmax[0], cs.vmax[1]), fmaxf(cs.vmax[2], cs.vmax[3]));
-                        const float v2 = __uint_as_float(min((__float_as_uint(fmaxf(vm, 1e-30f)) >> 23) + 1, 254u) << 23);
-                        if (v2 > vref) {
-                            grow *= vref / v2;
-                            vref = v2;
+                        const float e = float(int(__float_as_uint(fmaxf(vm, 1e-30f)) >> 23) - 126);
+                        if (e > vexp) {
+                            grow *= exp2_approx(vexp - e);
+                            vexp = e;
                         }
-                        vinv = 1.0f / vref;
                     }
-                    if (k > w.k0 && __any_sync(0xffffffffu, grow != 1.0f)) {
+                    l *= grow;
+                    if (j > j0 && __any_sync(0xffffffffu, grow != 1.0f)) {
                         // seldom: a rolled loop keeps its registers out of the way
 #pragma unroll 1
                         for (int o = 0; o < D; o += 16) {
                             uint32_t x[16];
                             tc::tmem_ld16_wait(to + o, x);
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * grow);
+                            for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * grow);
                             tc::tmem_st16(to + o, x);
                         }
                     }
-                    const float off = m == ninf ? 0.0f : m * c;
+                    float off = m == ninf ? 0.0f : m * c;
+                    if constexpr (kVRef) off += vexp;
                     const float2 c2 = make_float2(c, c), off2 = make_float2(-off, -off);
                     float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
                     auto weights = [&](const uint32_t (&x)[32], int ch) {
                         uint32_t pk[16];
 #pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
-                            const float2 y = tc::fma2(f2(x, j), c2, off2);
-                            float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-                            sum[(j >> 1) & 1] = tc::add2(sum[(j >> 1) & 1], e);
+                        for (int i = 0; i < 32; i += 4) {
+                            const float2 y0 = tc::fma2(f2(x, i), c2, off2), y1 = tc::fma2(f2(x, i + 2), c2, off2);
+                            float2 e0 = make_float2(exp2_approx(y0.x), exp2_approx(y0.y));
+                            float2 e1 = make_float2(exp2_approx(y1.x), exp2_approx(y1.y));
+                            sum[0] = tc::add2(sum[0], e0);
+                            sum[1] = tc::add2(sum[1], e1);
                             if constexpr (GS) {
-                                float2 vs = *reinterpret_cast<const float2 *>(cs.v + 32 * ch + j);
-                                if constexpr (kVRef) vs = tc::mul2(vs, make_float2(vinv, vinv));
-                                const float2 z = tc::mul2(e, vs);
-                                e.x = masked && e.x == 0.0f ? 0.0f : z.x;
-                                e.y = masked && e.y == 0.0f ? 0.0f : z.y;
+                                const float4 v4 = *reinterpret_cast<const float4 *>(cs.v + 32 * ch + i);
+                                e0 = tc::mul2(e0, make_float2(v4.x, v4.y));
+                                e1 = tc::mul2(e1, make_float2(v4.z, v4.w));
                             }
-                            pk[j >> 1] = tc::pack16<QK>(e.x, e.y);
+                            pk[i >> 1] = tc::pack16<QK>(e0.x, e0.y);
+                            pk[(i >> 1) + 1] = tc::pack16<QK>(e1.x, e1.y);
                         }
                         tc::tmem_st16(ts + 16 * ch, pk);
                     };
@@ -774,163 +916,258 @@ __global__ void __launch_bounds__(prefill_threads<TMA>(), 1)
                     weights(a, 0);
                     tc::tmem_ld32(ts + 64, a, 0);
                     weights(b, 1);
-                    tc::tmem_ld_wait32(a, 0);
+                    tc::tmem_ld32(ts + 96, b, 0);
                     hand(bars.p_half(sub));
-                    prepare(a, 2);
+                    tc::tmem_ld_wait32(a, 0);
+                    tc::tmem_ld_wait32(b, 0);
+                    scaled(a, 2);
                     weights(a, 2);
-                    weights(t, 3);
+                    scaled(b, 3);
+                    weights(b, 3);
                     hand(bars.p_full(sub));
                     sum[0] = tc::add2(sum[0], sum[1]);
                     l += sum[0].x + sum[0].y;
                 }
-                if (!ok || !warp_wait(bars.o_full(sub), item_n & 1, gone)) break;
-                ++item_n;
-                tc::fence_after();
-                const bool whole = w.k0 == 0 && w.k1 == w.units;
-                float fac = kVRef ? vref : 1.0f;
-                if constexpr (is_q8(CK) && !GS) fac = d.v_scale[w.h];
-                if (whole) {
-                    fac = l == 0.0f ? 0.0f : fac / l;
-                    const int tok = r / d.group;
-                    const int head = w.h * d.group + (r - tok * d.group);
-                    char *o_row = d.out + int64_t(w.s.s0 + tok) * d.o_b + int64_t(head) * d.o_h;
-                    float bad = 0.0f;
-#pragma unroll
-                    for (int o = 0; o < D; o += 32) {
-                        uint32_t a[32];
-                        tc::tmem_ld32(to + o, a, 0);
-                        tc::tmem_ld_wait32(a, 0);
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
-                            // a row without keys is zero whatever O holds
-                            const float x = l == 0.0f ? 0.0f : __uint_as_float(a[j]) * fac;
-                            const float y = l == 0.0f ? 0.0f : __uint_as_float(a[j + 1]) * fac;
-                            bad = fmaf(x, 0.0f, fmaf(y, 0.0f, bad));
-                            pk[j / 2] = tc::pack16<QK>(x, y);
-                        }
-                        if (live) {
-                            if (d.out_vec_ok) {
-#pragma unroll
-                                for (int j = 0; j < 16; j += 4)
-                                    *reinterpret_cast<uint4 *>(o_row + 2 * (o + 2 * j)) =
-                                        make_uint4(pk[j], pk[j + 1], pk[j + 2], pk[j + 3]);
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < 16; ++j) {
-                                    reinterpret_cast<uint16_t *>(o_row)[o + 2 * j] = uint16_t(pk[j]);
-                                    reinterpret_cast<uint16_t *>(o_row)[o + 2 * j + 1] = uint16_t(pk[j] >> 16);
-                                }
-                            }
-                        }
+                tile_n += nk;
+                if (!ok) break;
+                // accumulators of this segment, and their joining
+                const bool two = !split || nk > 1;              // both are in use
+                const uint32_t turn0 = outs[0]++, turn1 = outs[1];
+                if (two) ++outs[1];
+                float off = m == ninf ? m : m * c;
+                if constexpr (kVRef) off = m == ninf ? m : off + vexp;
+                float w0 = 1.0f, w1 = 0.0f;                     // weights of O (own) and warpgroup 1's
+                const bool join = split && two;
+                if (sub == 1) {
+                    if (!two) continue;
+                    if (join) {
+                        state[0] = off;
+                        state[128] = l;
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(bars.j_full());
+                        // O of this warpgroup is read by the other: not to be overwritten before
+                        ok = warp_wait(bars.j_empty(), joins & 1, gone);
+                        ++joins;
+                        if (!ok) break;
+                        continue;
                     }
-                    // not finite: weights of zero met values that are not; such a row is done again by itself
-                    unsigned redo = __ballot_sync(0xffffffffu, live && bad != 0.0f);
-                    if (redo) tc::fence_before();
-                    while (redo) {
-                        const int who = __ffs(redo) - 1;
-                        redo &= redo - 1;
-                        const int rr = __shfl_sync(0xffffffffu, r, who), ll = __shfl_sync(0xffffffffu, lim, who);
-                        const int tt = rr / d.group;
-                        redo_row<QK, CK, D>(d, d.block_tables + w.b * d.bt_b, int64_t(w.s.s0) + tt,
-                                            w.h * d.group + (rr - tt * d.group), ll, w.limit, 0, D);
-                    }
+                    ok = warp_wait(bars.o_full(1), turn1 & 1, gone);
                 } else {
-                    const int slot = 2 * blockIdx.x + (w.k0 == 0 ? 1 : 0);
-                    float *ml = f.part_ml + int64_t(slot) * 2 * kRowTile + sub * 128 + row;
-                    ml[0] = m == ninf ? m : m * c;
+                    ok = warp_wait(bars.o_full(0), turn0 & 1, gone);
+                    if (ok && join) {
+                        ok = warp_wait(bars.o_full(1), turn1 & 1, gone) && warp_wait(bars.j_full(), joins & 1, gone);
+                        ++joins;
+                    }
+                }
+                if (!ok) break;
+                tc::fence_after();
+                if (join) {
+                    const float m1 = state[0], l1 = state[128];
+                    const float top = fmaxf(off, m1);
+                    w0 = l == 0.0f || off == ninf ? 0.0f : exp2_approx(off - top);
+                    w1 = l1 == 0.0f || m1 == ninf ? 0.0f : exp2_approx(m1 - top);
+                    l = (w0 == 0.0f ? 0.0f : l * w0) + (w1 == 0.0f ? 0.0f : l1 * w1);
+                    off = top;
+                }
+                const bool whole = w.k0 == 0 && w.k1 == w.units;
+                float fac = 1.0f;
+                if constexpr (is_q8(CK) && !GS) fac = d.v_scale[w.h];
+                if (whole) fac = l == 0.0f ? 0.0f : fac / l;
+                if (l == 0.0f) w0 = w1 = 0.0f;                  // a row without keys is zero whatever O holds
+                w0 *= fac;
+                w1 *= fac;
+                const int tok = r / d.group;
+                const int head = w.h * d.group + (r - tok * d.group);
+                char *o_row = d.out + int64_t(w.s.s0 + tok) * d.o_b + int64_t(head) * d.o_h;
+                const int slot = 2 * blockIdx.x + (w.k0 == 0 ? 1 : 0);
+                const int prow = (split ? 0 : sub * 128) + row;
+                float4 *acc = reinterpret_cast<float4 *>(f.part_acc) + int64_t(slot) * (D / 4) * kRowTile + prow;
+                if (!whole) {
+                    float *ml = f.part_ml + int64_t(slot) * 2 * kRowTile + prow;
+                    ml[0] = off;
                     ml[kRowTile] = l;
-                    float4 *acc = reinterpret_cast<float4 *>(f.part_acc) +
-                                  int64_t(slot) * (D / 4) * kRowTile + sub * 128 + row;
+                }
+                float bad = 0.0f;
+#pragma unroll 1
+                for (int o = 0; o < D; o += 32) {
+                    if (idle) break;
+                    uint32_t a[32];
+                    tc::tmem_ld32(to + o, a, 0);
+                    tc::tmem_ld_wait32(a, 0);
 #pragma unroll
-                    for (int o = 0; o < D; o += 32) {
-                        uint32_t a[32];
-                        tc::tmem_ld32(to + o, a, 0);
-                        tc::tmem_ld_wait32(a, 0);
+                    for (int i = 0; i < 32; ++i) a[i] = w0 == 0.0f ? 0u : __float_as_uint(__uint_as_float(a[i]) * w0);
+                    if (join) {
+                        uint32_t b[32];
+                        tc::tmem_ld32(to + 128 + o, b, 0);
+                        tc::tmem_ld_wait32(b, 0);
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4)
-                            acc[(o + j) / 4 * kRowTile] =
-                                make_float4(__uint_as_float(a[j]) * fac, __uint_as_float(a[j + 1]) * fac,
-                                            __uint_as_float(a[j + 2]) * fac, __uint_as_float(a[j + 3]) * fac);
+                        for (int i = 0; i < 32; ++i)
+                            if (w1 != 0.0f)
+                                a[i] = __float_as_uint(fmaf(__uint_as_float(b[i]), w1, __uint_as_float(a[i])));
+                    }
+                    if (!whole) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            acc[(o + i) / 4 * kRowTile] = make_float4(__uint_as_float(a[i]), __uint_as_float(a[i + 1]),
+                                                                      __uint_as_float(a[i + 2]), __uint_as_float(a[i + 3]));
+                        continue;
+                    }
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        bad = fmaf(__uint_as_float(a[i]), 0.0f, fmaf(__uint_as_float(a[i + 1]), 0.0f, bad));
+                        pk[i / 2] = tc::pack16<QK>(__uint_as_float(a[i]), __uint_as_float(a[i + 1]));
+                    }
+                    if (!live) continue;
+                    if (f.out32) {
+                        tc::st_global32(o_row + 2 * o, pk);
+                        tc::st_global32(o_row + 2 * o + 32, pk + 8);
+                    } else if (d.out_vec_ok) {
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4)
+                            *reinterpret_cast<uint4 *>(o_row + 2 * (o + 2 * i)) = make_uint4(pk[i], pk[i + 1], pk[i + 2], pk[i + 3]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            reinterpret_cast<uint16_t *>(o_row)[o + 2 * i] = uint16_t(pk[i]);
+                            reinterpret_cast<uint16_t *>(o_row)[o + 2 * i + 1] = uint16_t(pk[i] >> 16);
+                        }
                     }
                 }
                 tc::fence_before();
+                if (join) {
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(bars.j_empty());
+                }
+                // not finite: weights of zero met values that are not; such a row is done again by itself
+                unsigned redo = __ballot_sync(0xffffffffu, whole && live && bad != 0.0f);
+                while (redo) {
+                    const int who = __ffs(redo) - 1;
+                    redo &= redo - 1;
+                    const int rr = __shfl_sync(0xffffffffu, r, who), ll = __shfl_sync(0xffffffffu, lim, who);
+                    const int tt = rr / d.group;
+                    redo_row<QK, CK, D>(d, d.block_tables + w.b * d.bt_b, int64_t(w.s.s0) + tt,
+                                        w.h * d.group + (rr - tt * d.group), ll, w.limit, 0, D);
+                }
             } while (w.next(p));
         }
     } else {
+        if constexpr (!TMA) {
+            if (warp < 12) tc::regs_dec<120>(); else tc::regs_dec<88>();
+        }
         if (warp == kMmaWarp) {
             // -------------------------------------------- the products
-            if (work && lane == 0) {
+            if (work) {
                 constexpr uint32_t id_qk = tc::instr_desc<BF, false, 128, 128>();
                 constexpr uint32_t id_pv = tc::instr_desc<BF, true, 128, D>();
+                const bool leader = tc::elect_one();
+                const uint32_t q_lo = tc::desc_lo(sm32 + L::q, 16), k_lo = tc::desc_lo(sm32 + L::ring, 16);
+                const uint32_t v_lo = tc::desc_lo(sm32 + L::ring, 16384);
                 uint32_t pos = 0, item = 0, n_p[2] = {0, 0};
                 Walk w = walk_from(p, st);
-                auto qk = [&](int i, uint32_t stage) {
+                // S[i] = Q[q] K^T of a ring stage
+                auto qk = [&](int i, int q, uint32_t stage) {
+                    const uint32_t a = q_lo + q * (L::kTile >> 4), b = k_lo + stage * (L::kTile >> 4), t = tmem + i * 128;
+                    if (leader) {
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        const uint32_t o = (ks >> 2) * 16384 + (ks & 3) * 32;
-                        tc::mma_ss(tmem + i * 128, tc::smem_desc(sm32 + L::q + i * L::kTile + o, 16, 1024),
-                                   tc::smem_desc(sm32 + L::ring + stage * L::kTile + o, 16, 1024), id_qk, ks > 0);
+                        for (int ks = 0; ks < D / 16; ++ks) {
+                            const uint32_t o = (ks >> 2) * (16384 >> 4) + (ks & 3) * (32 >> 4);
+                            tc::mma_ss(t, a + o, b + o, id_qk, ks > 0);
+                        }
+                        tc::commit(bars.s_full(i));
                     }
-                    tc::commit(bars.s_full(i));
+                };
+                // O[i] (+)= P[i] V, keys in two halves: the first half's products run
+                // while the others' weights are made
+                auto pv = [&](int i, int half, uint32_t stage, bool acc) {
+                    const uint32_t b = v_lo + stage * (L::kTile >> 4), t = tmem + i * 128;
+                    if (leader) {
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            tc::mma_ts(t + 256, t + (4 * half + ks) * 8, b + (4 * half + ks) * (2048 >> 4), id_pv,
+                                       ks > 0 || half > 0 || acc);
+                    }
+                };
+                auto release = [&](uint32_t bar) {
+                    if (leader) tc::commit(bar);
+                };
+                auto full = [&](uint32_t x) -> bool {
+                    const bool ok = warp_wait(bars.full(x % ST), (x / ST) & 1, gone);
+                    tc::fence_after();
+                    return ok;
+                };
+                auto weights = [&](int i, uint32_t vpos, bool acc, bool v_new) -> bool {
+                    bool ok = warp_wait(bars.p_half(i), n_p[i] & 1, gone);
+                    if (ok && v_new) ok = full(vpos);
+                    if (!ok) return false;
+                    tc::fence_after();
+                    pv(i, 0, vpos % ST, acc);
+                    ok = warp_wait(bars.p_full(i), n_p[i] & 1, gone);
+                    if (!ok) return false;
+                    ++n_p[i];
+                    tc::fence_after();
+                    pv(i, 1, vpos % ST, acc);
+                    return true;
                 };
                 bool ok = true;
                 do {
-                    const int ns = w.subtiles(), nk = w.k1 - w.k0;
-                    ok = bar_wait(bars.q_full(), item & 1, gone) &&
-                         bar_wait(bars.full(pos % ST), (pos / ST) & 1, gone);
+                    const int nk = w.k1 - w.k0;
+                    ok = warp_wait(bars.q_full(), item & 1, gone);
                     if (!ok) break;
                     tc::fence_after();
-                    for (int i = 0; i < ns; ++i) qk(i, pos % ST);
-                    tc::commit(bars.empty(pos % ST));
-                    if (nk == 1) tc::commit(bars.q_empty());
-                    for (int j = 0; j < nk && ok; ++j) {
-                        const uint32_t vpos = pos + 1, kpos = pos + 2;
-                        for (int i = 0; i < ns; ++i) {
-                            ok = bar_wait(bars.p_half(i), n_p[i] & 1, gone);
-                            if (ok && i == 0) ok = bar_wait(bars.full(vpos % ST), (vpos / ST) & 1, gone);
+                    if (w.subtiles() == 2) {
+                        ok = full(pos);
+                        if (!ok) break;
+                        qk(0, 0, pos % ST);
+                        qk(1, 1, pos % ST);
+                        release(bars.empty(pos % ST));
+                        if (nk == 1) release(bars.q_empty());
+                        for (int j = 0; j < nk; ++j, pos += 2) {
+                            const bool more = j + 1 < nk;
+                            const uint32_t kpos = pos + 2;
+                            ok = weights(0, pos + 1, j > 0, true);
+                            if (ok && more) ok = full(kpos);
                             if (!ok) break;
-                            tc::fence_after();
-                            // P in two halves: the first keys' products run while the others' weights are made
-                            auto pv = [&](int ks) {
-                                tc::mma_ts(tmem + 256 + i * 128, tmem + i * 128 + ks * 8,
-                                           tc::smem_desc(sm32 + L::ring + (vpos % ST) * L::kTile + ks * 2048, 16384, 1024),
-                                           id_pv, j > 0 || ks > 0);
-                            };
-#pragma unroll
-                            for (int ks = 0; ks < 4; ++ks) pv(ks);
-                            ok = bar_wait(bars.p_full(i), n_p[i] & 1, gone);
+                            if (more) qk(0, 0, kpos % ST); else release(bars.o_full(0));
+                            ok = weights(1, pos + 1, j > 0, false);
                             if (!ok) break;
-                            ++n_p[i];
-                            tc::fence_after();
-#pragma unroll
-                            for (int ks = 4; ks < 8; ++ks) pv(ks);
-                            if (j + 1 < nk) {
-                                if (i == 0) {
-                                    ok = bar_wait(bars.full(kpos % ST), (kpos / ST) & 1, gone);
-                                    if (!ok) break;
-                                    tc::fence_after();
-                                }
-                                qk(i, kpos % ST);
+                            if (more) qk(1, 1, kpos % ST); else release(bars.o_full(1));
+                            release(bars.empty((pos + 1) % ST));
+                            if (more) release(bars.empty(kpos % ST));
+                            if (j + 2 == nk) release(bars.q_empty());
+                        }
+                    } else {
+                        for (int j = 0; j < min(2, nk) && ok; ++j) {
+                            ok = full(pos + 2 * j);
+                            if (!ok) break;
+                            qk(j, 0, (pos + 2 * j) % ST);
+                            release(bars.empty((pos + 2 * j) % ST));
+                            if (j + 1 == nk) release(bars.q_empty());
+                        }
+                        for (int j = 0; j < nk && ok; ++j, pos += 2) {
+                            const int i = j & 1;
+                            const uint32_t kpos = pos + 4;
+                            ok = weights(i, pos + 1, j > 1, true);
+                            if (!ok) break;
+                            release(bars.empty((pos + 1) % ST));
+                            if (j + 2 < nk) {
+                                ok = full(kpos);
+                                if (!ok) break;
+                                qk(i, 0, kpos % ST);
+                                release(bars.empty(kpos % ST));
+                                if (j + 3 == nk) release(bars.q_empty());
                             } else {
-                                tc::commit(bars.o_full(i));
+                                release(bars.o_full(i));
                             }
                         }
-                        if (!ok) break;
-                        tc::commit(bars.empty(vpos % ST));
-                        if (j + 1 < nk) {
-                            tc::commit(bars.empty(kpos % ST));
-                            if (j + 2 == nk) tc::commit(bars.q_empty());
-                        }
-                        pos += 2;
                     }
                     ++item;
                 } while (ok && w.next(p));
             }
             __syncwarp();
-        } else if (warp >= kQWarp && warp < kQWarp + kQWarps) {
-            // -------------------------------------------- Q, a warp per subtile or one for both
-            const int first = warp - kQWarp;
+        } else if (warp >= kQWarp && warp < kQWarp + 2) {
+            // -------------------------------------------- Q, a warp per subtile
+            const int sub = warp - kQWarp;
             const bool negate = d.scale_log2 < 0.0f;
             constexpr int PPR = D / 8;                          // pieces per row
             constexpr int RPI = 32 / PPR;                       // rows per instruction
@@ -940,7 +1177,7 @@ __global__ void __launch_bounds__(prefill_threads<TMA>(), 1)
             if (work) w = walk_from(p, st);
             while (have) {
                 if (item > 0 && !warp_wait(bars.q_empty(), (item - 1) & 1, gone)) break;
-                for (int sub = first; sub < w.subtiles(); sub += kQWarps) {
+                if (sub < w.subtiles()) {
                     const int c = lane % PPR;
                     int r = w.tile * kRowTile + sub * 128 + lane / PPR;
                     int tok = r / d.group, g = r - tok * d.group;
@@ -956,12 +1193,8 @@ __global__ void __launch_bounds__(prefill_threads<TMA>(), 1)
                             ++tok;
                         }
                     }
-                }
-                tc::cp_async_wait_all();
-                for (int sub = first; negate && sub < w.subtiles(); sub += kQWarps) {
-                    const uint32_t dst = sm32 + L::q + sub * L::kTile;
-                    const int c = lane % PPR;
-                    for (int i = lane / PPR; i < 128; i += RPI) {
+                    tc::cp_async_wait_all();
+                    for (int i = negate ? lane / PPR : 128; i < 128; i += RPI) {
                         uint4 v = tc::ld_shared16(dst + piece_at(i, c));
                         v.x ^= 0x80008000u;
                         v.y ^= 0x80008000u;
@@ -976,7 +1209,7 @@ __global__ void __launch_bounds__(prefill_threads<TMA>(), 1)
                 ++item;
                 have = w.next(p);
             }
-            if (first == 0 && lane == 0) {
+            if (sub == 0 && lane == 0) {
                 // the row tile that this CTA begins and does not end
                 int4 ds = make_int4(0, 0, 0, -1);
                 if (work && !have && w.k0 == 0 && w.k1 < w.units) {
@@ -996,70 +1229,78 @@ __global__ void __launch_bounds__(prefill_threads<TMA>(), 1)
                 ptx::prefetch_tmap(&tmv);
             }
             if (work) {
-                Walk w = walk_from(p, st);
-                bool ok = true;
-                do {
-                    const int32_t *table = d.block_tables + w.b * d.bt_b;
-                    auto lookup = [&](int k) -> int {           // this lane's block of key tile k
-                        const int t = k * kKeyTile + lane * rows;
-                        return lane < nblk && t < w.limit ? table[int64_t(t >> d.block_shift) * d.bt_j] : -1;
-                    };
-                    int blk = lookup(w.k0);
-                    for (int k = w.k0; k < w.k1 && ok; ++k, ++tile_n) {
-                        const int t = k * kKeyTile + lane * rows;
-                        const bool want = lane < nblk && t < w.limit;
-                        const bool in = want && blk >= 0 && blk < d.num_blocks;
-                        if (want && !in) raise_err(d.err_flag, PKV_DEVERR_BLOCK_RANGE);
-                        const unsigned got = __ballot_sync(0xffffffffu, in);
-                        const int next = k + 1 < w.k1 ? lookup(k + 1) : -1;
-                        const uint32_t bytes = __popc(got) * box * (D / 64);
-                        const int slot0 = t & (d.block_size - 1);
-#pragma unroll
-                        for (int kv = 0; kv < 2; ++kv, ++pos) {
-                            const uint32_t stage = pos % ST;
-                            if (pos >= ST) ok = warp_wait(bars.empty(stage), (pos / ST - 1) & 1, gone);
-                            if (!ok) break;
-                            // V rows that nothing loads, or that no row sees, are zeroed: a weight of zero
-                            // must not meet what lies there
-                            const bool fix = kv == 1 && (__popc(got) < nblk || w.limit < (k + 1) * kKeyTile);
-                            const uint32_t bar = fix ? bars.tail() : bars.full(stage);
-                            const uint32_t dst = sm32 + L::ring + stage * L::kTile;
-                            if (lane == 0) {
-                                if (kv == 0) {
-                                    uint32_t there = 0;         // by groups of 8 rows
-                                    for (int i = 0; i < 16; ++i) there |= ((got >> ((i * 8) >> shift)) & 1u) << i;
-                                    cols[tile_n % L::kColSlots].mask[0] = there;
-                                }
-                                ptx::mbar_arrive_expect_tx(bar, bytes);
+                TileWalk tw{walk_from(p, st), 0};
+                tw.k = tw.w.k0;
+                // this lane's block of the tile, -1 where it wants none
+                auto lookup = [&]() -> int {
+                    const int t = tw.k * kKeyTile + lane * rows;
+                    return lane < nblk && t < tw.w.limit
+                               ? d.block_tables[tw.w.b * d.bt_b + int64_t(t >> d.block_shift) * d.bt_j] : -1;
+                };
+                int blk = lookup();
+                bool ok = true, more = true;
+                for (; more && ok; ++tile_n) {
+                    const int t = tw.k * kKeyTile + lane * rows, h = tw.w.h;
+                    const int limit = tw.w.limit - tw.k * kKeyTile;
+                    const bool want = lane < nblk && t < tw.w.limit;
+                    const bool in = want && blk >= 0 && blk < d.num_blocks;
+                    if (want && !in) raise_err(d.err_flag, PKV_DEVERR_BLOCK_RANGE);
+                    const unsigned got = __ballot_sync(0xffffffffu, in);
+                    const int now = blk, slot0 = t & (d.block_size - 1);
+                    more = tw.next(p);
+                    if (more) blk = lookup();
+                    const uint32_t bytes = __popc(got) * box * (D / 64);
+#pragma unroll 1
+                    for (int kv = 0; kv < 2; ++kv, ++pos) {
+                        const uint32_t stage = pos % ST;
+                        if (pos >= ST) ok = warp_wait(bars.empty(stage), (pos / ST - 1) & 1, gone);
+                        if (!ok) break;
+                        // V rows that nothing loads, or that no row sees, are zeroed: a weight of zero
+                        // must not meet what lies there
+                        const bool fix = kv == 1 && (__popc(got) < nblk || limit < kKeyTile);
+                        const uint32_t bar = fix ? bars.tail() : bars.full(stage);
+                        const uint32_t dst = sm32 + L::ring + stage * L::kTile;
+                        if (lane == 0) {
+                            if (kv == 0) {
+                                uint32_t there = 0;             // by groups of 8 rows
+                                for (int i = 0; i < 16; ++i) there |= ((got >> ((i * 8) >> shift)) & 1u) << i;
+                                cols[tile_n % L::kColSlots].mask[0] = there;
                             }
-                            __syncwarp();
-                            if (in) {
-#pragma unroll
-                                for (int c = 0; c < D / 64; ++c)
-                                    ptx::tma_load_4d(dst + c * 16384 + lane * box, kv ? &tmv : &tmk, bar, c * 64, slot0,
-                                                     w.h, blk);
-                            }
-                            if (fix) {
-                                ok = warp_wait(bar, fixes & 1, gone);
-                                ++fixes;
-                                if (!ok) break;
-                                for (int i = lane; i < kKeyTile * (D / 8); i += 32) {
-                                    const int rr = i / (D / 8);
-                                    if (k * kKeyTile + rr >= w.limit || !((got >> (rr >> shift)) & 1u))
-                                        tc::st_shared16(dst + piece_at(rr, i % (D / 8)), make_uint4(0, 0, 0, 0));
-                                }
-                                ptx::fence_proxy_async_smem();
-                                __syncwarp();
-                                if (lane == 0) ptx::mbar_arrive(bars.full(stage));
-                            }
+                            ptx::mbar_arrive_expect_tx(bar, bytes);
                         }
-                        blk = next;
+                        __syncwarp();
+                        if (in) {
+#pragma unroll
+                            for (int c = 0; c < D / 64; ++c)
+                                ptx::tma_load_4d(dst + c * 16384 + lane * box, kv ? &tmv : &tmk, bar, c * 64, slot0, h, now);
+                        }
+                        if (fix) {
+                            ok = warp_wait(bar, fixes & 1, gone);
+                            ++fixes;
+                            if (!ok) break;
+                            for (int i = lane; i < kKeyTile * (D / 8); i += 32) {
+                                const int rr = i / (D / 8);
+                                if (rr >= limit || !((got >> (rr >> shift)) & 1u))
+                                    tc::st_shared16(dst + piece_at(rr, i % (D / 8)), make_uint4(0, 0, 0, 0));
+                            }
+                            ptx::fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) ptx::mbar_arrive(bars.full(stage));
+                        }
                     }
-                } while (ok && w.next(p));
+                }
             }
         } else if (!TMA && warp < 12) {
-            // -------------------------------------------- K/V by loads, 32 rows of a tile per warp
-            load_rows<QK, CK, D, GS>(p, f, st, work, sm32 + L::ring, cols, bars, gone, warp - 8, lane);
+            if (work) {
+                if constexpr (FEED == kFeedCodes)
+                    convert_rows<QK, CK, D, GS>(p, st, sm, sm32, bars, gone, warp - 8, lane);
+                else if constexpr (FEED == kFeedCopy)
+                    copy_rows<CK, D>(p, st, sm32 + L::ring, cols, bars, gone, warp - 8, lane);
+            }
+        } else if (FEED == kFeedCodes && warp == 13) {
+            if constexpr (FEED == kFeedCodes) {
+                if (work) raw_codes<CK, D>(p, f, st, sm, sm32, bars, &tmk, &tmv, gone, lane);
+            }
         }
     }
     __syncthreads();

@@ -11,8 +11,9 @@ struct PrefillLaunch {
     const PrefillParams *p;
     int grid;
     bool join;                  // launch the join kernel too
-    bool tma;                   // K/V by TMA (tmk, tmv)
-    int rows_aligned;           // 3-bit rows at multiples of 4 bytes
+    bool tma;                   // K/V, or their raw codes, by TMA (tmk, tmv)
+    int raw_unit;               // else raw codes by loads of 4 bytes or 1
+    int out32;                  // output rows at multiples of 32 bytes
     void *desc, *part_ml, *part_acc;
     CUtensorMap tmk, tmv;
     cudaStream_t stream;

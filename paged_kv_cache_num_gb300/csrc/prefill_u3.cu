@@ -4,6 +4,6 @@
 namespace pkv {
 cudaError_t launch_prefill_u3(const PrefillLaunch &a)
 {
-    return a.p->d.q_is_bf16 ? launch_dim<kBF16, kU3, false, true>(a) : launch_dim<kF16, kU3, false, true>(a);
+    return a.p->d.q_is_bf16 ? launch_dim<kBF16, kU3, kFeedCodes, true>(a) : launch_dim<kF16, kU3, kFeedCodes, true>(a);
 }
 }  // namespace pkv

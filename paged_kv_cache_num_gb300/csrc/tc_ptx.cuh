@@ -98,14 +98,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[N])
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // ---------------------------------------------------------------- matrix descriptors
-// Shared-memory operand in 128-byte-swizzled rows: `lbo` the byte stride
-// between 64-element chunks of the contiguous dimension (operands whose
-// contiguous dimension is M or N), `sbo` between groups of 8 rows.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo)
-{
-    return uint64_t((addr & 0x3ffffu) >> 4) | (uint64_t(lbo >> 4) << 16) | (uint64_t(sbo >> 4) << 32) |
-           (uint64_t(1) << 46) | (uint64_t(2) << 61);
-}
+// Shared-memory operands in 128-byte-swizzled rows, groups of 8 rows 1024
+// bytes apart: the descriptor's low word holds the address and the byte
+// stride `lbo` between 64-element chunks of the contiguous dimension
+// (operands whose contiguous dimension is N), the high word is constant
+// (that group stride, the descriptor version, the swizzle).
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return ((addr & 0x3ffffu) >> 4) | ((lbo >> 4) << 16); }
 
 // Instruction descriptor: 16-bit operands of one type, fp32 accumulator.
 template <bool BF16, bool B_MN_MAJOR, int M, int N>
@@ -115,24 +114,32 @@ __device__ __forceinline__ constexpr uint32_t instr_desc()
            (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
 }
 
-// D[tmem] (+)= A[smem] * B[smem]
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc)
+// D[tmem] (+)= A[smem] * B[smem]; alo, blo: descriptor low words
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t alo, uint32_t blo, uint32_t idesc, bool acc)
 {
     asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(acc))
+        "{\n.reg .pred p;\n.reg .b64 a, b;\nsetp.ne.b32 p, %4, 0;\nmov.b64 a, {%1, %5};\nmov.b64 b, {%2, %5};\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}" ::"r"(d),
+        "r"(alo), "r"(blo), "r"(idesc), "r"(uint32_t(acc)), "n"(kDescHi)
         : "memory");
 }
 
 // D[tmem] (+)= A[tmem] * B[smem]
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t blo, uint32_t idesc, bool acc)
 {
     asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(acc))
+        "{\n.reg .pred p;\n.reg .b64 b;\nsetp.ne.b32 p, %4, 0;\nmov.b64 b, {%2, %5};\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}" ::"r"(d),
+        "r"(a), "r"(blo), "r"(idesc), "r"(uint32_t(acc)), "n"(kDescHi)
         : "memory");
+}
+
+// one lane of a converged warp
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+    return r != 0;
 }
 
 // arrive on `bar` once every earlier tcgen05 operation of this thread is done
@@ -191,6 +198,17 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return r;
 }
+
+// 32 bytes to global memory at once
+__device__ __forceinline__ void st_global32(void *p, const uint32_t *v)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+template <int N> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // two floats -> packed 16-bit pair (lo in the low half), nearest even
 template <int KIND>
