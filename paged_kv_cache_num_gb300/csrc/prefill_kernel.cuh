@@ -21,12 +21,15 @@
 // range of a row tile writes its rows; otherwise it writes an fp32 partial
 // (m, l, O), and prefill_join_kernel combines them.
 //
-// CTA.  Two softmax warpgroups (one per subtile, a thread per row), one warp
-// that issues the products (tcgen05.mma, accumulators and P in tensor
-// memory), warps that load Q, and the K/V producers.  While one subtile's
-// softmax runs the tensor core works on the other's products.  A row tile of
-// at most 128 rows has one subtile: then the warpgroups take its key tiles in
-// turn, with states of their own that are joined at the end.
+// CTA.  Two pairs of softmax warpgroups (one pair per subtile, two threads
+// per row, 64 keys of a tile each), one warp that issues the products
+// (tcgen05.mma, accumulators and P in tensor memory), warps that load Q, and
+// the K/V producers.  While one subtile's softmax runs the tensor core works
+// on the other's products: a subtile's scores wait for its last P V, which
+// waits for its softmax, so the softmax's latency bounds the tile rate, and
+// two threads per row halve it.  A row tile of at most 128 rows has one
+// subtile: then the pairs take its key tiles in turn, with states of their
+// own that are joined at the end.
 //
 // K/V.  16-bit caches in the flash layout: one warp issues TMA copies of
 // whole block pieces into the operand ring; x-vectorised 16-bit caches: four
@@ -250,9 +253,10 @@ struct Smem {
     static constexpr int cols = raw + kRaw * kRawTile;
     static constexpr int kColBytes = 2 * kKeyTile * 4 + 32;
     static constexpr int ones = cols + kColSlots * kColBytes;   // 128 ones
-    static constexpr int state = ones + 512;                    // warpgroup 1's (m, l) for the join
-    static constexpr int bars = state + 1024;
-    static constexpr int n_bars = 2 * kStages + 2 * kRaw + 2 + 4 * 2 + 1 + 2;
+    static constexpr int state = ones + 512;                    // pair 1's (m, l) for the join
+    static constexpr int maxima = state + 1024;                 // [subtile][half][row], then the sums likewise
+    static constexpr int bars = maxima + 4096;
+    static constexpr int n_bars = 2 * kStages + 2 * kRaw + 2 + 4 * 2 + 1 + 2 + 8;
     static constexpr int info = bars + 8 * n_bars;              // per raw stage: which blocks are there
     static constexpr int misc = (info + 4 * 8 + 15) / 16 * 16;
     static constexpr int total = misc + 128;
@@ -289,11 +293,13 @@ struct Bars {
     __device__ __forceinline__ uint32_t o_full(int i) const { return base + 8 * (2 * stages + 6 + i); }
     __device__ __forceinline__ uint32_t p_half(int i) const { return base + 8 * (2 * stages + 8 + i); }
     __device__ __forceinline__ uint32_t tail() const { return base + 8 * (2 * stages + 10); }
-    // the join of two warpgroups' states: warpgroup 1's is there, and has been read
+    // the join of two pairs' states: pair 1's is there, and has been read
     __device__ __forceinline__ uint32_t j_full() const { return base + 8 * (2 * stages + 11); }
     __device__ __forceinline__ uint32_t j_empty() const { return base + 8 * (2 * stages + 12); }
-    __device__ __forceinline__ uint32_t raw_full(int s) const { return base + 8 * (2 * stages + 13 + s); }
-    __device__ __forceinline__ uint32_t raw_empty(int s) const { return base + 8 * (2 * stages + 13 + raws + s); }
+    // two warps with the two halves of the same rows
+    __device__ __forceinline__ uint32_t pair(int sub, int quarter) const { return base + 8 * (2 * stages + 13 + 4 * sub + quarter); }
+    __device__ __forceinline__ uint32_t raw_full(int s) const { return base + 8 * (2 * stages + 21 + s); }
+    __device__ __forceinline__ uint32_t raw_empty(int s) const { return base + 8 * (2 * stages + 21 + raws + s); }
 };
 
 // Wait for a phase, giving up when it takes too long or another warp gave up.
@@ -689,12 +695,11 @@ __device__ __forceinline__ void convert_rows(const PrefillParams &p, const Start
 }
 
 // ---------------------------------------------------------------- the kernel
-// Warps 0-7 softmax, 8-11 producers; 16-bit caches by TMA have the products
-// among the latter, the others in a fourth warpgroup.  Registers: the pool is
-// what the block was launched with.
+// Warps 0-15 softmax, 16-19 producers; 16-bit caches by TMA have the products
+// among the latter, the others in a sixth warpgroup.
 enum Feed : int { kFeedTma, kFeedCopy, kFeedCodes };
 template <int CK> constexpr int feed_of(bool tma) { return is_coded<CK>() ? kFeedCodes : tma ? kFeedTma : kFeedCopy; }
-template <int FEED> constexpr int prefill_threads() { return FEED == kFeedTma ? 384 : 512; }
+template <int FEED> constexpr int prefill_threads() { return FEED == kFeedTma ? 640 : 768; }
 
 template <int QK, int CK, int D, int FEED, bool GS>
 __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
@@ -705,8 +710,8 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
     constexpr int ST = L::kStages;
     constexpr bool TMA = FEED == kFeedTma;
     constexpr bool BF = QK == kBF16;
-    constexpr int kMmaWarp = TMA ? 8 : 12;
-    constexpr int kQWarp = TMA ? 10 : 14;                       // two of them
+    constexpr int kMmaWarp = TMA ? 16 : 20;
+    constexpr int kQWarp = TMA ? 18 : 22;                       // two of them
     constexpr bool kVRef = GS && QK == kF16;                    // P relative to the V scales' magnitude
     const DecodeParams &d = p.d;
     extern __shared__ unsigned char smem_raw[];
@@ -733,13 +738,14 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
         ptx::mbar_init(bars.q_empty(), 1);
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(bars.s_full(i), 1);
-            ptx::mbar_init(bars.p_full(i), 4);
-            ptx::mbar_init(bars.p_half(i), 4);
+            ptx::mbar_init(bars.p_full(i), 8);
+            ptx::mbar_init(bars.p_half(i), 8);
+            for (int j = 0; j < 4; ++j) ptx::mbar_init(bars.pair(i, j), 2);
             ptx::mbar_init(bars.o_full(i), 1);
         }
         ptx::mbar_init(bars.tail(), 1);
         ptx::mbar_init(bars.j_full(), 4);
-        ptx::mbar_init(bars.j_empty(), 4);
+        ptx::mbar_init(bars.j_empty(), 8);
         ptx::fence_mbar_init();
         *gone = 0;
     }
@@ -753,20 +759,33 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
     const Start st = *start;
     const bool work = st.u1 > st.u0;
 
-    if (warp < 8) {
-        // ------------------------------------------------ softmax, a thread per row
-        if constexpr (!TMA) tc::regs_inc<152>();
-        const int sub = warp >> 2, row = threadIdx.x & 127;
-        const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + lanes + sub * 128, to = tmem + lanes + 256 + sub * 128;
-        float *state = reinterpret_cast<float *>(sm + L::state) + row;      // m, l of warpgroup 1
-        uint32_t tile_n = 0, mine_n = 0, joins = 0;             // key tiles of the CTA, of this warpgroup; joins
+    if (warp < 16) {
+        // ------------------------------------------------ softmax, two threads per row
+        const int sub = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, row = threadIdx.x & 127;
+        const uint32_t lanes = uint32_t(quarter * 32) << 16;
+        // this half's scores; its weights take the first 32 of these columns
+        const uint32_t ts = tmem + lanes + sub * 128 + half * 64;
+        constexpr int DH = D / 2;                               // output columns of a half
+        const uint32_t to = tmem + lanes + 256 + sub * 128 + half * DH;
+        float *state = reinterpret_cast<float *>(sm + L::state) + row;      // m, l of pair 1
+        float *own_max = reinterpret_cast<float *>(sm + L::maxima) + (2 * sub + half) * 128 + row;
+        float *other_max = reinterpret_cast<float *>(sm + L::maxima) + (2 * sub + 1 - half) * 128 + row;
+        uint32_t tile_n = 0, mine_n = 0, joins = 0, pairs = 0;  // key tiles of the CTA, of this pair; joins; exchanges
         uint32_t outs[2] = {0, 0};                              // accumulators completed so far
+        // the other half's value of this row
+        auto exchange = [&](int at, float x, float &y) -> bool {
+            own_max[at] = x;
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bars.pair(sub, quarter));
+            const bool ok = warp_wait(bars.pair(sub, quarter), pairs++ & 1, gone);
+            y = other_max[at];
+            return ok;
+        };
         if (work) {
             Walk w = walk_from(p, st);
             do {
                 const int nk = w.k1 - w.k0;
-                const bool split = w.subtiles() == 1;           // both warpgroups on one subtile
+                const bool split = w.subtiles() == 1;           // both pairs on one subtile
                 const int r = w.tile * kRowTile + (split ? 0 : sub * 128) + row;
                 const bool live = r < w.s.rows;
                 const bool idle = !__any_sync(0xffffffffu, live);
@@ -792,21 +811,22 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                         continue;
                     }
                     const ColSlot &cs = cols[(tile_n + j) % L::kColSlots];
-                    const float *kcol = cs.k;
+                    const float *kcol = cs.k + half * 64;
                     // keys behind the row's limit, and blocks that are not there
                     uint32_t there = cs.mask[0];
                     if constexpr (!TMA) there |= cs.mask[1] | cs.mask[2] | cs.mask[3];
-                    const int rel = lim - (w.k0 + j) * kKeyTile;
-                    if (__any_sync(0xffffffffu, rel < kKeyTile || there != 0xffffu)) {
+                    there = (there >> (8 * half)) & 0xffu;
+                    const int rel = lim - (w.k0 + j) * kKeyTile - half * 64;
+                    if (__any_sync(0xffffffffu, rel < 64 || there != 0xffu)) {
                         // few tiles: masked in place, in a rolled loop, before the others' path
 #pragma unroll 1
-                        for (int o = 0; o < kKeyTile; o += 16) {
+                        for (int o = 0; o < 64; o += 16) {
                             uint32_t x[16];
                             tc::tmem_ld16_wait(ts + o, x);
                             const uint32_t g = there >> (o >> 3);
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
-                                if constexpr (GS) x[i] = __float_as_uint(__uint_as_float(x[i]) * cs.k[o + i]);
+                                if constexpr (GS) x[i] = __float_as_uint(__uint_as_float(x[i]) * kcol[o + i]);
                                 if (o + i >= rel || !((g >> (i >> 3)) & 1u)) x[i] = 0xff800000u;
                             }
                             tc::tmem_st16(ts + o, x);
@@ -814,49 +834,42 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                         tc::tmem_st_wait();
                         kcol = reinterpret_cast<const float *>(sm + L::ones);
                     }
-                    // the tile's columns in four chunks of 32.  The first two stay in registers
-                    // from the maximum on; the others are read twice, which costs less
-                    // than the registers would.
-                    uint32_t a[32], b[32];
-                    tc::tmem_ld32(ts + 64, a, 0);
-                    tc::tmem_ld32(ts + 96, b, 0);
-                    auto scaled = [&](uint32_t (&x)[32], int ch) {
+                    // the half's 64 columns in four chunks of 16, read twice: for the
+                    // maximum and for the weights.  Kept in registers in between they would
+                    // cost the threads that a pair per row needs.
+                    uint32_t x[2][16];
+                    auto scaled = [&](uint32_t (&v)[16], int o) {
                         if constexpr (GS) {
 #pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                const float4 k4 = *reinterpret_cast<const float4 *>(kcol + 32 * ch + i);
-                                const float2 u = tc::mul2(f2(x, i), make_float2(k4.x, k4.y));
-                                const float2 v = tc::mul2(f2(x, i + 2), make_float2(k4.z, k4.w));
-                                x[i] = __float_as_uint(u.x);
-                                x[i + 1] = __float_as_uint(u.y);
-                                x[i + 2] = __float_as_uint(v.x);
-                                x[i + 3] = __float_as_uint(v.y);
+                            for (int i = 0; i < 16; i += 4) {
+                                const float4 k4 = *reinterpret_cast<const float4 *>(kcol + o + i);
+                                const float2 u = tc::mul2(f2(v, i), make_float2(k4.x, k4.y));
+                                const float2 y = tc::mul2(f2(v, i + 2), make_float2(k4.z, k4.w));
+                                v[i] = __float_as_uint(u.x);
+                                v[i + 1] = __float_as_uint(u.y);
+                                v[i + 2] = __float_as_uint(y.x);
+                                v[i + 3] = __float_as_uint(y.y);
                             }
                         }
                     };
                     float mx[4] = {ninf, ninf, ninf, ninf};
-                    auto largest = [&](const uint32_t (&x)[32]) {
+                    tc::tmem_ld16(ts, x[0]);
 #pragma unroll
-                        for (int u = 0; u < 32; u += 8)
+                    for (int q = 0; q < 4; ++q) {
+                        tc::tmem_ld_wait16(x[q & 1]);
+                        if (q < 3) tc::tmem_ld16(ts + 16 * (q + 1), x[(q + 1) & 1]);
+                        scaled(x[q & 1], 16 * q);
+#pragma unroll
+                        for (int u = 0; u < 16; u += 8)
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(x[u + i])), __uint_as_float(x[u + 4 + i]));
-                    };
-                    tc::tmem_ld_wait32(a, 0);
-                    tc::tmem_ld_wait32(b, 0);
-                    scaled(a, 2);
-                    largest(a);
-                    tc::tmem_ld32(ts, a, 0);
-                    scaled(b, 3);
-                    largest(b);
-                    tc::tmem_ld32(ts + 32, b, 0);
-                    tc::tmem_ld_wait32(a, 0);
-                    tc::tmem_ld_wait32(b, 0);
-                    scaled(a, 0);
-                    largest(a);
-                    scaled(b, 1);
-                    largest(b);
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                                mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(x[q & 1][u + i])), __uint_as_float(x[q & 1][u + 4 + i]));
+                    }
+                    tc::tmem_ld16(ts, x[0]);
+                    float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), others;
+                    ok = exchange(0, top, others);
+                    if (!ok) break;
+                    top = fmaxf(top, others);
                     float grow = 1.0f;                          // what O and l shrink by
                     if (top > m && (m == ninf || (top - m) * c > 8.0f)) {
                         grow = m == ninf ? 0.0f : exp2_approx((m - top) * c);
@@ -875,56 +888,49 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                     if (j > j0 && __any_sync(0xffffffffu, grow != 1.0f)) {
                         // seldom: a rolled loop keeps its registers out of the way
 #pragma unroll 1
-                        for (int o = 0; o < D; o += 16) {
-                            uint32_t x[16];
-                            tc::tmem_ld16_wait(to + o, x);
+                        for (int o = 0; o < DH; o += 16) {
+                            uint32_t y[16];
+                            tc::tmem_ld16_wait(to + o, y);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * grow);
-                            tc::tmem_st16(to + o, x);
+                            for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * grow);
+                            tc::tmem_st16(to + o, y);
                         }
                     }
                     float off = m == ninf ? 0.0f : m * c;
                     if constexpr (kVRef) off += vexp;
                     const float2 c2 = make_float2(c, c), off2 = make_float2(-off, -off);
                     float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
-                    auto weights = [&](const uint32_t (&x)[32], int ch) {
-                        uint32_t pk[16];
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            const float2 y0 = tc::fma2(f2(x, i), c2, off2), y1 = tc::fma2(f2(x, i + 2), c2, off2);
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t (&v)[16] = x[q & 1];
+                        tc::tmem_ld_wait16(v);
+                        if (q < 3) tc::tmem_ld16(ts + 16 * (q + 1), x[(q + 1) & 1]);
+                        scaled(v, 16 * q);
+                        uint32_t pk[8];
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4) {
+                            const float2 y0 = tc::fma2(f2(v, i), c2, off2), y1 = tc::fma2(f2(v, i + 2), c2, off2);
                             float2 e0 = make_float2(exp2_approx(y0.x), exp2_approx(y0.y));
                             float2 e1 = make_float2(exp2_approx(y1.x), exp2_approx(y1.y));
                             sum[0] = tc::add2(sum[0], e0);
                             sum[1] = tc::add2(sum[1], e1);
                             if constexpr (GS) {
-                                const float4 v4 = *reinterpret_cast<const float4 *>(cs.v + 32 * ch + i);
+                                const float4 v4 = *reinterpret_cast<const float4 *>(cs.v + half * 64 + 16 * q + i);
                                 e0 = tc::mul2(e0, make_float2(v4.x, v4.y));
                                 e1 = tc::mul2(e1, make_float2(v4.z, v4.w));
                             }
                             pk[i >> 1] = tc::pack16<QK>(e0.x, e0.y);
                             pk[(i >> 1) + 1] = tc::pack16<QK>(e1.x, e1.y);
                         }
-                        tc::tmem_st16(ts + 16 * ch, pk);
-                    };
-                    auto hand = [&](uint32_t bar) {
-                        tc::tmem_st_wait();
-                        tc::fence_before();
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(bar);
-                    };
-                    // P overwrites chunks 0 and 1, which are in registers by now
-                    weights(a, 0);
-                    tc::tmem_ld32(ts + 64, a, 0);
-                    weights(b, 1);
-                    tc::tmem_ld32(ts + 96, b, 0);
-                    hand(bars.p_half(sub));
-                    tc::tmem_ld_wait32(a, 0);
-                    tc::tmem_ld_wait32(b, 0);
-                    scaled(a, 2);
-                    weights(a, 2);
-                    scaled(b, 3);
-                    weights(b, 3);
-                    hand(bars.p_full(sub));
+                        // over columns that have been read for the last time
+                        tc::tmem_st8(ts + 8 * q, pk);
+                        if (q & 1) {                            // 32 of the half's keys are ready
+                            tc::tmem_st_wait();
+                            tc::fence_before();
+                            __syncwarp();
+                            if (lane == 0) ptx::mbar_arrive(q == 1 ? bars.p_half(sub) : bars.p_full(sub));
+                        }
+                    }
                     sum[0] = tc::add2(sum[0], sum[1]);
                     l += sum[0].x + sum[0].y;
                 }
@@ -934,18 +940,26 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                 const bool two = !split || nk > 1;              // both are in use
                 const uint32_t turn0 = outs[0]++, turn1 = outs[1];
                 if (two) ++outs[1];
+                if (sub == 1 && !two) continue;
+                if (!idle) {                                    // the row's sum over both halves
+                    float others;
+                    ok = exchange(512, l, others);
+                    l += others;
+                    if (!ok) break;
+                }
                 float off = m == ninf ? m : m * c;
                 if constexpr (kVRef) off = m == ninf ? m : off + vexp;
-                float w0 = 1.0f, w1 = 0.0f;                     // weights of O (own) and warpgroup 1's
+                float w0 = 1.0f, w1 = 0.0f;                     // weights of O (own) and pair 1's
                 const bool join = split && two;
                 if (sub == 1) {
-                    if (!two) continue;
                     if (join) {
-                        state[0] = off;
-                        state[128] = l;
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(bars.j_full());
-                        // O of this warpgroup is read by the other: not to be overwritten before
+                        if (half == 0) {
+                            state[0] = off;
+                            state[128] = l;
+                            __syncwarp();
+                            if (lane == 0) ptx::mbar_arrive(bars.j_full());
+                        }
+                        // O of this pair is read by the other: not to be overwritten before
                         ok = warp_wait(bars.j_empty(), joins & 1, gone);
                         ++joins;
                         if (!ok) break;
@@ -978,57 +992,53 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                 w1 *= fac;
                 const int tok = r / d.group;
                 const int head = w.h * d.group + (r - tok * d.group);
-                char *o_row = d.out + int64_t(w.s.s0 + tok) * d.o_b + int64_t(head) * d.o_h;
+                char *o_row = d.out + int64_t(w.s.s0 + tok) * d.o_b + int64_t(head) * d.o_h + half * DH * 2;
                 const int slot = 2 * blockIdx.x + (w.k0 == 0 ? 1 : 0);
                 const int prow = (split ? 0 : sub * 128) + row;
-                float4 *acc = reinterpret_cast<float4 *>(f.part_acc) + int64_t(slot) * (D / 4) * kRowTile + prow;
-                if (!whole) {
+                float4 *acc = reinterpret_cast<float4 *>(f.part_acc) + (int64_t(slot) * (D / 4) + half * (DH / 4)) * kRowTile + prow;
+                if (!whole && half == 0) {
                     float *ml = f.part_ml + int64_t(slot) * 2 * kRowTile + prow;
                     ml[0] = off;
                     ml[kRowTile] = l;
                 }
                 float bad = 0.0f;
 #pragma unroll 1
-                for (int o = 0; o < D; o += 32) {
-                    if (idle) break;
-                    uint32_t a[32];
-                    tc::tmem_ld32(to + o, a, 0);
-                    tc::tmem_ld_wait32(a, 0);
+                for (int o = 0; o < DH && !idle; o += 16) {
+                    uint32_t a[16];
+                    tc::tmem_ld16_wait(to + o, a);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) a[i] = w0 == 0.0f ? 0u : __float_as_uint(__uint_as_float(a[i]) * w0);
+                    for (int i = 0; i < 16; ++i) a[i] = w0 == 0.0f ? 0u : __float_as_uint(__uint_as_float(a[i]) * w0);
                     if (join) {
-                        uint32_t b[32];
-                        tc::tmem_ld32(to + 128 + o, b, 0);
-                        tc::tmem_ld_wait32(b, 0);
+                        uint32_t b[16];
+                        tc::tmem_ld16_wait(to + 128 + o, b);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
+                        for (int i = 0; i < 16; ++i)
                             if (w1 != 0.0f)
                                 a[i] = __float_as_uint(fmaf(__uint_as_float(b[i]), w1, __uint_as_float(a[i])));
                     }
                     if (!whole) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
+                        for (int i = 0; i < 16; i += 4)
                             acc[(o + i) / 4 * kRowTile] = make_float4(__uint_as_float(a[i]), __uint_as_float(a[i + 1]),
                                                                       __uint_as_float(a[i + 2]), __uint_as_float(a[i + 3]));
                         continue;
                     }
-                    uint32_t pk[16];
+                    uint32_t pk[8];
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
+                    for (int i = 0; i < 16; i += 2) {
                         bad = fmaf(__uint_as_float(a[i]), 0.0f, fmaf(__uint_as_float(a[i + 1]), 0.0f, bad));
                         pk[i / 2] = tc::pack16<QK>(__uint_as_float(a[i]), __uint_as_float(a[i + 1]));
                     }
                     if (!live) continue;
                     if (f.out32) {
                         tc::st_global32(o_row + 2 * o, pk);
-                        tc::st_global32(o_row + 2 * o + 32, pk + 8);
                     } else if (d.out_vec_ok) {
 #pragma unroll
-                        for (int i = 0; i < 16; i += 4)
+                        for (int i = 0; i < 8; i += 4)
                             *reinterpret_cast<uint4 *>(o_row + 2 * (o + 2 * i)) = make_uint4(pk[i], pk[i + 1], pk[i + 2], pk[i + 3]);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
+                        for (int i = 0; i < 8; ++i) {
                             reinterpret_cast<uint16_t *>(o_row)[o + 2 * i] = uint16_t(pk[i]);
                             reinterpret_cast<uint16_t *>(o_row)[o + 2 * i + 1] = uint16_t(pk[i] >> 16);
                         }
@@ -1039,7 +1049,7 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(bars.j_empty());
                 }
-                // not finite: weights of zero met values that are not; such a row is done again by itself
+                // not finite: weights of zero met values that are not; such a half row is done again by itself
                 unsigned redo = __ballot_sync(0xffffffffu, whole && live && bad != 0.0f);
                 while (redo) {
                     const int who = __ffs(redo) - 1;
@@ -1047,14 +1057,11 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                     const int rr = __shfl_sync(0xffffffffu, r, who), ll = __shfl_sync(0xffffffffu, lim, who);
                     const int tt = rr / d.group;
                     redo_row<QK, CK, D>(d, d.block_tables + w.b * d.bt_b, int64_t(w.s.s0) + tt,
-                                        w.h * d.group + (rr - tt * d.group), ll, w.limit, 0, D);
+                                        w.h * d.group + (rr - tt * d.group), ll, w.limit, half * DH, half * DH + DH);
                 }
             } while (w.next(p));
         }
     } else {
-        if constexpr (!TMA) {
-            if (warp < 12) tc::regs_dec<120>(); else tc::regs_dec<88>();
-        }
         if (warp == kMmaWarp) {
             // -------------------------------------------- the products
             if (work) {
@@ -1077,15 +1084,17 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                         tc::commit(bars.s_full(i));
                     }
                 };
-                // O[i] (+)= P[i] V, keys in two halves: the first half's products run
-                // while the others' weights are made
-                auto pv = [&](int i, int half, uint32_t stage, bool acc) {
+                // O[i] (+)= P[i] V, the first 32 keys of each half and then the others:
+                // the first ones' products run while the others' weights are made
+                auto pv = [&](int i, int part, uint32_t stage, bool acc) {
                     const uint32_t b = v_lo + stage * (L::kTile >> 4), t = tmem + i * 128;
                     if (leader) {
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            tc::mma_ts(t + 256, t + (4 * half + ks) * 8, b + (4 * half + ks) * (2048 >> 4), id_pv,
-                                       ks > 0 || half > 0 || acc);
+                        for (int u = 0; u < 4; ++u) {
+                            const int half = u >> 1, ks = 2 * part + (u & 1);       // 16 keys from 64 half + 16 ks
+                            tc::mma_ts(t + 256, t + 64 * half + 8 * ks, b + (4 * half + ks) * (2048 >> 4), id_pv,
+                                       u > 0 || part > 0 || acc);
+                        }
                     }
                 };
                 auto release = [&](uint32_t bar) {
@@ -1218,7 +1227,7 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                 }
                 f.desc[blockIdx.x] = ds;
             }
-        } else if (TMA && warp == 9) {
+        } else if (TMA && warp == 17) {
             // -------------------------------------------- K/V by TMA: whole blocks' pieces of 64 elements
             const int shift = min(d.block_shift, 7);            // rows per box
             const int rows = 1 << shift, nblk = kKeyTile >> shift;
@@ -1290,14 +1299,14 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                     }
                 }
             }
-        } else if (!TMA && warp < 12) {
+        } else if (!TMA && warp < 20) {
             if (work) {
                 if constexpr (FEED == kFeedCodes)
-                    convert_rows<QK, CK, D, GS>(p, st, sm, sm32, bars, gone, warp - 8, lane);
+                    convert_rows<QK, CK, D, GS>(p, st, sm, sm32, bars, gone, warp - 16, lane);
                 else if constexpr (FEED == kFeedCopy)
-                    copy_rows<CK, D>(p, st, sm32 + L::ring, cols, bars, gone, warp - 8, lane);
+                    copy_rows<CK, D>(p, st, sm32 + L::ring, cols, bars, gone, warp - 16, lane);
             }
-        } else if (FEED == kFeedCodes && warp == 13) {
+        } else if (FEED == kFeedCodes && warp == 21) {
             if constexpr (FEED == kFeedCodes) {
                 if (work) raw_codes<CK, D>(p, f, st, sm, sm32, bars, &tmk, &tmv, gone, lane);
             }

@@ -72,16 +72,27 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[N],
         : "memory");
 }
 
-// 16 columns, loaded and waited for
-__device__ __forceinline__ void tmem_ld16_wait(uint32_t addr, uint32_t (&r)[16])
+#define PKV_W16(c, r)                                                                                              \
+    c((r)[0]), c((r)[1]), c((r)[2]), c((r)[3]), c((r)[4]), c((r)[5]), c((r)[6]), c((r)[7]), c((r)[8]), c((r)[9]),  \
+        c((r)[10]), c((r)[11]), c((r)[12]), c((r)[13]), c((r)[14]), c((r)[15])
+
+// 16 columns
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16])
 {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15}, [%16];\ntcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(addr)
-        : "memory");
+        "%15}, [%16];"
+        : PKV_W16("=r", r)
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : PKV_W16("+r", r)::"memory");
+}
+__device__ __forceinline__ void tmem_ld16_wait(uint32_t addr, uint32_t (&r)[16])
+{
+    tmem_ld16(addr, r);
+    tmem_ld_wait16(r);
 }
 
 template <int N>
@@ -93,6 +104,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[N])
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -206,9 +224,6 @@ __device__ __forceinline__ void st_global32(void *p, const uint32_t *v)
                  "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
 }
-
-template <int N> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // two floats -> packed 16-bit pair (lo in the low half), nearest even
 template <int KIND>
