@@ -198,6 +198,8 @@ struct PrefillParams {
     const int32_t *q_starts;    // [batch + 1]
     int64_t qs_stride;
     int num_tokens;
+    int sub_rows;               // rows (token, head of the group) of a subtile: the whole tokens that fit into
+                                // 128, or 128 for groups above that
 };
 
 struct PrefillPlan {

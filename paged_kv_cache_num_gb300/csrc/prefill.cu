@@ -30,35 +30,61 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder()
     return fn;
 }
 
-// A box is one block's slots (at most 128) of one kv head.  16-bit caches:
-// (element, slot, kv head, block), 64 elements (one 128-byte swizzled row).
-// Codes: the whole rows as bytes, (byte, slot, kv head, block), or
-// x-vectorised (byte of a piece, slot, piece, kv head, block).
-bool cache_map(CUtensorMap *m, const char *base, const DecodeParams &d, int kind)
+// A box is one block's slots (at most 128) of one kv head.  K of 16-bit
+// caches: (element, slot, kv head, block), 64 elements (one 128-byte swizzled
+// row) wide; V: (element of a chunk of 64, slot, chunk, kv head, block), the
+// row's chunks together.  Codes: the whole rows as bytes, (byte, slot,
+// kv head, block), or x-vectorised (byte of a piece, slot, piece, kv head,
+// block).
+bool cache_map(CUtensorMap *m, const char *base, const DecodeParams &d, int kind, bool v)
 {
     auto enc = encoder();
     if (!enc || d.num_blocks == 0) return false;
     const bool coded = kind != kF16 && kind != kBF16;
     const int row = kind == kU3 ? 3 * d.head_dim / 8 : d.head_dim;
     const cuuint32_t slots = cuuint32_t(std::min(d.block_size, 128));
-    cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-    if (coded && d.c_chunk != 16) {
-        cuuint64_t dims[5] = {16, cuuint64_t(d.block_size), cuuint64_t(row / 16), cuuint64_t(d.num_kv_heads),
-                              cuuint64_t(d.num_blocks)};
-        cuuint64_t strides[4] = {cuuint64_t(d.c_slot), cuuint64_t(d.c_chunk), cuuint64_t(d.c_head), cuuint64_t(d.c_blk)};
-        cuuint32_t box[5] = {16, slots, cuuint32_t(row / 16), 1, 1};
-        return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<char *>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-    }
-    cuuint64_t dims[4] = {cuuint64_t(row), cuuint64_t(d.block_size), cuuint64_t(d.num_kv_heads), cuuint64_t(d.num_blocks)};
-    cuuint64_t strides[3] = {cuuint64_t(d.c_slot), cuuint64_t(d.c_head), cuuint64_t(d.c_blk)};
-    cuuint32_t box[4] = {cuuint32_t(coded ? row : 64), slots, 1, 1};
+    const cuuint64_t n_slots = cuuint64_t(d.block_size), heads = cuuint64_t(d.num_kv_heads), blocks = cuuint64_t(d.num_blocks);
+    const cuuint64_t slot = cuuint64_t(d.c_slot), head = cuuint64_t(d.c_head), block = cuuint64_t(d.c_blk);
     const CUtensorMapDataType type = coded ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                      : kind == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    return enc(m, type, 4, const_cast<char *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               coded ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    auto encode = [&](int rank, const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box) {
+        return enc(m, type, rank, const_cast<char *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   coded ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    if (coded && d.c_chunk != 16) {
+        const cuuint64_t dims[5] = {16, n_slots, cuuint64_t(row / 16), heads, blocks};
+        const cuuint64_t strides[4] = {slot, cuuint64_t(d.c_chunk), head, block};
+        const cuuint32_t box[5] = {16, slots, cuuint32_t(row / 16), 1, 1};
+        return encode(5, dims, strides, box);
+    }
+    if (!coded && v) {
+        const cuuint64_t dims[5] = {64, n_slots, cuuint64_t(row / 64), heads, blocks};
+        const cuuint64_t strides[4] = {slot, 128, head, block};
+        const cuuint32_t box[5] = {64, slots, cuuint32_t(row / 64), 1, 1};
+        return encode(5, dims, strides, box);
+    }
+    const cuuint64_t dims[4] = {cuuint64_t(row), n_slots, heads, blocks};
+    const cuuint64_t strides[3] = {slot, head, block};
+    const cuuint32_t box[4] = {cuuint32_t(coded ? row : 64), slots, 1, 1};
+    return encode(4, dims, strides, box);
+}
+
+// (element, q head, token) of q: boxes of 64 elements, a group's heads, a subtile's tokens
+bool q_map(CUtensorMap *m, const PrefillParams &p)
+{
+    auto enc = encoder();
+    const DecodeParams &d = p.d;
+    if (!enc || d.group > 128) return false;
+    const cuuint64_t dims[3] = {cuuint64_t(d.head_dim), cuuint64_t(d.num_heads), cuuint64_t(p.num_tokens)};
+    const cuuint64_t strides[2] = {cuuint64_t(d.q_h), cuuint64_t(d.q_b)};
+    const cuuint32_t box[3] = {64, cuuint32_t(d.group), cuuint32_t(p.sub_rows / d.group)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, d.q_is_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+               const_cast<char *>(d.q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -72,7 +98,7 @@ PrefillPlan plan_prefill(const PrefillParams &p, int, int sm_count)
     const DecodeParams &d = p.d;
     // an upper bound of the units, from the shapes alone: every sequence's
     // rows end in a row tile of their own, every tile sees the whole table
-    const int64_t tiles = int64_t(p.num_tokens) * d.group / 256 + d.batch;
+    const int64_t tiles = int64_t(p.num_tokens) * d.group / (2 * p.sub_rows) + d.batch;
     const int64_t keys = (int64_t(d.max_blocks) * d.block_size + 127) / 128;
     const int64_t units = tiles * d.num_kv_heads * std::max<int64_t>(keys, 1);
     pl.grid = int(std::max<int64_t>(1, std::min<int64_t>(units, sm_count)));
@@ -100,8 +126,10 @@ cudaError_t launch_prefill(const PrefillParams &p, const PrefillPlan &pl, int ca
     // by TMA where a map of the cache can be made (and, for 16-bit caches, the
     // rows are contiguous: x-vectorised ones take 16-byte copies)
     const bool coded = cache_kind != kF16 && cache_kind != kBF16;
-    a.tma = (coded || d.c_chunk == 16) && cache_map(&a.tmk, d.k_cache, d, cache_kind) &&
-            cache_map(&a.tmv, d.v_cache, d, cache_kind);
+    a.tma = (coded || d.c_chunk == 16) && cache_map(&a.tmk, d.k_cache, d, cache_kind, false) &&
+            cache_map(&a.tmv, d.v_cache, d, cache_kind, true);
+    // a negative scale's sign goes into Q, which then is copied by a warp
+    a.q_tma = d.scale_log2 >= 0.0f && q_map(&a.tmq, p);
     a.raw_unit = (reinterpret_cast<uintptr_t>(d.k_cache) | reinterpret_cast<uintptr_t>(d.v_cache) | uintptr_t(d.c_blk) |
                   uintptr_t(d.c_slot) | uintptr_t(d.c_head)) % 4 == 0 ? 4 : 1;
     switch (cache_kind) {

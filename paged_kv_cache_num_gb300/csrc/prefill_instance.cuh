@@ -19,9 +19,10 @@ cudaError_t launch_instance(const PrefillLaunch &a)
     f.part_ml = static_cast<float *>(a.part_ml);
     f.part_acc = static_cast<float *>(a.part_acc);
     f.out32 = a.out32;
+    f.q_tma = a.q_tma;
     f.raw_tma = a.tma;
     f.raw_unit = a.raw_unit;
-    e = launch_pdl(kernel, a.grid, prefill_threads<FEED>(), Smem<CK, D>::alloc, a.stream, *a.p, f, a.tmk, a.tmv);
+    e = launch_pdl(kernel, a.grid, prefill_threads<FEED>(), Smem<CK, D>::alloc, a.stream, *a.p, f, a.tmk, a.tmv, a.tmq);
     if (e != cudaSuccess || !a.join) return e;
     return launch_pdl(prefill_join_kernel<QK, CK, D>, dim3(a.grid, D / 16), kRowTile, 0, a.stream, *a.p, f);
 }

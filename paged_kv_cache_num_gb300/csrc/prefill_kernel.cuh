@@ -12,19 +12,20 @@
 //
 // Decomposition.  The rows of one (sequence, kv head) are its tokens times
 // the group's q heads, token major: a K/V tile read once serves all heads of
-// the group, and the causal border is as sharp as the rows allow.  256 of
-// them (two subtiles of 128) make a row tile; a unit of work is one row tile
-// times one tile of 128 keys that some of its rows see.  All units lie in one
-// flat order (sequence, kv head, row tile, key tile), and CTA i takes
-// [i N / S, (i + 1) N / S): equal work for any mix of lengths, decided on the
-// device (no host read of lengths; graph safe).  A CTA that has the whole key
-// range of a row tile writes its rows; otherwise it writes an fp32 partial
-// (m, l, O), and prefill_join_kernel combines them.
+// the group, and the causal border is as sharp as the rows allow.  Two
+// subtiles of 128 rows (the whole tokens that fit) make a row tile; a unit of
+// work is one row tile times one tile of 128 keys that some of its rows see.
+// All units lie in one flat order (sequence, kv head, row tile, key tile),
+// each row tile's preceded by kTileCost more for what it costs to begin and
+// end one, and CTA i takes [i N / S, (i + 1) N / S): equal work for any mix
+// of lengths, decided on the device (no host read of lengths; graph safe).
+// A CTA that has the whole key range of a row tile writes its rows; otherwise
+// it writes an fp32 partial (m, l, O), and prefill_join_kernel combines them.
 //
 // CTA.  Two pairs of softmax warpgroups (one pair per subtile, two threads
-// per row, 64 keys of a tile each), one warp that issues the products
-// (tcgen05.mma, accumulators and P in tensor memory), warps that load Q, and
-// the K/V producers.  While one subtile's softmax runs the tensor core works
+// per row, 64 keys of a tile each), a warp per subtile that issues its
+// products (tcgen05.mma, accumulators and P in tensor memory), one that loads
+// Q, and the K/V producers.  While one subtile's softmax runs the tensor core works
 // on the other's products: a subtile's scores wait for its last P V, which
 // waits for its softmax, so the softmax's latency bounds the tile rate, and
 // two threads per row halve it.  A row tile of at most 128 rows has one
@@ -52,13 +53,18 @@ struct PrefillFast {
     float *part_ml;             // [2 grid][2][256]
     float *part_acc;            // [2 grid][D / 4][256][4]
     int out32;                  // output rows at multiples of 32 bytes
+    int q_tma;                  // Q by TMA: a positive scale, a map of q
     int raw_tma;                // raw codes by TMA (else by loads of the producer warp)
     int raw_unit;               // ... of 4 bytes or 1
 };
 
 namespace {
 
-constexpr int kRowTile = 256;
+enum Feed : int { kFeedTma, kFeedCopy, kFeedCodes };
+template <int FEED> constexpr int prefill_threads() { return FEED == kFeedTma ? 640 : 768; }
+
+constexpr int kRowTile = 256;   // rows of a row tile, those between a subtile's whole tokens and 128 included
+constexpr int kTileCost = 2;    // beginning and ending a row tile costs as much as this many units
 constexpr int kKeyTile = 128;
 constexpr int kBins = 1024;
 constexpr uint64_t kPrefillTimeoutNs = 4000000000ull;
@@ -81,7 +87,7 @@ __device__ __forceinline__ Seq seq_load(const PrefillParams &p, int b, bool flag
     s.n = bad_q ? 0 : e - a;
     s.ctx = ctx < 0 ? 0 : ctx > cap ? cap : ctx;
     s.rows = s.n * p.d.group;
-    s.nt = (s.rows + kRowTile - 1) / kRowTile;
+    s.nt = (s.rows + 2 * p.sub_rows - 1) / (2 * p.sub_rows);
     return s;
 }
 
@@ -93,27 +99,31 @@ __device__ __forceinline__ int row_limit(const PrefillParams &p, const Seq &s, i
 // keys that some row of the tile sees
 __device__ __forceinline__ int tile_limit(const PrefillParams &p, const Seq &s, int tile)
 {
-    return row_limit(p, s, min((tile + 1) * kRowTile, s.rows) - 1);
+    return row_limit(p, s, min((tile + 1) * 2 * p.sub_rows, s.rows) - 1);
 }
 // units of a row tile: at least one, so that rows that see nothing are written
 __device__ __forceinline__ int tile_units(int limit) { return max(1, (limit + kKeyTile - 1) / kKeyTile); }
 
 // A CTA's walk over its segments: maximal runs of key tiles of one row tile.
+// `at` counts a row tile's cost units, its kTileCost first.
 struct Walk {
-    int64_t left;               // units from this segment on
+    int64_t left;               // cost units from this segment on
     Seq s;
-    int b, h, tile, k0, k1, units, limit;
-    __device__ __forceinline__ void shape(const PrefillParams &p)
+    int b, h, tile, at, k0, k1, units, limit;
+    __device__ __forceinline__ bool shape(const PrefillParams &p)
     {
         limit = tile_limit(p, s, tile);
         units = tile_units(limit);
-        k1 = int(min(int64_t(units), k0 + left));
+        const int end = int(min(int64_t(units + kTileCost), at + left));
+        k0 = max(0, at - kTileCost);
+        k1 = max(0, end - kTileCost);
+        return k1 > k0;
     }
     __device__ __forceinline__ bool next(const PrefillParams &p)
     {
-        left -= k1 - k0;
-        if (left <= 0) return false;
-        k0 = 0;
+        left -= k1 + kTileCost - at;
+        if (left <= kTileCost) return false;            // ends before the next row tile's first unit
+        at = 0;
         if (++tile == s.nt) {
             tile = 0;
             if (++h == p.d.num_kv_heads) {
@@ -121,16 +131,18 @@ struct Walk {
                 do s = seq_load(p, ++b, false); while (s.n == 0);
             }
         }
-        shape(p);
-        return true;
+        return shape(p);
     }
-    __device__ __forceinline__ int subtiles() const { return s.rows - tile * kRowTile > 128 ? 2 : 1; }
+    __device__ __forceinline__ int subtiles(const PrefillParams &p) const
+    {
+        return s.rows - tile * 2 * p.sub_rows > p.sub_rows ? 2 : 1;
+    }
 };
 
 struct Start {
-    int64_t u0, u1, total;      // this CTA's units, all units
+    int64_t u0, u1, total;      // this CTA's cost units, all of them
     int ctas;                   // CTAs that have work
-    int b, h, tile, k0;
+    int b, h, tile, at;
 };
 
 __device__ __forceinline__ Walk walk_from(const PrefillParams &p, const Start &st)
@@ -140,18 +152,18 @@ __device__ __forceinline__ Walk walk_from(const PrefillParams &p, const Start &s
     w.b = st.b;
     w.h = st.h;
     w.tile = st.tile;
-    w.k0 = st.k0;
+    w.at = st.at;
     w.s = seq_load(p, st.b, false);
     w.shape(p);
     return w;
 }
 
-// units of sequence s and one kv head, summed over `lanes` (a power of two)
+// cost units of sequence s and one kv head, summed over `lanes` (a power of two)
 // threads of a warp; every thread of the warp calls it
 __device__ __forceinline__ int64_t seq_units(const PrefillParams &p, const Seq &s, int lane, int lanes)
 {
     int64_t u = 0;
-    for (int i = lane; i < s.nt; i += lanes) u += tile_units(tile_limit(p, s, i));
+    for (int i = lane; i < s.nt; i += lanes) u += tile_units(tile_limit(p, s, i)) + kTileCost;
     for (int o = lanes >> 1; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
     return u;
 }
@@ -194,7 +206,8 @@ __device__ __forceinline__ void find_start(const PrefillParams &p, int64_t *bins
         __syncwarp();
         Start st{};
         st.total = total;
-        st.ctas = int(min(int64_t(gridDim.x), total));
+        // a share is more than kTileCost: every CTA with work has a unit
+        st.ctas = int(min(int64_t(gridDim.x), total / (kTileCost + 1)));
         if (int(blockIdx.x) < st.ctas) {
             st.u0 = blockIdx.x * total / st.ctas;
             st.u1 = (blockIdx.x + 1) * total / st.ctas;
@@ -213,7 +226,7 @@ __device__ __forceinline__ void find_start(const PrefillParams &p, int64_t *bins
             u -= st.h * su;
             const int c = (s.nt + 31) / 32;             // row tiles per lane
             int64_t mine = 0;
-            for (int i = lane * c; i < min((lane + 1) * c, s.nt); ++i) mine += tile_units(tile_limit(p, s, i));
+            for (int i = lane * c; i < min((lane + 1) * c, s.nt); ++i) mine += tile_units(tile_limit(p, s, i)) + kTileCost;
             int64_t x = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -224,14 +237,15 @@ __device__ __forceinline__ void find_start(const PrefillParams &p, int64_t *bins
             const int at = __popc(below);
             u -= at ? __shfl_sync(0xffffffffu, x, at - 1) : 0;
             for (st.tile = at * c;; ++st.tile) {
-                const int t = tile_units(tile_limit(p, s, st.tile));
+                const int t = tile_units(tile_limit(p, s, st.tile)) + kTileCost;
                 if (u < t) break;
                 u -= t;
             }
-            st.k0 = int(u);
+            st.at = int(u);
         }
         if (lane == 0) *out = st;
     }
+    ptx::fence_proxy_async_smem();          // the bins' place is written by asynchronous copies next
     __syncthreads();
 }
 
@@ -323,6 +337,26 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
     return __all_sync(0xffffffffu, bar_wait(bar, parity, gone));
 }
 
+// whether a phase is complete
+__device__ __forceinline__ bool warp_test(uint32_t bar, uint32_t parity)
+{
+    return __all_sync(0xffffffffu, ptx::mbar_test(bar, parity));
+}
+
+// Where tile T's K and V lie in the operand ring: TMA fills a ring of each
+// with a warp of its own, the others fill one in the order K, V, K, V ...
+template <int FEED, int ST>
+struct Ring {
+    static __device__ __forceinline__ uint32_t stage(uint32_t t, int kv)
+    {
+        return FEED == kFeedTma ? t % (ST / 2) + kv * (ST / 2) : (2 * t + kv) % ST;
+    }
+    static __device__ __forceinline__ uint32_t turn(uint32_t t, int kv)
+    {
+        return FEED == kFeedTma ? t / (ST / 2) : (2 * t + kv) / ST;
+    }
+};
+
 // byte offset of 16-byte piece `c` of row `r` in a tile of 128-byte swizzled
 // rows, [64-element chunk][128 rows][128 bytes]
 __device__ __forceinline__ uint32_t piece_at(int r, int c)
@@ -411,6 +445,75 @@ struct TileWalk {
         return true;
     }
 };
+
+// Q of a segment's row tile, once the products of the segment before have
+// read theirs: boxes of (64 elements, heads of the group, tokens) -- rows
+// behind the sequence's last are other rows of q, and nothing comes of them
+// -- or 16-byte copies.
+template <int D>
+__device__ __forceinline__ bool load_q(const PrefillParams &p, const PrefillFast &f, const Walk &w, uint32_t item,
+                                       uint32_t q, const Bars &bars, const CUtensorMap *tmq, volatile int *gone, int lane)
+{
+    const DecodeParams &d = p.d;
+    constexpr int kTile = 128 * D * 2;
+    constexpr int PPR = D / 8;                                  // pieces per row
+    constexpr int RPI = 32 / PPR;                               // rows per instruction
+    if (item > 0 && !warp_wait(bars.q_empty(), (item - 1) & 1, gone)) return false;
+    const int ns = w.subtiles(p);
+    if (f.q_tma) {
+        if (lane == 0) {
+            const int toks = p.sub_rows / d.group;
+            ptx::mbar_arrive_expect_tx(bars.q_full(), uint32_t(ns * p.sub_rows * D * 2));
+            for (int sub = 0; sub < ns; ++sub)
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                    ptx::tma_load_3d(q + sub * kTile + c * 16384, tmq, bars.q_full(), c * 64, w.h * d.group,
+                                     w.s.s0 + (2 * w.tile + sub) * toks);
+        }
+        __syncwarp();
+        return true;
+    }
+    for (int sub = 0; sub < ns; ++sub) {
+        const int c = lane % PPR;
+        int r = (2 * w.tile + sub) * p.sub_rows + lane / PPR;
+        int tok = r / d.group, g = r - tok * d.group;
+#pragma unroll 4
+        for (int i = lane / PPR; i < 128; i += RPI, r += RPI) {
+            const bool in = i < p.sub_rows && r < w.s.rows;
+            const char *src = d.q + int64_t(w.s.s0 + tok) * d.q_b + int64_t(w.h * d.group + g) * d.q_h + 16 * c;
+            tc::cp_async16(q + sub * kTile + piece_at(i, c), in ? src : d.q, in);
+            g += RPI;
+            while (g >= d.group) {
+                g -= d.group;
+                ++tok;
+            }
+        }
+    }
+    tc::cp_async_wait_all();
+    // a negative scale's sign, on the pieces that this lane copied
+    for (int i = d.scale_log2 < 0.0f ? lane : ns * 128 * PPR; i < ns * 128 * PPR; i += 32) {
+        const uint32_t at = q + i / (128 * PPR) * kTile + piece_at((i / PPR) & 127, i % PPR);
+        uint4 v = tc::ld_shared16(at);
+        v.x ^= 0x80008000u;
+        v.y ^= 0x80008000u;
+        v.z ^= 0x80008000u;
+        v.w ^= 0x80008000u;
+        tc::st_shared16(at, v);
+    }
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(bars.q_full());
+    return true;
+}
+
+// The row tile that a CTA begins and does not end, and the CTA that ends it;
+// w: its walk after the last segment.
+__device__ __forceinline__ int4 split_end(const Walk &w, const Start &st, bool done)
+{
+    if (!done || w.k0 != 0 || w.k1 >= w.units) return make_int4(0, 0, 0, -1);
+    const int64_t end = st.u1 - w.left - w.k1 + w.units;       // next() has taken the segment's cost off `left`
+    return make_int4(w.b, w.h, w.tile, int((end * st.ctas + st.total - 1) / st.total) - 1);
+}
 
 // 16-bit rows by 16-byte copies, rows 32 lw .. 32 lw + 31 of every tile by
 // one warp: a lane copies its row's pieces (neighbouring slots are neighbours
@@ -697,21 +800,18 @@ __device__ __forceinline__ void convert_rows(const PrefillParams &p, const Start
 // ---------------------------------------------------------------- the kernel
 // Warps 0-15 softmax, 16-19 producers; 16-bit caches by TMA have the products
 // among the latter, the others in a sixth warpgroup.
-enum Feed : int { kFeedTma, kFeedCopy, kFeedCodes };
-template <int CK> constexpr int feed_of(bool tma) { return is_coded<CK>() ? kFeedCodes : tma ? kFeedTma : kFeedCopy; }
-template <int FEED> constexpr int prefill_threads() { return FEED == kFeedTma ? 640 : 768; }
-
 template <int QK, int CK, int D, int FEED, bool GS>
 __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
     prefill_kernel(PrefillParams p, PrefillFast f, const __grid_constant__ CUtensorMap tmk,
-                   const __grid_constant__ CUtensorMap tmv)
+                   const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmq)
 {
     using L = Smem<CK, D>;
     constexpr int ST = L::kStages;
     constexpr bool TMA = FEED == kFeedTma;
     constexpr bool BF = QK == kBF16;
-    constexpr int kMmaWarp = TMA ? 16 : 20;
-    constexpr int kQWarp = TMA ? 18 : 22;                       // two of them
+    constexpr int kMmaWarp = TMA ? 16 : 20;                     // two of them
+    constexpr int kQWarp = TMA ? 19 : 23;                       // by TMA that of V too
+    using R = Ring<FEED, ST>;
     constexpr bool kVRef = GS && QK == kF16;                    // P relative to the V scales' magnitude
     const DecodeParams &d = p.d;
     extern __shared__ unsigned char smem_raw[];
@@ -728,14 +828,14 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) {
             ptx::mbar_init(bars.full(i), TMA ? 1 : 4);
-            ptx::mbar_init(bars.empty(i), 1);
+            ptx::mbar_init(bars.empty(i), 2);
         }
         for (int i = 0; i < L::kRaw; ++i) {
             ptx::mbar_init(bars.raw_full(i), 1);
             ptx::mbar_init(bars.raw_empty(i), 4);
         }
-        ptx::mbar_init(bars.q_full(), 2);
-        ptx::mbar_init(bars.q_empty(), 1);
+        ptx::mbar_init(bars.q_full(), 1);
+        ptx::mbar_init(bars.q_empty(), 2);
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(bars.s_full(i), 1);
             ptx::mbar_init(bars.p_full(i), 8);
@@ -785,9 +885,9 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
             Walk w = walk_from(p, st);
             do {
                 const int nk = w.k1 - w.k0;
-                const bool split = w.subtiles() == 1;           // both pairs on one subtile
-                const int r = w.tile * kRowTile + (split ? 0 : sub * 128) + row;
-                const bool live = r < w.s.rows;
+                const bool split = w.subtiles(p) == 1;          // both pairs on one subtile
+                const int r = w.tile * 2 * p.sub_rows + (split ? 0 : sub * p.sub_rows) + row;
+                const bool live = row < p.sub_rows && r < w.s.rows;
                 const bool idle = !__any_sync(0xffffffffu, live);
                 const int lim = live ? row_limit(p, w.s, r) : 0;
                 float c = fabsf(d.scale_log2);
@@ -1062,181 +1162,114 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
             } while (w.next(p));
         }
     } else {
-        if (warp == kMmaWarp) {
+        if (warp == kMmaWarp || warp == kMmaWarp + 1) {
             // -------------------------------------------- the products
             if (work) {
                 constexpr uint32_t id_qk = tc::instr_desc<BF, false, 128, 128>();
                 constexpr uint32_t id_pv = tc::instr_desc<BF, true, 128, D>();
                 const bool leader = tc::elect_one();
+                // V tiles: [64-element chunk][128 rows]; by TMA [block][chunk][rows of a block]
+                const int rows = min(d.block_size, 128);
+                const uint32_t v_lbo = TMA ? rows * 128 : 16384, v_sbo = TMA && rows == 8 ? 128 * D / 8 : 1024;
                 const uint32_t q_lo = tc::desc_lo(sm32 + L::q, 16), k_lo = tc::desc_lo(sm32 + L::ring, 16);
-                const uint32_t v_lo = tc::desc_lo(sm32 + L::ring, 16384);
-                uint32_t pos = 0, item = 0, n_p[2] = {0, 0};
-                Walk w = walk_from(p, st);
-                // S[i] = Q[q] K^T of a ring stage
-                auto qk = [&](int i, int q, uint32_t stage) {
-                    const uint32_t a = q_lo + q * (L::kTile >> 4), b = k_lo + stage * (L::kTile >> 4), t = tmem + i * 128;
+                const uint32_t v_lo = tc::desc_lo(sm32 + L::ring, v_lbo), v_hi = tc::desc_hi(v_sbo);
+                uint32_t v_at[8];                               // 16 keys each, in units of 16 bytes
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v_at[i] = TMA ? ((16 * i / rows) * (rows * D * 2) + ((16 * i) & (rows - 1)) * 128) >> 4 : 16 * i * 128 >> 4;
+                const int i = warp - kMmaWarp;                  // the subtile
+                const uint32_t ti = tmem + i * 128;
+                // S = Q K^T of a ring stage
+                auto qk = [&](int q, uint32_t stage) {
+                    const uint32_t a = q_lo + q * (L::kTile >> 4), b = k_lo + stage * (L::kTile >> 4);
                     if (leader) {
 #pragma unroll
                         for (int ks = 0; ks < D / 16; ++ks) {
                             const uint32_t o = (ks >> 2) * (16384 >> 4) + (ks & 3) * (32 >> 4);
-                            tc::mma_ss(t, a + o, b + o, id_qk, ks > 0);
+                            tc::mma_ss(ti, a + o, b + o, id_qk, ks > 0);
                         }
                         tc::commit(bars.s_full(i));
                     }
                 };
-                // O[i] (+)= P[i] V, the first 32 keys of each half and then the others:
-                // the first ones' products run while the others' weights are made
-                auto pv = [&](int i, int part, uint32_t stage, bool acc) {
-                    const uint32_t b = v_lo + stage * (L::kTile >> 4), t = tmem + i * 128;
+                // O (+)= P V, the first 32 keys of each half and then the others: the
+                // first ones' products run while the others' weights are made
+                auto pv = [&](int part, uint32_t stage, bool acc) {
+                    const uint32_t b = v_lo + stage * (L::kTile >> 4);
                     if (leader) {
 #pragma unroll
                         for (int u = 0; u < 4; ++u) {
                             const int half = u >> 1, ks = 2 * part + (u & 1);       // 16 keys from 64 half + 16 ks
-                            tc::mma_ts(t + 256, t + 64 * half + 8 * ks, b + (4 * half + ks) * (2048 >> 4), id_pv,
+                            tc::mma_ts(ti + 256, ti + 64 * half + 8 * ks, b + v_at[4 * half + ks], v_hi, id_pv,
                                        u > 0 || part > 0 || acc);
                         }
                     }
                 };
-                auto release = [&](uint32_t bar) {
-                    if (leader) tc::commit(bar);
+                // a stage is free when both subtiles have used it; on a row tile of one
+                // subtile each of its key tiles has one user, who counts twice
+                auto release = [&](uint32_t bar, bool twice) {
+                    if (leader) {
+                        tc::commit(bar);
+                        if (twice) tc::commit(bar);
+                    }
                 };
-                auto full = [&](uint32_t x) -> bool {
-                    const bool ok = warp_wait(bars.full(x % ST), (x / ST) & 1, gone);
-                    tc::fence_after();
-                    return ok;
-                };
-                auto weights = [&](int i, uint32_t vpos, bool acc, bool v_new) -> bool {
-                    bool ok = warp_wait(bars.p_half(i), n_p[i] & 1, gone);
-                    if (ok && v_new) ok = full(vpos);
-                    if (!ok) return false;
-                    tc::fence_after();
-                    pv(i, 0, vpos % ST, acc);
-                    ok = warp_wait(bars.p_full(i), n_p[i] & 1, gone);
-                    if (!ok) return false;
-                    ++n_p[i];
-                    tc::fence_after();
-                    pv(i, 1, vpos % ST, acc);
-                    return true;
-                };
+                uint32_t tile_n = 0, item = 0, n_p = 0;
+                Walk w = walk_from(p, st);
                 bool ok = true;
                 do {
                     const int nk = w.k1 - w.k0;
+                    const bool split = w.subtiles(p) == 1;
+                    const int step = split ? 2 : 1, j0 = split ? i : 0;
                     ok = warp_wait(bars.q_full(), item & 1, gone);
                     if (!ok) break;
                     tc::fence_after();
-                    if (w.subtiles() == 2) {
-                        ok = full(pos);
+                    for (int j = j0; j < nk; j += step, ++n_p) {
+                        const bool last = j + step >= nk;
+                        const uint32_t t = tile_n + j, ks = R::stage(t, 0), vs = R::stage(t, 1);
+                        ok = warp_wait(bars.full(ks), R::turn(t, 0) & 1, gone);
                         if (!ok) break;
-                        qk(0, 0, pos % ST);
-                        qk(1, 1, pos % ST);
-                        release(bars.empty(pos % ST));
-                        if (nk == 1) release(bars.q_empty());
-                        for (int j = 0; j < nk; ++j, pos += 2) {
-                            const bool more = j + 1 < nk;
-                            const uint32_t kpos = pos + 2;
-                            ok = weights(0, pos + 1, j > 0, true);
-                            if (ok && more) ok = full(kpos);
-                            if (!ok) break;
-                            if (more) qk(0, 0, kpos % ST); else release(bars.o_full(0));
-                            ok = weights(1, pos + 1, j > 0, false);
-                            if (!ok) break;
-                            if (more) qk(1, 1, kpos % ST); else release(bars.o_full(1));
-                            release(bars.empty((pos + 1) % ST));
-                            if (more) release(bars.empty(kpos % ST));
-                            if (j + 2 == nk) release(bars.q_empty());
-                        }
-                    } else {
-                        for (int j = 0; j < min(2, nk) && ok; ++j) {
-                            ok = full(pos + 2 * j);
-                            if (!ok) break;
-                            qk(j, 0, (pos + 2 * j) % ST);
-                            release(bars.empty((pos + 2 * j) % ST));
-                            if (j + 1 == nk) release(bars.q_empty());
-                        }
-                        for (int j = 0; j < nk && ok; ++j, pos += 2) {
-                            const int i = j & 1;
-                            const uint32_t kpos = pos + 4;
-                            ok = weights(i, pos + 1, j > 1, true);
-                            if (!ok) break;
-                            release(bars.empty((pos + 1) % ST));
-                            if (j + 2 < nk) {
-                                ok = full(kpos);
-                                if (!ok) break;
-                                qk(i, 0, kpos % ST);
-                                release(bars.empty(kpos % ST));
-                                if (j + 3 == nk) release(bars.q_empty());
-                            } else {
-                                release(bars.o_full(i));
-                            }
-                        }
+                        tc::fence_after();
+                        qk(split ? 0 : i, ks);
+                        release(bars.empty(ks), split);
+                        if (last) release(bars.q_empty(), false);
+                        ok = warp_wait(bars.full(vs), R::turn(t, 1) & 1, gone) && warp_wait(bars.p_half(i), n_p & 1, gone);
+                        if (!ok) break;
+                        tc::fence_after();
+                        pv(0, vs, j > j0);
+                        ok = warp_wait(bars.p_full(i), n_p & 1, gone);
+                        if (!ok) break;
+                        tc::fence_after();
+                        pv(1, vs, true);
+                        release(bars.empty(vs), split);
+                        if (last) release(bars.o_full(i), false);
                     }
+                    if (!ok) break;
+                    if (j0 >= nk && lane == 0) ptx::mbar_arrive(bars.q_empty());    // had nothing to do
+                    tile_n += nk;
                     ++item;
-                } while (ok && w.next(p));
+                } while (w.next(p));
             }
             __syncwarp();
-        } else if (warp >= kQWarp && warp < kQWarp + 2) {
-            // -------------------------------------------- Q, a warp per subtile
-            const int sub = warp - kQWarp;
-            const bool negate = d.scale_log2 < 0.0f;
-            constexpr int PPR = D / 8;                          // pieces per row
-            constexpr int RPI = 32 / PPR;                       // rows per instruction
+        } else if (!TMA && warp == kQWarp) {
+            // -------------------------------------------- Q
             Walk w;
             uint32_t item = 0;
             bool have = work;
             if (work) w = walk_from(p, st);
             while (have) {
-                if (item > 0 && !warp_wait(bars.q_empty(), (item - 1) & 1, gone)) break;
-                if (sub < w.subtiles()) {
-                    const int c = lane % PPR;
-                    int r = w.tile * kRowTile + sub * 128 + lane / PPR;
-                    int tok = r / d.group, g = r - tok * d.group;
-                    const uint32_t dst = sm32 + L::q + sub * L::kTile;
-#pragma unroll 4
-                    for (int i = lane / PPR; i < 128; i += RPI, r += RPI) {
-                        const bool in = r < w.s.rows;
-                        const char *src = d.q + int64_t(w.s.s0 + tok) * d.q_b + int64_t(w.h * d.group + g) * d.q_h + 16 * c;
-                        tc::cp_async16(dst + piece_at(i, c), in ? src : d.q, in);
-                        g += RPI;
-                        while (g >= d.group) {
-                            g -= d.group;
-                            ++tok;
-                        }
-                    }
-                    tc::cp_async_wait_all();
-                    for (int i = negate ? lane / PPR : 128; i < 128; i += RPI) {
-                        uint4 v = tc::ld_shared16(dst + piece_at(i, c));
-                        v.x ^= 0x80008000u;
-                        v.y ^= 0x80008000u;
-                        v.z ^= 0x80008000u;
-                        v.w ^= 0x80008000u;
-                        tc::st_shared16(dst + piece_at(i, c), v);
-                    }
-                }
-                ptx::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bars.q_full());
-                ++item;
+                if (!load_q<D>(p, f, w, item++, sm32 + L::q, bars, &tmq, gone, lane)) break;
                 have = w.next(p);
             }
-            if (sub == 0 && lane == 0) {
-                // the row tile that this CTA begins and does not end
-                int4 ds = make_int4(0, 0, 0, -1);
-                if (work && !have && w.k0 == 0 && w.k1 < w.units) {
-                    const int64_t end = st.u1 - w.k1 + w.units;
-                    ds = make_int4(w.b, w.h, w.tile, int((end * st.ctas + st.total - 1) / st.total) - 1);
-                }
-                f.desc[blockIdx.x] = ds;
-            }
-        } else if (TMA && warp == 17) {
-            // -------------------------------------------- K/V by TMA: whole blocks' pieces of 64 elements
+            if (lane == 0) f.desc[blockIdx.x] = split_end(w, st, work && !have);
+        } else if (TMA) {
+            // -------------------------------------------- K (warp 18) and V (19) by TMA: whole blocks.  K boxes are
+            // 64 elements wide, V's take the row's 64-element chunks together.  V's warp
+            // loads Q too, before a segment's V, which is needed later
+            const int kv = warp - 18;
+            const CUtensorMap *map = kv ? &tmv : &tmk;
             const int shift = min(d.block_shift, 7);            // rows per box
             const int rows = 1 << shift, nblk = kKeyTile >> shift;
-            const uint32_t box = uint32_t(rows) * 128u;
-            uint32_t pos = 0, tile_n = 0, fixes = 0;
-            if (lane == 0) {
-                ptx::prefetch_tmap(&tmk);
-                ptx::prefetch_tmap(&tmv);
-            }
+            uint32_t tile_n = 0, fixes = 0;
+            if (lane == 0) ptx::prefetch_tmap(map);
             if (work) {
                 TileWalk tw{walk_from(p, st), 0};
                 tw.k = tw.w.k0;
@@ -1248,7 +1281,12 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                 };
                 int blk = lookup();
                 bool ok = true, more = true;
+                uint32_t item = 0;
                 for (; more && ok; ++tile_n) {
+                    if (kv == 1 && tw.k == tw.w.k0) {
+                        ok = load_q<D>(p, f, tw.w, item++, sm32 + L::q, bars, &tmq, gone, lane);
+                        if (!ok) break;
+                    }
                     const int t = tw.k * kKeyTile + lane * rows, h = tw.w.h;
                     const int limit = tw.w.limit - tw.k * kKeyTile;
                     const bool want = lane < nblk && t < tw.w.limit;
@@ -1258,55 +1296,60 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                     const int now = blk, slot0 = t & (d.block_size - 1);
                     more = tw.next(p);
                     if (more) blk = lookup();
-                    const uint32_t bytes = __popc(got) * box * (D / 64);
-#pragma unroll 1
-                    for (int kv = 0; kv < 2; ++kv, ++pos) {
-                        const uint32_t stage = pos % ST;
-                        if (pos >= ST) ok = warp_wait(bars.empty(stage), (pos / ST - 1) & 1, gone);
-                        if (!ok) break;
-                        // V rows that nothing loads, or that no row sees, are zeroed: a weight of zero
-                        // must not meet what lies there
-                        const bool fix = kv == 1 && (__popc(got) < nblk || limit < kKeyTile);
-                        const uint32_t bar = fix ? bars.tail() : bars.full(stage);
-                        const uint32_t dst = sm32 + L::ring + stage * L::kTile;
-                        if (lane == 0) {
-                            if (kv == 0) {
-                                uint32_t there = 0;             // by groups of 8 rows
-                                for (int i = 0; i < 16; ++i) there |= ((got >> ((i * 8) >> shift)) & 1u) << i;
-                                cols[tile_n % L::kColSlots].mask[0] = there;
-                            }
-                            ptx::mbar_arrive_expect_tx(bar, bytes);
+                    const uint32_t stage = R::stage(tile_n, kv), turn = R::turn(tile_n, kv);
+                    if (turn > 0) ok = warp_wait(bars.empty(stage), (turn - 1) & 1, gone);
+                    if (!ok) break;
+                    // V rows that nothing loads, or that no row sees, are zeroed: a weight of zero
+                    // must not meet what lies there
+                    const bool fix = kv == 1 && (__popc(got) < nblk || limit < kKeyTile);
+                    const uint32_t bar = fix ? bars.tail() : bars.full(stage);
+                    const uint32_t dst = sm32 + L::ring + stage * L::kTile;
+                    if (lane == 0) {
+                        if (kv == 0) {
+                            uint32_t there = 0;                 // by groups of 8 rows
+                            for (int i = 0; i < 16; ++i) there |= ((got >> ((i * 8) >> shift)) & 1u) << i;
+                            cols[tile_n % L::kColSlots].mask[0] = there;
                         }
-                        __syncwarp();
-                        if (in) {
+                        ptx::mbar_arrive_expect_tx(bar, uint32_t(__popc(got) * rows * D * 2));
+                    }
+                    __syncwarp();
+                    if (in) {
+                        if (kv) {
+                            ptx::tma_load_5d(dst + lane * rows * D * 2, map, bar, 0, slot0, 0, h, now);
+                        } else {
 #pragma unroll
                             for (int c = 0; c < D / 64; ++c)
-                                ptx::tma_load_4d(dst + c * 16384 + lane * box, kv ? &tmv : &tmk, bar, c * 64, slot0, h, now);
-                        }
-                        if (fix) {
-                            ok = warp_wait(bar, fixes & 1, gone);
-                            ++fixes;
-                            if (!ok) break;
-                            for (int i = lane; i < kKeyTile * (D / 8); i += 32) {
-                                const int rr = i / (D / 8);
-                                if (rr >= limit || !((got >> (rr >> shift)) & 1u))
-                                    tc::st_shared16(dst + piece_at(rr, i % (D / 8)), make_uint4(0, 0, 0, 0));
-                            }
-                            ptx::fence_proxy_async_smem();
-                            __syncwarp();
-                            if (lane == 0) ptx::mbar_arrive(bars.full(stage));
+                                ptx::tma_load_4d(dst + c * 16384 + lane * rows * 128, map, bar, c * 64, slot0, h, now);
                         }
                     }
+                    if (fix) {
+                        ok = warp_wait(bar, fixes & 1, gone);
+                        ++fixes;
+                        if (!ok) break;
+                        for (int i = lane; i < kKeyTile * (D / 8); i += 32) {
+                            const int rr = i / (D / 8), c = i % (D / 8), in_blk = rr & (rows - 1);
+                            if (rr >= limit || !((got >> (rr >> shift)) & 1u))
+                                tc::st_shared16(dst + (rr >> shift) * rows * D * 2 + (c >> 3) * rows * 128 + in_blk * 128 +
+                                                    (((c & 7) ^ (in_blk & 7)) << 4),
+                                                make_uint4(0, 0, 0, 0));
+                        }
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(bars.full(stage));
+                    }
                 }
+                if (kv == 1 && lane == 0) f.desc[blockIdx.x] = split_end(tw.w, st, ok);
+            } else if (kv == 1 && lane == 0) {
+                f.desc[blockIdx.x] = make_int4(0, 0, 0, -1);
             }
-        } else if (!TMA && warp < 20) {
+        } else if (warp < 20) {
             if (work) {
                 if constexpr (FEED == kFeedCodes)
                     convert_rows<QK, CK, D, GS>(p, st, sm, sm32, bars, gone, warp - 16, lane);
                 else if constexpr (FEED == kFeedCopy)
                     copy_rows<CK, D>(p, st, sm32 + L::ring, cols, bars, gone, warp - 16, lane);
             }
-        } else if (FEED == kFeedCodes && warp == 21) {
+        } else if (FEED == kFeedCodes && warp == 22) {
             if constexpr (FEED == kFeedCodes) {
                 if (work) raw_codes<CK, D>(p, f, st, sm, sm32, bars, &tmk, &tmv, gone, lane);
             }
@@ -1338,8 +1381,8 @@ __global__ void __launch_bounds__(kRowTile) prefill_join_kernel(PrefillParams p,
     if (ds.w < 0) return;
     const DecodeParams &d = p.d;
     const Seq s = seq_load(p, ds.x, false);
-    const int row = threadIdx.x, r = ds.z * kRowTile + row;
-    const bool live = r < s.rows;
+    const int row = threadIdx.x, r = (2 * ds.z + (row >> 7)) * p.sub_rows + (row & 127);
+    const bool live = (row & 127) < p.sub_rows && r < s.rows;
     const int lim = live ? row_limit(p, s, r) : 0;
     const int tok = r / d.group, head = ds.y * d.group + (r - tok * d.group);
     const int c0 = blockIdx.y * 16;

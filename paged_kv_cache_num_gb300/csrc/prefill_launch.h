@@ -15,7 +15,8 @@ struct PrefillLaunch {
     int raw_unit;               // else raw codes by loads of 4 bytes or 1
     int out32;                  // output rows at multiples of 32 bytes
     void *desc, *part_ml, *part_acc;
-    CUtensorMap tmk, tmv;
+    bool q_tma;                 // Q by TMA (tmq)
+    CUtensorMap tmk, tmv, tmq;
     cudaStream_t stream;
 };
 

@@ -116,11 +116,12 @@ __device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8])
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // ---------------------------------------------------------------- matrix descriptors
-// Shared-memory operands in 128-byte-swizzled rows, groups of 8 rows 1024
-// bytes apart: the descriptor's low word holds the address and the byte
-// stride `lbo` between 64-element chunks of the contiguous dimension
-// (operands whose contiguous dimension is N), the high word is constant
-// (that group stride, the descriptor version, the swizzle).
+// Shared-memory operands in 128-byte-swizzled rows: the descriptor's low word
+// holds the address and the byte stride `lbo` between 64-element chunks of the
+// contiguous dimension (operands whose contiguous dimension is N), the high
+// word the byte stride `sbo` between groups of 8 rows, the descriptor's
+// version and the swizzle.
+__device__ __forceinline__ constexpr uint32_t desc_hi(uint32_t sbo) { return (sbo >> 4) | (1u << 14) | (2u << 29); }
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return ((addr & 0x3ffffu) >> 4) | ((lbo >> 4) << 16); }
 
@@ -143,12 +144,12 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t alo, uint32_t blo, u
 }
 
 // D[tmem] (+)= A[tmem] * B[smem]
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t blo, uint32_t idesc, bool acc)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t blo, uint32_t bhi, uint32_t idesc, bool acc)
 {
     asm volatile(
         "{\n.reg .pred p;\n.reg .b64 b;\nsetp.ne.b32 p, %4, 0;\nmov.b64 b, {%2, %5};\n"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}" ::"r"(d),
-        "r"(a), "r"(blo), "r"(idesc), "r"(uint32_t(acc)), "n"(kDescHi)
+        "r"(a), "r"(blo), "r"(idesc), "r"(uint32_t(acc)), "r"(bhi)
         : "memory");
 }
 
