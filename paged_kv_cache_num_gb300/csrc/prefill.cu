@@ -128,8 +128,10 @@ cudaError_t launch_prefill(const PrefillParams &p, const PrefillPlan &pl, int ca
     const bool coded = cache_kind != kF16 && cache_kind != kBF16;
     a.tma = (coded || d.c_chunk == 16) && cache_map(&a.tmk, d.k_cache, d, cache_kind, false) &&
             cache_map(&a.tmv, d.v_cache, d, cache_kind, true);
-    // a negative scale's sign goes into Q, which then is copied by a warp
-    a.q_tma = d.scale_log2 >= 0.0f && q_map(&a.tmq, p);
+    // a negative scale's sign goes into Q: where bf16 Q becomes f16 in any case,
+    // or by a warp that copies it
+    a.flip_q = d.scale_log2 < 0.0f && coded && d.q_is_bf16;
+    a.q_tma = (d.scale_log2 >= 0.0f || a.flip_q) && q_map(&a.tmq, p);
     a.raw_unit = (reinterpret_cast<uintptr_t>(d.k_cache) | reinterpret_cast<uintptr_t>(d.v_cache) | uintptr_t(d.c_blk) |
                   uintptr_t(d.c_slot) | uintptr_t(d.c_head)) % 4 == 0 ? 4 : 1;
     switch (cache_kind) {

@@ -20,6 +20,7 @@ cudaError_t launch_instance(const PrefillLaunch &a)
     f.part_acc = static_cast<float *>(a.part_acc);
     f.out32 = a.out32;
     f.q_tma = a.q_tma;
+    f.flip_q = a.flip_q;
     f.raw_tma = a.tma;
     f.raw_unit = a.raw_unit;
     e = launch_pdl(kernel, a.grid, prefill_threads<FEED>(), Smem<CK, D>::alloc, a.stream, *a.p, f, a.tmk, a.tmv, a.tmq);

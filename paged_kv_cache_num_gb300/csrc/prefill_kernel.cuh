@@ -22,23 +22,24 @@
 // A CTA that has the whole key range of a row tile writes its rows; otherwise
 // it writes an fp32 partial (m, l, O), and prefill_join_kernel combines them.
 //
-// CTA.  Two pairs of softmax warpgroups (one pair per subtile, two threads
-// per row, 64 keys of a tile each), a warp per subtile that issues its
-// products (tcgen05.mma, accumulators and P in tensor memory), one that loads
-// Q, and the K/V producers.  While one subtile's softmax runs the tensor core works
-// on the other's products: a subtile's scores wait for its last P V, which
-// waits for its softmax, so the softmax's latency bounds the tile rate, and
-// two threads per row halve it.  A row tile of at most 128 rows has one
-// subtile: then the pairs take its key tiles in turn, with states of their
-// own that are joined at the end.
+// CTA.  Two softmax warpgroups (one per subtile, a thread per row), a warp per
+// subtile that issues its products (tcgen05.mma, accumulators and P in tensor
+// memory), one that loads Q, and the K/V producers.  While one subtile's
+// softmax runs the tensor core works on the other's products: a subtile's
+// scores wait for its last P V (they share tensor memory), which waits for its
+// softmax, so that chain bounds the tile rate.  A row tile of at most 128 rows
+// has one subtile: then the warpgroups take its key tiles in turn, with states
+// of their own that are joined at the end.
 //
 // K/V.  16-bit caches in the flash layout: one warp issues TMA copies of
 // whole block pieces into the operand ring; x-vectorised 16-bit caches: four
 // warps copy 16-byte pieces.  One-byte and 3-bit caches: one warp issues TMA
 // copies of the raw codes, four warps convert them into the operand ring.
-// Codes are converted exactly (every code of every kind is a number of both
-// 16-bit types); their scales are applied in fp32: per-head scales to c and
-// to the result, per-row scales to the columns of S and of P.
+// Codes become f16 exactly (every code of every kind is an f16 number); their
+// scales are applied in fp32: per-head scales to c and to the result, per-row
+// scales to the columns of S and of P.  bf16 queries of such caches are
+// brought to f16 by a power of two per row, exactly but for elements below
+// 2^-39 of the row's largest.
 #pragma once
 
 #include <type_traits>
@@ -53,7 +54,8 @@ struct PrefillFast {
     float *part_ml;             // [2 grid][2][256]
     float *part_acc;            // [2 grid][D / 4][256][4]
     int out32;                  // output rows at multiples of 32 bytes
-    int q_tma;                  // Q by TMA: a positive scale, a map of q
+    int q_tma;                  // Q by TMA
+    int flip_q;                 // a negative scale's sign is still to be given to Q
     int raw_tma;                // raw codes by TMA (else by loads of the producer warp)
     int raw_unit;               // ... of 4 bytes or 1
 };
@@ -61,7 +63,7 @@ struct PrefillFast {
 namespace {
 
 enum Feed : int { kFeedTma, kFeedCopy, kFeedCodes };
-template <int FEED> constexpr int prefill_threads() { return FEED == kFeedTma ? 640 : 768; }
+template <int FEED> constexpr int prefill_threads() { return FEED == kFeedTma ? 384 : 512; }
 
 constexpr int kRowTile = 256;   // rows of a row tile, those between a subtile's whole tokens and 128 included
 constexpr int kTileCost = 2;    // beginning and ending a row tile costs as much as this many units
@@ -267,10 +269,10 @@ struct Smem {
     static constexpr int cols = raw + kRaw * kRawTile;
     static constexpr int kColBytes = 2 * kKeyTile * 4 + 32;
     static constexpr int ones = cols + kColSlots * kColBytes;   // 128 ones
-    static constexpr int state = ones + 512;                    // pair 1's (m, l) for the join
-    static constexpr int maxima = state + 1024;                 // [subtile][half][row], then the sums likewise
-    static constexpr int bars = maxima + 4096;
-    static constexpr int n_bars = 2 * kStages + 2 * kRaw + 2 + 4 * 2 + 1 + 2 + 8;
+    static constexpr int state = ones + 512;                    // warpgroup 1's (m, l) for the join
+    static constexpr int q_scale = state + 1024;                // per row of subtile 0
+    static constexpr int bars = q_scale + 512;
+    static constexpr int n_bars = 2 * kStages + 2 * kRaw + 2 + 4 * 2 + 1 + 2 + 1;
     static constexpr int info = bars + 8 * n_bars;              // per raw stage: which blocks are there
     static constexpr int misc = (info + 4 * 8 + 15) / 16 * 16;
     static constexpr int total = misc + 128;
@@ -305,15 +307,15 @@ struct Bars {
     __device__ __forceinline__ uint32_t s_full(int i) const { return base + 8 * (2 * stages + 2 + i); }
     __device__ __forceinline__ uint32_t p_full(int i) const { return base + 8 * (2 * stages + 4 + i); }
     __device__ __forceinline__ uint32_t o_full(int i) const { return base + 8 * (2 * stages + 6 + i); }
-    __device__ __forceinline__ uint32_t p_half(int i) const { return base + 8 * (2 * stages + 8 + i); }
+    __device__ __forceinline__ uint32_t p_most(int i) const { return base + 8 * (2 * stages + 8 + i); }
     __device__ __forceinline__ uint32_t tail() const { return base + 8 * (2 * stages + 10); }
-    // the join of two pairs' states: pair 1's is there, and has been read
+    // the join of two warpgroups' states: warpgroup 1's is there, and has been read
     __device__ __forceinline__ uint32_t j_full() const { return base + 8 * (2 * stages + 11); }
     __device__ __forceinline__ uint32_t j_empty() const { return base + 8 * (2 * stages + 12); }
-    // two warps with the two halves of the same rows
-    __device__ __forceinline__ uint32_t pair(int sub, int quarter) const { return base + 8 * (2 * stages + 13 + 4 * sub + quarter); }
-    __device__ __forceinline__ uint32_t raw_full(int s) const { return base + 8 * (2 * stages + 21 + s); }
-    __device__ __forceinline__ uint32_t raw_empty(int s) const { return base + 8 * (2 * stages + 21 + raws + s); }
+    // bf16 Q that is to become f16
+    __device__ __forceinline__ uint32_t q_raw() const { return base + 8 * (2 * stages + 13); }
+    __device__ __forceinline__ uint32_t raw_full(int s) const { return base + 8 * (2 * stages + 14 + s); }
+    __device__ __forceinline__ uint32_t raw_empty(int s) const { return base + 8 * (2 * stages + 14 + raws + s); }
 };
 
 // Wait for a phase, giving up when it takes too long or another warp gave up.
@@ -370,66 +372,49 @@ template <int N> __device__ __forceinline__ float2 f2(const uint32_t (&x)[N], in
 }
 
 // ---------------------------------------------------------------- codes -> 16 bits
-__device__ __forceinline__ uint32_t sub16x2(uint32_t a, uint32_t b, bool bf16)
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b)
 {
     uint32_t r;
-    if (bf16)
-        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    else
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
-// four one-byte codes -> four 16-bit numbers, exactly
-template <int QK, int CK>
-__device__ __forceinline__ uint2 q8x4_to_16(uint32_t w)
+// four one-byte codes -> four f16 numbers, exactly
+template <int CK>
+__device__ __forceinline__ uint2 q8x4_to_f16(uint32_t w)
 {
-    if constexpr (CK == kI8) {
-        const uint32_t u = w ^ 0x80808080u;                     // c + 128
-        if constexpr (QK == kF16) {                             // 1024 + (c + 128), minus 1152
-            return make_uint2(sub16x2(ptx::prmt(u, 0x64646464u, 0x4140), 0x64806480u, false),
-                              sub16x2(ptx::prmt(u, 0x64646464u, 0x4342), 0x64806480u, false));
-        } else {                                                // 2^23 + (c + 128) in fp32, minus 2^23 + 128
-            float f[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                f[j] = __uint_as_float(ptx::prmt(u, 0x4b000000u, 0x7540 | j)) - 8388736.0f;
-            return make_uint2(tc::pack16<kBF16>(f[0], f[1]), tc::pack16<kBF16>(f[2], f[3]));
-        }
-    } else {
-        uint32_t lo, hi;
-        if constexpr (CK == kE4M3)
-            asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\ncvt.rn.f16x2.e4m3x2 %0, l;\ncvt.rn.f16x2.e4m3x2 %1, h;\n}"
-                : "=r"(lo), "=r"(hi) : "r"(w));
-        else
-            asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\ncvt.rn.f16x2.e5m2x2 %0, l;\ncvt.rn.f16x2.e5m2x2 %1, h;\n}"
-                : "=r"(lo), "=r"(hi) : "r"(w));
-        if constexpr (QK == kF16) {
-            return make_uint2(lo, hi);
-        } else {
-            const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
-            const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-            return make_uint2(tc::pack16<kBF16>(a.x, a.y), tc::pack16<kBF16>(b.x, b.y));
-        }
+    uint32_t lo, hi;
+    if constexpr (CK == kI8) {                                  // 1024 + (c + 128), minus 1152
+        const uint32_t u = w ^ 0x80808080u;
+        lo = sub_f16x2(ptx::prmt(u, 0x64646464u, 0x4140), 0x64806480u);
+        hi = sub_f16x2(ptx::prmt(u, 0x64646464u, 0x4342), 0x64806480u);
+    } else if constexpr (CK == kE4M3) {
+        asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\ncvt.rn.f16x2.e4m3x2 %0, l;\ncvt.rn.f16x2.e4m3x2 %1, h;\n}"
+            : "=r"(lo), "=r"(hi) : "r"(w));
+    } else {                                                    // e5m2 is the upper byte of an f16 number
+        lo = ptx::prmt(w, 0u, 0x1404);
+        hi = ptx::prmt(w, 0u, 0x3424);
     }
+    return make_uint2(lo, hi);
 }
 
-// eight 3-bit codes (the low 24 bits of w) minus their zero point, as 16-bit
-// numbers: the code under a power of two whose unit step is 1.  zero2: the
-// zero point twice (bf16), or 1024 more (f16)
-template <int QK>
-__device__ __forceinline__ uint4 u3x8_to_16(uint32_t w, uint32_t zero2)
+// eight 3-bit codes (the low 24 bits of w) minus their zero point, as f16
+// numbers: the code in the last place of 1024, minus 1024 + zero (twice)
+__device__ __forceinline__ uint4 u3x8_to_f16(uint32_t w, uint32_t zero2)
 {
-    // bf16 takes the zero point off in a second step: 128 + z need not be a bf16 number
-    constexpr uint32_t magic = QK == kBF16 ? 0x43004300u : 0x64006400u;     // 128, 1024
     uint32_t o[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const uint32_t x = w >> (6 * j);
-        const uint32_t u = (x & 7u) | ((x << 13) & 0x70000u) | magic;
-        o[j] = QK == kBF16 ? sub16x2(sub16x2(u, magic, true), zero2, true) : sub16x2(u, zero2, false);
+        o[j] = sub_f16x2((x & 7u) | ((x << 13) & 0x70000u) | 0x64006400u, zero2);
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// bf16 pair -> f16 pair times s, a power of two
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, float s)
+{
+    return tc::pack16<kF16>(__uint_as_float(w << 16) * s, __uint_as_float(w & 0xffff0000u) * s);
 }
 
 // ---------------------------------------------------------------- K/V producers
@@ -449,10 +434,11 @@ struct TileWalk {
 // Q of a segment's row tile, once the products of the segment before have
 // read theirs: boxes of (64 elements, heads of the group, tokens) -- rows
 // behind the sequence's last are other rows of q, and nothing comes of them
-// -- or 16-byte copies.
+// -- or 16-byte copies; then `full` completes a phase.
 template <int D>
 __device__ __forceinline__ bool load_q(const PrefillParams &p, const PrefillFast &f, const Walk &w, uint32_t item,
-                                       uint32_t q, const Bars &bars, const CUtensorMap *tmq, volatile int *gone, int lane)
+                                       uint32_t q, const Bars &bars, uint32_t full, const CUtensorMap *tmq,
+                                       volatile int *gone, int lane)
 {
     const DecodeParams &d = p.d;
     constexpr int kTile = 128 * D * 2;
@@ -463,11 +449,11 @@ __device__ __forceinline__ bool load_q(const PrefillParams &p, const PrefillFast
     if (f.q_tma) {
         if (lane == 0) {
             const int toks = p.sub_rows / d.group;
-            ptx::mbar_arrive_expect_tx(bars.q_full(), uint32_t(ns * p.sub_rows * D * 2));
+            ptx::mbar_arrive_expect_tx(full, uint32_t(ns * p.sub_rows * D * 2));
             for (int sub = 0; sub < ns; ++sub)
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c)
-                    ptx::tma_load_3d(q + sub * kTile + c * 16384, tmq, bars.q_full(), c * 64, w.h * d.group,
+                    ptx::tma_load_3d(q + sub * kTile + c * 16384, tmq, full, c * 64, w.h * d.group,
                                      w.s.s0 + (2 * w.tile + sub) * toks);
         }
         __syncwarp();
@@ -491,7 +477,7 @@ __device__ __forceinline__ bool load_q(const PrefillParams &p, const PrefillFast
     }
     tc::cp_async_wait_all();
     // a negative scale's sign, on the pieces that this lane copied
-    for (int i = d.scale_log2 < 0.0f ? lane : ns * 128 * PPR; i < ns * 128 * PPR; i += 32) {
+    for (int i = d.scale_log2 < 0.0f && !f.flip_q ? lane : ns * 128 * PPR; i < ns * 128 * PPR; i += 32) {
         const uint32_t at = q + i / (128 * PPR) * kTile + piece_at((i / PPR) & 127, i % PPR);
         uint4 v = tc::ld_shared16(at);
         v.x ^= 0x80008000u;
@@ -502,7 +488,7 @@ __device__ __forceinline__ bool load_q(const PrefillParams &p, const PrefillFast
     }
     ptx::fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(bars.q_full());
+    if (lane == 0) ptx::mbar_arrive(full);
     return true;
 }
 
@@ -659,7 +645,7 @@ __device__ __forceinline__ void raw_codes(const PrefillParams &p, const PrefillF
 // Raw codes -> operand ring, rows 32 lw .. 32 lw + 31 of every tile by one
 // warp (lane = row for the scales).  The loop over a row's pieces is rolled:
 // four roles share the SM's instruction cache.
-template <int QK, int CK, int D, bool GS>
+template <int CK, int D, bool GS>
 __device__ __forceinline__ void convert_rows(const PrefillParams &p, const Start &st, unsigned char *sm, uint32_t sm32,
                                              const Bars &bars, volatile int *gone, int lw, int lane)
 {
@@ -768,17 +754,17 @@ __device__ __forceinline__ void convert_rows(const PrefillParams &p, const Start
                     const uint32_t *src = reinterpret_cast<const uint32_t *>(from + rr * RB + 12 * c);
                     const uint32_t w0 = there ? src[0] : 0u, w1 = there ? src[1] : 0u, w2 = there ? src[2] : 0u;
                     const float z = __shfl_sync(0xffffffffu, zero[kv], r);
-                    const uint32_t z2 = QK == kBF16 ? tc::pack16<QK>(z, z) : tc::pack16<QK>(1024.0f + z, 1024.0f + z);
+                    const uint32_t z2 = tc::pack16<kF16>(1024.0f + z, 1024.0f + z);
                     const uint32_t fl[4] = {w0, __funnelshift_r(w0, w1, 24), __funnelshift_r(w1, w2, 16), w2 >> 8};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) tc::st_shared16(dst + piece_at(rr, 4 * c + j), u3x8_to_16<QK>(fl[j], z2));
+                    for (int j = 0; j < 4; ++j) tc::st_shared16(dst + piece_at(rr, 4 * c + j), u3x8_to_f16(fl[j], z2));
                 } else {
                     const unsigned char *src =
                         xv ? from + (rr >> shift) * rows * RB + c * rows * 16 + (rr & (rows - 1)) * 16 : from + rr * RB + 16 * c;
                     uint4 v = *reinterpret_cast<const uint4 *>(src);
                     if (!there) v = make_uint4(0, 0, 0, 0);
-                    const uint2 a = q8x4_to_16<QK, CK>(v.x), b = q8x4_to_16<QK, CK>(v.y);
-                    const uint2 e = q8x4_to_16<QK, CK>(v.z), g = q8x4_to_16<QK, CK>(v.w);
+                    const uint2 a = q8x4_to_f16<CK>(v.x), b = q8x4_to_f16<CK>(v.y);
+                    const uint2 e = q8x4_to_f16<CK>(v.z), g = q8x4_to_f16<CK>(v.w);
                     const uint4 o0 = make_uint4(a.x, a.y, b.x, b.y), o1 = make_uint4(e.x, e.y, g.x, g.y);
                     const bool swap = D == 128 && !xv && (c >> 2);
                     tc::st_shared16(dst + piece_at(rr, 2 * c + swap), swap ? o1 : o0);
@@ -798,8 +784,8 @@ __device__ __forceinline__ void convert_rows(const PrefillParams &p, const Start
 }
 
 // ---------------------------------------------------------------- the kernel
-// Warps 0-15 softmax, 16-19 producers; 16-bit caches by TMA have the products
-// among the latter, the others in a sixth warpgroup.
+// Warps 0-7 softmax, 8-11 producers; 16-bit caches by TMA have the products
+// among the latter, the others in a fourth warpgroup.
 template <int QK, int CK, int D, int FEED, bool GS>
 __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
     prefill_kernel(PrefillParams p, PrefillFast f, const __grid_constant__ CUtensorMap tmk,
@@ -808,11 +794,12 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
     using L = Smem<CK, D>;
     constexpr int ST = L::kStages;
     constexpr bool TMA = FEED == kFeedTma;
-    constexpr bool BF = QK == kBF16;
-    constexpr int kMmaWarp = TMA ? 16 : 20;                     // two of them
-    constexpr int kQWarp = TMA ? 19 : 23;                       // by TMA that of V too
+    constexpr int OK = is_coded<CK>() ? int(kF16) : QK;         // operands of the products
+    constexpr bool kRawQ = OK != QK;                            // bf16 Q becomes f16
+    constexpr int kMmaWarp = TMA ? 8 : 12;                     // two of them
+    constexpr int kQWarp = TMA ? 11 : 15;                       // by TMA that of V too
     using R = Ring<FEED, ST>;
-    constexpr bool kVRef = GS && QK == kF16;                    // P relative to the V scales' magnitude
+    constexpr bool kVRef = GS;                                  // P relative to the V scales' magnitude
     const DecodeParams &d = p.d;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *sm = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -834,18 +821,18 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
             ptx::mbar_init(bars.raw_full(i), 1);
             ptx::mbar_init(bars.raw_empty(i), 4);
         }
-        ptx::mbar_init(bars.q_full(), 1);
+        ptx::mbar_init(bars.q_full(), kRawQ ? 8 : 1);
+        ptx::mbar_init(bars.q_raw(), 1);
         ptx::mbar_init(bars.q_empty(), 2);
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(bars.s_full(i), 1);
-            ptx::mbar_init(bars.p_full(i), 8);
-            ptx::mbar_init(bars.p_half(i), 8);
-            for (int j = 0; j < 4; ++j) ptx::mbar_init(bars.pair(i, j), 2);
+            ptx::mbar_init(bars.p_full(i), 4);
+            ptx::mbar_init(bars.p_most(i), 4);
             ptx::mbar_init(bars.o_full(i), 1);
         }
         ptx::mbar_init(bars.tail(), 1);
         ptx::mbar_init(bars.j_full(), 4);
-        ptx::mbar_init(bars.j_empty(), 8);
+        ptx::mbar_init(bars.j_empty(), 4);
         ptx::fence_mbar_init();
         *gone = 0;
     }
@@ -859,43 +846,73 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
     const Start st = *start;
     const bool work = st.u1 > st.u0;
 
-    if (warp < 16) {
-        // ------------------------------------------------ softmax, two threads per row
-        const int sub = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, row = threadIdx.x & 127;
-        const uint32_t lanes = uint32_t(quarter * 32) << 16;
-        // this half's scores; its weights take the first 32 of these columns
-        const uint32_t ts = tmem + lanes + sub * 128 + half * 64;
-        constexpr int DH = D / 2;                               // output columns of a half
-        const uint32_t to = tmem + lanes + 256 + sub * 128 + half * DH;
-        float *state = reinterpret_cast<float *>(sm + L::state) + row;      // m, l of pair 1
-        float *own_max = reinterpret_cast<float *>(sm + L::maxima) + (2 * sub + half) * 128 + row;
-        float *other_max = reinterpret_cast<float *>(sm + L::maxima) + (2 * sub + 1 - half) * 128 + row;
-        uint32_t tile_n = 0, mine_n = 0, joins = 0, pairs = 0;  // key tiles of the CTA, of this pair; joins; exchanges
-        uint32_t outs[2] = {0, 0};                              // accumulators completed so far
-        // the other half's value of this row
-        auto exchange = [&](int at, float x, float &y) -> bool {
-            own_max[at] = x;
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(bars.pair(sub, quarter));
-            const bool ok = warp_wait(bars.pair(sub, quarter), pairs++ & 1, gone);
-            y = other_max[at];
-            return ok;
-        };
+    if (warp < 8) {
+        // ------------------------------------------------ softmax, a thread per row
+        const int sub = warp >> 2, row = threadIdx.x & 127;
+        const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + sub * 128, to = tmem + lanes + 256 + sub * 128;
+        float *state = reinterpret_cast<float *>(sm + L::state) + row;      // m, l of warpgroup 1
+        float *q_scale = reinterpret_cast<float *>(sm + L::q_scale) + row;
+        uint32_t tile_n = 0, mine_n = 0, joins = 0, item = 0;   // key tiles of the CTA, of this warpgroup; joins; segments
+        uint32_t outs1 = 0;                                     // segments that use warpgroup 1's accumulators
         if (work) {
             Walk w = walk_from(p, st);
             do {
                 const int nk = w.k1 - w.k0;
-                const bool split = w.subtiles(p) == 1;          // both pairs on one subtile
+                const bool split = w.subtiles(p) == 1;          // both warpgroups on one subtile
+                const bool two = !split || nk > 1;              // both accumulators are in use
                 const int r = w.tile * 2 * p.sub_rows + (split ? 0 : sub * p.sub_rows) + row;
                 const bool live = row < p.sub_rows && r < w.s.rows;
                 const bool idle = !__any_sync(0xffffffffu, live);
                 const int lim = live ? row_limit(p, w.s, r) : 0;
                 float c = fabsf(d.scale_log2);
                 if constexpr (is_q8(CK) && !GS) c *= fabsf(d.k_scale[w.h]);
+                bool ok = true;
+                if constexpr (kRawQ) {
+                    // this row of Q to f16, in place: its largest element to [2^14, 2^15)
+                    float back = 1.0f;
+                    ok = warp_wait(bars.q_raw(), item & 1, gone);
+                    if (!ok) break;
+                    if (!split || sub == 0) {
+                        const uint32_t q = sm32 + L::q + sub * L::kTile;
+                        uint32_t top = 0;
+#pragma unroll 4
+                        for (int i = 0; i < D / 8; ++i) {
+                            const uint4 v = tc::ld_shared16(q + piece_at(row, i));
+                            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) top = max(top, max((x[j] << 16) & 0x7fff0000u, x[j] & 0x7fff0000u));
+                        }
+                        // exponents that keep both powers of two normal; the sign of the scale goes along
+                        const int e = min(max(int(top >> 23), 16), 254);
+                        const float s = __uint_as_float(uint32_t(127 + 14 + 127 - e > 254 ? 254 : 268 - e) << 23);
+                        back = __uint_as_float(uint32_t(254 - (__float_as_uint(s) >> 23)) << 23);
+                        const float sg = f.flip_q ? -s : s;
+#pragma unroll 4
+                        for (int i = 0; i < D / 8; ++i) {
+                            uint4 v = tc::ld_shared16(q + piece_at(row, i));
+                            v.x = bf16x2_to_f16x2(v.x, sg);
+                            v.y = bf16x2_to_f16x2(v.y, sg);
+                            v.z = bf16x2_to_f16x2(v.z, sg);
+                            v.w = bf16x2_to_f16x2(v.w, sg);
+                            tc::st_shared16(q + piece_at(row, i), v);
+                        }
+                        if (split) q_scale[0] = back;
+                        ptx::fence_proxy_async_smem();
+                    }
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(bars.q_full());
+                    if (split && sub == 1) {
+                        ok = warp_wait(bars.q_full(), item & 1, gone);
+                        if (!ok) break;
+                        back = q_scale[0];
+                    }
+                    c *= back;
+                }
+                ++item;
                 c = fmaxf(c, 1e-30f);                           // keeps 0 * -inf out: masked weights stay zero
                 const float ninf = -__int_as_float(0x7f800000);
                 float m = ninf, l = 0.0f, vexp = -1000.0f;
-                bool ok = true;
                 const int step = split ? 2 : 1, j0 = split ? sub : 0;
                 for (int j = j0; j < nk; j += step, ++mine_n) {
                     ok = warp_wait(bars.s_full(sub), mine_n & 1, gone);
@@ -905,22 +922,21 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                         tc::fence_before();
                         __syncwarp();
                         if (lane == 0) {
-                            ptx::mbar_arrive(bars.p_half(sub));
+                            ptx::mbar_arrive(bars.p_most(sub));
                             ptx::mbar_arrive(bars.p_full(sub));
                         }
                         continue;
                     }
                     const ColSlot &cs = cols[(tile_n + j) % L::kColSlots];
-                    const float *kcol = cs.k + half * 64;
+                    const float *kcol = cs.k;
                     // keys behind the row's limit, and blocks that are not there
                     uint32_t there = cs.mask[0];
                     if constexpr (!TMA) there |= cs.mask[1] | cs.mask[2] | cs.mask[3];
-                    there = (there >> (8 * half)) & 0xffu;
-                    const int rel = lim - (w.k0 + j) * kKeyTile - half * 64;
-                    if (__any_sync(0xffffffffu, rel < 64 || there != 0xffu)) {
+                    const int rel = lim - (w.k0 + j) * kKeyTile;
+                    if (__any_sync(0xffffffffu, rel < kKeyTile || there != 0xffffu)) {
                         // few tiles: masked in place, in a rolled loop, before the others' path
 #pragma unroll 1
-                        for (int o = 0; o < 64; o += 16) {
+                        for (int o = 0; o < kKeyTile; o += 16) {
                             uint32_t x[16];
                             tc::tmem_ld16_wait(ts + o, x);
                             const uint32_t g = there >> (o >> 3);
@@ -934,14 +950,13 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                         tc::tmem_st_wait();
                         kcol = reinterpret_cast<const float *>(sm + L::ones);
                     }
-                    // the half's 64 columns in four chunks of 16, read twice: for the
-                    // maximum and for the weights.  Kept in registers in between they would
-                    // cost the threads that a pair per row needs.
-                    uint32_t x[2][16];
-                    auto scaled = [&](uint32_t (&v)[16], int o) {
+                    // the tile's columns in four chunks of 32, read twice, for the maximum and
+                    // for the weights: that costs less than the registers would
+                    uint32_t x[2][32];
+                    auto scaled = [&](uint32_t (&v)[32], int o) {
                         if constexpr (GS) {
 #pragma unroll
-                            for (int i = 0; i < 16; i += 4) {
+                            for (int i = 0; i < 32; i += 4) {
                                 const float4 k4 = *reinterpret_cast<const float4 *>(kcol + o + i);
                                 const float2 u = tc::mul2(f2(v, i), make_float2(k4.x, k4.y));
                                 const float2 y = tc::mul2(f2(v, i + 2), make_float2(k4.z, k4.w));
@@ -953,23 +968,20 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                         }
                     };
                     float mx[4] = {ninf, ninf, ninf, ninf};
-                    tc::tmem_ld16(ts, x[0]);
+                    tc::tmem_ld32(ts, x[0], 0);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        tc::tmem_ld_wait16(x[q & 1]);
-                        if (q < 3) tc::tmem_ld16(ts + 16 * (q + 1), x[(q + 1) & 1]);
-                        scaled(x[q & 1], 16 * q);
+                        tc::tmem_ld_wait32(x[q & 1], 0);
+                        // after the last chunk the first again
+                        tc::tmem_ld32(ts + 32 * ((q + 1) & 3), x[(q + 1) & 1], 0);
+                        scaled(x[q & 1], 32 * q);
 #pragma unroll
-                        for (int u = 0; u < 16; u += 8)
+                        for (int u = 0; u < 32; u += 8)
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
                                 mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(x[q & 1][u + i])), __uint_as_float(x[q & 1][u + 4 + i]));
                     }
-                    tc::tmem_ld16(ts, x[0]);
-                    float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), others;
-                    ok = exchange(0, top, others);
-                    if (!ok) break;
-                    top = fmaxf(top, others);
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     float grow = 1.0f;                          // what O and l shrink by
                     if (top > m && (m == ninf || (top - m) * c > 8.0f)) {
                         grow = m == ninf ? 0.0f : exp2_approx((m - top) * c);
@@ -988,7 +1000,7 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                     if (j > j0 && __any_sync(0xffffffffu, grow != 1.0f)) {
                         // seldom: a rolled loop keeps its registers out of the way
 #pragma unroll 1
-                        for (int o = 0; o < DH; o += 16) {
+                        for (int o = 0; o < D; o += 16) {
                             uint32_t y[16];
                             tc::tmem_ld16_wait(to + o, y);
 #pragma unroll
@@ -1002,33 +1014,33 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                     float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        uint32_t (&v)[16] = x[q & 1];
-                        tc::tmem_ld_wait16(v);
-                        if (q < 3) tc::tmem_ld16(ts + 16 * (q + 1), x[(q + 1) & 1]);
-                        scaled(v, 16 * q);
-                        uint32_t pk[8];
+                        uint32_t (&v)[32] = x[q & 1];
+                        tc::tmem_ld_wait32(v, 0);
+                        if (q < 3) tc::tmem_ld32(ts + 32 * (q + 1), x[(q + 1) & 1], 0);
+                        scaled(v, 32 * q);
+                        uint32_t pk[16];
 #pragma unroll
-                        for (int i = 0; i < 16; i += 4) {
+                        for (int i = 0; i < 32; i += 4) {
                             const float2 y0 = tc::fma2(f2(v, i), c2, off2), y1 = tc::fma2(f2(v, i + 2), c2, off2);
                             float2 e0 = make_float2(exp2_approx(y0.x), exp2_approx(y0.y));
                             float2 e1 = make_float2(exp2_approx(y1.x), exp2_approx(y1.y));
                             sum[0] = tc::add2(sum[0], e0);
                             sum[1] = tc::add2(sum[1], e1);
                             if constexpr (GS) {
-                                const float4 v4 = *reinterpret_cast<const float4 *>(cs.v + half * 64 + 16 * q + i);
+                                const float4 v4 = *reinterpret_cast<const float4 *>(cs.v + 32 * q + i);
                                 e0 = tc::mul2(e0, make_float2(v4.x, v4.y));
                                 e1 = tc::mul2(e1, make_float2(v4.z, v4.w));
                             }
-                            pk[i >> 1] = tc::pack16<QK>(e0.x, e0.y);
-                            pk[(i >> 1) + 1] = tc::pack16<QK>(e1.x, e1.y);
+                            pk[i >> 1] = tc::pack16<OK>(e0.x, e0.y);
+                            pk[(i >> 1) + 1] = tc::pack16<OK>(e1.x, e1.y);
                         }
                         // over columns that have been read for the last time
-                        tc::tmem_st8(ts + 8 * q, pk);
-                        if (q & 1) {                            // 32 of the half's keys are ready
+                        tc::tmem_st16(ts + 16 * q, pk);
+                        if (q >= 2) {                           // 96 keys, then all
                             tc::tmem_st_wait();
                             tc::fence_before();
                             __syncwarp();
-                            if (lane == 0) ptx::mbar_arrive(q == 1 ? bars.p_half(sub) : bars.p_full(sub));
+                            if (lane == 0) ptx::mbar_arrive(q == 2 ? bars.p_most(sub) : bars.p_full(sub));
                         }
                     }
                     sum[0] = tc::add2(sum[0], sum[1]);
@@ -1037,29 +1049,20 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                 tile_n += nk;
                 if (!ok) break;
                 // accumulators of this segment, and their joining
-                const bool two = !split || nk > 1;              // both are in use
-                const uint32_t turn0 = outs[0]++, turn1 = outs[1];
-                if (two) ++outs[1];
-                if (sub == 1 && !two) continue;
-                if (!idle) {                                    // the row's sum over both halves
-                    float others;
-                    ok = exchange(512, l, others);
-                    l += others;
-                    if (!ok) break;
-                }
+                const uint32_t turn0 = item - 1, turn1 = outs1;
+                if (two) ++outs1;
                 float off = m == ninf ? m : m * c;
                 if constexpr (kVRef) off = m == ninf ? m : off + vexp;
-                float w0 = 1.0f, w1 = 0.0f;                     // weights of O (own) and pair 1's
+                float w0 = 1.0f, w1 = 0.0f;                     // weights of O (own) and warpgroup 1's
                 const bool join = split && two;
                 if (sub == 1) {
+                    if (!two) continue;
                     if (join) {
-                        if (half == 0) {
-                            state[0] = off;
-                            state[128] = l;
-                            __syncwarp();
-                            if (lane == 0) ptx::mbar_arrive(bars.j_full());
-                        }
-                        // O of this pair is read by the other: not to be overwritten before
+                        state[0] = off;
+                        state[128] = l;
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(bars.j_full());
+                        // O of this warpgroup is read by the other: not to be overwritten before
                         ok = warp_wait(bars.j_empty(), joins & 1, gone);
                         ++joins;
                         if (!ok) break;
@@ -1092,18 +1095,18 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                 w1 *= fac;
                 const int tok = r / d.group;
                 const int head = w.h * d.group + (r - tok * d.group);
-                char *o_row = d.out + int64_t(w.s.s0 + tok) * d.o_b + int64_t(head) * d.o_h + half * DH * 2;
+                char *o_row = d.out + int64_t(w.s.s0 + tok) * d.o_b + int64_t(head) * d.o_h;
                 const int slot = 2 * blockIdx.x + (w.k0 == 0 ? 1 : 0);
                 const int prow = (split ? 0 : sub * 128) + row;
-                float4 *acc = reinterpret_cast<float4 *>(f.part_acc) + (int64_t(slot) * (D / 4) + half * (DH / 4)) * kRowTile + prow;
-                if (!whole && half == 0) {
+                float4 *acc = reinterpret_cast<float4 *>(f.part_acc) + int64_t(slot) * (D / 4) * kRowTile + prow;
+                if (!whole) {
                     float *ml = f.part_ml + int64_t(slot) * 2 * kRowTile + prow;
                     ml[0] = off;
                     ml[kRowTile] = l;
                 }
                 float bad = 0.0f;
 #pragma unroll 1
-                for (int o = 0; o < DH && !idle; o += 16) {
+                for (int o = 0; o < D && !idle; o += 16) {
                     uint32_t a[16];
                     tc::tmem_ld16_wait(to + o, a);
 #pragma unroll
@@ -1149,7 +1152,7 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(bars.j_empty());
                 }
-                // not finite: weights of zero met values that are not; such a half row is done again by itself
+                // not finite: weights of zero met values that are not; such a row is done again by itself
                 unsigned redo = __ballot_sync(0xffffffffu, whole && live && bad != 0.0f);
                 while (redo) {
                     const int who = __ffs(redo) - 1;
@@ -1157,7 +1160,7 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                     const int rr = __shfl_sync(0xffffffffu, r, who), ll = __shfl_sync(0xffffffffu, lim, who);
                     const int tt = rr / d.group;
                     redo_row<QK, CK, D>(d, d.block_tables + w.b * d.bt_b, int64_t(w.s.s0) + tt,
-                                        w.h * d.group + (rr - tt * d.group), ll, w.limit, half * DH, half * DH + DH);
+                                        w.h * d.group + (rr - tt * d.group), ll, w.limit, 0, D);
                 }
             } while (w.next(p));
         }
@@ -1165,8 +1168,8 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
         if (warp == kMmaWarp || warp == kMmaWarp + 1) {
             // -------------------------------------------- the products
             if (work) {
-                constexpr uint32_t id_qk = tc::instr_desc<BF, false, 128, 128>();
-                constexpr uint32_t id_pv = tc::instr_desc<BF, true, 128, D>();
+                constexpr uint32_t id_qk = tc::instr_desc<OK == kBF16, false, 128, 128>();
+                constexpr uint32_t id_pv = tc::instr_desc<OK == kBF16, true, 128, D>();
                 const bool leader = tc::elect_one();
                 // V tiles: [64-element chunk][128 rows]; by TMA [block][chunk][rows of a block]
                 const int rows = min(d.block_size, 128);
@@ -1191,17 +1194,15 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                         tc::commit(bars.s_full(i));
                     }
                 };
-                // O (+)= P V, the first 32 keys of each half and then the others: the
-                // first ones' products run while the others' weights are made
-                auto pv = [&](int part, uint32_t stage, bool acc) {
+                // O (+)= P V, the first 96 keys and then the others: the first ones' products
+                // run while the others' weights are made
+                auto pv = [&](int from, int to, uint32_t stage, bool acc) {
                     const uint32_t b = v_lo + stage * (L::kTile >> 4);
                     if (leader) {
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const int half = u >> 1, ks = 2 * part + (u & 1);       // 16 keys from 64 half + 16 ks
-                            tc::mma_ts(ti + 256, ti + 64 * half + 8 * ks, b + v_at[4 * half + ks], v_hi, id_pv,
-                                       u > 0 || part > 0 || acc);
-                        }
+                        for (int ks = 0; ks < 8; ++ks)
+                            if (ks >= from && ks < to)
+                                tc::mma_ts(ti + 256, ti + 8 * ks, b + v_at[ks], v_hi, id_pv, ks > 0 || acc);
                     }
                 };
                 // a stage is free when both subtiles have used it; on a row tile of one
@@ -1222,24 +1223,34 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                     ok = warp_wait(bars.q_full(), item & 1, gone);
                     if (!ok) break;
                     tc::fence_after();
+                    auto next_k = [&](uint32_t t) -> bool {
+                        const bool there = warp_wait(bars.full(R::stage(t, 0)), R::turn(t, 0) & 1, gone);
+                        tc::fence_after();
+                        return there;
+                    };
+                    if (j0 < nk && !next_k(tile_n + j0)) break;
+                    // K of tile j is there
                     for (int j = j0; j < nk; j += step, ++n_p) {
                         const bool last = j + step >= nk;
                         const uint32_t t = tile_n + j, ks = R::stage(t, 0), vs = R::stage(t, 1);
-                        ok = warp_wait(bars.full(ks), R::turn(t, 0) & 1, gone);
-                        if (!ok) break;
-                        tc::fence_after();
                         qk(split ? 0 : i, ks);
                         release(bars.empty(ks), split);
                         if (last) release(bars.q_empty(), false);
-                        ok = warp_wait(bars.full(vs), R::turn(t, 1) & 1, gone) && warp_wait(bars.p_half(i), n_p & 1, gone);
+                        ok = warp_wait(bars.full(vs), R::turn(t, 1) & 1, gone) && warp_wait(bars.p_most(i), n_p & 1, gone);
                         if (!ok) break;
                         tc::fence_after();
-                        pv(0, vs, j > j0);
-                        ok = warp_wait(bars.p_full(i), n_p & 1, gone);
+                        pv(0, 6, vs, j > j0);
+                        // the next tile's K, before the wait that the next scores depend on -- but in a
+                        // ring of three, K two tiles on takes this V's place
+                        const bool early = !split || FEED == kFeedTma || ST > 3;
+                        if (!last && early) ok = next_k(t + step);
+                        ok = ok && warp_wait(bars.p_full(i), n_p & 1, gone);
                         if (!ok) break;
                         tc::fence_after();
-                        pv(1, vs, true);
+                        pv(6, 8, vs, true);
                         release(bars.empty(vs), split);
+                        if (!last && !early) ok = next_k(t + step);
+                        if (!ok) break;
                         if (last) release(bars.o_full(i), false);
                     }
                     if (!ok) break;
@@ -1256,15 +1267,15 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
             bool have = work;
             if (work) w = walk_from(p, st);
             while (have) {
-                if (!load_q<D>(p, f, w, item++, sm32 + L::q, bars, &tmq, gone, lane)) break;
+                if (!load_q<D>(p, f, w, item++, sm32 + L::q, bars, kRawQ ? bars.q_raw() : bars.q_full(), &tmq, gone, lane)) break;
                 have = w.next(p);
             }
             if (lane == 0) f.desc[blockIdx.x] = split_end(w, st, work && !have);
         } else if (TMA) {
-            // -------------------------------------------- K (warp 18) and V (19) by TMA: whole blocks.  K boxes are
+            // -------------------------------------------- K (warp 10) and V (11) by TMA: whole blocks.  K boxes are
             // 64 elements wide, V's take the row's 64-element chunks together.  V's warp
             // loads Q too, before a segment's V, which is needed later
-            const int kv = warp - 18;
+            const int kv = warp - 10;
             const CUtensorMap *map = kv ? &tmv : &tmk;
             const int shift = min(d.block_shift, 7);            // rows per box
             const int rows = 1 << shift, nblk = kKeyTile >> shift;
@@ -1284,7 +1295,7 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                 uint32_t item = 0;
                 for (; more && ok; ++tile_n) {
                     if (kv == 1 && tw.k == tw.w.k0) {
-                        ok = load_q<D>(p, f, tw.w, item++, sm32 + L::q, bars, &tmq, gone, lane);
+                        ok = load_q<D>(p, f, tw.w, item++, sm32 + L::q, bars, bars.q_full(), &tmq, gone, lane);
                         if (!ok) break;
                     }
                     const int t = tw.k * kKeyTile + lane * rows, h = tw.w.h;
@@ -1342,14 +1353,14 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
             } else if (kv == 1 && lane == 0) {
                 f.desc[blockIdx.x] = make_int4(0, 0, 0, -1);
             }
-        } else if (warp < 20) {
+        } else if (warp < 12) {
             if (work) {
                 if constexpr (FEED == kFeedCodes)
-                    convert_rows<QK, CK, D, GS>(p, st, sm, sm32, bars, gone, warp - 16, lane);
+                    convert_rows<CK, D, GS>(p, st, sm, sm32, bars, gone, warp - 8, lane);
                 else if constexpr (FEED == kFeedCopy)
-                    copy_rows<CK, D>(p, st, sm32 + L::ring, cols, bars, gone, warp - 16, lane);
+                    copy_rows<CK, D>(p, st, sm32 + L::ring, cols, bars, gone, warp - 8, lane);
             }
-        } else if (FEED == kFeedCodes && warp == 22) {
+        } else if (FEED == kFeedCodes && warp == 14) {
             if constexpr (FEED == kFeedCodes) {
                 if (work) raw_codes<CK, D>(p, f, st, sm, sm32, bars, &tmk, &tmv, gone, lane);
             }

@@ -16,6 +16,7 @@ struct PrefillLaunch {
     int out32;                  // output rows at multiples of 32 bytes
     void *desc, *part_ml, *part_acc;
     bool q_tma;                 // Q by TMA (tmq)
+    bool flip_q;                // the kernel gives a negative scale's sign to Q where it converts it
     CUtensorMap tmk, tmv, tmq;
     cudaStream_t stream;
 };
