@@ -24,7 +24,8 @@
 //
 // CTA.  Two softmax warpgroups (one per subtile, a thread per row), a warp per
 // subtile that issues its products (tcgen05.mma, accumulators and P in tensor
-// memory), one that loads Q, and the K/V producers.  While one subtile's
+// memory), a warpgroup that writes finished accumulators out while the next
+// row tile is under way, a warp that loads Q, and the K/V producers.  While one subtile's
 // softmax runs the tensor core works on the other's products: a subtile's
 // scores wait for its last P V (they share tensor memory), which waits for its
 // softmax, so that chain bounds the tile rate.  A row tile of at most 128 rows
@@ -63,7 +64,7 @@ struct PrefillFast {
 namespace {
 
 enum Feed : int { kFeedTma, kFeedCopy, kFeedCodes };
-template <int FEED> constexpr int prefill_threads() { return FEED == kFeedTma ? 384 : 512; }
+template <int FEED> constexpr int prefill_threads() { return FEED == kFeedTma ? 512 : 640; }
 
 constexpr int kRowTile = 256;   // rows of a row tile, those between a subtile's whole tokens and 128 included
 constexpr int kTileCost = 2;    // beginning and ending a row tile costs as much as this many units
@@ -269,10 +270,10 @@ struct Smem {
     static constexpr int cols = raw + kRaw * kRawTile;
     static constexpr int kColBytes = 2 * kKeyTile * 4 + 32;
     static constexpr int ones = cols + kColSlots * kColBytes;   // 128 ones
-    static constexpr int state = ones + 512;                    // warpgroup 1's (m, l) for the join
-    static constexpr int q_scale = state + 1024;                // per row of subtile 0
+    static constexpr int state = ones + 512;                    // (m, l) of a row tile's rows: [subtile][2][128]
+    static constexpr int q_scale = state + 2048;                // per row of subtile 0
     static constexpr int bars = q_scale + 512;
-    static constexpr int n_bars = 2 * kStages + 2 * kRaw + 2 + 4 * 2 + 1 + 2 + 1;
+    static constexpr int n_bars = 2 * kStages + 2 * kRaw + 2 + 4 * 2 + 1 + 4 + 1;
     static constexpr int info = bars + 8 * n_bars;              // per raw stage: which blocks are there
     static constexpr int misc = (info + 4 * 8 + 15) / 16 * 16;
     static constexpr int total = misc + 128;
@@ -309,13 +310,13 @@ struct Bars {
     __device__ __forceinline__ uint32_t o_full(int i) const { return base + 8 * (2 * stages + 6 + i); }
     __device__ __forceinline__ uint32_t p_most(int i) const { return base + 8 * (2 * stages + 8 + i); }
     __device__ __forceinline__ uint32_t tail() const { return base + 8 * (2 * stages + 10); }
-    // the join of two warpgroups' states: warpgroup 1's is there, and has been read
-    __device__ __forceinline__ uint32_t j_full() const { return base + 8 * (2 * stages + 11); }
-    __device__ __forceinline__ uint32_t j_empty() const { return base + 8 * (2 * stages + 12); }
+    // a subtile's rows are finished (their m and l are there), and have been read
+    __device__ __forceinline__ uint32_t e_full(int i) const { return base + 8 * (2 * stages + 11 + i); }
+    __device__ __forceinline__ uint32_t e_empty(int i) const { return base + 8 * (2 * stages + 13 + i); }
     // bf16 Q that is to become f16
-    __device__ __forceinline__ uint32_t q_raw() const { return base + 8 * (2 * stages + 13); }
-    __device__ __forceinline__ uint32_t raw_full(int s) const { return base + 8 * (2 * stages + 14 + s); }
-    __device__ __forceinline__ uint32_t raw_empty(int s) const { return base + 8 * (2 * stages + 14 + raws + s); }
+    __device__ __forceinline__ uint32_t q_raw() const { return base + 8 * (2 * stages + 15); }
+    __device__ __forceinline__ uint32_t raw_full(int s) const { return base + 8 * (2 * stages + 16 + s); }
+    __device__ __forceinline__ uint32_t raw_empty(int s) const { return base + 8 * (2 * stages + 16 + raws + s); }
 };
 
 // Wait for a phase, giving up when it takes too long or another warp gave up.
@@ -398,15 +399,19 @@ __device__ __forceinline__ uint2 q8x4_to_f16(uint32_t w)
     return make_uint2(lo, hi);
 }
 
-// eight 3-bit codes (the low 24 bits of w) minus their zero point, as f16
-// numbers: the code in the last place of 1024, minus 1024 + zero (twice)
-__device__ __forceinline__ uint4 u3x8_to_f16(uint32_t w, uint32_t zero2)
+// eight 3-bit codes (the low 24 bits of w) minus their zero point z, as f16
+// numbers.  Of 12 bits x with codes a b c d, x + (x << 13) has a at bit 0, b
+// at 16, c at 6 and d at 22: under 0x6400 they are 1024 + a and 1024 + 64 c;
+// z0 = -1024 - z, z6 = -16 - z (twice each).
+__device__ __forceinline__ uint4 u3x8_to_f16(uint32_t w, uint32_t z0, uint32_t z6)
 {
     uint32_t o[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const uint32_t x = w >> (6 * j);
-        o[j] = sub_f16x2((x & 7u) | ((x << 13) & 0x70000u) | 0x64006400u, zero2);
+    for (int j = 0; j < 2; ++j) {
+        const uint32_t y = ((w >> (12 * j)) & 0xfffu) * 0x2001u;
+        const uint32_t lo = (y & 0x00070007u) | 0x64006400u, hi = (y & 0x01c001c0u) | 0x64006400u;
+        asm("add.rn.f16x2 %0, %1, %2;" : "=r"(o[2 * j]) : "r"(lo), "r"(z0));
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(o[2 * j + 1]) : "r"(hi), "r"(0x24002400u), "r"(z6));
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
@@ -733,42 +738,67 @@ __device__ __forceinline__ void convert_rows(const PrefillParams &p, const Start
             }
             const unsigned char *from = sm + L::raw + rs * L::kRawTile;
             const uint32_t dst = sm32 + L::ring + s * L::kTile;
-#pragma unroll 2
-            for (int i = 0; i < kPieces; ++i) {
-                // lane -> (row, piece) so that the 8 lanes of a load or store phase
-                // hit different banks
-                int r, c;
-                if constexpr (CK == kU3) {
-                    r = (lane >> 1) + 16 * (i & 1);
-                    c = (lane & 1) + 2 * (i >> 1);
-                } else if (xv) {
-                    r = lane;
-                    c = i;
-                } else {
-                    r = i * (32 / kPieces) + lane / kPieces;
-                    c = lane % kPieces;
-                }
-                const int rr = 32 * lw + r;
-                const bool there = (ok >> r) & 1u;
-                if constexpr (CK == kU3) {
-                    const uint32_t *src = reinterpret_cast<const uint32_t *>(from + rr * RB + 12 * c);
-                    const uint32_t w0 = there ? src[0] : 0u, w1 = there ? src[1] : 0u, w2 = there ? src[2] : 0u;
-                    const float z = __shfl_sync(0xffffffffu, zero[kv], r);
-                    const uint32_t z2 = tc::pack16<kF16>(1024.0f + z, 1024.0f + z);
-                    const uint32_t fl[4] = {w0, __funnelshift_r(w0, w1, 24), __funnelshift_r(w1, w2, 16), w2 >> 8};
+            const bool all = ok == 0xffffffffu;
+            // lane -> (row, piece) so that the 8 lanes of a load or store phase hit
+            // different banks; four pieces' loads before their conversion
+            if constexpr (CK == kU3) {
+                const int r = lane >> 1, rr = 32 * lw + r, h = lane & 1;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) tc::st_shared16(dst + piece_at(rr, 4 * c + j), u3x8_to_f16(fl[j], z2));
-                } else {
-                    const unsigned char *src =
-                        xv ? from + (rr >> shift) * rows * RB + c * rows * 16 + (rr & (rows - 1)) * 16 : from + rr * RB + 16 * c;
-                    uint4 v = *reinterpret_cast<const uint4 *>(src);
+                for (int b = 0; b < 2; ++b) {                   // rows r and r + 16
+                    const float z = __shfl_sync(0xffffffffu, zero[kv], r + 16 * b);
+                    const bool there = (ok >> (r + 16 * b)) & 1u;
+                    const uint32_t z0 = tc::pack16<kF16>(-1024.0f - z, -1024.0f - z);
+                    const uint32_t z6 = tc::pack16<kF16>(-16.0f - z, -16.0f - z);
+                    uint32_t w[kPieces / 2][3];
+                    const uint32_t *src = reinterpret_cast<const uint32_t *>(from + (rr + 16 * b) * RB + 12 * h);
+#pragma unroll
+                    for (int i = 0; i < kPieces / 2; ++i)
+#pragma unroll
+                        for (int j = 0; j < 3; ++j) w[i][j] = there ? src[6 * i + j] : 0u;
+#pragma unroll
+                    for (int i = 0; i < kPieces / 2; ++i) {
+                        const uint32_t fl[4] = {w[i][0], __funnelshift_r(w[i][0], w[i][1], 24),
+                                                __funnelshift_r(w[i][1], w[i][2], 16), w[i][2] >> 8};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            tc::st_shared16(dst + i * 16384 + b * 2048 + piece_at(rr, 4 * h + j), u3x8_to_f16(fl[j], z0, z6));
+                    }
+                }
+            } else if (xv) {
+                const int rr = 32 * lw + lane;
+                const unsigned char *src = from + (rr >> shift) * rows * RB + (rr & (rows - 1)) * 16;
+                const bool there = (ok >> lane) & 1u;
+#pragma unroll 2
+                for (int c = 0; c < kPieces; ++c) {
+                    uint4 v = *reinterpret_cast<const uint4 *>(src + c * rows * 16);
                     if (!there) v = make_uint4(0, 0, 0, 0);
-                    const uint2 a = q8x4_to_f16<CK>(v.x), b = q8x4_to_f16<CK>(v.y);
-                    const uint2 e = q8x4_to_f16<CK>(v.z), g = q8x4_to_f16<CK>(v.w);
-                    const uint4 o0 = make_uint4(a.x, a.y, b.x, b.y), o1 = make_uint4(e.x, e.y, g.x, g.y);
-                    const bool swap = D == 128 && !xv && (c >> 2);
-                    tc::st_shared16(dst + piece_at(rr, 2 * c + swap), swap ? o1 : o0);
-                    tc::st_shared16(dst + piece_at(rr, 2 * c + 1 - swap), swap ? o0 : o1);
+                    const uint2 a = q8x4_to_f16<CK>(v.x), e = q8x4_to_f16<CK>(v.y);
+                    const uint2 g = q8x4_to_f16<CK>(v.z), k = q8x4_to_f16<CK>(v.w);
+                    tc::st_shared16(dst + piece_at(rr, 2 * c), make_uint4(a.x, a.y, e.x, e.y));
+                    tc::st_shared16(dst + piece_at(rr, 2 * c + 1), make_uint4(g.x, g.y, k.x, k.y));
+                }
+            } else {
+                // 8 rows and four of a row's pieces at a time; at head_dim 128 odd rows take
+                // the other four
+                const int r = lane >> 2, rr = 32 * lw + r;
+#pragma unroll
+                for (int b = 0; b < kPieces / 4; ++b) {
+                    const int c = (lane & 3) | (kPieces == 8 ? ((b ^ r) & 1) << 2 : 0);
+                    const unsigned char *src = from + rr * RB + 16 * c;
+                    const uint32_t at0 = dst + piece_at(rr, 2 * c), at1 = dst + piece_at(rr, 2 * c + 1);
+                    uint4 v[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        v[i] = *reinterpret_cast<const uint4 *>(src + i * 8 * RB);
+                        if (!all && !((ok >> (r + 8 * i)) & 1u)) v[i] = make_uint4(0, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint2 a = q8x4_to_f16<CK>(v[i].x), e = q8x4_to_f16<CK>(v[i].y);
+                        const uint2 g = q8x4_to_f16<CK>(v[i].z), k = q8x4_to_f16<CK>(v[i].w);
+                        tc::st_shared16(at0 + i * 1024, make_uint4(a.x, a.y, e.x, e.y));
+                        tc::st_shared16(at1 + i * 1024, make_uint4(g.x, g.y, k.x, k.y));
+                    }
                 }
             }
             ptx::fence_proxy_async_smem();
@@ -784,8 +814,9 @@ __device__ __forceinline__ void convert_rows(const PrefillParams &p, const Start
 }
 
 // ---------------------------------------------------------------- the kernel
-// Warps 0-7 softmax, 8-11 producers; 16-bit caches by TMA have the products
-// among the latter, the others in a fourth warpgroup.
+// Warps 0-7 softmax; 16-bit caches by TMA: 8 and 9 products, 10 K, 11 V and Q,
+// 12-15 output; the others: 8-11 producers, 12 and 13 products, 14 raw codes,
+// 15 Q, 16-19 output.
 template <int QK, int CK, int D, int FEED, bool GS>
 __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
     prefill_kernel(PrefillParams p, PrefillFast f, const __grid_constant__ CUtensorMap tmk,
@@ -798,6 +829,8 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
     constexpr bool kRawQ = OK != QK;                            // bf16 Q becomes f16
     constexpr int kMmaWarp = TMA ? 8 : 12;                     // two of them
     constexpr int kQWarp = TMA ? 11 : 15;                       // by TMA that of V too
+    constexpr int kOutWarp = TMA ? 12 : 16;                     // four of them
+    constexpr int CH = TMA ? 32 : 16;                           // columns that a softmax thread reads at a time
     using R = Ring<FEED, ST>;
     constexpr bool kVRef = GS;                                  // P relative to the V scales' magnitude
     const DecodeParams &d = p.d;
@@ -828,11 +861,11 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
             ptx::mbar_init(bars.s_full(i), 1);
             ptx::mbar_init(bars.p_full(i), 4);
             ptx::mbar_init(bars.p_most(i), 4);
+            ptx::mbar_init(bars.e_full(i), 4);
+            ptx::mbar_init(bars.e_empty(i), 4);
             ptx::mbar_init(bars.o_full(i), 1);
         }
         ptx::mbar_init(bars.tail(), 1);
-        ptx::mbar_init(bars.j_full(), 4);
-        ptx::mbar_init(bars.j_empty(), 4);
         ptx::fence_mbar_init();
         *gone = 0;
     }
@@ -851,10 +884,10 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
         const int sub = warp >> 2, row = threadIdx.x & 127;
         const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + sub * 128, to = tmem + lanes + 256 + sub * 128;
-        float *state = reinterpret_cast<float *>(sm + L::state) + row;      // m, l of warpgroup 1
+        float *state = reinterpret_cast<float *>(sm + L::state) + sub * 256 + row;
         float *q_scale = reinterpret_cast<float *>(sm + L::q_scale) + row;
-        uint32_t tile_n = 0, mine_n = 0, joins = 0, item = 0;   // key tiles of the CTA, of this warpgroup; joins; segments
-        uint32_t outs1 = 0;                                     // segments that use warpgroup 1's accumulators
+        uint32_t tile_n = 0, mine_n = 0, item = 0, outs = 0;    // key tiles of the CTA, of this warpgroup; segments, and
+                                                                // those that use this warpgroup's accumulators
         if (work) {
             Walk w = walk_from(p, st);
             do {
@@ -864,7 +897,7 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                 const int r = w.tile * 2 * p.sub_rows + (split ? 0 : sub * p.sub_rows) + row;
                 const bool live = row < p.sub_rows && r < w.s.rows;
                 const bool idle = !__any_sync(0xffffffffu, live);
-                const int lim = live ? row_limit(p, w.s, r) : 0;
+                const int lim = live ? row_limit(p, w.s, r) : 1 << 30;      // rows that are not there need no mask
                 float c = fabsf(d.scale_log2);
                 if constexpr (is_q8(CK) && !GS) c *= fabsf(d.k_scale[w.h]);
                 bool ok = true;
@@ -918,6 +951,12 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                     ok = warp_wait(bars.s_full(sub), mine_n & 1, gone);
                     if (!ok) break;
                     tc::fence_after();
+                    // the accumulators are overwritten from here on: their last contents are out
+                    if (j == j0 && outs > 0) {
+                        ok = warp_wait(bars.e_empty(sub), (outs - 1) & 1, gone);
+                        if (!ok) break;
+                        tc::fence_after();
+                    }
                     if (idle) {                                 // no row of the warp is there
                         tc::fence_before();
                         __syncwarp();
@@ -950,13 +989,14 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                         tc::tmem_st_wait();
                         kcol = reinterpret_cast<const float *>(sm + L::ones);
                     }
-                    // the tile's columns in four chunks of 32, read twice, for the maximum and
-                    // for the weights: that costs less than the registers would
-                    uint32_t x[2][32];
-                    auto scaled = [&](uint32_t (&v)[32], int o) {
+                    // the tile's columns in chunks, read twice, for the maximum and for the
+                    // weights: that costs less than the registers would
+                    constexpr int NC = kKeyTile / CH;
+                    uint32_t x[2][CH];
+                    auto scaled = [&](uint32_t (&v)[CH], int o) {
                         if constexpr (GS) {
 #pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
+                            for (int i = 0; i < CH; i += 4) {
                                 const float4 k4 = *reinterpret_cast<const float4 *>(kcol + o + i);
                                 const float2 u = tc::mul2(f2(v, i), make_float2(k4.x, k4.y));
                                 const float2 y = tc::mul2(f2(v, i + 2), make_float2(k4.z, k4.w));
@@ -968,15 +1008,15 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                         }
                     };
                     float mx[4] = {ninf, ninf, ninf, ninf};
-                    tc::tmem_ld32(ts, x[0], 0);
+                    tc::tmem_ld(ts, x[0]);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        tc::tmem_ld_wait32(x[q & 1], 0);
+                    for (int q = 0; q < NC; ++q) {
+                        tc::tmem_ld_wait(x[q & 1]);
                         // after the last chunk the first again
-                        tc::tmem_ld32(ts + 32 * ((q + 1) & 3), x[(q + 1) & 1], 0);
-                        scaled(x[q & 1], 32 * q);
+                        tc::tmem_ld(ts + CH * ((q + 1) % NC), x[(q + 1) & 1]);
+                        scaled(x[q & 1], CH * q);
 #pragma unroll
-                        for (int u = 0; u < 32; u += 8)
+                        for (int u = 0; u < CH; u += 8)
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
                                 mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(x[q & 1][u + i])), __uint_as_float(x[q & 1][u + 4 + i]));
@@ -1013,21 +1053,21 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                     const float2 c2 = make_float2(c, c), off2 = make_float2(-off, -off);
                     float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t (&v)[32] = x[q & 1];
-                        tc::tmem_ld_wait32(v, 0);
-                        if (q < 3) tc::tmem_ld32(ts + 32 * (q + 1), x[(q + 1) & 1], 0);
-                        scaled(v, 32 * q);
-                        uint32_t pk[16];
+                    for (int q = 0; q < NC; ++q) {
+                        uint32_t (&v)[CH] = x[q & 1];
+                        tc::tmem_ld_wait(v);
+                        if (q < NC - 1) tc::tmem_ld(ts + CH * (q + 1), x[(q + 1) & 1]);
+                        scaled(v, CH * q);
+                        uint32_t pk[CH / 2];
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
+                        for (int i = 0; i < CH; i += 4) {
                             const float2 y0 = tc::fma2(f2(v, i), c2, off2), y1 = tc::fma2(f2(v, i + 2), c2, off2);
                             float2 e0 = make_float2(exp2_approx(y0.x), exp2_approx(y0.y));
                             float2 e1 = make_float2(exp2_approx(y1.x), exp2_approx(y1.y));
                             sum[0] = tc::add2(sum[0], e0);
                             sum[1] = tc::add2(sum[1], e1);
                             if constexpr (GS) {
-                                const float4 v4 = *reinterpret_cast<const float4 *>(cs.v + 32 * q + i);
+                                const float4 v4 = *reinterpret_cast<const float4 *>(cs.v + CH * q + i);
                                 e0 = tc::mul2(e0, make_float2(v4.x, v4.y));
                                 e1 = tc::mul2(e1, make_float2(v4.z, v4.w));
                             }
@@ -1035,12 +1075,12 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                             pk[(i >> 1) + 1] = tc::pack16<OK>(e1.x, e1.y);
                         }
                         // over columns that have been read for the last time
-                        tc::tmem_st16(ts + 16 * q, pk);
-                        if (q >= 2) {                           // 96 keys, then all
+                        tc::tmem_st(ts + CH / 2 * q, pk);
+                        if (CH * (q + 1) == 96 || q == NC - 1) {        // 96 keys, then all
                             tc::tmem_st_wait();
                             tc::fence_before();
                             __syncwarp();
-                            if (lane == 0) ptx::mbar_arrive(q == 2 ? bars.p_most(sub) : bars.p_full(sub));
+                            if (lane == 0) ptx::mbar_arrive(q < NC - 1 ? bars.p_most(sub) : bars.p_full(sub));
                         }
                     }
                     sum[0] = tc::add2(sum[0], sum[1]);
@@ -1048,121 +1088,127 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                 }
                 tile_n += nk;
                 if (!ok) break;
-                // accumulators of this segment, and their joining
-                const uint32_t turn0 = item - 1, turn1 = outs1;
-                if (two) ++outs1;
+                if (sub == 1 && !two) continue;
                 float off = m == ninf ? m : m * c;
                 if constexpr (kVRef) off = m == ninf ? m : off + vexp;
-                float w0 = 1.0f, w1 = 0.0f;                     // weights of O (own) and warpgroup 1's
-                const bool join = split && two;
-                if (sub == 1) {
-                    if (!two) continue;
-                    if (join) {
-                        state[0] = off;
-                        state[128] = l;
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(bars.j_full());
-                        // O of this warpgroup is read by the other: not to be overwritten before
-                        ok = warp_wait(bars.j_empty(), joins & 1, gone);
-                        ++joins;
-                        if (!ok) break;
-                        continue;
-                    }
-                    ok = warp_wait(bars.o_full(1), turn1 & 1, gone);
-                } else {
-                    ok = warp_wait(bars.o_full(0), turn0 & 1, gone);
-                    if (ok && join) {
-                        ok = warp_wait(bars.o_full(1), turn1 & 1, gone) && warp_wait(bars.j_full(), joins & 1, gone);
-                        ++joins;
-                    }
-                }
-                if (!ok) break;
-                tc::fence_after();
-                if (join) {
-                    const float m1 = state[0], l1 = state[128];
-                    const float top = fmaxf(off, m1);
-                    w0 = l == 0.0f || off == ninf ? 0.0f : exp2_approx(off - top);
-                    w1 = l1 == 0.0f || m1 == ninf ? 0.0f : exp2_approx(m1 - top);
-                    l = (w0 == 0.0f ? 0.0f : l * w0) + (w1 == 0.0f ? 0.0f : l1 * w1);
-                    off = top;
-                }
+                state[0] = off;
+                state[128] = l;
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bars.e_full(sub));
+                ++outs;
+            } while (w.next(p));
+        }
+    } else if (warp >= kOutWarp) {
+        // ------------------------------------------------ finished rows, a thread per row
+        const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+        const int row = (warp & 3) * 32 + lane;
+        const float ninf = -__int_as_float(0x7f800000);
+        const float *states = reinterpret_cast<const float *>(sm + L::state) + row;
+        uint32_t outs[2] = {0, 0};                              // segments that use each accumulator
+        if (work) {
+            Walk w = walk_from(p, st);
+            bool ok = true;
+            do {
+                const bool split = w.subtiles(p) == 1, join = split && w.k1 - w.k0 > 1;
                 const bool whole = w.k0 == 0 && w.k1 == w.units;
-                float fac = 1.0f;
-                if constexpr (is_q8(CK) && !GS) fac = d.v_scale[w.h];
-                if (whole) fac = l == 0.0f ? 0.0f : fac / l;
-                if (l == 0.0f) w0 = w1 = 0.0f;                  // a row without keys is zero whatever O holds
-                w0 *= fac;
-                w1 *= fac;
-                const int tok = r / d.group;
-                const int head = w.h * d.group + (r - tok * d.group);
-                char *o_row = d.out + int64_t(w.s.s0 + tok) * d.o_b + int64_t(head) * d.o_h;
-                const int slot = 2 * blockIdx.x + (w.k0 == 0 ? 1 : 0);
-                const int prow = (split ? 0 : sub * 128) + row;
-                float4 *acc = reinterpret_cast<float4 *>(f.part_acc) + int64_t(slot) * (D / 4) * kRowTile + prow;
-                if (!whole) {
-                    float *ml = f.part_ml + int64_t(slot) * 2 * kRowTile + prow;
-                    ml[0] = off;
-                    ml[kRowTile] = l;
-                }
-                float bad = 0.0f;
-#pragma unroll 1
-                for (int o = 0; o < D && !idle; o += 16) {
-                    uint32_t a[16];
-                    tc::tmem_ld16_wait(to + o, a);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) a[i] = w0 == 0.0f ? 0u : __float_as_uint(__uint_as_float(a[i]) * w0);
+                for (int sub = 0; sub < (split ? 1 : 2); ++sub) {
+                    const int r = w.tile * 2 * p.sub_rows + sub * p.sub_rows + row;
+                    const bool live = row < p.sub_rows && r < w.s.rows;
+                    const bool idle = !__any_sync(0xffffffffu, live);
+                    const uint32_t to = tmem + lanes + 256 + sub * 128;
+                    for (int i = sub; i < (join ? 2 : sub + 1); ++i) {
+                        ok = ok && warp_wait(bars.e_full(i), outs[i] & 1, gone) && warp_wait(bars.o_full(i), outs[i] & 1, gone);
+                        ++outs[i];
+                    }
+                    if (!ok) break;
+                    tc::fence_after();
+                    float off = states[sub * 256], l = states[sub * 256 + 128];
+                    float w0 = 1.0f, w1 = 0.0f;                 // weights of this O and of warpgroup 1's
                     if (join) {
-                        uint32_t b[16];
-                        tc::tmem_ld16_wait(to + 128 + o, b);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (w1 != 0.0f)
-                                a[i] = __float_as_uint(fmaf(__uint_as_float(b[i]), w1, __uint_as_float(a[i])));
+                        const float m1 = states[256], l1 = states[384];
+                        const float top = fmaxf(off, m1);
+                        w0 = l == 0.0f || off == ninf ? 0.0f : exp2_approx(off - top);
+                        w1 = l1 == 0.0f || m1 == ninf ? 0.0f : exp2_approx(m1 - top);
+                        l = (w0 == 0.0f ? 0.0f : l * w0) + (w1 == 0.0f ? 0.0f : l1 * w1);
+                        off = top;
                     }
+                    float fac = 1.0f;
+                    if constexpr (is_q8(CK) && !GS) fac = d.v_scale[w.h];
+                    if (whole) fac = l == 0.0f ? 0.0f : fac / l;
+                    if (l == 0.0f) w0 = w1 = 0.0f;              // a row without keys is zero whatever O holds
+                    w0 *= fac;
+                    w1 *= fac;
+                    const int tok = r / d.group;
+                    const int head = w.h * d.group + (r - tok * d.group);
+                    char *o_row = d.out + int64_t(w.s.s0 + tok) * d.o_b + int64_t(head) * d.o_h;
+                    const int slot = 2 * blockIdx.x + (w.k0 == 0 ? 1 : 0);
+                    const int prow = sub * 128 + row;
+                    float4 *acc = reinterpret_cast<float4 *>(f.part_acc) + int64_t(slot) * (D / 4) * kRowTile + prow;
                     if (!whole) {
-#pragma unroll
-                        for (int i = 0; i < 16; i += 4)
-                            acc[(o + i) / 4 * kRowTile] = make_float4(__uint_as_float(a[i]), __uint_as_float(a[i + 1]),
-                                                                      __uint_as_float(a[i + 2]), __uint_as_float(a[i + 3]));
-                        continue;
+                        float *ml = f.part_ml + int64_t(slot) * 2 * kRowTile + prow;
+                        ml[0] = off;
+                        ml[kRowTile] = l;
                     }
-                    uint32_t pk[8];
+                    float bad = 0.0f;
+#pragma unroll 1
+                    for (int o = 0; o < D && !idle; o += 16) {
+                        uint32_t a[16];
+                        tc::tmem_ld16_wait(to + o, a);
 #pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        bad = fmaf(__uint_as_float(a[i]), 0.0f, fmaf(__uint_as_float(a[i + 1]), 0.0f, bad));
-                        pk[i / 2] = tc::pack16<QK>(__uint_as_float(a[i]), __uint_as_float(a[i + 1]));
-                    }
-                    if (!live) continue;
-                    if (f.out32) {
-                        tc::st_global32(o_row + 2 * o, pk);
-                    } else if (d.out_vec_ok) {
+                        for (int i = 0; i < 16; ++i) a[i] = w0 == 0.0f ? 0u : __float_as_uint(__uint_as_float(a[i]) * w0);
+                        if (join) {
+                            uint32_t b[16];
+                            tc::tmem_ld16_wait(to + 128 + o, b);
 #pragma unroll
-                        for (int i = 0; i < 8; i += 4)
-                            *reinterpret_cast<uint4 *>(o_row + 2 * (o + 2 * i)) = make_uint4(pk[i], pk[i + 1], pk[i + 2], pk[i + 3]);
-                    } else {
+                            for (int i = 0; i < 16; ++i)
+                                if (w1 != 0.0f)
+                                    a[i] = __float_as_uint(fmaf(__uint_as_float(b[i]), w1, __uint_as_float(a[i])));
+                        }
+                        if (!whole) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            reinterpret_cast<uint16_t *>(o_row)[o + 2 * i] = uint16_t(pk[i]);
-                            reinterpret_cast<uint16_t *>(o_row)[o + 2 * i + 1] = uint16_t(pk[i] >> 16);
+                            for (int i = 0; i < 16; i += 4)
+                                acc[(o + i) / 4 * kRowTile] = make_float4(__uint_as_float(a[i]), __uint_as_float(a[i + 1]),
+                                                                          __uint_as_float(a[i + 2]), __uint_as_float(a[i + 3]));
+                            continue;
+                        }
+                        uint32_t pk[8];
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) {
+                            bad = fmaf(__uint_as_float(a[i]), 0.0f, fmaf(__uint_as_float(a[i + 1]), 0.0f, bad));
+                            pk[i / 2] = tc::pack16<QK>(__uint_as_float(a[i]), __uint_as_float(a[i + 1]));
+                        }
+                        if (!live) continue;
+                        if (f.out32) {
+                            tc::st_global32(o_row + 2 * o, pk);
+                        } else if (d.out_vec_ok) {
+#pragma unroll
+                            for (int i = 0; i < 8; i += 4)
+                                *reinterpret_cast<uint4 *>(o_row + 2 * (o + 2 * i)) = make_uint4(pk[i], pk[i + 1], pk[i + 2], pk[i + 3]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                reinterpret_cast<uint16_t *>(o_row)[o + 2 * i] = uint16_t(pk[i]);
+                                reinterpret_cast<uint16_t *>(o_row)[o + 2 * i + 1] = uint16_t(pk[i] >> 16);
+                            }
                         }
                     }
-                }
-                tc::fence_before();
-                if (join) {
+                    tc::fence_before();
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(bars.j_empty());
+                    if (lane == 0) {
+                        ptx::mbar_arrive(bars.e_empty(sub));
+                        if (join) ptx::mbar_arrive(bars.e_empty(1));
+                    }
+                    // not finite: weights of zero met values that are not; such a row is done again by itself
+                    unsigned redo = __ballot_sync(0xffffffffu, whole && live && bad != 0.0f);
+                    while (redo) {
+                        const int who = __ffs(redo) - 1;
+                        redo &= redo - 1;
+                        const int rr = __shfl_sync(0xffffffffu, r, who), tt = rr / d.group;
+                        redo_row<QK, CK, D>(d, d.block_tables + w.b * d.bt_b, int64_t(w.s.s0) + tt,
+                                            w.h * d.group + (rr - tt * d.group), row_limit(p, w.s, rr), w.limit, 0, D);
+                    }
                 }
-                // not finite: weights of zero met values that are not; such a row is done again by itself
-                unsigned redo = __ballot_sync(0xffffffffu, whole && live && bad != 0.0f);
-                while (redo) {
-                    const int who = __ffs(redo) - 1;
-                    redo &= redo - 1;
-                    const int rr = __shfl_sync(0xffffffffu, r, who), ll = __shfl_sync(0xffffffffu, lim, who);
-                    const int tt = rr / d.group;
-                    redo_row<QK, CK, D>(d, d.block_tables + w.b * d.bt_b, int64_t(w.s.s0) + tt,
-                                        w.h * d.group + (rr - tt * d.group), ll, w.limit, 0, D);
-                }
-            } while (w.next(p));
+            } while (ok && w.next(p));
         }
     } else {
         if (warp == kMmaWarp || warp == kMmaWarp + 1) {
@@ -1205,13 +1251,23 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                                 tc::mma_ts(ti + 256, ti + 8 * ks, b + v_at[ks], v_hi, id_pv, ks > 0 || acc);
                     }
                 };
-                // a stage is free when both subtiles have used it; on a row tile of one
-                // subtile each of its key tiles has one user, who counts twice
-                auto release = [&](uint32_t bar, bool twice) {
-                    if (leader) {
-                        tc::commit(bar);
-                        if (twice) tc::commit(bar);
+                auto release = [&](uint32_t bar) {
+                    if (leader) tc::commit(bar);
+                };
+                // A stage is free when both warps are done with it.  On a row tile of one
+                // subtile a key tile has one user; the other warp looks on, so that it sees
+                // every phase of a stage's barrier in turn.
+                auto there = [&](uint32_t t, int kv) -> bool {
+                    const bool ok = warp_wait(bars.full(R::stage(t, kv)), R::turn(t, kv) & 1, gone);
+                    tc::fence_after();
+                    return ok;
+                };
+                auto look_on = [&](uint32_t t) -> bool {
+                    for (int kv = 0; kv < 2; ++kv) {
+                        if (!there(t, kv)) return false;
+                        if (leader) ptx::mbar_arrive(bars.empty(R::stage(t, kv)));
                     }
+                    return true;
                 };
                 uint32_t tile_n = 0, item = 0, n_p = 0;
                 Walk w = walk_from(p, st);
@@ -1223,35 +1279,31 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                     ok = warp_wait(bars.q_full(), item & 1, gone);
                     if (!ok) break;
                     tc::fence_after();
-                    auto next_k = [&](uint32_t t) -> bool {
-                        const bool there = warp_wait(bars.full(R::stage(t, 0)), R::turn(t, 0) & 1, gone);
-                        tc::fence_after();
-                        return there;
-                    };
-                    if (j0 < nk && !next_k(tile_n + j0)) break;
+                    if (j0 == 1) ok = look_on(tile_n);
+                    ok = ok && (j0 >= nk || there(tile_n + j0, 0));
                     // K of tile j is there
-                    for (int j = j0; j < nk; j += step, ++n_p) {
+                    for (int j = j0; ok && j < nk; j += step, ++n_p) {
                         const bool last = j + step >= nk;
                         const uint32_t t = tile_n + j, ks = R::stage(t, 0), vs = R::stage(t, 1);
                         qk(split ? 0 : i, ks);
-                        release(bars.empty(ks), split);
-                        if (last) release(bars.q_empty(), false);
-                        ok = warp_wait(bars.full(vs), R::turn(t, 1) & 1, gone) && warp_wait(bars.p_most(i), n_p & 1, gone);
+                        release(bars.empty(ks));
+                        if (last) release(bars.q_empty());
+                        ok = there(t, 1) && warp_wait(bars.p_most(i), n_p & 1, gone);
                         if (!ok) break;
                         tc::fence_after();
                         pv(0, 6, vs, j > j0);
                         // the next tile's K, before the wait that the next scores depend on -- but in a
                         // ring of three, K two tiles on takes this V's place
                         const bool early = !split || FEED == kFeedTma || ST > 3;
-                        if (!last && early) ok = next_k(t + step);
+                        if (split && j + 1 < nk) ok = look_on(t + 1);
+                        if (!last && early) ok = ok && there(t + step, 0);
                         ok = ok && warp_wait(bars.p_full(i), n_p & 1, gone);
                         if (!ok) break;
                         tc::fence_after();
                         pv(6, 8, vs, true);
-                        release(bars.empty(vs), split);
-                        if (!last && !early) ok = next_k(t + step);
-                        if (!ok) break;
-                        if (last) release(bars.o_full(i), false);
+                        release(bars.empty(vs));
+                        if (last) release(bars.o_full(i));
+                        if (!last && !early) ok = there(t + step, 0);
                     }
                     if (!ok) break;
                     if (j0 >= nk && lane == 0) ptx::mbar_arrive(bars.q_empty());    // had nothing to do
