@@ -136,6 +136,10 @@ struct Walk {
         }
         return shape(p);
     }
+    // which warpgroups take key tile k: one of them, or (2) both
+    __device__ __forceinline__ int set(const PrefillParams &p, int k) const { return subtiles(p) == 2 ? 2 : (k - k0) & 1; }
+    // tokens of the sequence that the key tiles reach
+    __device__ __forceinline__ int reach() const { return min(s.ctx, units * kKeyTile); }
     __device__ __forceinline__ int subtiles(const PrefillParams &p) const
     {
         return s.rows - tile * 2 * p.sub_rows > p.sub_rows ? 2 : 1;
@@ -263,7 +267,7 @@ struct Smem {
     static constexpr int kStages = (kCoded ? 3 : 4) * (D == 128 ? 1 : 2);
     static constexpr int kRaw = kCoded ? kStages : 0;           // stages of raw codes
     static constexpr int kRawTile = kCoded ? 128 * raw_row<CK, D>() : 0;
-    static constexpr int kColSlots = D == 128 ? 4 : 8;          // see ColSlot
+    static constexpr int kColSlots = (kCoded ? 4 : 8) * (D == 128 ? 1 : 2);      // see ColSlot
     static constexpr int q = 0;
     static constexpr int ring = 2 * kTile;
     static constexpr int raw = ring + kStages * kTile;
@@ -273,7 +277,7 @@ struct Smem {
     static constexpr int state = ones + 512;                    // (m, l) of a row tile's rows: [subtile][2][128]
     static constexpr int q_scale = state + 2048;                // per row of subtile 0
     static constexpr int bars = q_scale + 512;
-    static constexpr int n_bars = 2 * kStages + 2 * kRaw + 2 + 4 * 2 + 1 + 4 + 1;
+    static constexpr int n_bars = 4 * kStages + 2 * kRaw + 2 + 4 * 2 + 1 + 4 + 1;
     static constexpr int info = bars + 8 * n_bars;              // per raw stage: which blocks are there
     static constexpr int misc = (info + 4 * 8 + 15) / 16 * 16;
     static constexpr int total = misc + 128;
@@ -286,11 +290,11 @@ struct Smem {
 
 // Column data of a key tile: scales of its 128 K and V rows, the largest V
 // scale of each 32 rows, and which groups of 8 rows are there.  Tile T's is
-// written once the ring has room for K of tile T.  With 2 R stages that is
-// when the scores of tile T - R are done, and so the softmax of tile
-// T - R - 2 at the latest (scores run at most two tiles ahead of a softmax):
-// R + 2 slots are enough (R = 2 or 4).  With three (six) stages it is when
-// P V of tile T - 2 (the scores of tile T - 3) are done: 2 (5) slots.
+// written once the ring has room for K of tile T.  With a ring of R tiles of K
+// that is when the scores of tile T - R are done; the tiles whose softmax may
+// still be under way then are fewer than 2 R + 2 (each subtile has one, at most
+// a tile's worth of the ring behind the other), and with three (six) stages,
+// where V of tile T - 2 (T - 4) is done too, fewer than 3 (5).
 struct ColSlot {
     float k[kKeyTile];
     float v[kKeyTile];
@@ -301,22 +305,24 @@ struct ColSlot {
 struct Bars {
     uint32_t base;
     int stages, raws;
-    __device__ __forceinline__ uint32_t full(int s) const { return base + 8 * s; }
-    __device__ __forceinline__ uint32_t empty(int s) const { return base + 8 * (stages + s); }
-    __device__ __forceinline__ uint32_t q_full() const { return base + 8 * (2 * stages); }
-    __device__ __forceinline__ uint32_t q_empty() const { return base + 8 * (2 * stages + 1); }
-    __device__ __forceinline__ uint32_t s_full(int i) const { return base + 8 * (2 * stages + 2 + i); }
-    __device__ __forceinline__ uint32_t p_full(int i) const { return base + 8 * (2 * stages + 4 + i); }
-    __device__ __forceinline__ uint32_t o_full(int i) const { return base + 8 * (2 * stages + 6 + i); }
-    __device__ __forceinline__ uint32_t p_most(int i) const { return base + 8 * (2 * stages + 8 + i); }
-    __device__ __forceinline__ uint32_t tail() const { return base + 8 * (2 * stages + 10); }
+    // A stage that is filled: for subtile 0 or 1 alone, or (set 2) for both, so
+    // that whoever waits on one of these barriers waits for each of its phases
+    __device__ __forceinline__ uint32_t full(int set, int s) const { return base + 8 * (set * stages + s); }
+    __device__ __forceinline__ uint32_t empty(int s) const { return base + 8 * (3 * stages + s); }
+    __device__ __forceinline__ uint32_t q_full() const { return base + 8 * (4 * stages); }
+    __device__ __forceinline__ uint32_t q_empty() const { return base + 8 * (4 * stages + 1); }
+    __device__ __forceinline__ uint32_t s_full(int i) const { return base + 8 * (4 * stages + 2 + i); }
+    __device__ __forceinline__ uint32_t p_full(int i) const { return base + 8 * (4 * stages + 4 + i); }
+    __device__ __forceinline__ uint32_t o_full(int i) const { return base + 8 * (4 * stages + 6 + i); }
+    __device__ __forceinline__ uint32_t p_most(int i) const { return base + 8 * (4 * stages + 8 + i); }
+    __device__ __forceinline__ uint32_t tail() const { return base + 8 * (4 * stages + 10); }
     // a subtile's rows are finished (their m and l are there), and have been read
-    __device__ __forceinline__ uint32_t e_full(int i) const { return base + 8 * (2 * stages + 11 + i); }
-    __device__ __forceinline__ uint32_t e_empty(int i) const { return base + 8 * (2 * stages + 13 + i); }
+    __device__ __forceinline__ uint32_t e_full(int i) const { return base + 8 * (4 * stages + 11 + i); }
+    __device__ __forceinline__ uint32_t e_empty(int i) const { return base + 8 * (4 * stages + 13 + i); }
     // bf16 Q that is to become f16
-    __device__ __forceinline__ uint32_t q_raw() const { return base + 8 * (2 * stages + 15); }
-    __device__ __forceinline__ uint32_t raw_full(int s) const { return base + 8 * (2 * stages + 16 + s); }
-    __device__ __forceinline__ uint32_t raw_empty(int s) const { return base + 8 * (2 * stages + 16 + raws + s); }
+    __device__ __forceinline__ uint32_t q_raw() const { return base + 8 * (4 * stages + 15); }
+    __device__ __forceinline__ uint32_t raw_full(int s) const { return base + 8 * (4 * stages + 16 + s); }
+    __device__ __forceinline__ uint32_t raw_empty(int s) const { return base + 8 * (4 * stages + 16 + raws + s); }
 };
 
 // Wait for a phase, giving up when it takes too long or another warp gave up.
@@ -521,18 +527,18 @@ __device__ __forceinline__ void copy_rows(const PrefillParams &p, const Start &s
     TileWalk tw{walk_from(p, st), 0};
     tw.k = tw.w.k0;
     uint32_t pos = 0, tile_n = 0;
-    int pending = -1;
+    uint32_t pending = 0;                                       // barrier of the stage in hand
     auto flush = [&](bool all) {
-        if (pending < 0) return;
+        if (pending == 0) return;
         if (all) tc::cp_async_wait<0>(); else tc::cp_async_wait<1>();
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bars.full(pending));
-        pending = -1;
+        if (lane == 0) ptx::mbar_arrive(pending);
+        pending = 0;
     };
     do {
         const int t = tw.k * kKeyTile + row;
-        bool in = t < tw.w.limit;
+        bool in = t < tw.w.reach();
         int64_t blk = 0;
         if (in) {
             blk = d.block_tables[tw.w.b * d.bt_b + int64_t(t >> d.block_shift) * d.bt_j];
@@ -543,6 +549,7 @@ __device__ __forceinline__ void copy_rows(const PrefillParams &p, const Start &s
         }
         const int64_t at = in ? blk * d.c_blk + int64_t(t & (d.block_size - 1)) * d.c_slot + tw.w.h * d.c_head : 0;
         const unsigned got = __ballot_sync(0xffffffffu, in);
+        const int set = tw.w.set(p, tw.k);
         for (int kv = 0; kv < 2; ++kv, ++pos) {
             // never wait for room with a stage in hand
             if (!__all_sync(0xffffffffu, pos < ST || ptx::mbar_try_wait(bars.empty(pos % ST), (pos / ST - 1) & 1)))
@@ -560,7 +567,7 @@ __device__ __forceinline__ void copy_rows(const PrefillParams &p, const Start &s
             for (int c = 0; c < D / 8; ++c) tc::cp_async16(dst + piece_at(row, c), src + (in ? c * d.c_chunk : 0), in);
             tc::cp_async_commit();
             flush(false);
-            pending = int(pos % ST);
+            pending = bars.full(set, pos % ST);
         }
         ++tile_n;
     } while (tw.next(p));
@@ -589,7 +596,7 @@ __device__ __forceinline__ void raw_codes(const PrefillParams &p, const PrefillF
     // this lane's block of the tile, -1 where it wants none
     auto lookup = [&]() -> int {
         const int t = tw.k * kKeyTile + lane * rows;
-        return lane < nblk && t < tw.w.limit
+        return lane < nblk && t < tw.w.reach()
                    ? d.block_tables[tw.w.b * d.bt_b + int64_t(t >> d.block_shift) * d.bt_j] : -1;
     };
     uint32_t pos = 0;
@@ -597,7 +604,7 @@ __device__ __forceinline__ void raw_codes(const PrefillParams &p, const PrefillF
     bool more = true;
     while (more) {
         const int t = tw.k * kKeyTile + lane * rows, h = tw.w.h;
-        const bool want = lane < nblk && t < tw.w.limit;
+        const bool want = lane < nblk && t < tw.w.reach();
         const bool in = want && blk >= 0 && blk < d.num_blocks;
         if (want && !in) raise_err(d.err_flag, PKV_DEVERR_BLOCK_RANGE);
         const unsigned got = __ballot_sync(0xffffffffu, in);
@@ -669,29 +676,29 @@ __device__ __forceinline__ void convert_rows(const PrefillParams &p, const Start
     uint32_t pos = 0, tile_n = 0;
     // scales of this lane's row: a tile ahead, its table entry two ahead
     int64_t entry = -1;
-    float ks = 0.0f, vs = 0.0f, kz = 0.0f, vz = 0.0f;
+    uint32_t ks = 0, vs = 0, kz = 0, vz = 0;                    // as stored: nothing waits for them before their use
     TileWalk ahead = tw;
     bool ahead_more = GS;
     auto fetch = [&]() {
         const int t = ahead.k * kKeyTile + row;
-        entry = t < ahead.w.limit
+        entry = t < ahead.w.reach()
                     ? d.block_tables[ahead.w.b * d.bt_b + int64_t(t >> d.block_shift) * d.bt_j] : -1;
     };
     auto scales = [&](const TileWalk &x) {
-        ks = vs = kz = vz = 0.0f;
+        ks = vs = kz = vz = 0;
         if (entry < 0 || entry >= d.num_blocks) return;
         const int64_t slot = (x.k * kKeyTile + row) & (d.block_size - 1);
         if constexpr (CK == kU3) {
             const int64_t m = entry * d.m_blk + slot * d.m_slot + x.w.h * d.m_head;
             const int64_t z = entry * d.z_blk + slot * d.z_slot + x.w.h * d.z_head;
-            ks = __half2float(__ushort_as_half(__ldg(d.k_qs + m)));
-            vs = __half2float(__ushort_as_half(__ldg(d.v_qs + m)));
-            kz = float(__ldg(d.k_qz + z));
-            vz = float(__ldg(d.v_qz + z));
+            ks = __ldg(d.k_qs + m);
+            vs = __ldg(d.v_qs + m);
+            kz = __ldg(d.k_qz + z);
+            vz = __ldg(d.v_qz + z);
         } else {
             const int64_t m = entry * d.gs_blk + slot * d.gs_slot + x.w.h * d.gs_head;
-            ks = __ldg(d.k_gs + m);
-            vs = __ldg(d.v_gs + m);
+            ks = __float_as_uint(__ldg(d.k_gs + m));
+            vs = __float_as_uint(__ldg(d.v_gs + m));
         }
     };
     if constexpr (GS) {
@@ -702,8 +709,9 @@ __device__ __forceinline__ void convert_rows(const PrefillParams &p, const Start
     }
     bool more = true;
     while (more) {
-        const int limit = tw.w.limit - tw.k * kKeyTile;         // rows of the tile that are wanted
-        const float zero[2] = {kz, vz};
+        const int limit = tw.w.reach() - tw.k * kKeyTile;       // rows of the tile that are wanted
+        const int set = tw.w.set(p, tw.k);
+        const uint32_t kz_now = kz, vz_now = vz;
         unsigned ok = 0;
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv, ++pos) {
@@ -715,9 +723,12 @@ __device__ __forceinline__ void convert_rows(const PrefillParams &p, const Start
                 ok = __ballot_sync(0xffffffffu, row < limit && ((got >> (row >> shift)) & 1u));
                 ColSlot &cs = cols[tile_n % L::kColSlots];
                 if constexpr (GS) {
-                    cs.k[row] = ks;
-                    cs.v[row] = vs;
-                    float mx = vs;
+                    auto value = [](uint32_t x) {
+                        return CK == kU3 ? __half2float(__ushort_as_half(uint16_t(x))) : __uint_as_float(x);
+                    };
+                    cs.k[row] = value(ks);
+                    cs.v[row] = value(vs);
+                    float mx = value(vs);
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
                     if (lane == 0) cs.vmax[lw] = mx;
@@ -745,7 +756,7 @@ __device__ __forceinline__ void convert_rows(const PrefillParams &p, const Start
                 const int r = lane >> 1, rr = 32 * lw + r, h = lane & 1;
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {                   // rows r and r + 16
-                    const float z = __shfl_sync(0xffffffffu, zero[kv], r + 16 * b);
+                    const float z = float(__shfl_sync(0xffffffffu, kv ? vz_now : kz_now, r + 16 * b));
                     const bool there = (ok >> (r + 16 * b)) & 1u;
                     const uint32_t z0 = tc::pack16<kF16>(-1024.0f - z, -1024.0f - z);
                     const uint32_t z6 = tc::pack16<kF16>(-16.0f - z, -16.0f - z);
@@ -804,7 +815,7 @@ __device__ __forceinline__ void convert_rows(const PrefillParams &p, const Start
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                ptx::mbar_arrive(bars.full(s));
+                ptx::mbar_arrive(bars.full(set, s));
                 ptx::mbar_arrive(bars.raw_empty(rs));
             }
         }
@@ -814,7 +825,7 @@ __device__ __forceinline__ void convert_rows(const PrefillParams &p, const Start
 }
 
 // ---------------------------------------------------------------- the kernel
-// Warps 0-7 softmax; 16-bit caches by TMA: 8 and 9 products, 10 K, 11 V and Q,
+// Warps 0-7 softmax; 16-bit caches by TMA: 8 and 9 products, 10 K and Q, 11 V,
 // 12-15 output; the others: 8-11 producers, 12 and 13 products, 14 raw codes,
 // 15 Q, 16-19 output.
 template <int QK, int CK, int D, int FEED, bool GS>
@@ -847,7 +858,7 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) {
-            ptx::mbar_init(bars.full(i), TMA ? 1 : 4);
+            for (int set = 0; set < 3; ++set) ptx::mbar_init(bars.full(set, i), TMA ? 1 : 4);
             ptx::mbar_init(bars.empty(i), 2);
         }
         for (int i = 0; i < L::kRaw; ++i) {
@@ -1205,7 +1216,7 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                         redo &= redo - 1;
                         const int rr = __shfl_sync(0xffffffffu, r, who), tt = rr / d.group;
                         redo_row<QK, CK, D>(d, d.block_tables + w.b * d.bt_b, int64_t(w.s.s0) + tt,
-                                            w.h * d.group + (rr - tt * d.group), row_limit(p, w.s, rr), w.limit, 0, D);
+                                            w.h * d.group + (rr - tt * d.group), row_limit(p, w.s, rr), w.reach(), 0, D);
                     }
                 }
             } while (ok && w.next(p));
@@ -1254,20 +1265,20 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                 auto release = [&](uint32_t bar) {
                     if (leader) tc::commit(bar);
                 };
-                // A stage is free when both warps are done with it.  On a row tile of one
-                // subtile a key tile has one user; the other warp looks on, so that it sees
-                // every phase of a stage's barrier in turn.
-                auto there = [&](uint32_t t, int kv) -> bool {
-                    const bool ok = warp_wait(bars.full(R::stage(t, kv)), R::turn(t, kv) & 1, gone);
+                // a stage is free when both subtiles have used it; on a row tile of one
+                // subtile each key tile has one user, who counts twice
+                auto done = [&](uint32_t stage, bool twice) {
+                    release(bars.empty(stage));
+                    if (twice) release(bars.empty(stage));
+                };
+                uint32_t phases[2] = {0, 0};                    // by stage: this subtile's own set, the common one
+                auto there = [&](uint32_t t, int kv, bool split) -> bool {
+                    const uint32_t s = R::stage(t, kv);
+                    const bool ok = warp_wait(bars.full(split ? i : 2, s), (phases[split ? 0 : 1] >> s) & 1, gone);
+                    phases[0] ^= uint32_t(split) << s;
+                    phases[1] ^= uint32_t(!split) << s;
                     tc::fence_after();
                     return ok;
-                };
-                auto look_on = [&](uint32_t t) -> bool {
-                    for (int kv = 0; kv < 2; ++kv) {
-                        if (!there(t, kv)) return false;
-                        if (leader) ptx::mbar_arrive(bars.empty(R::stage(t, kv)));
-                    }
-                    return true;
                 };
                 uint32_t tile_n = 0, item = 0, n_p = 0;
                 Walk w = walk_from(p, st);
@@ -1279,31 +1290,29 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                     ok = warp_wait(bars.q_full(), item & 1, gone);
                     if (!ok) break;
                     tc::fence_after();
-                    if (j0 == 1) ok = look_on(tile_n);
-                    ok = ok && (j0 >= nk || there(tile_n + j0, 0));
+                    ok = j0 >= nk || there(tile_n + j0, 0, split);
                     // K of tile j is there
                     for (int j = j0; ok && j < nk; j += step, ++n_p) {
                         const bool last = j + step >= nk;
                         const uint32_t t = tile_n + j, ks = R::stage(t, 0), vs = R::stage(t, 1);
                         qk(split ? 0 : i, ks);
-                        release(bars.empty(ks));
+                        done(ks, split);
                         if (last) release(bars.q_empty());
-                        ok = there(t, 1) && warp_wait(bars.p_most(i), n_p & 1, gone);
+                        ok = there(t, 1, split) && warp_wait(bars.p_most(i), n_p & 1, gone);
                         if (!ok) break;
                         tc::fence_after();
                         pv(0, 6, vs, j > j0);
                         // the next tile's K, before the wait that the next scores depend on -- but in a
                         // ring of three, K two tiles on takes this V's place
                         const bool early = !split || FEED == kFeedTma || ST > 3;
-                        if (split && j + 1 < nk) ok = look_on(t + 1);
-                        if (!last && early) ok = ok && there(t + step, 0);
+                        if (!last && early) ok = there(t + step, 0, split);
                         ok = ok && warp_wait(bars.p_full(i), n_p & 1, gone);
                         if (!ok) break;
                         tc::fence_after();
                         pv(6, 8, vs, true);
-                        release(bars.empty(vs));
+                        done(vs, split);
                         if (last) release(bars.o_full(i));
-                        if (!last && !early) ok = there(t + step, 0);
+                        if (!last && !early) ok = there(t + step, 0, split);
                     }
                     if (!ok) break;
                     if (j0 >= nk && lane == 0) ptx::mbar_arrive(bars.q_empty());    // had nothing to do
@@ -1325,8 +1334,8 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
             if (lane == 0) f.desc[blockIdx.x] = split_end(w, st, work && !have);
         } else if (TMA) {
             // -------------------------------------------- K (warp 10) and V (11) by TMA: whole blocks.  K boxes are
-            // 64 elements wide, V's take the row's 64-element chunks together.  V's warp
-            // loads Q too, before a segment's V, which is needed later
+            // 64 elements wide, V's take the row's 64-element chunks together.  K's warp
+            // loads Q too: both are needed at once
             const int kv = warp - 10;
             const CUtensorMap *map = kv ? &tmv : &tmk;
             const int shift = min(d.block_shift, 7);            // rows per box
@@ -1339,20 +1348,21 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                 // this lane's block of the tile, -1 where it wants none
                 auto lookup = [&]() -> int {
                     const int t = tw.k * kKeyTile + lane * rows;
-                    return lane < nblk && t < tw.w.limit
+                    return lane < nblk && t < tw.w.reach()
                                ? d.block_tables[tw.w.b * d.bt_b + int64_t(t >> d.block_shift) * d.bt_j] : -1;
                 };
                 int blk = lookup();
                 bool ok = true, more = true;
                 uint32_t item = 0;
                 for (; more && ok; ++tile_n) {
-                    if (kv == 1 && tw.k == tw.w.k0) {
+                    if (kv == 0 && tw.k == tw.w.k0) {
                         ok = load_q<D>(p, f, tw.w, item++, sm32 + L::q, bars, bars.q_full(), &tmq, gone, lane);
                         if (!ok) break;
                     }
                     const int t = tw.k * kKeyTile + lane * rows, h = tw.w.h;
-                    const int limit = tw.w.limit - tw.k * kKeyTile;
-                    const bool want = lane < nblk && t < tw.w.limit;
+                    const int limit = tw.w.reach() - tw.k * kKeyTile;
+                    const int set = tw.w.set(p, tw.k);
+                    const bool want = lane < nblk && t < tw.w.reach();
                     const bool in = want && blk >= 0 && blk < d.num_blocks;
                     if (want && !in) raise_err(d.err_flag, PKV_DEVERR_BLOCK_RANGE);
                     const unsigned got = __ballot_sync(0xffffffffu, in);
@@ -1362,10 +1372,10 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                     const uint32_t stage = R::stage(tile_n, kv), turn = R::turn(tile_n, kv);
                     if (turn > 0) ok = warp_wait(bars.empty(stage), (turn - 1) & 1, gone);
                     if (!ok) break;
-                    // V rows that nothing loads, or that no row sees, are zeroed: a weight of zero
-                    // must not meet what lies there
+                    // V rows that nothing loads, or behind the context, are zeroed: a weight of
+                    // zero must not meet what lies there
                     const bool fix = kv == 1 && (__popc(got) < nblk || limit < kKeyTile);
-                    const uint32_t bar = fix ? bars.tail() : bars.full(stage);
+                    const uint32_t bar = fix ? bars.tail() : bars.full(set, stage);
                     const uint32_t dst = sm32 + L::ring + stage * L::kTile;
                     if (lane == 0) {
                         if (kv == 0) {
@@ -1398,11 +1408,11 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                         }
                         ptx::fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(bars.full(stage));
+                        if (lane == 0) ptx::mbar_arrive(bars.full(set, stage));
                     }
                 }
-                if (kv == 1 && lane == 0) f.desc[blockIdx.x] = split_end(tw.w, st, ok);
-            } else if (kv == 1 && lane == 0) {
+                if (kv == 0 && lane == 0) f.desc[blockIdx.x] = split_end(tw.w, st, ok);
+            } else if (kv == 0 && lane == 0) {
                 f.desc[blockIdx.x] = make_int4(0, 0, 0, -1);
             }
         } else if (warp < 12) {
@@ -1501,7 +1511,7 @@ __global__ void __launch_bounds__(kRowTile) prefill_join_kernel(PrefillParams p,
         todo &= todo - 1;
         redo_row<QK, CK, D>(d, d.block_tables + ds.x * d.bt_b, int64_t(s.s0) + __shfl_sync(0xffffffffu, tok, who),
                             __shfl_sync(0xffffffffu, head, who), __shfl_sync(0xffffffffu, lim, who),
-                            tile_limit(p, s, ds.z), c0, c0 + 16);
+                            min(s.ctx, tile_units(tile_limit(p, s, ds.z)) * kKeyTile), c0, c0 + 16);
     }
 }
 
