@@ -23,7 +23,7 @@ cudaError_t launch_instance(const PrefillLaunch &a)
     f.flip_q = a.flip_q;
     f.raw_tma = a.tma;
     f.raw_unit = a.raw_unit;
-    e = launch_pdl(kernel, a.grid, prefill_threads<FEED>(), Smem<CK, D>::alloc, a.stream, *a.p, f, a.tmk, a.tmv, a.tmq);
+    e = launch_pdl(kernel, a.grid, prefill_threads<CK, FEED>(), Smem<CK, D>::alloc, a.stream, *a.p, f, a.tmk, a.tmv, a.tmq);
     if (e != cudaSuccess || !a.join) return e;
     return launch_pdl(prefill_join_kernel<QK, CK, D>, dim3(a.grid, D / 16), kRowTile, 0, a.stream, *a.p, f);
 }

@@ -64,7 +64,13 @@ struct PrefillFast {
 namespace {
 
 enum Feed : int { kFeedTma, kFeedCopy, kFeedCodes };
-template <int FEED> constexpr int prefill_threads() { return FEED == kFeedTma ? 512 : 640; }
+// warps that convert codes: 3-bit ones take the most work and have room
+template <int CK> constexpr int conv_warps() { return CK == kU3 ? 8 : 4; }
+
+template <int CK, int FEED> constexpr int prefill_threads()
+{
+    return FEED == kFeedTma ? 512 : FEED == kFeedCodes ? 512 + 32 * conv_warps<CK>() : 640;
+}
 
 constexpr int kRowTile = 256;   // rows of a row tile, those between a subtile's whole tokens and 128 included
 constexpr int kTileCost = 2;    // beginning and ending a row tile costs as much as this many units
@@ -272,7 +278,7 @@ struct Smem {
     static constexpr int ring = 2 * kTile;
     static constexpr int raw = ring + kStages * kTile;
     static constexpr int cols = raw + kRaw * kRawTile;
-    static constexpr int kColBytes = 2 * kKeyTile * 4 + 32;
+    static constexpr int kColBytes = 2 * kKeyTile * 4 + 64;
     static constexpr int ones = cols + kColSlots * kColBytes;   // 128 ones
     static constexpr int state = ones + 512;                    // (m, l) of a row tile's rows: [subtile][2][128]
     static constexpr int q_scale = state + 2048;                // per row of subtile 0
@@ -289,7 +295,7 @@ struct Smem {
 };
 
 // Column data of a key tile: scales of its 128 K and V rows, the largest V
-// scale of each 32 rows, and which groups of 8 rows are there.  Tile T's is
+// scale of each producer warp's rows, and which groups of 8 rows are there.  Tile T's is
 // written once the ring has room for K of tile T.  With a ring of R tiles of K
 // that is when the scores of tile T - R are done; the tiles whose softmax may
 // still be under way then are fewer than 2 R + 2 (each subtile has one, at most
@@ -298,8 +304,8 @@ struct Smem {
 struct ColSlot {
     float k[kKeyTile];
     float v[kKeyTile];
-    float vmax[4];
-    uint32_t mask[4];           // 4 bits per 32 rows (one word per loader warp; word 0 holds all 16 for the TMA producer)
+    float vmax[8];              // by producer warp, unused ones 0
+    uint32_t mask[8];           // likewise: the bits of its groups of 8 rows
 };
 
 struct Bars {
@@ -654,9 +660,8 @@ __device__ __forceinline__ void raw_codes(const PrefillParams &p, const PrefillF
     }
 }
 
-// Raw codes -> operand ring, rows 32 lw .. 32 lw + 31 of every tile by one
-// warp (lane = row for the scales).  The loop over a row's pieces is rolled:
-// four roles share the SM's instruction cache.
+// Raw codes -> operand ring, 128 / conv_warps rows of every tile by one warp
+// (lane = row for the scales).
 template <int CK, int D, bool GS>
 __device__ __forceinline__ void convert_rows(const PrefillParams &p, const Start &st, unsigned char *sm, uint32_t sm32,
                                              const Bars &bars, volatile int *gone, int lw, int lane)
@@ -668,7 +673,8 @@ __device__ __forceinline__ void convert_rows(const PrefillParams &p, const Start
     const DecodeParams &d = p.d;
     const uint32_t *info = reinterpret_cast<const uint32_t *>(sm + L::info);
     ColSlot *cols = reinterpret_cast<ColSlot *>(sm + L::cols);
-    const int row = 32 * lw + lane;
+    constexpr int NR = kKeyTile / conv_warps<CK>();             // rows of this warp: 32 or 16
+    const int row0 = NR * lw, row = row0 + lane % NR;
     const int shift = min(d.block_shift, 7), rows = 1 << shift;
     const bool xv = d.c_chunk != 16 && CK != kU3;
     TileWalk tw{walk_from(p, st), 0};
@@ -720,7 +726,7 @@ __device__ __forceinline__ void convert_rows(const PrefillParams &p, const Start
             if (pos >= ST && !warp_wait(bars.empty(s), (pos / ST - 1) & 1, gone)) return;
             if (kv == 0) {
                 const unsigned got = info[rs];
-                ok = __ballot_sync(0xffffffffu, row < limit && ((got >> (row >> shift)) & 1u));
+                ok = __ballot_sync(0xffffffffu, row < limit && ((got >> (row >> shift)) & 1u));     // twice 16 rows, or 32
                 ColSlot &cs = cols[tile_n % L::kColSlots];
                 if constexpr (GS) {
                     auto value = [](uint32_t x) {
@@ -736,7 +742,7 @@ __device__ __forceinline__ void convert_rows(const PrefillParams &p, const Start
                 if (lane == 0) {
                     uint32_t there = 0;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) there |= ((ok >> (8 * i)) & 0xffu ? 1u : 0u) << (4 * lw + i);
+                    for (int i = 0; i < NR / 8; ++i) there |= ((ok >> (8 * i)) & 0xffu ? 1u : 0u) << (NR / 8 * lw + i);
                     cs.mask[lw] = there;
                 }
                 if constexpr (GS) {                             // the next tile's scales, the one after's entry
@@ -753,30 +759,27 @@ __device__ __forceinline__ void convert_rows(const PrefillParams &p, const Start
             // lane -> (row, piece) so that the 8 lanes of a load or store phase hit
             // different banks; four pieces' loads before their conversion
             if constexpr (CK == kU3) {
-                const int r = lane >> 1, rr = 32 * lw + r, h = lane & 1;
+                const int r = lane >> 1, rr = row0 + r, h = lane & 1;
+                const float z = float(__shfl_sync(0xffffffffu, kv ? vz_now : kz_now, r));
+                const bool there = (ok >> r) & 1u;
+                const uint32_t z0 = tc::pack16<kF16>(-1024.0f - z, -1024.0f - z);
+                const uint32_t z6 = tc::pack16<kF16>(-16.0f - z, -16.0f - z);
+                uint32_t w[kPieces / 2][3];
+                const uint32_t *src = reinterpret_cast<const uint32_t *>(from + rr * RB + 12 * h);
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {                   // rows r and r + 16
-                    const float z = float(__shfl_sync(0xffffffffu, kv ? vz_now : kz_now, r + 16 * b));
-                    const bool there = (ok >> (r + 16 * b)) & 1u;
-                    const uint32_t z0 = tc::pack16<kF16>(-1024.0f - z, -1024.0f - z);
-                    const uint32_t z6 = tc::pack16<kF16>(-16.0f - z, -16.0f - z);
-                    uint32_t w[kPieces / 2][3];
-                    const uint32_t *src = reinterpret_cast<const uint32_t *>(from + (rr + 16 * b) * RB + 12 * h);
+                for (int i = 0; i < kPieces / 2; ++i)
 #pragma unroll
-                    for (int i = 0; i < kPieces / 2; ++i)
+                    for (int j = 0; j < 3; ++j) w[i][j] = there ? src[6 * i + j] : 0u;
 #pragma unroll
-                        for (int j = 0; j < 3; ++j) w[i][j] = there ? src[6 * i + j] : 0u;
+                for (int i = 0; i < kPieces / 2; ++i) {
+                    const uint32_t fl[4] = {w[i][0], __funnelshift_r(w[i][0], w[i][1], 24),
+                                            __funnelshift_r(w[i][1], w[i][2], 16), w[i][2] >> 8};
 #pragma unroll
-                    for (int i = 0; i < kPieces / 2; ++i) {
-                        const uint32_t fl[4] = {w[i][0], __funnelshift_r(w[i][0], w[i][1], 24),
-                                                __funnelshift_r(w[i][1], w[i][2], 16), w[i][2] >> 8};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            tc::st_shared16(dst + i * 16384 + b * 2048 + piece_at(rr, 4 * h + j), u3x8_to_f16(fl[j], z0, z6));
-                    }
+                    for (int j = 0; j < 4; ++j)
+                        tc::st_shared16(dst + i * 16384 + piece_at(rr, 4 * h + j), u3x8_to_f16(fl[j], z0, z6));
                 }
             } else if (xv) {
-                const int rr = 32 * lw + lane;
+                const int rr = row;
                 const unsigned char *src = from + (rr >> shift) * rows * RB + (rr & (rows - 1)) * 16;
                 const bool there = (ok >> lane) & 1u;
 #pragma unroll 2
@@ -791,7 +794,7 @@ __device__ __forceinline__ void convert_rows(const PrefillParams &p, const Start
             } else {
                 // 8 rows and four of a row's pieces at a time; at head_dim 128 odd rows take
                 // the other four
-                const int r = lane >> 2, rr = 32 * lw + r;
+                const int r = lane >> 2, rr = row0 + r;
 #pragma unroll
                 for (int b = 0; b < kPieces / 4; ++b) {
                     const int c = (lane & 3) | (kPieces == 8 ? ((b ^ r) & 1) << 2 : 0);
@@ -827,9 +830,9 @@ __device__ __forceinline__ void convert_rows(const PrefillParams &p, const Start
 // ---------------------------------------------------------------- the kernel
 // Warps 0-7 softmax; 16-bit caches by TMA: 8 and 9 products, 10 K and Q, 11 V,
 // 12-15 output; the others: 8-11 producers, 12 and 13 products, 14 raw codes,
-// 15 Q, 16-19 output.
+// 15 Q, 16-19 output, and for 3-bit codes 20-23 producers.
 template <int QK, int CK, int D, int FEED, bool GS>
-__global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
+__global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
     prefill_kernel(PrefillParams p, PrefillFast f, const __grid_constant__ CUtensorMap tmk,
                    const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmq)
 {
@@ -841,6 +844,7 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
     constexpr int kMmaWarp = TMA ? 8 : 12;                     // two of them
     constexpr int kQWarp = TMA ? 11 : 15;                       // by TMA that of V too
     constexpr int kOutWarp = TMA ? 12 : 16;                     // four of them
+    constexpr int kProducers = FEED == kFeedCodes ? conv_warps<CK>() : 4;
     constexpr int CH = TMA ? 32 : 16;                           // columns that a softmax thread reads at a time
     using R = Ring<FEED, ST>;
     constexpr bool kVRef = GS;                                  // P relative to the V scales' magnitude
@@ -858,12 +862,12 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) {
-            for (int set = 0; set < 3; ++set) ptx::mbar_init(bars.full(set, i), TMA ? 1 : 4);
+            for (int set = 0; set < 3; ++set) ptx::mbar_init(bars.full(set, i), TMA ? 1 : kProducers);
             ptx::mbar_init(bars.empty(i), 2);
         }
         for (int i = 0; i < L::kRaw; ++i) {
             ptx::mbar_init(bars.raw_full(i), 1);
-            ptx::mbar_init(bars.raw_empty(i), 4);
+            ptx::mbar_init(bars.raw_empty(i), kProducers);
         }
         ptx::mbar_init(bars.q_full(), kRawQ ? 8 : 1);
         ptx::mbar_init(bars.q_raw(), 1);
@@ -881,6 +885,7 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
         *gone = 0;
     }
     if (threadIdx.x < 128) reinterpret_cast<float *>(sm + L::ones)[threadIdx.x] = 1.0f;
+    if (threadIdx.x < 16 * L::kColSlots) (reinterpret_cast<uint32_t *>(cols[threadIdx.x / 16].vmax))[threadIdx.x % 16] = 0u;
     if (warp == kMmaWarp) tc::tmem_alloc(ptx::smem_u32(tmem_at), 512);
     griddep_wait();
     griddep_launch_dependents();
@@ -982,18 +987,21 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                     // keys behind the row's limit, and blocks that are not there
                     uint32_t there = cs.mask[0];
                     if constexpr (!TMA) there |= cs.mask[1] | cs.mask[2] | cs.mask[3];
+                    if constexpr (kProducers == 8) there |= cs.mask[4] | cs.mask[5] | cs.mask[6] | cs.mask[7];
                     const int rel = lim - (w.k0 + j) * kKeyTile;
-                    if (__any_sync(0xffffffffu, rel < kKeyTile || there != 0xffffu)) {
+                    const int seen = there == 0xffffu ? __reduce_min_sync(0xffffffffu, max(rel, 0)) : 0;    // by all rows
+                    if (seen < kKeyTile) {
                         // few tiles: masked in place, in a rolled loop, before the others' path
 #pragma unroll 1
-                        for (int o = 0; o < kKeyTile; o += 16) {
+                        for (int o = GS ? 0 : seen & ~15; o < kKeyTile; o += 16) {
                             uint32_t x[16];
                             tc::tmem_ld16_wait(ts + o, x);
                             const uint32_t g = there >> (o >> 3);
+                            const int n = rel - o;
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
                                 if constexpr (GS) x[i] = __float_as_uint(__uint_as_float(x[i]) * kcol[o + i]);
-                                if (o + i >= rel || !((g >> (i >> 3)) & 1u)) x[i] = 0xff800000u;
+                                if (i >= n || !((g >> (i >> 3)) & 1u)) x[i] = 0xff800000u;
                             }
                             tc::tmem_st16(ts + o, x);
                         }
@@ -1040,7 +1048,9 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                     }
                     if constexpr (kVRef) {
                         // 2^vexp at or above the V scales so far: P times a scale stays in f16's range
-                        const float vm = fmaxf(fmaxf(cs.vmax[0], cs.vmax[1]), fmaxf(cs.vmax[2], cs.vmax[3]));
+                        float vm = fmaxf(fmaxf(cs.vmax[0], cs.vmax[1]), fmaxf(cs.vmax[2], cs.vmax[3]));
+                        if constexpr (kProducers == 8)
+                            vm = fmaxf(vm, fmaxf(fmaxf(cs.vmax[4], cs.vmax[5]), fmaxf(cs.vmax[6], cs.vmax[7])));
                         const float e = float(int(__float_as_uint(fmaxf(vm, 1e-30f)) >> 23) - 126);
                         if (e > vexp) {
                             grow *= exp2_approx(vexp - e);
@@ -1109,7 +1119,7 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
                 ++outs;
             } while (w.next(p));
         }
-    } else if (warp >= kOutWarp) {
+    } else if (warp >= kOutWarp && warp < kOutWarp + 4) {
         // ------------------------------------------------ finished rows, a thread per row
         const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
         const int row = (warp & 3) * 32 + lane;
@@ -1415,10 +1425,10 @@ __global__ void __launch_bounds__(prefill_threads<FEED>(), 1)
             } else if (kv == 0 && lane == 0) {
                 f.desc[blockIdx.x] = make_int4(0, 0, 0, -1);
             }
-        } else if (warp < 12) {
+        } else if (warp < 12 || warp >= 20) {
             if (work) {
                 if constexpr (FEED == kFeedCodes)
-                    convert_rows<CK, D, GS>(p, st, sm, sm32, bars, gone, warp - 8, lane);
+                    convert_rows<CK, D, GS>(p, st, sm, sm32, bars, gone, warp < 12 ? warp - 8 : warp - 16, lane);
                 else if constexpr (FEED == kFeedCopy)
                     copy_rows<CK, D>(p, st, sm32 + L::ring, cols, bars, gone, warp - 8, lane);
             }

@@ -8,6 +8,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 import threading
 from dataclasses import dataclass
 from typing import Optional
@@ -87,12 +88,12 @@ def lib():
                                                    ctypes.c_int, P, P]
             L.pkv_decode_step.argtypes = [TP, TP, TP, TP, TP, TP, CP, TP, TP, ctypes.c_float, TP,
                                           ctypes.c_int, P, ctypes.c_size_t, P, P]
-            L.pkv_kv_append_dynamic.argtypes = [TP, TP, TP, CP, P, P]
-            L.pkv_kv_gather.argtypes = [CP, TP, TP, TP, P, P]
-            L.pkv_paged_prefill_workspace.argtypes = [TP, CP, TP, ctypes.POINTER(ctypes.c_size_t)]
-            L.pkv_paged_prefill_launches.argtypes = [TP, CP, TP, ctypes.POINTER(ctypes.c_int32)]
-            L.pkv_paged_prefill.argtypes = [TP, CP, TP, TP, TP, ctypes.c_float, TP, P,
-                                            ctypes.c_size_t, P, P]
+            # descriptors of these as packed bytes (_packed)
+            L.pkv_kv_append_dynamic.argtypes = [P, P, P, P, P, P]
+            L.pkv_kv_gather.argtypes = [P, P, P, P, P, P]
+            L.pkv_paged_prefill_workspace.argtypes = [P, P, P, P]
+            L.pkv_paged_prefill_launches.argtypes = [P, P, P, P]
+            L.pkv_paged_prefill.argtypes = [P, P, P, P, P, ctypes.c_float, P, P, ctypes.c_size_t, P, P]
             L.pkv_noalloc_scratch_bytes.restype = ctypes.c_size_t
             L.pkv_pack3.argtypes = [P, P, ctypes.c_int64, P]
             L.pkv_unpack3.argtypes = [P, P, ctypes.c_int64, P]
@@ -113,19 +114,23 @@ def _check(rc: int):
         raise PkvError(rc, lib().pkv_last_error().decode())
 
 
-def _desc(t: Optional[torch.Tensor], code: Optional[int] = None) -> _Tensor:
-    d = _Tensor()
-    if t is None:
-        return d
-    if t.dim() > 4:
+_PACK = struct.Struct("@Pii8q").pack          # pkv_tensor
+_PAD = ((0, 0, 0, 0), (0, 0, 0), (0, 0), (0,), ())
+
+
+def _packed(t: torch.Tensor, code: Optional[int] = None) -> bytes:
+    """A pkv_tensor as bytes."""
+    sh, st = t.shape, t.stride()
+    n = len(sh)
+    if n > 4:
         raise ValueError("at most 4 dims")
-    d.data = t.data_ptr() if t.numel() > 0 else 0
-    d.dtype = _TORCH_CODES[t.dtype] if code is None else code
-    d.ndim = t.dim()
-    for i in range(t.dim()):
-        d.shape[i] = t.shape[i]
-        d.stride[i] = t.stride(i)
-    return d
+    pad = _PAD[n]
+    return _PACK(t.data_ptr() if 0 not in sh else 0, _TORCH_CODES[t.dtype] if code is None else code, n,
+                 *sh, *pad, *st, *pad)
+
+
+def _desc(t: Optional[torch.Tensor], code: Optional[int] = None) -> _Tensor:
+    return _Tensor() if t is None else _Tensor.from_buffer_copy(_packed(t, code))
 
 
 def _xvec_desc(t: torch.Tensor, code: int) -> _Tensor:
@@ -158,35 +163,32 @@ def _need_cuda(*ts):
             raise ValueError("all tensors must be CUDA tensors")
 
 
-class _on_device:
-    """Checks that every tensor is on one CUDA device, makes that device and
-    `stream` (or the device's current stream) current inside the block -- so
-    that what the call allocates belongs to the stream that uses it -- and
-    gives the stream's handle."""
+def _one_device(*ts) -> int:
+    """The CUDA device that every tensor is on."""
+    dev = None
+    for t in ts:
+        if t is not None:
+            i = t.get_device()
+            if i != dev:
+                if i < 0:
+                    raise ValueError("all tensors must be CUDA tensors")
+                if dev is not None:
+                    raise ValueError("all tensors must be on one device, got cuda:%d and cuda:%d" % (dev, i))
+                dev = i
+    return dev
 
-    def __init__(self, stream, *ts):
-        _need_cuda(*ts)
-        devices = {t.device for t in ts if t is not None}
-        if len(devices) > 1:
-            raise ValueError("all tensors must be on one device, got %s" % sorted(map(str, devices)))
-        self.device = devices.pop()
-        if stream is not None and stream.device != self.device:
-            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, self.device))
-        self.given = stream
 
-    def __enter__(self):
-        if self.given is None and torch.cuda.current_device() == self.device.index:
-            self.guard = None
-            return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-        stream = self.given if self.given is not None else torch.cuda.current_stream(self.device)
-        self.guard = torch.cuda.stream(stream)
-        self.guard.__enter__()
-        return ctypes.c_void_p(stream.cuda_stream)
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-        return False
+def _elsewhere(dev: int, stream):
+    """None when device `dev` is current and no stream is given; else a
+    context in which they are, so that what the call allocates belongs to the
+    stream that uses it."""
+    if stream is None:
+        if torch.cuda.current_device() == dev:
+            return None
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device_index != dev:
+        raise ValueError("the stream is on cuda:%d, the tensors on cuda:%d" % (stream.device_index, dev))
+    return torch.cuda.stream(stream)
 
 
 @dataclass
@@ -381,13 +383,25 @@ def kv_append_scaled(k_new, v_new, k_new_scale, v_new_scale, slot_mapping, cache
                                       _ptr(err_flag), _stream(stream)))
 
 
+def _raw_stream(dev: int) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):      # the same handle, without a Stream object
+    _raw_stream = torch._C._cuda_getCurrentRawStream    # noqa: F811
+
+
 def kv_append_dynamic(k_new, v_new, slot_mapping, cache: KVCache, err_flag=None, stream=None):
     """kv_append for a cache with per-token scales that computes each row's
     scales, amax / (the format's largest value), and stores them with it."""
-    with _on_device(stream, k_new, v_new, slot_mapping, err_flag, *cache.tensors()) as s:
-        _check(lib().pkv_kv_append_dynamic(ctypes.byref(_desc(k_new)), ctypes.byref(_desc(v_new)),
-                                           ctypes.byref(_desc(slot_mapping)),
-                                           ctypes.byref(cache._struct()), _ptr(err_flag), s))
+    dev = _one_device(k_new, v_new, slot_mapping, err_flag, *cache.tensors())
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return kv_append_dynamic(k_new, v_new, slot_mapping, cache, err_flag)
+    _check(lib().pkv_kv_append_dynamic(_packed(k_new), _packed(v_new), _packed(slot_mapping),
+                                       ctypes.byref(cache._struct()),
+                                       None if err_flag is None else err_flag.data_ptr(), _raw_stream(dev)))
 
 
 def kv_gather(cache: KVCache, slot_mapping, dtype: Optional[torch.dtype] = None, k_out=None, v_out=None,
@@ -396,7 +410,12 @@ def kv_gather(cache: KVCache, slot_mapping, dtype: Optional[torch.dtype] = None,
     [num_tokens, Hkv, D].  Without k_out / v_out they are allocated in `dtype`
     (the cache's own for 16-bit caches, else bfloat16), zero where
     slot_mapping < 0; given buffers keep those rows as they were."""
-    with _on_device(stream, slot_mapping, k_out, v_out, err_flag, *cache.tensors()) as s:
+    dev = _one_device(slot_mapping, k_out, v_out, err_flag, *cache.tensors())
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return kv_gather(cache, slot_mapping, dtype, k_out, v_out, err_flag)
+    if k_out is None or v_out is None:
         if dtype is None:
             given = k_out if k_out is not None else v_out
             dtype = given.dtype if given is not None else \
@@ -406,24 +425,23 @@ def kv_gather(cache: KVCache, slot_mapping, dtype: Optional[torch.dtype] = None,
             k_out = torch.zeros(shape, dtype=dtype, device=slot_mapping.device)
         if v_out is None:
             v_out = torch.zeros(shape, dtype=dtype, device=slot_mapping.device)
-        _check(lib().pkv_kv_gather(ctypes.byref(cache._struct()), ctypes.byref(_desc(slot_mapping)),
-                                   ctypes.byref(_desc(k_out)), ctypes.byref(_desc(v_out)),
-                                   _ptr(err_flag), s))
+    _check(lib().pkv_kv_gather(ctypes.byref(cache._struct()), _packed(slot_mapping), _packed(k_out), _packed(v_out),
+                               None if err_flag is None else err_flag.data_ptr(), _raw_stream(dev)))
     return k_out, v_out
 
 
 def prefill_workspace_bytes(q, cache: KVCache, block_tables) -> int:
     n = ctypes.c_size_t(0)
-    _check(lib().pkv_paged_prefill_workspace(ctypes.byref(_desc(q)), ctypes.byref(cache._struct()),
-                                             ctypes.byref(_desc(block_tables)), ctypes.byref(n)))
+    _check(lib().pkv_paged_prefill_workspace(_packed(q), ctypes.byref(cache._struct()), _packed(block_tables),
+                                             ctypes.byref(n)))
     return int(n.value)
 
 
 def prefill_launches(q, cache: KVCache, block_tables) -> int:
     """Kernel launches one paged_prefill call with these arguments makes."""
     n = ctypes.c_int32(0)
-    _check(lib().pkv_paged_prefill_launches(ctypes.byref(_desc(q)), ctypes.byref(cache._struct()),
-                                            ctypes.byref(_desc(block_tables)), ctypes.byref(n)))
+    _check(lib().pkv_paged_prefill_launches(_packed(q), ctypes.byref(cache._struct()), _packed(block_tables),
+                                            ctypes.byref(n)))
     return int(n.value)
 
 
@@ -433,23 +451,21 @@ def paged_prefill(q, cache: KVCache, block_tables, q_starts, context_lens,
     sequence b owns rows q_starts[b] .. q_starts[b + 1] - 1, the last tokens of
     its context_lens[b] cached ones (their K/V are appended before).  Without
     `out` one is allocated, zero in the rows that no sequence owns."""
-    with _on_device(stream, q, block_tables, q_starts, context_lens, out, workspace, err_flag,
-                    *cache.tensors()) as s:
-        if sm_scale is None:
-            sm_scale = 1.0 / math.sqrt(q.shape[-1])
-        if out is None:
-            out = torch.zeros_like(q, memory_format=torch.contiguous_format)
-        if workspace is None:
-            need = prefill_workspace_bytes(q, cache, block_tables)
-            if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        ws_n = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        _check(lib().pkv_paged_prefill(ctypes.byref(_desc(q)), ctypes.byref(cache._struct()),
-                                       ctypes.byref(_desc(block_tables)),
-                                       ctypes.byref(_desc(q_starts)),
-                                       ctypes.byref(_desc(context_lens)), float(sm_scale),
-                                       ctypes.byref(_desc(out)), _ptr(workspace), ws_n,
-                                       _ptr(err_flag), s))
+    dev = _one_device(q, block_tables, q_starts, context_lens, out, workspace, err_flag, *cache.tensors())
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return paged_prefill(q, cache, block_tables, q_starts, context_lens, sm_scale, out, workspace, err_flag)
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(q.shape[-1])
+    if out is None:
+        out = torch.zeros_like(q, memory_format=torch.contiguous_format)
+    if workspace is None:
+        workspace = torch.empty(prefill_workspace_bytes(q, cache, block_tables), dtype=torch.uint8, device=q.device)
+    _check(lib().pkv_paged_prefill(_packed(q), ctypes.byref(cache._struct()), _packed(block_tables),
+                                   _packed(q_starts), _packed(context_lens), sm_scale, _packed(out),
+                                   workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                   None if err_flag is None else err_flag.data_ptr(), _raw_stream(dev)))
     return out
 
 

@@ -156,18 +156,21 @@ def test_python_refusals(m):
 
 
 class _Fake:
-    """Stands for a CUDA tensor or stream of a device this machine has not."""
+    """Stands for a tensor or stream of a CUDA device that this machine has not."""
 
     def __init__(self, dev):
-        self.device, self.is_cuda = torch.device(dev), True
+        self.device_index = dev
+
+    def get_device(self):
+        return self.device_index
 
 
 def test_mixed_devices_are_refused(m):
     with pytest.raises(ValueError, match="one device"):
-        m._on_device(None, _Fake("cuda:0"), _Fake("cuda:1"))
+        m._one_device(_Fake(0), None, _Fake(1))
     with pytest.raises(ValueError, match="the stream is on"):
-        m._on_device(_Fake("cuda:1"), _Fake("cuda:0"), None)
-    assert m._on_device(_Fake("cuda:0"), _Fake("cuda:0"), None).device.index == 0
+        m._elsewhere(0, _Fake(1))
+    assert m._one_device(_Fake(1), None, _Fake(1)) == 1
 
 
 def test_more_than_four_dims_are_refused(m):
