@@ -270,8 +270,10 @@ template <int CK, int D>
 struct Smem {
     static constexpr bool kCoded = is_coded<CK>();
     static constexpr int kTile = 128 * D * 2;                   // bytes of 128 operand rows
-    static constexpr int kStages = (kCoded ? 3 : 4) * (D == 128 ? 1 : 2);
-    static constexpr int kRaw = kCoded ? kStages : 0;           // stages of raw codes
+    // stages of operands and of raw codes: what fits.  One-byte codes have three
+    // operand stages, the others four
+    static constexpr int kStages = (kCoded && CK != kU3 ? 3 : 4) * (D == 128 ? 1 : 2);
+    static constexpr int kRaw = kCoded ? 3 * (D == 128 ? 1 : 2) : 0;
     static constexpr int kRawTile = kCoded ? 128 * raw_row<CK, D>() : 0;
     static constexpr int kColSlots = (kCoded ? 4 : 8) * (D == 128 ? 1 : 2);      // see ColSlot
     static constexpr int q = 0;
@@ -279,8 +281,7 @@ struct Smem {
     static constexpr int raw = ring + kStages * kTile;
     static constexpr int cols = raw + kRaw * kRawTile;
     static constexpr int kColBytes = 2 * kKeyTile * 4 + 64;
-    static constexpr int ones = cols + kColSlots * kColBytes;   // 128 ones
-    static constexpr int state = ones + 512;                    // (m, l) of a row tile's rows: [subtile][2][128]
+    static constexpr int state = cols + kColSlots * kColBytes;  // (m, l) of a row tile's rows: [subtile][2][128]
     static constexpr int q_scale = state + 2048;                // per row of subtile 0
     static constexpr int bars = q_scale + 512;
     static constexpr int n_bars = 4 * kStages + 2 * kRaw + 2 + 4 * 2 + 1 + 4 + 1;
@@ -732,7 +733,7 @@ __device__ __forceinline__ void convert_rows(const PrefillParams &p, const Start
                     auto value = [](uint32_t x) {
                         return CK == kU3 ? __half2float(__ushort_as_half(uint16_t(x))) : __uint_as_float(x);
                     };
-                    cs.k[row] = value(ks);
+                    cs.k[row] = fmaxf(value(ks), 1.17549435e-38f);
                     cs.v[row] = value(vs);
                     float mx = value(vs);
 #pragma unroll
@@ -884,7 +885,6 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
         ptx::fence_mbar_init();
         *gone = 0;
     }
-    if (threadIdx.x < 128) reinterpret_cast<float *>(sm + L::ones)[threadIdx.x] = 1.0f;
     if (threadIdx.x < 16 * L::kColSlots) (reinterpret_cast<uint32_t *>(cols[threadIdx.x / 16].vmax))[threadIdx.x % 16] = 0u;
     if (warp == kMmaWarp) tc::tmem_alloc(ptx::smem_u32(tmem_at), 512);
     griddep_wait();
@@ -983,7 +983,6 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                         continue;
                     }
                     const ColSlot &cs = cols[(tile_n + j) % L::kColSlots];
-                    const float *kcol = cs.k;
                     // keys behind the row's limit, and blocks that are not there
                     uint32_t there = cs.mask[0];
                     if constexpr (!TMA) there |= cs.mask[1] | cs.mask[2] | cs.mask[3];
@@ -993,38 +992,36 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                     if (seen < kKeyTile) {
                         // few tiles: masked in place, in a rolled loop, before the others' path
 #pragma unroll 1
-                        for (int o = GS ? 0 : seen & ~15; o < kKeyTile; o += 16) {
+                        for (int o = seen & ~15; o < kKeyTile; o += 16) {
                             uint32_t x[16];
                             tc::tmem_ld16_wait(ts + o, x);
                             const uint32_t g = there >> (o >> 3);
                             const int n = rel - o;
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                if constexpr (GS) x[i] = __float_as_uint(__uint_as_float(x[i]) * kcol[o + i]);
+                            for (int i = 0; i < 16; ++i)
                                 if (i >= n || !((g >> (i >> 3)) & 1u)) x[i] = 0xff800000u;
-                            }
                             tc::tmem_st16(ts + o, x);
                         }
                         tc::tmem_st_wait();
-                        kcol = reinterpret_cast<const float *>(sm + L::ones);
                     }
                     // the tile's columns in chunks, read twice, for the maximum and for the
                     // weights: that costs less than the registers would
                     constexpr int NC = kKeyTile / CH;
                     uint32_t x[2][CH];
+                    // per-row K scales: the scores are scaled on the way to the maximum and put
+                    // back.  A scale of zero must not meet a masked score's -inf: at least 2^-126
                     auto scaled = [&](uint32_t (&v)[CH], int o) {
-                        if constexpr (GS) {
 #pragma unroll
-                            for (int i = 0; i < CH; i += 4) {
-                                const float4 k4 = *reinterpret_cast<const float4 *>(kcol + o + i);
-                                const float2 u = tc::mul2(f2(v, i), make_float2(k4.x, k4.y));
-                                const float2 y = tc::mul2(f2(v, i + 2), make_float2(k4.z, k4.w));
-                                v[i] = __float_as_uint(u.x);
-                                v[i + 1] = __float_as_uint(u.y);
-                                v[i + 2] = __float_as_uint(y.x);
-                                v[i + 3] = __float_as_uint(y.y);
-                            }
+                        for (int i = 0; i < CH; i += 4) {
+                            const float4 k4 = *reinterpret_cast<const float4 *>(cs.k + o + i);
+                            const float2 u = tc::mul2(f2(v, i), make_float2(k4.x, k4.y));
+                            const float2 y = tc::mul2(f2(v, i + 2), make_float2(k4.z, k4.w));
+                            v[i] = __float_as_uint(u.x);
+                            v[i + 1] = __float_as_uint(u.y);
+                            v[i + 2] = __float_as_uint(y.x);
+                            v[i + 3] = __float_as_uint(y.y);
                         }
+                        tc::tmem_st(ts + o, v);
                     };
                     float mx[4] = {ninf, ninf, ninf, ninf};
                     tc::tmem_ld(ts, x[0]);
@@ -1032,13 +1029,17 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                     for (int q = 0; q < NC; ++q) {
                         tc::tmem_ld_wait(x[q & 1]);
                         // after the last chunk the first again
-                        tc::tmem_ld(ts + CH * ((q + 1) % NC), x[(q + 1) & 1]);
-                        scaled(x[q & 1], CH * q);
+                        if (!GS || q < NC - 1) tc::tmem_ld(ts + CH * ((q + 1) % NC), x[(q + 1) & 1]);
+                        if constexpr (GS) scaled(x[q & 1], CH * q);
 #pragma unroll
                         for (int u = 0; u < CH; u += 8)
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
                                 mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(x[q & 1][u + i])), __uint_as_float(x[q & 1][u + 4 + i]));
+                    }
+                    if constexpr (GS) {
+                        tc::tmem_st_wait();
+                        tc::tmem_ld(ts, x[0]);
                     }
                     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     float grow = 1.0f;                          // what O and l shrink by
@@ -1078,7 +1079,6 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                         uint32_t (&v)[CH] = x[q & 1];
                         tc::tmem_ld_wait(v);
                         if (q < NC - 1) tc::tmem_ld(ts + CH * (q + 1), x[(q + 1) & 1]);
-                        scaled(v, CH * q);
                         uint32_t pk[CH / 2];
 #pragma unroll
                         for (int i = 0; i < CH; i += 4) {

@@ -118,6 +118,7 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[32]) { tmem
 __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[16]) { tmem_ld16(addr, r); }
 __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) { tmem_ld_wait32(r, 0); }
 __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16]) { tmem_ld_wait16(r); }
+__device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[32]) { tmem_st32(addr, r, 0); }
 __device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[16]) { tmem_st16(addr, r); }
 __device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[8]) { tmem_st8(addr, r); }
 
