@@ -1171,10 +1171,8 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                         ml[kRowTile] = l;
                     }
                     float bad = 0.0f;
-#pragma unroll 1
-                    for (int o = 0; o < D && !idle; o += 16) {
-                        uint32_t a[16];
-                        tc::tmem_ld16_wait(to + o, a);
+                    // 16 columns at o, in `a`, while the next are on their way
+                    auto columns = [&](int o, uint32_t (&a)[16]) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) a[i] = w0 == 0.0f ? 0u : __float_as_uint(__uint_as_float(a[i]) * w0);
                         if (join) {
@@ -1190,7 +1188,7 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                             for (int i = 0; i < 16; i += 4)
                                 acc[(o + i) / 4 * kRowTile] = make_float4(__uint_as_float(a[i]), __uint_as_float(a[i + 1]),
                                                                           __uint_as_float(a[i + 2]), __uint_as_float(a[i + 3]));
-                            continue;
+                            return;
                         }
                         uint32_t pk[8];
 #pragma unroll
@@ -1198,7 +1196,7 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                             bad = fmaf(__uint_as_float(a[i]), 0.0f, fmaf(__uint_as_float(a[i + 1]), 0.0f, bad));
                             pk[i / 2] = tc::pack16<QK>(__uint_as_float(a[i]), __uint_as_float(a[i + 1]));
                         }
-                        if (!live) continue;
+                        if (!live) return;
                         if (f.out32) {
                             tc::st_global32(o_row + 2 * o, pk);
                         } else if (d.out_vec_ok) {
@@ -1211,6 +1209,19 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                                 reinterpret_cast<uint16_t *>(o_row)[o + 2 * i] = uint16_t(pk[i]);
                                 reinterpret_cast<uint16_t *>(o_row)[o + 2 * i + 1] = uint16_t(pk[i] >> 16);
                             }
+                        }
+                    };
+                    if (!idle) {
+                        uint32_t a[16], b[16];
+                        tc::tmem_ld16(to, a);
+#pragma unroll 1
+                        for (int o = 0; o < D; o += 32) {
+                            tc::tmem_ld_wait16(a);
+                            tc::tmem_ld16(to + o + 16, b);
+                            columns(o, a);
+                            tc::tmem_ld_wait16(b);
+                            if (o + 32 < D) tc::tmem_ld16(to + o + 32, a);
+                            columns(o + 16, b);
                         }
                     }
                     tc::fence_before();
