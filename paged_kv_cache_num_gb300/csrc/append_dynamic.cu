@@ -7,7 +7,16 @@
 // A row is read once: head_dim / 16 lanes hold 16 elements each in
 // registers (two 16-byte loads), the maximum is a shuffle reduction among
 // them, and each lane stores its 16 codes as one 16-byte piece, which is
-// also a piece of the x-vectorised layout.
+// also a piece of the x-vectorised layout.  Bound by HBM; what it spends
+// besides is the division per element:
+//
+// RN(x / s) through the correctly rounded reciprocal r = RN(1 / s): q = x r,
+// q' = q + (x - q s) r is within an ulp of x / s, and then q'' = q' +
+// (x - q' s) r, whose residual is exact in one FMA, is RN(x / s)
+// (Markstein's theorem).  The residual is exact while it does not underflow:
+// with s >= 2^-80 it is for every quotient that any of the casts sees
+// (2^-17 and above).  Rows below that, and rows with infinities or NaN, take
+// the division instruction.
 #include <type_traits>
 
 #include "append_common.cuh"
@@ -20,12 +29,20 @@ template <int Q8> __device__ __forceinline__ float q8_max()
     return Q8 == kE4M3 ? 448.0f : Q8 == kE5M2 ? 57344.0f : 127.0f;
 }
 
+__device__ __forceinline__ float quotient(float x, float s, float r)
+{
+    const float q = x * r;
+    const float q1 = fmaf(fmaf(-q, s, x), r, q);
+    return copysignf(fmaf(fmaf(-q1, s, x), r, q1), x);         // -0 stays -0
+}
+
 template <int SRC, bool VEC, int Q8, int LPR>
 __global__ void __launch_bounds__(kAppendThreads) append_dynamic_kernel(AppendParams p)
 {
     griddep_wait();
     griddep_launch_dependents();
     constexpr int RPW = 32 / LPR;                   // rows per warp
+    constexpr uint32_t kInf = SRC == kBF16 ? 0x7f80u : 0x7c00u;
     const int lane = threadIdx.x & 31;
     const int sub = lane % LPR;
     const int64_t warp = (blockIdx.x * int64_t(blockDim.x) + threadIdx.x) >> 5;
@@ -55,27 +72,64 @@ __global__ void __launch_bounds__(kAppendThreads) append_dynamic_kernel(AppendPa
                 for (int j = 0; j < 8; ++j) e[j] = uint32_t(s2[2 * j]) | (uint32_t(s2[2 * j + 1]) << 16);
             }
         }
-        float a = 0.0f;
+        // magnitudes order like their bits
+        uint32_t top2 = 0u;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float lo = fabsf(h2f<SRC>(uint16_t(e[j]))), hi = fabsf(h2f<SRC>(uint16_t(e[j] >> 16)));
-            // NaN fails the comparison too
-            if (lo < __int_as_float(0x7f800000)) a = fmaxf(a, lo);
-            if (hi < __int_as_float(0x7f800000)) a = fmaxf(a, hi);
-        }
+        for (int j = 0; j < 8; ++j) top2 = __vmaxu2(top2, e[j] & 0x7fff7fffu);
+        uint32_t top = max(top2 & 0xffffu, top2 >> 16);
 #pragma unroll
-        for (int o = 1; o < LPR; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-        const float s = fmaxf(__fdiv_rn(a, q8_max<Q8>()), 1.17549435e-38f);
-        if (live) {
-            uint32_t c[4];
+        for (int o = 1; o < LPR; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const bool odd = __any_sync(0xffffffffu, top >= kInf);      // infinities or NaN in one of the warp's rows
+        if (odd) {
+            top = 0u;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                float2 x;
-                x.x = __fdiv_rn(h2f<SRC>(uint16_t(e[j])), s);
-                x.y = __fdiv_rn(h2f<SRC>(uint16_t(e[j] >> 16)), s);
-                const uint32_t two = q8x2_encode<Q8>(x);
-                if (j & 1) c[j >> 1] |= two << 16; else c[j >> 1] = two;
+                const uint32_t lo = e[j] & 0x7fffu, hi = (e[j] >> 16) & 0x7fffu;
+                top = max(top, max(lo < kInf ? lo : 0u, hi < kInf ? hi : 0u));
             }
+#pragma unroll
+            for (int o = 1; o < LPR; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        }
+        const float s = fmaxf(__fdiv_rn(h2f<SRC>(uint16_t(top)), q8_max<Q8>()), 1.17549435e-38f);
+        // rows without a token (all zero here) do not count
+        const bool plain = !odd && __all_sync(0xffffffffu, s >= 8.271806e-25f || top == 0u);
+        uint32_t c[4];
+        if (plain) {
+            const float r = __frcp_rn(s);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float q[4];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    q[2 * i] = quotient(h2f<SRC>(uint16_t(e[2 * j + i])), s, r);
+                    q[2 * i + 1] = quotient(h2f<SRC>(uint16_t(e[2 * j + i] >> 16)), s, r);
+                }
+                if constexpr (Q8 == kI8) {
+                    // |q| rounds to 127 at most; 1.5 2^23 + q rounds q to an integer, half to even
+                    uint32_t n[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) n[i] = __float_as_uint(__fadd_rn(q[i], 12582912.0f));
+                    c[j] = __byte_perm(__byte_perm(n[0], n[1], 0x0040), __byte_perm(n[2], n[3], 0x0040), 0x5410);
+                } else {
+                    c[j] = q8x2_encode<Q8>(make_float2(q[0], q[1])) | (q8x2_encode<Q8>(make_float2(q[2], q[3])) << 16);
+                }
+            }
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < 8; ++j) {
+                uint32_t ej = e[0];
+#pragma unroll
+                for (int i = 1; i < 8; ++i) ej = j == i ? e[i] : ej;
+                float2 x;
+                x.x = __fdiv_rn(h2f<SRC>(uint16_t(ej)), s);
+                x.y = __fdiv_rn(h2f<SRC>(uint16_t(ej >> 16)), s);
+                const uint32_t two = q8x2_encode<Q8>(x) << (16 * (j & 1));
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if ((j >> 1) == i) c[i] = j & 1 ? c[i] | two : two;
+            }
+        }
+        if (live) {
             char *dst = (kv ? p.v_cache : p.k_cache) + blk * p.c_blk + off * p.c_slot + h * p.c_head + sub * p.c_chunk;
             *reinterpret_cast<uint4 *>(dst) = make_uint4(c[0], c[1], c[2], c[3]);
             if (sub == 0) (kv ? p.v_gs : p.k_gs)[blk * p.gs_blk + off * p.gs_slot + h * p.gs_head] = s;

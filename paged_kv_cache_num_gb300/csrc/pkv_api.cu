@@ -707,8 +707,11 @@ int pkv_kv_gather(const pkv_cache *cache, const pkv_tensor *slot_mapping, const 
     p.k_head = k_out->stride[1] * 2;
     p.v_tok = v_out->stride[0] * 2;
     p.v_head = v_out->stride[1] * 2;
-    p.vec16 = aligned(k_out->data, 16) && aligned(v_out->data, 16) && p.k_tok % 16 == 0 && p.k_head % 16 == 0 &&
-              p.v_tok % 16 == 0 && p.v_head % 16 == 0;
+    const uintptr_t outs = reinterpret_cast<uintptr_t>(k_out->data) | reinterpret_cast<uintptr_t>(v_out->data) |
+                           uintptr_t(p.k_tok) | uintptr_t(p.k_head) | uintptr_t(p.v_tok) | uintptr_t(p.v_head);
+    p.align = outs % 32 == 0 ? 32 : outs % 16 == 0 ? 16 : 2;
+    p.word_rows = (reinterpret_cast<uintptr_t>(p.c.k_cache) | reinterpret_cast<uintptr_t>(p.c.v_cache) |
+                   uintptr_t(p.c.c_blk) | uintptr_t(p.c.c_slot) | uintptr_t(p.c.c_head)) % 4 == 0;
     p.err_flag = err_flag;
     return launch_status(pkv::launch_gather(p, ci.kind, k_out->dtype, as_stream(stream)), "kv_gather kernel");
 }

@@ -186,7 +186,8 @@ struct GatherParams {
     char *v_out;
     int64_t k_tok, k_head;      // byte strides
     int64_t v_tok, v_head;
-    int vec16;                  // output rows 16-byte aligned
+    int align;                  // output rows at multiples of this many bytes: 32, 16 or 2
+    int word_rows;              // 3-bit rows at multiples of 4 bytes
     int32_t *err_flag;
 };
 
