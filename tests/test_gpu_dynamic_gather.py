@@ -274,3 +274,41 @@ def test_more_than_32_bits_of_bytes(pkv):
     ko, vo = pkv.kv_gather(cache, slots)
     want = (codes.view(torch.float8_e4m3fn).float() * s[..., None]).bfloat16()
     assert torch.equal(ko.cpu(), want) and torch.equal(vo.cpu(), want)
+
+
+@pytest.mark.parametrize("dtype,bits", [(torch.bfloat16, 8), (torch.float16, 11)])
+@pytest.mark.parametrize("kind", ["e4m3", "e5m2", "i8"])
+def test_dynamic_append_every_quotient(pkv, kind, dtype, bits):
+    """Rows whose largest element has each significand, with every number of
+    the type below it down to 2^-18 of it: the codes are those of the fp32
+    division and the cast (as torch does them on the GPU)."""
+    D, H, BS = 128, 8, 16
+    tops = torch.arange(2 ** (bits - 1), 2 ** bits, device=DEV)
+    if bits == 11:
+        tops = tops[torch.randperm(tops.numel(), generator=torch.Generator(device=DEV).manual_seed(38), device=DEV)[:128]]
+    mant = torch.arange(2 ** (bits - 1), 2 ** bits, device=DEV, dtype=torch.float32)
+    x = torch.cat([mant * 2.0 ** -e for e in range(19)])                    # below 2^bits
+    x = torch.cat([x, -x])
+    x = torch.cat([x, x.new_zeros(-x.numel() % (D - 1))]).view(-1, D - 1)
+    rows = torch.cat([x.new_zeros((x.shape[0], 1)), x], 1)                  # [R, D], the largest goes first
+    all_rows = rows[None].expand(tops.numel(), -1, -1).clone()
+    top = tops.float()[:, None, None]
+    all_rows = torch.where(all_rows.abs() > top, torch.zeros_like(all_rows), all_rows)
+    all_rows[:, :, 0] = top[:, :, 0]
+    flat = (all_rows.view(-1, D) / 64).to(dtype)                            # exact: a power of two
+    n = -(-flat.shape[0] // H) * H
+    flat = torch.cat([flat, flat.new_zeros((n - flat.shape[0], D))])
+    k = flat.view(-1, H, D)
+    T = k.shape[0]
+    cache = pkv.KVCache.allocate(kind, T // BS + 1, BS, H, D, fill=0, scale_mode="token")
+    slots = torch.arange(T, device=DEV)
+    pkv.kv_append_dynamic(k, k, slots, cache)
+    a = k.float().abs().amax(-1)
+    s = (a / torch.full((), R.QMAX[kind], device=DEV)).clamp(min=2.0 ** -126)
+    y = k.float() / s[..., None]
+    want = y.round().clamp(-127, 127).to(torch.int8) if kind == "i8" else \
+        y.clamp(-R.QMAX[kind], R.QMAX[kind]).to(R.CODE[kind]).view(torch.uint8)
+    got = cache.k_cache.view(-1, H, D)[:T]
+    assert torch.equal(got, want)
+    assert torch.equal(cache.v_cache.view(-1, H, D)[:T], want)
+    assert torch.equal(cache.k_scales.reshape(-1, H)[:T], s)
