@@ -75,6 +75,13 @@ template <int CK, int FEED> constexpr int prefill_threads()
 constexpr int kRowTile = 256;   // rows of a row tile, those between a subtile's whole tokens and 128 included
 constexpr int kTileCost = 2;    // beginning and ending a row tile costs as much as this many units
 constexpr int kKeyTile = 128;
+// P is handed to its product after this many keys and after all.  The early
+// hand-over gets the issuing warp past its waits for V and for the
+// accumulators while the other weights are made; the fewer keys go with it, the
+// less the two subtiles' products are cut up in the tensor core's queue (a
+// 12001-token prompt: 833 us with 16, 856 with 32, 921 with 64, 952 with 96,
+// 904 without; a third hand-over in between 914 to 947).
+constexpr int kFirst = 16;
 constexpr int kBins = 1024;
 constexpr uint64_t kPrefillTimeoutNs = 4000000000ull;
 
@@ -321,7 +328,7 @@ struct Bars {
     __device__ __forceinline__ uint32_t s_full(int i) const { return base + 8 * (4 * stages + 2 + i); }
     __device__ __forceinline__ uint32_t p_full(int i) const { return base + 8 * (4 * stages + 4 + i); }
     __device__ __forceinline__ uint32_t o_full(int i) const { return base + 8 * (4 * stages + 6 + i); }
-    __device__ __forceinline__ uint32_t p_most(int i) const { return base + 8 * (4 * stages + 8 + i); }
+    __device__ __forceinline__ uint32_t p_first(int i) const { return base + 8 * (4 * stages + 8 + i); }
     __device__ __forceinline__ uint32_t tail() const { return base + 8 * (4 * stages + 10); }
     // a subtile's rows are finished (their m and l are there), and have been read
     __device__ __forceinline__ uint32_t e_full(int i) const { return base + 8 * (4 * stages + 11 + i); }
@@ -846,7 +853,7 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
     constexpr int kQWarp = TMA ? 11 : 15;                       // by TMA that of V too
     constexpr int kOutWarp = TMA ? 12 : 16;                     // four of them
     constexpr int kProducers = FEED == kFeedCodes ? conv_warps<CK>() : 4;
-    constexpr int CH = TMA ? 32 : 16;                           // columns that a softmax thread reads at a time
+    constexpr int CH = 16;                                      // columns that a softmax thread reads at a time
     using R = Ring<FEED, ST>;
     constexpr bool kVRef = GS;                                  // P relative to the V scales' magnitude
     const DecodeParams &d = p.d;
@@ -876,7 +883,7 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(bars.s_full(i), 1);
             ptx::mbar_init(bars.p_full(i), 4);
-            ptx::mbar_init(bars.p_most(i), 4);
+            ptx::mbar_init(bars.p_first(i), 4);
             ptx::mbar_init(bars.e_full(i), 4);
             ptx::mbar_init(bars.e_empty(i), 4);
             ptx::mbar_init(bars.o_full(i), 1);
@@ -977,7 +984,7 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                         tc::fence_before();
                         __syncwarp();
                         if (lane == 0) {
-                            ptx::mbar_arrive(bars.p_most(sub));
+                            ptx::mbar_arrive(bars.p_first(sub));
                             ptx::mbar_arrive(bars.p_full(sub));
                         }
                         continue;
@@ -1097,11 +1104,11 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                         }
                         // over columns that have been read for the last time
                         tc::tmem_st(ts + CH / 2 * q, pk);
-                        if (CH * (q + 1) == 96 || q == NC - 1) {        // 96 keys, then all
+                        if (CH * (q + 1) == kFirst || q == NC - 1) {    // the first keys, then all
                             tc::tmem_st_wait();
                             tc::fence_before();
                             __syncwarp();
-                            if (lane == 0) ptx::mbar_arrive(q < NC - 1 ? bars.p_most(sub) : bars.p_full(sub));
+                            if (lane == 0) ptx::mbar_arrive(q < NC - 1 ? bars.p_first(sub) : bars.p_full(sub));
                         }
                     }
                     sum[0] = tc::add2(sum[0], sum[1]);
@@ -1272,8 +1279,7 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                         tc::commit(bars.s_full(i));
                     }
                 };
-                // O (+)= P V, the first 96 keys and then the others: the first ones' products
-                // run while the others' weights are made
+                // O (+)= P V, the first keys and then the others
                 auto pv = [&](int from, int to, uint32_t stage, bool acc) {
                     const uint32_t b = v_lo + stage * (L::kTile >> 4);
                     if (leader) {
@@ -1319,10 +1325,10 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                         qk(split ? 0 : i, ks);
                         done(ks, split);
                         if (last) release(bars.q_empty());
-                        ok = there(t, 1, split) && warp_wait(bars.p_most(i), n_p & 1, gone);
+                        ok = there(t, 1, split) && warp_wait(bars.p_first(i), n_p & 1, gone);
                         if (!ok) break;
                         tc::fence_after();
-                        pv(0, 6, vs, j > j0);
+                        pv(0, kFirst / 16, vs, j > j0);
                         // the next tile's K, before the wait that the next scores depend on -- but in a
                         // ring of three, K two tiles on takes this V's place
                         const bool early = !split || FEED == kFeedTma || ST > 3;
@@ -1330,7 +1336,7 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                         ok = ok && warp_wait(bars.p_full(i), n_p & 1, gone);
                         if (!ok) break;
                         tc::fence_after();
-                        pv(6, 8, vs, true);
+                        pv(kFirst / 16, 8, vs, true);
                         done(vs, split);
                         if (last) release(bars.o_full(i));
                         if (!last && !early) ok = there(t + step, 0, split);
