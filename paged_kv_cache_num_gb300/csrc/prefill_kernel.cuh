@@ -82,6 +82,14 @@ constexpr int kKeyTile = 128;
 // 12001-token prompt: 833 us with 16, 856 with 32, 921 with 64, 952 with 96,
 // 904 without; a third hand-over in between 914 to 947).
 constexpr int kFirst = 16;
+// In long segments the two subtiles' softmax take turns: run at the same time
+// they share the exponential unit and then leave it idle together while both
+// wait for products (12001-token prompt: 846 to 972 us without, depending on
+// how the two happen to fall, 845 to 861 us with; e4m3 chunks 667 to 629 us).
+// In short segments the order costs more than it brings (packed prompts 157
+// us without, 177 with), and so it does with scales per row, whose softmax is
+// long enough by itself (3-bit chunks 180 us without, 216 with).
+constexpr int kTurnTiles = 16;
 constexpr int kBins = 1024;
 constexpr uint64_t kPrefillTimeoutNs = 4000000000ull;
 
@@ -291,7 +299,7 @@ struct Smem {
     static constexpr int state = cols + kColSlots * kColBytes;  // (m, l) of a row tile's rows: [subtile][2][128]
     static constexpr int q_scale = state + 2048;                // per row of subtile 0
     static constexpr int bars = q_scale + 512;
-    static constexpr int n_bars = 4 * kStages + 2 * kRaw + 2 + 4 * 2 + 1 + 4 + 1;
+    static constexpr int n_bars = 4 * kStages + 2 * kRaw + 2 + 4 * 2 + 1 + 4 + 1 + 2;
     static constexpr int info = bars + 8 * n_bars;              // per raw stage: which blocks are there
     static constexpr int misc = (info + 4 * 8 + 15) / 16 * 16;
     static constexpr int total = misc + 128;
@@ -335,8 +343,10 @@ struct Bars {
     __device__ __forceinline__ uint32_t e_empty(int i) const { return base + 8 * (4 * stages + 13 + i); }
     // bf16 Q that is to become f16
     __device__ __forceinline__ uint32_t q_raw() const { return base + 8 * (4 * stages + 15); }
-    __device__ __forceinline__ uint32_t raw_full(int s) const { return base + 8 * (4 * stages + 16 + s); }
-    __device__ __forceinline__ uint32_t raw_empty(int s) const { return base + 8 * (4 * stages + 16 + raws + s); }
+    // subtile i is through a tile's softmax (long segments of two subtiles)
+    __device__ __forceinline__ uint32_t turn(int i) const { return base + 8 * (4 * stages + 16 + i); }
+    __device__ __forceinline__ uint32_t raw_full(int s) const { return base + 8 * (4 * stages + 18 + s); }
+    __device__ __forceinline__ uint32_t raw_empty(int s) const { return base + 8 * (4 * stages + 18 + raws + s); }
 };
 
 // Wait for a phase, giving up when it takes too long or another warp gave up.
@@ -884,6 +894,7 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
             ptx::mbar_init(bars.s_full(i), 1);
             ptx::mbar_init(bars.p_full(i), 4);
             ptx::mbar_init(bars.p_first(i), 4);
+            ptx::mbar_init(bars.turn(i), 4);
             ptx::mbar_init(bars.e_full(i), 4);
             ptx::mbar_init(bars.e_empty(i), 4);
             ptx::mbar_init(bars.o_full(i), 1);
@@ -909,6 +920,7 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
         const uint32_t ts = tmem + lanes + sub * 128, to = tmem + lanes + 256 + sub * 128;
         float *state = reinterpret_cast<float *>(sm + L::state) + sub * 256 + row;
         float *q_scale = reinterpret_cast<float *>(sm + L::q_scale) + row;
+        uint32_t turns = 0;                                     // tiles taken in turn
         uint32_t tile_n = 0, mine_n = 0, item = 0, outs = 0;    // key tiles of the CTA, of this warpgroup; segments, and
                                                                 // those that use this warpgroup's accumulators
         if (work) {
@@ -970,6 +982,7 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                 const float ninf = -__int_as_float(0x7f800000);
                 float m = ninf, l = 0.0f, vexp = -1000.0f;
                 const int step = split ? 2 : 1, j0 = split ? sub : 0;
+                const bool in_turn = !GS && !split && nk >= kTurnTiles;
                 for (int j = j0; j < nk; j += step, ++mine_n) {
                     ok = warp_wait(bars.s_full(sub), mine_n & 1, gone);
                     if (!ok) break;
@@ -980,12 +993,18 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                         if (!ok) break;
                         tc::fence_after();
                     }
+                    if (in_turn) {
+                        if (sub == 1 || turns > 0) ok = warp_wait(bars.turn(1 - sub), (turns + sub - 1) & 1, gone);
+                        ++turns;
+                        if (!ok) break;
+                    }
                     if (idle) {                                 // no row of the warp is there
                         tc::fence_before();
                         __syncwarp();
                         if (lane == 0) {
                             ptx::mbar_arrive(bars.p_first(sub));
                             ptx::mbar_arrive(bars.p_full(sub));
+                            if (in_turn) ptx::mbar_arrive(bars.turn(sub));
                         }
                         continue;
                     }
@@ -1102,6 +1121,7 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                             pk[i >> 1] = tc::pack16<OK>(e0.x, e0.y);
                             pk[(i >> 1) + 1] = tc::pack16<OK>(e1.x, e1.y);
                         }
+                        if (in_turn && q == NC - 2 && lane == 0) ptx::mbar_arrive(bars.turn(sub));
                         // over columns that have been read for the last time
                         tc::tmem_st(ts + CH / 2 * q, pk);
                         if (CH * (q + 1) == kFirst || q == NC - 1) {    // the first keys, then all

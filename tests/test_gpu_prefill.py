@@ -342,6 +342,80 @@ def test_other_stream(pkv):
         assert torch.equal(o, out)
 
 
+def test_thousands_of_sequences(pkv):
+    """More sequences than the kernel counts one by one."""
+    g = torch.Generator().manual_seed(31)
+    new = torch.randint(0, 3, (2500,), generator=g).tolist()
+    ctx = [n + int(torch.randint(0, 20, (1,), generator=g)) for n in new]
+    case(pkv, "bf16", "bf16", new=new, ctx=ctx, H=1, G=1, D=64, BS=8, seed=31)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_row_tiles_of_every_size(pkv, kind):
+    """Runs of row tiles with one and two subtiles and key tiles odd and even
+    in number, many per CTA, in one call and again."""
+    new = [129, 1, 260, 33, 64, 1, 300, 140, 5, 513, 100, 31] * 6
+    g = torch.Generator().manual_seed(32)
+    ctx = [n + int(torch.randint(0, 700, (1,), generator=g)) for n in new]
+    args, out, scale = case(pkv, kind, "bf16", new=new, ctx=ctx, H=2, G=2, seed=32)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for _ in range(20):
+        assert torch.equal(pkv.paged_prefill(*args, sm_scale=scale, err_flag=err), out)
+    assert int(err.item()) == 0
+
+
+def test_two_streams_at_once(pkv):
+    """Calls on two streams, each with a workspace of its own."""
+    a, out_a, scale = case(pkv, "bf16", "bf16", new=[300, 40], ctx=[300, 1000], H=2, G=4, seed=33)
+    b, out_b, _ = case(pkv, "e4m3", "bf16", new=[200, 7], ctx=[900, 1000], H=2, G=4, seed=34)
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = [(pkv.paged_prefill(*a, sm_scale=scale, stream=s), pkv.paged_prefill(*b, sm_scale=scale, stream=t))
+           for _ in range(8)]
+    torch.cuda.synchronize()
+    for x, y in got:
+        assert torch.equal(x, out_a) and torch.equal(y, out_b)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_packed_rows_off_the_word(pkv, D):
+    """3-bit rows at odd byte strides (no tensor map, no 4-byte loads)."""
+    BS, H, G, ctx, new = 16, 2, 3, [70, 200], [70, 9]
+    bt, P = R.tables(ctx, BS, seed=35)
+    cache, kv, vv = R.make_cache(pkv, "u3", P, BS, H, D, seed=35)
+    row = 3 * D // 8
+    halves = []
+    for t in (cache.k_cache, cache.v_cache):
+        wide = torch.zeros((P, (BS * H * (row + 1) + 15) // 16 * 16), dtype=torch.uint8, device=DEV)
+        view = wide.as_strided((P, BS, H, row), (wide.stride(0), H * (row + 1), row + 1, 1))
+        view.copy_(t)
+        halves.append(view)
+    odd = pkv.KVCache("u3", *halves, k_qscale=cache.k_qscale, k_qzero=cache.k_qzero, v_qscale=cache.v_qscale,
+                      v_qzero=cache.v_qzero)
+    q = torch.randn((79, H * G, D), generator=torch.Generator().manual_seed(36)).bfloat16()
+    st = starts_of(new)
+    dev = [torch.tensor(x, dtype=torch.int32, device=DEV) for x in (st, ctx)]
+    out = pkv.paged_prefill(q.to(DEV), odd, bt.to(DEV), *dev)
+    check(out, R.prefill(q, kv, vv, bt, st, ctx, D ** -0.5), torch.bfloat16, D, float(vv.abs().max()))
+    slots = torch.arange(P * BS, device=DEV)
+    for x, y in zip(pkv.kv_gather(odd, slots), pkv.kv_gather(cache, slots)):
+        assert torch.equal(x, y)
+
+
+def test_no_blocks_and_no_table(pkv):
+    """An empty pool, or a block table without columns: nothing to see."""
+    q = torch.randn((5, 4, 64), generator=torch.Generator().manual_seed(37)).half().to(DEV)
+    st = torch.tensor([0, 5], dtype=torch.int32, device=DEV)
+    k = torch.zeros((0, 16, 2, 64), dtype=torch.float16, device=DEV)
+    for cache, cols, ctx, flag in ((pkv.KVCache("f16", k, k), 2, 20, pkv.pkv.DEVERR_BLOCK_RANGE),
+                                   (pkv.KVCache.allocate("f16", 3, 16, 2, 64, fill=255), 0, 0, 0),
+                                   (pkv.KVCache.allocate("f16", 3, 16, 2, 64, fill=255), 0, 7, pkv.pkv.DEVERR_CONTEXT_RANGE)):
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        out = pkv.paged_prefill(q, cache, torch.zeros((1, cols), dtype=torch.int32, device=DEV), st,
+                                torch.tensor([ctx], dtype=torch.int32, device=DEV), err_flag=err)
+        assert int(err.item()) == flag and (out == 0).all()
+
+
 def test_far_blocks(pkv):
     """Blocks beyond 2^32 bytes into the pool."""
     BS, H, D, G = 16, 8, 128, 1
