@@ -316,8 +316,12 @@ int pkv_kv_gather(const pkv_cache *cache, const pkv_tensor *slot_mapping, const 
  *   hold.  Supported: every cache dtype, layout and scale granularity;
  *   head_dim 64 or 128; block_size a power of two from 8 to 256; num_heads a
  *   multiple of num_kv_heads; num_tokens * (num_heads / num_kv_heads) <
- *   2^30; batch < 2^20.  Dequantised F16 / BF16 products take the codes
- *   exactly; scales are applied in fp32.
+ *   2^30; batch < 2^20.  The products take F16 / BF16 rows
+ *   as they are and codes exactly as F16; BF16 queries of a coded cache
+ *   become F16 by a power of two per row (exactly but for elements below
+ *   2^-31 of the row's largest, which are off by at most 2^-39 of it);
+ *   scales are applied in fp32, and the weights are rounded once to the
+ *   product's type.
  *   Bad data never faults: a block id outside [0, num_blocks) is left out
  *   (PKV_DEVERR_BLOCK_RANGE); a context length below 0 counts as 0 and one
  *   above the table's capacity as that capacity
