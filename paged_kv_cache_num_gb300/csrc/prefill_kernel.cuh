@@ -25,22 +25,27 @@
 // CTA.  Two softmax warpgroups (one per subtile, a thread per row), a warp per
 // subtile that issues its products (tcgen05.mma, accumulators and P in tensor
 // memory), a warpgroup that writes finished accumulators out while the next
-// row tile is under way, a warp that loads Q, and the K/V producers.  While one subtile's
-// softmax runs the tensor core works on the other's products: a subtile's
-// scores wait for its last P V (they share tensor memory), which waits for its
-// softmax, so that chain bounds the tile rate.  A row tile of at most 128 rows
-// has one subtile: then the warpgroups take its key tiles in turn, with states
-// of their own that are joined at the end.
+// row tile is under way, a warp that loads Q, and the K/V producers.  While
+// one subtile's softmax runs the tensor core works on the other's products: a
+// subtile's scores wait for its last P V (they share tensor memory), which
+// waits for its softmax, so that chain bounds the tile rate (about 3400 clocks
+// per pair of subtiles, whose products alone take 2048; 12001-token prompt, 32
+// q over 8 kv heads: 0.88 to 0.90 ms, 1310 to 1340 TFLOP/s, 0.69 of the
+// measured cuBLAS rate).  A row tile of at most 128 rows has one subtile: then
+// the warpgroups take its key tiles in turn, with states of their own that are
+// joined at the end; few rows over long contexts run at HBM's rate that way.
 //
 // K/V.  16-bit caches in the flash layout: one warp issues TMA copies of
 // whole block pieces into the operand ring; x-vectorised 16-bit caches: four
 // warps copy 16-byte pieces.  One-byte and 3-bit caches: one warp issues TMA
-// copies of the raw codes, four warps convert them into the operand ring.
+// copies of the raw codes, four (3-bit: eight) warps convert them into the
+// operand ring.  (3-bit rows at head_dim 64 are 24 bytes, which no tensor map
+// takes: that warp loads them.)
 // Codes become f16 exactly (every code of every kind is an f16 number); their
 // scales are applied in fp32: per-head scales to c and to the result, per-row
 // scales to the columns of S and of P.  bf16 queries of such caches are
 // brought to f16 by a power of two per row, exactly but for elements below
-// 2^-39 of the row's largest.
+// 2^-31 of the row's largest, which are rounded to multiples of 2^-38 of it.
 #pragma once
 
 #include <type_traits>
@@ -73,7 +78,10 @@ template <int CK, int FEED> constexpr int prefill_threads()
 }
 
 constexpr int kRowTile = 256;   // rows of a row tile, those between a subtile's whole tokens and 128 included
-constexpr int kTileCost = 2;    // beginning and ending a row tile costs as much as this many units
+// Beginning and ending a row tile costs as much as this many units.  (16 prompts
+// of 60 to 1500 tokens: 155, 156, 162, 167 us with 1, 2, 3, 4; few tokens over
+// long contexts: 70, 67, 66, 65 us.)
+constexpr int kTileCost = 2;
 constexpr int kKeyTile = 128;
 // P is handed to its product after this many keys and after all.  The early
 // hand-over gets the issuing warp past its waits for V and for the
@@ -311,12 +319,13 @@ struct Smem {
 };
 
 // Column data of a key tile: scales of its 128 K and V rows, the largest V
-// scale of each producer warp's rows, and which groups of 8 rows are there.  Tile T's is
-// written once the ring has room for K of tile T.  With a ring of R tiles of K
-// that is when the scores of tile T - R are done; the tiles whose softmax may
-// still be under way then are fewer than 2 R + 2 (each subtile has one, at most
-// a tile's worth of the ring behind the other), and with three (six) stages,
-// where V of tile T - 2 (T - 4) is done too, fewer than 3 (5).
+// scale of each producer warp's rows, and which groups of 8 rows are there.
+// Tile T's is written once the ring has room for K of tile T.  With a ring of
+// R tiles of K that is when the scores of tile T - R are done; the tiles whose
+// softmax may still be under way then are fewer than 2 R + 2 (each subtile has
+// one, at most a tile's worth of the ring behind the other), and with three
+// (six) stages, where V of tile T - 2 (T - 4) is done too, fewer than 3 (5).
+// So 16-bit caches have 8 (head_dim 64: 16) slots, coded ones 4 (8).
 struct ColSlot {
     float k[kKeyTile];
     float v[kKeyTile];
@@ -654,21 +663,56 @@ __device__ __forceinline__ void raw_codes(const PrefillParams &p, const PrefillF
             } else {
                 const char *cache = kv ? d.v_cache : d.k_cache;
                 unsigned char *to = sm + L::raw + s * L::kRawTile;
-                for (int i = 0; i < kKeyTile; ++i) {
-                    const int b = __shfl_sync(0xffffffffu, now, i >> shift);
-                    const int o = __shfl_sync(0xffffffffu, slot0, i >> shift) + (i & (rows - 1));
-                    if (!((got >> (i >> shift)) & 1u)) continue;
-                    const char *src = cache + b * d.c_blk + o * d.c_slot + h * d.c_head;
-                    for (int j = lane * f.raw_unit; j < RB; j += 32 * f.raw_unit) {
-                        const bool xv = d.c_chunk != 16 && CK != kU3;
-                        const char *from = xv ? src + (j >> 4) * d.c_chunk + (j & 15) : src + j;
-                        unsigned char *at = to + (i >> shift) * rows * RB +
-                                            (xv ? (j >> 4) * rows * 16 + (i & (rows - 1)) * 16 + (j & 15)
-                                                : (i & (rows - 1)) * RB + j);
-                        if (f.raw_unit == 4)
-                            *reinterpret_cast<uint32_t *>(at) = __ldg(reinterpret_cast<const uint32_t *>(from));
-                        else
-                            *at = __ldg(reinterpret_cast<const unsigned char *>(from));
+                if constexpr (RB == 24) {
+                    // a lane takes rows, a row's six words in flight together
+                    // (a row at a time as below: 3327 us where this takes 243)
+#pragma unroll 1
+                    for (int i = lane; i < kKeyTile; i += 32) {
+                        const int in_blk = i & (rows - 1);
+                        const int b = __shfl_sync(0xffffffffu, now, i >> shift);
+                        const int o = __shfl_sync(0xffffffffu, slot0, i >> shift) + in_blk;
+                        if ((got >> (i >> shift)) & 1u) {
+                            const char *src = cache + b * d.c_blk + o * d.c_slot + h * d.c_head;
+                            unsigned char *at = to + i * RB;
+                            uint32_t x[6];
+#pragma unroll
+                            for (int j = 0; j < 6; ++j) {
+                                if (f.raw_unit == 4) {
+                                    x[j] = __ldg(reinterpret_cast<const uint32_t *>(src) + j);
+                                } else {
+                                    x[j] = 0;
+#pragma unroll 1
+                                    for (int k = 0; k < 4; ++k)
+                                        x[j] |= uint32_t(__ldg(reinterpret_cast<const unsigned char *>(src) + 4 * j + k))
+                                                << (8 * k);
+                                }
+                            }
+#pragma unroll
+                            for (int j = 0; j < 6; ++j) reinterpret_cast<uint32_t *>(at)[j] = x[j];
+                        }
+                        __syncwarp();
+                    }
+                } else {
+                    // Strides or a base that no tensor map takes: rare, so a short
+                    // loop, since this code shares the instruction cache with the
+                    // softmax (rows in flight as above: e4m3 chunks that never come
+                    // here 615 -> 640 us, unrolled 702).
+                    for (int i = 0; i < kKeyTile; ++i) {
+                        const int b = __shfl_sync(0xffffffffu, now, i >> shift);
+                        const int o = __shfl_sync(0xffffffffu, slot0, i >> shift) + (i & (rows - 1));
+                        if (!((got >> (i >> shift)) & 1u)) continue;
+                        const char *src = cache + b * d.c_blk + o * d.c_slot + h * d.c_head;
+                        for (int j = lane * f.raw_unit; j < RB; j += 32 * f.raw_unit) {
+                            const bool xv = d.c_chunk != 16 && CK != kU3;
+                            const char *from = xv ? src + (j >> 4) * d.c_chunk + (j & 15) : src + j;
+                            unsigned char *at = to + (i >> shift) * rows * RB +
+                                                (xv ? (j >> 4) * rows * 16 + (i & (rows - 1)) * 16 + (j & 15)
+                                                    : (i & (rows - 1)) * RB + j);
+                            if (f.raw_unit == 4)
+                                *reinterpret_cast<uint32_t *>(at) = __ldg(reinterpret_cast<const uint32_t *>(from));
+                            else
+                                *at = __ldg(reinterpret_cast<const unsigned char *>(from));
+                        }
                     }
                 }
                 __syncwarp();
