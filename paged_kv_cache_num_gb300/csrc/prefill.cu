@@ -132,8 +132,8 @@ cudaError_t launch_prefill(const PrefillParams &p, const PrefillPlan &pl, int ca
     // or by a warp that copies it
     a.flip_q = d.scale_log2 < 0.0f && coded && d.q_is_bf16;
     a.q_tma = (d.scale_log2 >= 0.0f || a.flip_q) && q_map(&a.tmq, p);
-    a.raw_unit = (reinterpret_cast<uintptr_t>(d.k_cache) | reinterpret_cast<uintptr_t>(d.v_cache) | uintptr_t(d.c_blk) |
-                  uintptr_t(d.c_slot) | uintptr_t(d.c_head)) % 4 == 0 ? 4 : 1;
+    const uintptr_t at = uintptr_t(d.c_slot) | uintptr_t(d.c_head);        // blocks lie on multiples of 16 bytes
+    a.raw_unit = at % 8 == 0 ? 8 : at % 4 == 0 ? 4 : 1;
     switch (cache_kind) {
     case kF16:
     case kBF16: return launch_prefill_16(a);

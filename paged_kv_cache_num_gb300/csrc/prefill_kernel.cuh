@@ -63,7 +63,7 @@ struct PrefillFast {
     int q_tma;                  // Q by TMA
     int flip_q;                 // a negative scale's sign is still to be given to Q
     int raw_tma;                // raw codes by TMA (else by loads of the producer warp)
-    int raw_unit;               // ... of 4 bytes or 1
+    int raw_unit;               // ... 3-bit rows in pieces of 8 bytes, 4 or 1
 };
 
 namespace {
@@ -547,8 +547,8 @@ __device__ __forceinline__ int4 split_end(const Walk &w, const Start &st, bool d
 
 // 16-bit rows by 16-byte copies, rows 32 lw .. 32 lw + 31 of every tile by
 // one warp: a lane copies its row's pieces (neighbouring slots are neighbours
-// in the x-vectorised layout).  A stage is handed over once the next one's
-// copies are under way.
+// in the x-vectorised layout).  A stage is handed over once the third behind it
+// is under way, or as soon as there is no room to go on.
 template <int CK, int D>
 __device__ __forceinline__ void copy_rows(const PrefillParams &p, const Start &st, uint32_t ring, ColSlot *cols,
                                           const Bars &bars, volatile int *gone, int lw, int lane)
@@ -560,34 +560,44 @@ __device__ __forceinline__ void copy_rows(const PrefillParams &p, const Start &s
     TileWalk tw{walk_from(p, st), 0};
     tw.k = tw.w.k0;
     uint32_t pos = 0, tile_n = 0;
-    uint32_t pending = 0;                                       // barrier of the stage in hand
-    auto flush = [&](bool all) {
-        if (pending == 0) return;
-        if (all) tc::cp_async_wait<0>(); else tc::cp_async_wait<1>();
+    uint32_t p0 = 0, p1 = 0, p2 = 0;                            // barriers of the stages in hand, the oldest first
+    auto arrive = [&]() {                                       // the oldest is there
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(pending);
-        pending = 0;
+        if (lane == 0) ptx::mbar_arrive(p0);
+        p0 = p1;
+        p1 = p2;
+        p2 = 0;
     };
-    do {
+    auto flush = [&]() {
+        if (p2 != 0) { tc::cp_async_wait<2>(); arrive(); }
+        if (p1 != 0) { tc::cp_async_wait<1>(); arrive(); }
+        if (p0 != 0) { tc::cp_async_wait<0>(); arrive(); }
+    };
+    auto lookup = [&]() -> int {                                // this row's block of the tile, -1 where it wants none
         const int t = tw.k * kKeyTile + row;
-        bool in = t < tw.w.reach();
-        int64_t blk = 0;
-        if (in) {
-            blk = d.block_tables[tw.w.b * d.bt_b + int64_t(t >> d.block_shift) * d.bt_j];
-            if (blk < 0 || blk >= d.num_blocks) {
-                raise_err(d.err_flag, PKV_DEVERR_BLOCK_RANGE);
-                in = false;
-            }
-        }
-        const int64_t at = in ? blk * d.c_blk + int64_t(t & (d.block_size - 1)) * d.c_slot + tw.w.h * d.c_head : 0;
+        return t < tw.w.reach() ? d.block_tables[tw.w.b * d.bt_b + int64_t(t >> d.block_shift) * d.bt_j] : -1;
+    };
+    int next_blk = lookup();
+    bool more = true;
+    while (more) {
+        const int t = tw.k * kKeyTile + row, h = tw.w.h;
+        const bool want = t < tw.w.reach();
+        const int64_t blk = next_blk;
+        const bool in = want && blk >= 0 && blk < d.num_blocks;
+        if (want && !in) raise_err(d.err_flag, PKV_DEVERR_BLOCK_RANGE);
+        const int64_t at = in ? blk * d.c_blk + int64_t(t & (d.block_size - 1)) * d.c_slot + h * d.c_head : 0;
         const unsigned got = __ballot_sync(0xffffffffu, in);
         const int set = tw.w.set(p, tw.k);
+        more = tw.next(p);
+        if (more) next_blk = lookup();                          // a tile ahead
         for (int kv = 0; kv < 2; ++kv, ++pos) {
             // never wait for room with a stage in hand
-            if (!__all_sync(0xffffffffu, pos < ST || ptx::mbar_try_wait(bars.empty(pos % ST), (pos / ST - 1) & 1)))
-                flush(true);
-            if (pos >= ST && !warp_wait(bars.empty(pos % ST), (pos / ST - 1) & 1, gone)) return;
+            if (pos >= ST && p0 != 0 && !warp_test(bars.empty(pos % ST), (pos / ST - 1) & 1)) flush();
+            if (pos >= ST && !warp_wait(bars.empty(pos % ST), (pos / ST - 1) & 1, gone)) {
+                tc::cp_async_wait<0>();
+                return;
+            }
             if (kv == 0 && lane == 0) {
                 uint32_t there = 0;
 #pragma unroll
@@ -599,18 +609,24 @@ __device__ __forceinline__ void copy_rows(const PrefillParams &p, const Start &s
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) tc::cp_async16(dst + piece_at(row, c), src + (in ? c * d.c_chunk : 0), in);
             tc::cp_async_commit();
-            flush(false);
-            pending = bars.full(set, pos % ST);
+            const uint32_t bar = bars.full(set, pos % ST);
+            if (p2 != 0) {
+                tc::cp_async_wait<3>();
+                arrive();
+                p2 = bar;
+            } else {
+                (p0 == 0 ? p0 : p1 == 0 ? p1 : p2) = bar;
+            }
         }
         ++tile_n;
-    } while (tw.next(p));
-    flush(true);
+    }
+    flush();
 }
 
 // Raw codes of every tile into the raw ring, by one warp: one TMA copy per
 // block, [rows][row bytes], or [16-byte piece][rows][16] of an x-vectorised
-// cache; or by loads where no tensor map can be made.
-template <int CK, int D>
+// cache; or by copies of 16 bytes or less where no tensor map can be made.
+template <int CK, int D, bool TMA>
 __device__ __forceinline__ void raw_codes(const PrefillParams &p, const PrefillFast &f, const Start &st, unsigned char *sm,
                                           uint32_t sm32, const Bars &bars, const CUtensorMap *tmk, const CUtensorMap *tmv,
                                           volatile int *gone, int lane)
@@ -622,7 +638,7 @@ __device__ __forceinline__ void raw_codes(const PrefillParams &p, const PrefillF
     uint32_t *info = reinterpret_cast<uint32_t *>(sm + L::info);
     TileWalk tw{walk_from(p, st), 0};
     tw.k = tw.w.k0;
-    if (lane == 0) {
+    if (TMA && lane == 0) {
         ptx::prefetch_tmap(tmk);
         ptx::prefetch_tmap(tmv);
     }
@@ -632,7 +648,13 @@ __device__ __forceinline__ void raw_codes(const PrefillParams &p, const PrefillF
         return lane < nblk && t < tw.w.reach()
                    ? d.block_tables[tw.w.b * d.bt_b + int64_t(t >> d.block_shift) * d.bt_j] : -1;
     };
-    uint32_t pos = 0;
+    uint32_t pos = 0, pending = 0;                              // barrier of a stage that loads are still filling
+    auto flush = [&]() {
+        tc::cp_async_wait<0>();
+        __syncwarp();
+        if (lane == 0 && pending != 0) ptx::mbar_arrive(pending);
+        pending = 0;
+    };
     int blk = lookup();
     bool more = true;
     while (more) {
@@ -647,10 +669,16 @@ __device__ __forceinline__ void raw_codes(const PrefillParams &p, const PrefillF
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv, ++pos) {
             const uint32_t s = pos % L::kRaw;
-            if (pos >= L::kRaw && !warp_wait(bars.raw_empty(s), (pos / L::kRaw - 1) & 1, gone)) return;
+            if (pos >= L::kRaw) {                               // never wait for room with a stage in hand
+                if (!TMA && pending != 0 && !warp_test(bars.raw_empty(s), (pos / L::kRaw - 1) & 1)) flush();
+                if (!warp_wait(bars.raw_empty(s), (pos / L::kRaw - 1) & 1, gone)) {
+                    tc::cp_async_wait<0>();
+                    return;
+                }
+            }
             if (lane == 0) info[s] = got;
             const uint32_t dst = sm32 + L::raw + s * L::kRawTile;
-            if (f.raw_tma) {
+            if constexpr (TMA) {
                 if (lane == 0) ptx::mbar_arrive_expect_tx(bars.raw_full(s), uint32_t(__popc(got) * rows * RB));
                 __syncwarp();
                 if (in) {
@@ -661,65 +689,50 @@ __device__ __forceinline__ void raw_codes(const PrefillParams &p, const PrefillF
                         ptx::tma_load_5d(dst + lane * rows * RB, m, bars.raw_full(s), 0, slot0, 0, h, now);
                 }
             } else {
+                // a lane takes rows; one stage is filled while the one before
+                // arrives.  Short loops: this code shares the instruction cache
+                // with the softmax (unrolled: e4m3 chunks that never come here
+                // 615 -> 702 us).
                 const char *cache = kv ? d.v_cache : d.k_cache;
-                unsigned char *to = sm + L::raw + s * L::kRawTile;
-                if constexpr (RB == 24) {
-                    // a lane takes rows, a row's six words in flight together
-                    // (a row at a time as below: 3327 us where this takes 243)
+                const bool xv = d.c_chunk != 16 && CK != kU3;
 #pragma unroll 1
-                    for (int i = lane; i < kKeyTile; i += 32) {
-                        const int in_blk = i & (rows - 1);
-                        const int b = __shfl_sync(0xffffffffu, now, i >> shift);
-                        const int o = __shfl_sync(0xffffffffu, slot0, i >> shift) + in_blk;
-                        if ((got >> (i >> shift)) & 1u) {
-                            const char *src = cache + b * d.c_blk + o * d.c_slot + h * d.c_head;
-                            unsigned char *at = to + i * RB;
-                            uint32_t x[6];
-#pragma unroll
-                            for (int j = 0; j < 6; ++j) {
-                                if (f.raw_unit == 4) {
-                                    x[j] = __ldg(reinterpret_cast<const uint32_t *>(src) + j);
-                                } else {
-                                    x[j] = 0;
-#pragma unroll 1
-                                    for (int k = 0; k < 4; ++k)
-                                        x[j] |= uint32_t(__ldg(reinterpret_cast<const unsigned char *>(src) + 4 * j + k))
-                                                << (8 * k);
-                                }
-                            }
-#pragma unroll
-                            for (int j = 0; j < 6; ++j) reinterpret_cast<uint32_t *>(at)[j] = x[j];
-                        }
-                        __syncwarp();
-                    }
-                } else {
-                    // Strides or a base that no tensor map takes: rare, so a short
-                    // loop, since this code shares the instruction cache with the
-                    // softmax (rows in flight as above: e4m3 chunks that never come
-                    // here 615 -> 640 us, unrolled 702).
-                    for (int i = 0; i < kKeyTile; ++i) {
-                        const int b = __shfl_sync(0xffffffffu, now, i >> shift);
-                        const int o = __shfl_sync(0xffffffffu, slot0, i >> shift) + (i & (rows - 1));
-                        if (!((got >> (i >> shift)) & 1u)) continue;
+                for (int i = lane; i < kKeyTile; i += 32) {
+                    const int in_blk = i & (rows - 1);
+                    const int b = __shfl_sync(0xffffffffu, now, i >> shift);
+                    const int o = __shfl_sync(0xffffffffu, slot0, i >> shift) + in_blk;
+                    if ((got >> (i >> shift)) & 1u) {
                         const char *src = cache + b * d.c_blk + o * d.c_slot + h * d.c_head;
-                        for (int j = lane * f.raw_unit; j < RB; j += 32 * f.raw_unit) {
-                            const bool xv = d.c_chunk != 16 && CK != kU3;
-                            const char *from = xv ? src + (j >> 4) * d.c_chunk + (j & 15) : src + j;
-                            unsigned char *at = to + (i >> shift) * rows * RB +
-                                                (xv ? (j >> 4) * rows * 16 + (i & (rows - 1)) * 16 + (j & 15)
-                                                    : (i & (rows - 1)) * RB + j);
-                            if (f.raw_unit == 4)
-                                *reinterpret_cast<uint32_t *>(at) = __ldg(reinterpret_cast<const uint32_t *>(from));
-                            else
-                                *at = __ldg(reinterpret_cast<const unsigned char *>(from));
+                        const uint32_t at = dst + (i >> shift) * rows * RB + in_blk * (xv ? 16 : RB);
+                        if constexpr (CK != kU3) {
+#pragma unroll 1
+                            for (int j = 0; j < RB / 16; ++j)
+                                tc::cp_async16(at + j * (xv ? rows * 16 : 16), src + j * d.c_chunk, true);
+                        } else if (f.raw_unit == 8) {
+#pragma unroll 1
+                            for (int j = 0; j < RB; j += 8) tc::cp_async_small<8>(at + j, src + j);
+                        } else if (f.raw_unit == 4) {
+#pragma unroll 1
+                            for (int j = 0; j < RB; j += 4) tc::cp_async_small<4>(at + j, src + j);
+                        } else {
+                            unsigned char *to = sm + (at - sm32);
+#pragma unroll 1
+                            for (int j = 0; j < RB; ++j)
+                                to[j] = __ldg(reinterpret_cast<const unsigned char *>(src) + j);
                         }
                     }
+                    __syncwarp();
                 }
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bars.raw_full(s));
+                tc::cp_async_commit();
+                if (pending != 0) {
+                    tc::cp_async_wait<1>();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(pending);
+                }
+                pending = bars.raw_full(s);
             }
         }
     }
+    if constexpr (!TMA) flush();
 }
 
 // Raw codes -> operand ring, 128 / conv_warps rows of every tile by one warp
@@ -1515,7 +1528,11 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
             }
         } else if (FEED == kFeedCodes && warp == 14) {
             if constexpr (FEED == kFeedCodes) {
-                if (work) raw_codes<CK, D>(p, f, st, sm, sm32, bars, &tmk, &tmv, gone, lane);
+                constexpr bool kCanMap = raw_row<CK, D>() % 16 == 0;
+                if (work && kCanMap && f.raw_tma)
+                    raw_codes<CK, D, kCanMap>(p, f, st, sm, sm32, bars, &tmk, &tmv, gone, lane);
+                else if (work)
+                    raw_codes<CK, D, false>(p, f, st, sm, sm32, bars, &tmk, &tmv, gone, lane);
             }
         }
     }

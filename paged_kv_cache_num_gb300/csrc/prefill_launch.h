@@ -12,7 +12,7 @@ struct PrefillLaunch {
     int grid;
     bool join;                  // launch the join kernel too
     bool tma;                   // K/V, or their raw codes, by TMA (tmk, tmv)
-    int raw_unit;               // else raw codes by loads of 4 bytes or 1
+    int raw_unit;               // else raw codes by copies; 3-bit rows in pieces of 8 bytes, 4 or 1
     int out32;                  // output rows at multiples of 32 bytes
     void *desc, *part_ml, *part_acc;
     bool q_tma;                 // Q by TMA (tmq)
