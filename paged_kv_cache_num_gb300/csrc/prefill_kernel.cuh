@@ -547,7 +547,7 @@ __device__ __forceinline__ int4 split_end(const Walk &w, const Start &st, bool d
 
 // 16-bit rows by 16-byte copies, rows 32 lw .. 32 lw + 31 of every tile by
 // one warp: a lane copies its row's pieces (neighbouring slots are neighbours
-// in the x-vectorised layout).  A stage is handed over once the third behind it
+// in the x-vectorised layout).  A stage is handed over once the second behind it
 // is under way, or as soon as there is no room to go on.
 template <int CK, int D>
 __device__ __forceinline__ void copy_rows(const PrefillParams &p, const Start &st, uint32_t ring, ColSlot *cols,
@@ -561,18 +561,14 @@ __device__ __forceinline__ void copy_rows(const PrefillParams &p, const Start &s
     tw.k = tw.w.k0;
     uint32_t pos = 0, tile_n = 0;
     uint32_t p0 = 0, p1 = 0, p2 = 0;                            // barriers of the stages in hand, the oldest first
-    auto arrive = [&]() {                                       // the oldest is there
+    auto hand_over = [&]() {                                    // the oldest, once it is there
+        if (p2 != 0) tc::cp_async_wait<2>(); else if (p1 != 0) tc::cp_async_wait<1>(); else tc::cp_async_wait<0>();
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(p0);
         p0 = p1;
         p1 = p2;
         p2 = 0;
-    };
-    auto flush = [&]() {
-        if (p2 != 0) { tc::cp_async_wait<2>(); arrive(); }
-        if (p1 != 0) { tc::cp_async_wait<1>(); arrive(); }
-        if (p0 != 0) { tc::cp_async_wait<0>(); arrive(); }
     };
     auto lookup = [&]() -> int {                                // this row's block of the tile, -1 where it wants none
         const int t = tw.k * kKeyTile + row;
@@ -593,7 +589,7 @@ __device__ __forceinline__ void copy_rows(const PrefillParams &p, const Start &s
         if (more) next_blk = lookup();                          // a tile ahead
         for (int kv = 0; kv < 2; ++kv, ++pos) {
             // never wait for room with a stage in hand
-            if (pos >= ST && p0 != 0 && !warp_test(bars.empty(pos % ST), (pos / ST - 1) & 1)) flush();
+            while (pos >= ST && p0 != 0 && !warp_test(bars.empty(pos % ST), (pos / ST - 1) & 1)) hand_over();
             if (pos >= ST && !warp_wait(bars.empty(pos % ST), (pos / ST - 1) & 1, gone)) {
                 tc::cp_async_wait<0>();
                 return;
@@ -610,17 +606,12 @@ __device__ __forceinline__ void copy_rows(const PrefillParams &p, const Start &s
             for (int c = 0; c < D / 8; ++c) tc::cp_async16(dst + piece_at(row, c), src + (in ? c * d.c_chunk : 0), in);
             tc::cp_async_commit();
             const uint32_t bar = bars.full(set, pos % ST);
-            if (p2 != 0) {
-                tc::cp_async_wait<3>();
-                arrive();
-                p2 = bar;
-            } else {
-                (p0 == 0 ? p0 : p1 == 0 ? p1 : p2) = bar;
-            }
+            (p0 == 0 ? p0 : p1 == 0 ? p1 : p2) = bar;
+            if (p2 != 0) hand_over();
         }
         ++tile_n;
     }
-    flush();
+    while (p0 != 0) hand_over();
 }
 
 // Raw codes of every tile into the raw ring, by one warp: one TMA copy per
