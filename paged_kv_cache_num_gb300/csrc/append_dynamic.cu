@@ -114,9 +114,15 @@ __global__ void __launch_bounds__(kAppendThreads) append_dynamic_kernel(AppendPa
     const int sub = lane % LPR;
     const int64_t warp = (blockIdx.x * int64_t(blockDim.x) + threadIdx.x) >> 5;
     const int64_t warps = (int64_t(gridDim.x) * blockDim.x) >> 5;
-    Walk2 w(warp * RPW + lane / LPR, warps * RPW, p.num_kv_heads);
-    while (__any_sync(0xffffffffu, w.major < p.num_tokens)) {
-        const int64_t t = w.major;
+    // A warp's rows: neighbouring heads of a token; in x-vectorised caches, whose
+    // 16-byte pieces of neighbouring slots are neighbours, RPW tokens of a head
+    // (60001 tokens of 8 heads of 128: 104 -> 77 us).
+    const bool tokens = p.c_chunk != 16;
+    const int row = lane / LPR;
+    Walk2 w(tokens ? warp : warp * RPW + row, tokens ? warps : warps * RPW, p.num_kv_heads);
+    for (;; w.next()) {
+        const int64_t t = tokens ? w.major * RPW + row : w.major;
+        if (!__any_sync(0xffffffffu, t < p.num_tokens)) break;
         const int h = w.minor;
         int64_t blk = 0, off = 0;
         const bool live = t < p.num_tokens && resolve_slot(p, t, blk, off);
@@ -150,7 +156,6 @@ __global__ void __launch_bounds__(kAppendThreads) append_dynamic_kernel(AppendPa
                 if (sub == 0) (kv ? p.v_gs : p.k_gs)[gs] = s;
             }
         }
-        w.next();
     }
 }
 
