@@ -402,6 +402,46 @@ def test_packed_rows_off_the_word(pkv, D):
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("pad", [4, 8, 16])
+def test_packed_rows_apart(pkv, pad, D):
+    """3-bit rows in wider slots; each CTA takes more key tiles than are in flight."""
+    BS, H, G, ctx, new = 16, 4, 8, [2300, 1100], [1300, 3]
+    bt, P = R.tables(ctx, BS, seed=38)
+    cache, kv, vv = R.make_cache(pkv, "u3", P, BS, H, D, seed=38)
+    row = 3 * D // 8 + pad
+    halves = []
+    for t in (cache.k_cache, cache.v_cache):
+        view = torch.full((P, BS, H, row), 255, dtype=torch.uint8, device=DEV)[..., :3 * D // 8]
+        view.copy_(t)
+        halves.append(view)
+    apart = pkv.KVCache("u3", *halves, k_qscale=cache.k_qscale, k_qzero=cache.k_qzero, v_qscale=cache.v_qscale,
+                        v_qzero=cache.v_qzero)
+    q = torch.randn((1303, H * G, D), generator=torch.Generator().manual_seed(39)).bfloat16()
+    st = starts_of(new)
+    dev = [torch.tensor(x, dtype=torch.int32, device=DEV) for x in (st, ctx)]
+    out = pkv.paged_prefill(q.to(DEV), apart, bt.to(DEV), *dev)
+    check(out, R.prefill(q, kv, vv, bt, st, ctx, D ** -0.5), torch.bfloat16, D, float(vv.abs().max()))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("kind", ["bf16", "f16", "e4m3"])
+@pytest.mark.parametrize("BS", [8, 64])
+def test_xvec_long(pkv, kind, D, BS):
+    """X-vectorised caches; each CTA takes more key tiles than are in flight,
+    in row tiles of one subtile and of two."""
+    case(pkv, kind, "f16" if kind == "f16" else "bf16", new=[1300, 5, 1, 140], ctx=[2300, 2003, 1, 900], H=4, G=8,
+         layout="xvec", D=D, BS=BS, seed=40)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("kind,scales", [("bf16", "head"), ("e4m3", "token"), ("e5m2", "block"), ("i8", "head"),
+                                         ("i8", "token"), ("u3", "head")])
+def test_long_shares(pkv, kind, scales, D):
+    """Row-major caches, likewise."""
+    case(pkv, kind, "bf16", new=[1300, 5, 1, 140], ctx=[2300, 2003, 1, 900], H=4, G=8, scales=scales, D=D, seed=41)
+
+
 def test_no_blocks_and_no_table(pkv):
     """An empty pool, or a block table without columns: nothing to see."""
     q = torch.randn((5, 4, 64), generator=torch.Generator().manual_seed(37)).half().to(DEV)
