@@ -321,7 +321,10 @@ int pkv_kv_gather(const pkv_cache *cache, const pkv_tensor *slot_mapping, const 
  *   become F16 by a power of two per row (exactly but for elements below
  *   2^-31 of the row's largest, which are off by at most 2^-39 of it);
  *   scales are applied in fp32, and the weights are rounded once to the
- *   product's type.
+ *   product's type: by themselves, or, with scales per row or block, times the
+ *   V scale, relative to the largest such product of the keys that the row
+ *   sees (one far below it is off by at most 2^-20 of it).  Such V scales are
+ *   zero or from 2^-80 to 2^80.
  *   Bad data never faults: a block id outside [0, num_blocks) is left out
  *   (PKV_DEVERR_BLOCK_RANGE); a context length below 0 counts as 0 and one
  *   above the table's capacity as that capacity

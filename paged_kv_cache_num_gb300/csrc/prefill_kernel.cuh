@@ -43,7 +43,9 @@
 // takes: that warp loads them.)
 // Codes become f16 exactly (every code of every kind is an f16 number); their
 // scales are applied in fp32: per-head scales to c and to the result, per-row
-// scales to the columns of S and of P.  bf16 queries of such caches are
+// scales to the columns of S and of P, whose product is what P's operand holds:
+// there the reference m is of the largest c S + log2(V scale) that the row sees
+// (see kScaleSpread).  bf16 queries of such caches are
 // brought to f16 by a power of two per row, exactly but for elements below
 // 2^-31 of the row's largest, which are rounded to multiples of 2^-38 of it.
 #pragma once
@@ -98,6 +100,20 @@ constexpr int kFirst = 16;
 // us without, 177 with), and so it does with scales per row, whose softmax is
 // long enough by itself (3-bit chunks 180 us without, 216 with).
 constexpr int kTurnTiles = 16;
+// Scales per row: weights times V scales become the second product's operand, so
+// they are held relative to their own largest value, L = max of weight times
+// scale over the keys that the row sees; what is far below it loses bits in f16's
+// subnormals (2^-25 of the reference at most), as any sum of 16-bit terms does.  Where
+// the V scales of a key tile lie within 2^kScaleSpread of each other, and every row
+// of the warp sees all of it, the tile's maxima of score and scale bound L from above by at
+// most 2^(kScaleSpread + 1); else each row takes its maximum column by column
+// over the keys that it sees, with the scales' exponents, in a pass of its own.
+// Exponents are clamped to +-kScaleExp: the sum of weights, relative to the same
+// reference, then stays below 2^(80 + 8 + 31).
+constexpr int kScaleSpread = 4;
+constexpr int kScaleExp = 80;
+// log2 of a scale, at most 1 above it, from its biased exponent
+__device__ __forceinline__ float scale_exp(uint32_t e) { return float(min(max(int(e) - 126, -kScaleExp), kScaleExp)); }
 constexpr int kBins = 1024;
 constexpr uint64_t kPrefillTimeoutNs = 4000000000ull;
 
@@ -303,7 +319,7 @@ struct Smem {
     static constexpr int ring = 2 * kTile;
     static constexpr int raw = ring + kStages * kTile;
     static constexpr int cols = raw + kRaw * kRawTile;
-    static constexpr int kColBytes = 2 * kKeyTile * 4 + 64;
+    static constexpr int kColBytes = 3 * kKeyTile * 4 + 64;
     static constexpr int state = cols + kColSlots * kColBytes;  // (m, l) of a row tile's rows: [subtile][2][128]
     static constexpr int q_scale = state + 2048;                // per row of subtile 0
     static constexpr int bars = q_scale + 512;
@@ -318,8 +334,8 @@ struct Smem {
     static_assert(sizeof(Start) <= 96, "misc");
 };
 
-// Column data of a key tile: scales of its 128 K and V rows, the largest V
-// scale of each producer warp's rows, and which groups of 8 rows are there.
+// Column data of a key tile: scales of its 128 K and V rows and the V scales'
+// exponents, their range by producer warp, and which groups of 8 rows are there.
 // Tile T's is written once the ring has room for K of tile T.  With a ring of
 // R tiles of K that is when the scores of tile T - R are done; the tiles whose
 // softmax may still be under way then are fewer than 2 R + 2 (each subtile has
@@ -329,7 +345,9 @@ struct Smem {
 struct ColSlot {
     float k[kKeyTile];
     float v[kKeyTile];
-    float vmax[8];              // by producer warp, unused ones 0
+    float v_log2[kKeyTile];     // of the V scale, at most 1 above it, clamped
+    uint32_t vexp[8];           // by producer warp, unused ones 0: biased exponent of its rows' largest V scale, and
+                                // in the low half 255 minus the smallest one's
     uint32_t mask[8];           // likewise: the bits of its groups of 8 rows
 };
 
@@ -800,10 +818,10 @@ __device__ __forceinline__ void convert_rows(const PrefillParams &p, const Start
                     };
                     cs.k[row] = fmaxf(value(ks), 1.17549435e-38f);
                     cs.v[row] = value(vs);
-                    float mx = value(vs);
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                    if (lane == 0) cs.vmax[lw] = mx;
+                    const uint32_t e = (__float_as_uint(value(vs)) >> 23) & 0xffu;
+                    cs.v_log2[row] = scale_exp(e);
+                    const uint32_t hi = __reduce_max_sync(0xffffffffu, e), lo = __reduce_min_sync(0xffffffffu, e);
+                    if (lane == 0) cs.vexp[lw] = (hi << 16) | (255u - lo);
                 }
                 if (lane == 0) {
                     uint32_t there = 0;
@@ -913,7 +931,6 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
     constexpr int kProducers = FEED == kFeedCodes ? conv_warps<CK>() : 4;
     constexpr int CH = 16;                                      // columns that a softmax thread reads at a time
     using R = Ring<FEED, ST>;
-    constexpr bool kVRef = GS;                                  // P relative to the V scales' magnitude
     const DecodeParams &d = p.d;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *sm = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -951,7 +968,7 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
         ptx::fence_mbar_init();
         *gone = 0;
     }
-    if (threadIdx.x < 16 * L::kColSlots) (reinterpret_cast<uint32_t *>(cols[threadIdx.x / 16].vmax))[threadIdx.x % 16] = 0u;
+    if (threadIdx.x < 16 * L::kColSlots) (cols[threadIdx.x / 16].vexp)[threadIdx.x % 16] = 0u;
     if (warp == kMmaWarp) tc::tmem_alloc(ptx::smem_u32(tmem_at), 512);
     griddep_wait();
     griddep_launch_dependents();
@@ -1028,7 +1045,7 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                 ++item;
                 c = fmaxf(c, 1e-30f);                           // keeps 0 * -inf out: masked weights stay zero
                 const float ninf = -__int_as_float(0x7f800000);
-                float m = ninf, l = 0.0f, vexp = -1000.0f;
+                float m = ninf, l = 0.0f;                       // m: of S, or (GS) of c S + log2(V scale)
                 const int step = split ? 2 : 1, j0 = split ? sub : 0;
                 const bool in_turn = !GS && !split && nk >= kTurnTiles;
                 for (int j = j0; j < nk; j += step, ++mine_n) {
@@ -1063,7 +1080,7 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                     if constexpr (kProducers == 8) there |= cs.mask[4] | cs.mask[5] | cs.mask[6] | cs.mask[7];
                     const int rel = lim - (w.k0 + j) * kKeyTile;
                     const int seen = there == 0xffffu ? __reduce_min_sync(0xffffffffu, max(rel, 0)) : 0;    // by all rows
-                    if (seen < kKeyTile) {
+                    if (!GS && seen < kKeyTile) {
                         // few tiles: masked in place, in a rolled loop, before the others' path
 #pragma unroll 1
                         for (int o = seen & ~15; o < kKeyTile; o += 16) {
@@ -1111,26 +1128,45 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                             for (int i = 0; i < 4; ++i)
                                 mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(x[q & 1][u + i])), __uint_as_float(x[q & 1][u + 4 + i]));
                     }
+                    float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     if constexpr (GS) {
                         tc::tmem_st_wait();
+                        uint32_t ve = __vmaxu2(__vmaxu2(cs.vexp[0], cs.vexp[1]), __vmaxu2(cs.vexp[2], cs.vexp[3]));
+                        if constexpr (kProducers == 8)
+                            ve = __vmaxu2(ve, __vmaxu2(__vmaxu2(cs.vexp[4], cs.vexp[5]), __vmaxu2(cs.vexp[6], cs.vexp[7])));
+                        if (seen < kKeyTile || (ve >> 16) + (ve & 0xffffu) > 255u + kScaleSpread) {
+                            // the scaled scores are masked here, and the maximum taken column by
+                            // column: what a row does not see has no part in it
+                            top = ninf;
+#pragma unroll 1
+                            for (int o = 0; o < kKeyTile; o += 16) {
+                                uint32_t y[16];
+                                tc::tmem_ld16_wait(ts + o, y);
+                                const uint32_t g = there >> (o >> 3);
+                                const int n = rel - o;
+#pragma unroll
+                                for (int i = 0; i < 16; i += 4) {
+                                    const float4 e4 = *reinterpret_cast<const float4 *>(cs.v_log2 + o + i);
+                                    const float e[4] = {e4.x, e4.y, e4.z, e4.w};
+#pragma unroll
+                                    for (int u = 0; u < 4; ++u) {
+                                        if (i + u >= n || !((g >> (i >> 3)) & 1u)) y[i + u] = 0xff800000u;
+                                        top = fmaxf(top, fmaf(__uint_as_float(y[i + u]), c, e[u]));
+                                    }
+                                }
+                                tc::tmem_st16(ts + o, y);
+                            }
+                            tc::tmem_st_wait();
+                        } else {
+                            top = fmaf(top, c, scale_exp(ve >> 16));
+                        }
                         tc::tmem_ld(ts, x[0]);
                     }
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     float grow = 1.0f;                          // what O and l shrink by
-                    if (top > m && (m == ninf || (top - m) * c > 8.0f)) {
-                        grow = m == ninf ? 0.0f : exp2_approx((m - top) * c);
+                    const float unit = GS ? 1.0f : c;
+                    if (top > m && (m == ninf || (top - m) * unit > 8.0f)) {
+                        grow = m == ninf ? 0.0f : exp2_approx((m - top) * unit);
                         m = top;
-                    }
-                    if constexpr (kVRef) {
-                        // 2^vexp at or above the V scales so far: P times a scale stays in f16's range
-                        float vm = fmaxf(fmaxf(cs.vmax[0], cs.vmax[1]), fmaxf(cs.vmax[2], cs.vmax[3]));
-                        if constexpr (kProducers == 8)
-                            vm = fmaxf(vm, fmaxf(fmaxf(cs.vmax[4], cs.vmax[5]), fmaxf(cs.vmax[6], cs.vmax[7])));
-                        const float e = float(int(__float_as_uint(fmaxf(vm, 1e-30f)) >> 23) - 126);
-                        if (e > vexp) {
-                            grow *= exp2_approx(vexp - e);
-                            vexp = e;
-                        }
                     }
                     l *= grow;
                     if (j > j0 && __any_sync(0xffffffffu, grow != 1.0f)) {
@@ -1144,8 +1180,7 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                             tc::tmem_st16(to + o, y);
                         }
                     }
-                    float off = m == ninf ? 0.0f : m * c;
-                    if constexpr (kVRef) off += vexp;
+                    const float off = m == ninf ? 0.0f : m * unit;
                     const float2 c2 = make_float2(c, c), off2 = make_float2(-off, -off);
                     float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
 #pragma unroll
@@ -1185,9 +1220,7 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                 tile_n += nk;
                 if (!ok) break;
                 if (sub == 1 && !two) continue;
-                float off = m == ninf ? m : m * c;
-                if constexpr (kVRef) off = m == ninf ? m : off + vexp;
-                state[0] = off;
+                state[0] = GS || m == ninf ? m : m * c;
                 state[128] = l;
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(bars.e_full(sub));
