@@ -1252,19 +1252,25 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                     if (!ok) break;
                     tc::fence_after();
                     float off = states[sub * 256], l = states[sub * 256 + 128];
-                    float w0 = 1.0f, w1 = 0.0f;                 // weights of this O and of warpgroup 1's
+                    // weights of this O and of warpgroup 1's.  An O without keys (l = 0) holds anything
+                    // and has no part; every other one has, so that what is not finite stays: a weight
+                    // that underflows makes infinities NaN, and scores that are all NaN (a maximum of
+                    // -inf, l NaN) make the row NaN
+                    float w0 = 1.0f, w1 = 0.0f;
+                    const bool use0 = l != 0.0f;
+                    bool use1 = false;
                     if (join) {
                         const float m1 = states[256], l1 = states[384];
+                        use1 = l1 != 0.0f;
                         const float top = fmaxf(off, m1);
-                        w0 = l == 0.0f || off == ninf ? 0.0f : exp2_approx(off - top);
-                        w1 = l1 == 0.0f || m1 == ninf ? 0.0f : exp2_approx(m1 - top);
-                        l = (w0 == 0.0f ? 0.0f : l * w0) + (w1 == 0.0f ? 0.0f : l1 * w1);
+                        w0 = !use0 ? 0.0f : off == ninf ? l : exp2_approx(off - top);
+                        w1 = !use1 ? 0.0f : m1 == ninf ? l1 : exp2_approx(m1 - top);
+                        l = fmaf(l, w0, l1 * w1);
                         off = top;
                     }
                     float fac = 1.0f;
                     if constexpr (is_q8(CK) && !GS) fac = d.v_scale[w.h];
                     if (whole) fac = l == 0.0f ? 0.0f : fac / l;
-                    if (l == 0.0f) w0 = w1 = 0.0f;              // a row without keys is zero whatever O holds
                     w0 *= fac;
                     w1 *= fac;
                     const int tok = r / d.group;
@@ -1282,13 +1288,13 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                     // 16 columns at o, in `a`, while the next are on their way
                     auto columns = [&](int o, uint32_t (&a)[16]) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) a[i] = w0 == 0.0f ? 0u : __float_as_uint(__uint_as_float(a[i]) * w0);
+                        for (int i = 0; i < 16; ++i) a[i] = use0 ? __float_as_uint(__uint_as_float(a[i]) * w0) : 0u;
                         if (join) {
                             uint32_t b[16];
                             tc::tmem_ld16_wait(to + 128 + o, b);
 #pragma unroll
                             for (int i = 0; i < 16; ++i)
-                                if (w1 != 0.0f)
+                                if (use1)
                                     a[i] = __float_as_uint(fmaf(__uint_as_float(b[i]), w1, __uint_as_float(a[i])));
                         }
                         if (!whole) {
