@@ -321,8 +321,8 @@ struct Smem {
     static constexpr int cols = raw + kRaw * kRawTile;
     static constexpr int kColBytes = 3 * kKeyTile * 4 + 64;
     static constexpr int state = cols + kColSlots * kColBytes;  // (m, l) of a row tile's rows: [subtile][2][128]
-    static constexpr int q_scale = state + 2048;                // per row of subtile 0
-    static constexpr int bars = q_scale + 512;
+    static constexpr int q_scale = state + 2048;                // per row of subtile 0, of even and of odd segments
+    static constexpr int bars = q_scale + 1024;
     static constexpr int n_bars = 4 * kStages + 2 * kRaw + 2 + 4 * 2 + 1 + 4 + 1 + 2;
     static constexpr int info = bars + 8 * n_bars;              // per raw stage: which blocks are there
     static constexpr int misc = (info + 4 * 8 + 15) / 16 * 16;
@@ -1006,6 +1006,10 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                     float back = 1.0f;
                     ok = warp_wait(bars.q_raw(), item & 1, gone);
                     if (!ok) break;
+                    // two places in turn: nothing orders this segment's write after warpgroup 1's read
+                    // of the one before, but q_full of the one between does (every warp arrives there
+                    // after its read)
+                    float *scale_at = q_scale + 128 * (item & 1);
                     if (!split || sub == 0) {
                         const uint32_t q = sm32 + L::q + sub * L::kTile;
                         uint32_t top = 0;
@@ -1030,7 +1034,7 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                             v.w = bf16x2_to_f16x2(v.w, sg);
                             tc::st_shared16(q + piece_at(row, i), v);
                         }
-                        if (split) q_scale[0] = back;
+                        if (split) *scale_at = back;
                         ptx::fence_proxy_async_smem();
                     }
                     __syncwarp();
@@ -1038,7 +1042,7 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                     if (split && sub == 1) {
                         ok = warp_wait(bars.q_full(), item & 1, gone);
                         if (!ok) break;
-                        back = q_scale[0];
+                        back = *scale_at;
                     }
                     c *= back;
                 }
