@@ -816,7 +816,7 @@ __device__ __forceinline__ void convert_rows(const PrefillParams &p, const Start
                     auto value = [](uint32_t x) {
                         return CK == kU3 ? __half2float(__ushort_as_half(uint16_t(x))) : __uint_as_float(x);
                     };
-                    cs.k[row] = fmaxf(value(ks), 1.17549435e-38f);
+                    cs.k[row] = value(ks);
                     cs.v[row] = value(vs);
                     const uint32_t e = (__float_as_uint(value(vs)) >> 23) & 0xffu;
                     cs.v_log2[row] = scale_exp(e);
@@ -1104,7 +1104,8 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                     constexpr int NC = kKeyTile / CH;
                     uint32_t x[2][CH];
                     // per-row K scales: the scores are scaled on the way to the maximum and put
-                    // back.  A scale of zero must not meet a masked score's -inf: at least 2^-126
+                    // back.  They are masked after that: the scales of hidden keys are then no matter,
+                    // and one that is NaN stays so where it is seen
                     auto scaled = [&](uint32_t (&v)[CH], int o) {
 #pragma unroll
                         for (int i = 0; i < CH; i += 4) {

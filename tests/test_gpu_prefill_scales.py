@@ -85,7 +85,7 @@ def test_one_large_scale(pkv, kind, scales, bits, dtype):
 
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("value", [float("inf"), float("nan"), 1e38])
-@pytest.mark.parametrize("what", ["v"])
+@pytest.mark.parametrize("what", ["k", "v"])
 @pytest.mark.parametrize("kind,scales", FORMS)
 def test_hidden_scale_of_no_use(pkv, kind, scales, what, value, D):
     """A later token's scale that is infinite, NaN or next to the largest
