@@ -105,7 +105,9 @@ PrefillPlan plan_prefill(const PrefillParams &p, int, int sm_count)
     pl.join = keys > 1 && pl.grid > 1;
     pl.launches = pl.join ? 2 : 1;
     pl.workspace_bytes = round256(size_t(pl.grid) * sizeof(int4));
-    if (pl.join) pl.workspace_bytes += size_t(pl.grid) * 2 * 256 * (2 + size_t(d.head_dim)) * sizeof(float);
+    if (pl.join)
+        pl.workspace_bytes += round256(size_t(pl.grid) * sizeof(PrefillStart)) + round256(size_t(pl.grid) * sizeof(int)) +
+                              size_t(pl.grid) * 2 * 256 * (2 + size_t(d.head_dim)) * sizeof(float);
     return pl;
 }
 
@@ -119,6 +121,10 @@ cudaError_t launch_prefill(const PrefillParams &p, const PrefillPlan &pl, int ca
     char *w = static_cast<char *>(ws);
     a.desc = w;
     w += round256(size_t(pl.grid) * sizeof(int4));
+    a.starts = w;
+    w += round256(size_t(pl.grid) * sizeof(PrefillStart));
+    a.redo = w;
+    w += round256(size_t(pl.grid) * sizeof(int));
     a.part_ml = w;
     a.part_acc = w + size_t(pl.grid) * 2 * 256 * 2 * sizeof(float);
     const DecodeParams &d = p.d;

@@ -16,6 +16,9 @@ cudaError_t launch_instance(const PrefillLaunch &a)
     if (e != cudaSuccess) return e;
     PrefillFast f{};
     f.desc = static_cast<int4 *>(a.desc);
+    f.starts = static_cast<Start *>(a.starts);
+    f.redo = static_cast<int *>(a.redo);
+    f.later = a.join;
     f.part_ml = static_cast<float *>(a.part_ml);
     f.part_acc = static_cast<float *>(a.part_acc);
     f.out32 = a.out32;

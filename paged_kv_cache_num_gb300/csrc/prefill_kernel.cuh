@@ -52,13 +52,19 @@
 
 #include <type_traits>
 
+#include "prefill_launch.h"
 #include "prefill_row.cuh"
 #include "tc_ptx.cuh"
 
 namespace pkv {
 
+using Start = PrefillStart;
+
 struct PrefillFast {
     int4 *desc;                 // [grid] (sequence, kv head, row tile, last CTA) of the row tile split at a CTA's end
+    int *redo;                  // [grid] whether the CTA has written rows that are not finite
+    Start *starts;              // [grid] ... and then its share
+    int later;                  // such rows are looked through by the join kernel (else at once)
     float *part_ml;             // [2 grid][2][256]
     float *part_acc;            // [2 grid][D / 4][256][4]
     int out32;                  // output rows at multiples of 32 bytes
@@ -189,12 +195,6 @@ struct Walk {
     {
         return s.rows - tile * 2 * p.sub_rows > p.sub_rows ? 2 : 1;
     }
-};
-
-struct Start {
-    int64_t u0, u1, total;      // this CTA's cost units, all of them
-    int ctas;                   // CTAs that have work
-    int b, h, tile, at;
 };
 
 __device__ __forceinline__ Walk walk_from(const PrefillParams &p, const Start &st)
@@ -938,6 +938,7 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
     Start *start = reinterpret_cast<Start *>(sm + L::misc);
     volatile int *gone = reinterpret_cast<volatile int *>(sm + L::misc + 96);
     uint32_t *tmem_at = reinterpret_cast<uint32_t *>(sm + L::misc + 104);
+    volatile int *not_finite = reinterpret_cast<volatile int *>(sm + L::misc + 108);
     ColSlot *cols = reinterpret_cast<ColSlot *>(sm + L::cols);
     static_assert(sizeof(ColSlot) == L::kColBytes, "column slots");
     const Bars bars{sm32 + L::bars, ST, L::kRaw};
@@ -967,6 +968,7 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
         ptx::mbar_init(bars.tail(), 1);
         ptx::fence_mbar_init();
         *gone = 0;
+        *not_finite = 0;
     }
     if (threadIdx.x < 16 * L::kColSlots) (cols[threadIdx.x / 16].vexp)[threadIdx.x % 16] = 0u;
     if (warp == kMmaWarp) tc::tmem_alloc(ptx::smem_u32(tmem_at), 512);
@@ -1349,14 +1351,19 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                         ptx::mbar_arrive(bars.e_empty(sub));
                         if (join) ptx::mbar_arrive(bars.e_empty(1));
                     }
-                    // not finite: weights of zero met values that are not; such a row is done again by itself
+                    // not finite: weights of zero may have met values that are not; such a row is done
+                    // again by itself, here (with at most a key tile to a row) or by the join kernel
                     unsigned redo = __ballot_sync(0xffffffffu, whole && live && bad != 0.0f);
+                    if (f.later) {
+                        if (redo && lane == 0) *not_finite = 1;
+                        redo = 0;
+                    }
                     while (redo) {
                         const int who = __ffs(redo) - 1;
                         redo &= redo - 1;
                         const int rr = __shfl_sync(0xffffffffu, r, who), tt = rr / d.group;
-                        redo_row<QK, CK, D>(d, d.block_tables + w.b * d.bt_b, int64_t(w.s.s0) + tt,
-                                            w.h * d.group + (rr - tt * d.group), row_limit(p, w.s, rr), w.reach(), 0, D);
+                        redo_row<QK, CK, D, 1>(d, d.block_tables + w.b * d.bt_b, int64_t(w.s.s0) + tt,
+                                            w.h * d.group + (rr - tt * d.group), row_limit(p, w.s, rr), w.reach());
                     }
                 }
             } while (ok && w.next(p));
@@ -1572,6 +1579,10 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
         }
     }
     __syncthreads();
+    if (f.later && threadIdx.x == 0) {
+        f.redo[blockIdx.x] = *not_finite;
+        if (*not_finite) f.starts[blockIdx.x] = *start;
+    }
     if (*gone) {
         // copies and products under way end by themselves
         const uint64_t t0 = ptx::globaltimer();
@@ -1584,78 +1595,137 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
     if (warp == kMmaWarp) tc::tmem_free(tmem, 512);
 }
 
+constexpr int kJoinWarps = kRowTile / 32;
+
+// row of the sequence at place i of a row tile's parts
+__device__ __forceinline__ int tile_row(const PrefillParams &p, int tile, int i)
+{
+    return (2 * tile + (i >> 7)) * p.sub_rows + (i & 127);
+}
+
+// The join kernel's rows that are not finite (see redo_row).  todo: by warp of
+// the block, those of the 32 rows that it has joined 16 columns of.  Kept out
+// of the kernel's body, whose registers it would take.
+template <int QK, int CK, int D>
+__device__ __noinline__ void redo_rows(const PrefillParams &p, const PrefillFast &f, const unsigned *todo)
+{
+    const DecodeParams &d = p.d;
+    const int warp = threadIdx.x >> 5;
+    const int4 ds = f.desc[blockIdx.x];
+    if (ds.w >= 0) {
+        const Seq s = seq_load(p, ds.x, false);
+        const int hi = min(s.ctx, tile_units(tile_limit(p, s, ds.z)) * kKeyTile);
+        constexpr int kSlices = D / 16;
+        int n = 0;
+        for (int g = 0; g < kJoinWarps; g += kSlices) {         // warps of the same rows
+            unsigned rows = 0;
+            for (int i = 0; i < kSlices; ++i) rows |= todo[g + i];
+            for (; rows; rows &= rows - 1) {
+                if (n++ % kJoinWarps != warp) continue;
+                const int at = (blockIdx.y * kJoinWarps + g) / kSlices * 32 + __ffs(rows) - 1;
+                const int r = tile_row(p, ds.z, at), tok = r / d.group;
+                redo_row<QK, CK, D, 4>(d, d.block_tables + ds.x * d.bt_b, int64_t(s.s0) + tok,
+                                    ds.y * d.group + (r - tok * d.group), row_limit(p, s, r), hi);
+            }
+        }
+    }
+    const int warps = gridDim.x * gridDim.y * kJoinWarps, me = (blockIdx.y * gridDim.x + blockIdx.x) * kJoinWarps + warp;
+    int n = 0;                                      // rows of the tiles before, modulo `warps`
+    for (int c = 0; c < int(gridDim.x); ++c) {
+        if (!f.redo[c]) continue;
+        Walk w = walk_from(p, f.starts[c]);
+        do {
+            if (w.k0 != 0 || w.k1 != w.units) continue;         // joined: by its first CTA's blocks
+            const int r0 = w.tile * 2 * p.sub_rows, rows = min(2 * p.sub_rows, w.s.rows - r0);
+            for (int i = (me - n + warps) % warps; i < rows; i += warps) {
+                const int r = r0 + i, tok = r / d.group;
+                redo_row<QK, CK, D, 4>(d, d.block_tables + w.b * d.bt_b, int64_t(w.s.s0) + tok,
+                                    w.h * d.group + (r - tok * d.group), row_limit(p, w.s, r), w.reach());
+            }
+            n = (n + rows) % warps;
+        } while (w.next(p));
+    }
+}
+
 // Joins the row tile that CTA blockIdx.x begins and a later one ends: with
 // M = max m_i, out = sum O_i 2^(m_i - M) / sum l_i 2^(m_i - M).  A thread per
-// row, 16 columns per block row of the grid; the parts lie column major, so
-// the reads of a warp are whole lines.
+// row and 16 columns, all columns of a row by one block; the parts lie column
+// major, so the reads of a warp are whole lines.
+//
+// Rows that are not finite (see redo_row) are done again here, with the whole
+// grid: those of a joined tile by the warps of their block in turn, those of
+// whole tiles, in CTAs that have marked themselves, by all warps of the grid in
+// turn.  Nothing waits for them.
 template <int QK, int CK, int D>
-__global__ void __launch_bounds__(kRowTile) prefill_join_kernel(PrefillParams p, PrefillFast f)
+__global__ void __launch_bounds__(kRowTile, 2) prefill_join_kernel(const __grid_constant__ PrefillParams p,
+                                                                const __grid_constant__ PrefillFast f)
 {
     griddep_wait();
     griddep_launch_dependents();
-    const int4 ds = f.desc[blockIdx.x];
-    if (ds.w < 0) return;
+    constexpr int kSlices = D / 16;                 // of a row's columns
+    __shared__ unsigned todo[kJoinWarps];
     const DecodeParams &d = p.d;
-    const Seq s = seq_load(p, ds.x, false);
-    const int row = threadIdx.x, r = (2 * ds.z + (row >> 7)) * p.sub_rows + (row & 127);
-    const bool live = (row & 127) < p.sub_rows && r < s.rows;
-    const int lim = live ? row_limit(p, s, r) : 0;
-    const int tok = r / d.group, head = ds.y * d.group + (r - tok * d.group);
-    const int c0 = blockIdx.y * 16;
-    const int first = blockIdx.x, last = ds.w;
-    auto slot = [&](int i) -> int64_t { return 2 * i + (i == first ? 1 : 0); };
-    const float ninf = -__int_as_float(0x7f800000);
-    bool redo = false;
-    if (live) {
-        float m = ninf;
-        for (int i = first; i <= last; ++i) m = fmaxf(m, f.part_ml[slot(i) * 2 * kRowTile + row]);
-        float l = 0.0f, acc[16];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int4 ds = f.desc[blockIdx.x];
+    int again = 0;
+    for (int i = threadIdx.x; i < int(gridDim.x); i += kRowTile) again |= f.redo[i];
+    unsigned mine = 0;
+    if (ds.w >= 0) {
+        const Seq s = seq_load(p, ds.x, false);
+        const int part = blockIdx.y * kJoinWarps + warp, row = part / kSlices * 32 + lane, c0 = part % kSlices * 16;
+        const int r = tile_row(p, ds.z, row);
+        const bool live = (row & 127) < p.sub_rows && r < s.rows;
+        const int first = blockIdx.x, last = ds.w;
+        auto slot = [&](int i) -> int64_t { return 2 * i + (i == first ? 1 : 0); };
+        const float ninf = -__int_as_float(0x7f800000);
+        bool redo = false;
+        if (live) {
+            const int tok = r / d.group, head = ds.y * d.group + (r - tok * d.group);
+            float m = ninf;
+            for (int i = first; i <= last; ++i) m = fmaxf(m, f.part_ml[slot(i) * 2 * kRowTile + row]);
+            float l = 0.0f, acc[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) acc[j] = 0.0f;
-        for (int i = first; i <= last; ++i) {
-            const float *ml = f.part_ml + slot(i) * 2 * kRowTile + row;
-            const float wgt = ml[0] == ninf ? 0.0f : exp2_approx(ml[0] - m);
-            const float li = ml[kRowTile];
-            // a part without keys (l = 0) has no O, whatever lies there
-            if (li == 0.0f) continue;
-            l = fmaf(li, wgt, l);
-            const float4 *a = reinterpret_cast<const float4 *>(f.part_acc) + (slot(i) * (D / 4) + c0 / 4) * kRowTile + row;
+            for (int j = 0; j < 16; ++j) acc[j] = 0.0f;
+            for (int i = first; i <= last; ++i) {
+                const float *ml = f.part_ml + slot(i) * 2 * kRowTile + row;
+                const float wgt = ml[0] == ninf ? 0.0f : exp2_approx(ml[0] - m);
+                const float li = ml[kRowTile];
+                // a part without keys (l = 0) has no O, whatever lies there
+                if (li == 0.0f) continue;
+                l = fmaf(li, wgt, l);
+                const float4 *a = reinterpret_cast<const float4 *>(f.part_acc) + (slot(i) * (D / 4) + c0 / 4) * kRowTile + row;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float4 v = a[j * kRowTile];
-                acc[4 * j] = fmaf(v.x, wgt, acc[4 * j]);
-                acc[4 * j + 1] = fmaf(v.y, wgt, acc[4 * j + 1]);
-                acc[4 * j + 2] = fmaf(v.z, wgt, acc[4 * j + 2]);
-                acc[4 * j + 3] = fmaf(v.w, wgt, acc[4 * j + 3]);
+                for (int j = 0; j < 4; ++j) {
+                    const float4 v = a[j * kRowTile];
+                    acc[4 * j] = fmaf(v.x, wgt, acc[4 * j]);
+                    acc[4 * j + 1] = fmaf(v.y, wgt, acc[4 * j + 1]);
+                    acc[4 * j + 2] = fmaf(v.z, wgt, acc[4 * j + 2]);
+                    acc[4 * j + 3] = fmaf(v.w, wgt, acc[4 * j + 3]);
+                }
+            }
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            float bad = 0.0f;
+            uint32_t pk[8];
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+                bad = fmaf(acc[j] * inv, 0.0f, fmaf(acc[j + 1] * inv, 0.0f, bad));
+                pk[j / 2] = tc::pack16<QK>(acc[j] * inv, acc[j + 1] * inv);
+            }
+            redo = bad != 0.0f;
+            char *o = d.out + int64_t(s.s0 + tok) * d.o_b + int64_t(head) * d.o_h + 2 * c0;
+            if (d.out_vec_ok) {
+                reinterpret_cast<uint4 *>(o)[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                reinterpret_cast<uint4 *>(o)[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    reinterpret_cast<uint16_t *>(o)[j] = uint16_t(pk[j >> 1] >> (16 * (j & 1)));
             }
         }
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        float bad = 0.0f;
-        uint32_t pk[8];
-#pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-            bad = fmaf(acc[j] * inv, 0.0f, fmaf(acc[j + 1] * inv, 0.0f, bad));
-            pk[j / 2] = tc::pack16<QK>(acc[j] * inv, acc[j + 1] * inv);
-        }
-        redo = bad != 0.0f;
-        char *o = d.out + int64_t(s.s0 + tok) * d.o_b + int64_t(head) * d.o_h + 2 * c0;
-        if (d.out_vec_ok) {
-            reinterpret_cast<uint4 *>(o)[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-            reinterpret_cast<uint4 *>(o)[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                reinterpret_cast<uint16_t *>(o)[j] = uint16_t(pk[j >> 1] >> (16 * (j & 1)));
-        }
+        mine = __ballot_sync(0xffffffffu, redo);
+        if (lane == 0) todo[warp] = mine;
     }
-    unsigned todo = __ballot_sync(0xffffffffu, redo);
-    while (todo) {
-        const int who = __ffs(todo) - 1;
-        todo &= todo - 1;
-        redo_row<QK, CK, D>(d, d.block_tables + ds.x * d.bt_b, int64_t(s.s0) + __shfl_sync(0xffffffffu, tok, who),
-                            __shfl_sync(0xffffffffu, head, who), __shfl_sync(0xffffffffu, lim, who),
-                            min(s.ctx, tile_units(tile_limit(p, s, ds.z)) * kKeyTile), c0, c0 + 16);
-    }
+    if (__syncthreads_or(again | int(mine != 0u))) redo_rows<QK, CK, D>(p, f, todo);
 }
 
 }  // namespace

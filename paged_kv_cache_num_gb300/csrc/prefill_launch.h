@@ -7,6 +7,13 @@
 
 namespace pkv {
 
+// A CTA's share of the work, as find_start finds it.
+struct PrefillStart {
+    int64_t u0, u1, total;      // this CTA's cost units, all of them
+    int ctas;                   // CTAs that have work
+    int b, h, tile, at;
+};
+
 struct PrefillLaunch {
     const PrefillParams *p;
     int grid;
@@ -14,7 +21,7 @@ struct PrefillLaunch {
     bool tma;                   // K/V, or their raw codes, by TMA (tmk, tmv)
     int raw_unit;               // else raw codes by copies; 3-bit rows in pieces of 8 bytes, 4 or 1
     int out32;                  // output rows at multiples of 32 bytes
-    void *desc, *part_ml, *part_acc;
+    void *desc, *starts, *redo, *part_ml, *part_acc;
     bool q_tma;                 // Q by TMA (tmq)
     bool flip_q;                // the kernel gives a negative scale's sign to Q where it converts it
     CUtensorMap tmk, tmv, tmq;
