@@ -121,7 +121,10 @@ constexpr int kScaleExp = 80;
 // log2 of a scale, at most 1 above it, from its biased exponent
 __device__ __forceinline__ float scale_exp(uint32_t e) { return float(min(max(int(e) - 126, -kScaleExp), kScaleExp)); }
 constexpr int kBins = 1024;
-constexpr uint64_t kPrefillTimeoutNs = 4000000000ull;
+// A wait gives up after this long and as much again for each key tile of the
+// table's rows: some waits last a whole segment (2^24 key tiles at the longest,
+// about 1 us each; 5 us in the slowest form).
+constexpr uint64_t kPrefillTimeoutNs = 4000000000ull, kPrefillTimeoutTileNs = 50000ull;
 
 // One (sequence)'s lengths, cleaned: n = 0 for a sequence that is left out.
 struct Seq {
@@ -376,14 +379,15 @@ struct Bars {
     __device__ __forceinline__ uint32_t raw_empty(int s) const { return base + 8 * (4 * stages + 18 + raws + s); }
 };
 
-// Wait for a phase, giving up when it takes too long or another warp gave up.
+// Wait for a phase, giving up when it takes too long (the limit lies behind
+// `gone`) or another warp gave up.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *gone)
 {
     if (ptx::mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = ptx::globaltimer();
     uint32_t n = 0;
     while (!ptx::mbar_try_wait(bar, parity)) {
-        if ((++n & 15u) == 0 && (*gone || ptx::globaltimer() - t0 > kPrefillTimeoutNs)) {
+        if ((++n & 15u) == 0 && (*gone || ptx::globaltimer() - t0 > *reinterpret_cast<volatile uint64_t *>(gone + 4))) {
             *gone = 1;
             return false;
         }
@@ -968,6 +972,8 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
         ptx::mbar_init(bars.tail(), 1);
         ptx::fence_mbar_init();
         *gone = 0;
+        *reinterpret_cast<volatile uint64_t *>(gone + 4) =
+            kPrefillTimeoutNs + kPrefillTimeoutTileNs * uint64_t((int64_t(d.max_blocks) << d.block_shift) / kKeyTile);
         *not_finite = 0;
     }
     if (threadIdx.x < 16 * L::kColSlots) (cols[threadIdx.x / 16].vexp)[threadIdx.x % 16] = 0u;
