@@ -1123,6 +1123,11 @@ decode_tma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             }
             // ---------------- online softmax per q head (columns), log2 units
             const bool partial = valid < BS;   // only a sequence's last block
+            // With V scales per block or token P' = weight times scale is what
+            // is packed to f16, so the running max is that of score +
+            // log2(scale), by the scale's exponent: P' is then at most about
+            // one, whatever the scales, and its largest term keeps its bits.
+            // (The sums of weights have the same reference.)
             // one group of head columns: scores scg, running max mg / sums lg,
             // int8 offsets zsg / q1g, accumulators og; P^T as the B operand of
             // the PV product in pbg: each 8-token half of a tile (rows =
@@ -1131,6 +1136,14 @@ decode_tma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             auto softmax_group = [&](float (*scg)[4], float *mg, float *lg, float *zsg, const float *q1g,
                                      uint32_t (*pbg)[2], float (*og)[4]) {
                 float mx[2] = {NEG_INF, NEG_INF};
+                [[maybe_unused]] float vexp[T::KT][2];
+                if constexpr (T::kFp8 && gscale) {
+#pragma unroll
+                    for (int t = 0; t < T::KT; ++t)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r)
+                            vexp[t][r] = scale_exp((__float_as_uint(row_vs(16 * t + gid + 8 * r)) >> 23) & 0xffu);
+                }
 #pragma unroll
                 for (int t = 0; t < T::KT; ++t) {
 #pragma unroll
@@ -1142,6 +1155,7 @@ decode_tma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                             v = tok < valid ? v : NEG_INF;
                         }
                         scg[t][e] = v;
+                        if constexpr (T::kFp8 && gscale) v += vexp[t][e >> 1];
                         mx[e & 1] = fmaxf(mx[e & 1], v);
                     }
                 }

@@ -114,12 +114,9 @@ constexpr int kTurnTiles = 16;
 // of the warp sees all of it, the tile's maxima of score and scale bound L from above by at
 // most 2^(kScaleSpread + 1); else each row takes its maximum column by column
 // over the keys that it sees, with the scales' exponents, in a pass of its own.
-// Exponents are clamped to +-kScaleExp: the sum of weights, relative to the same
+// Exponents are clamped (scale_exp): the sum of weights, relative to the same
 // reference, then stays below 2^(80 + 8 + 31).
 constexpr int kScaleSpread = 4;
-constexpr int kScaleExp = 80;
-// log2 of a scale, at most 1 above it, from its biased exponent
-__device__ __forceinline__ float scale_exp(uint32_t e) { return float(min(max(int(e) - 126, -kScaleExp), kScaleExp)); }
 constexpr int kBins = 1024;
 // A wait gives up after this long and as much again for each key tile of the
 // table's rows: some waits last a whole segment (2^24 key tiles at the longest,
