@@ -1187,7 +1187,12 @@ decode_tma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                         lg[0] += p0;
                         lg[1] += p1;
                         // per-block / per-token V scales fold into P' = p * scale
-                        const float vsr = T::kFp8 && gscale ? row_vs(16 * t + gid + 8 * r) : 1.0f;
+                        // (those behind the context may hold anything)
+                        float vsr = 1.0f;
+                        if constexpr (T::kFp8 && gscale) {
+                            const int tok = 16 * t + gid + 8 * r;
+                            vsr = partial && tok >= valid ? 0.0f : row_vs(tok);
+                        }
                         float q0, q1;
                         const uint32_t w = T::kBF ? pack_bf16(p0, p1, q0, q1) : pack_f16(p0 * vsr, p1 * vsr, q0, q1);
                         if constexpr (CK == kI8) {   // the PV operand's offset: sum of P' as rounded
