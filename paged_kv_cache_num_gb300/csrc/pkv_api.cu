@@ -769,7 +769,7 @@ int check_prefill_common(const pkv_tensor *q, const pkv_cache *cache, const pkv_
     d.q_is_bf16 = q->dtype == PKV_DTYPE_BF16;
     p.num_tokens = int(T);
     p.sub_rows = d.group <= 128 ? 128 / d.group * d.group : 128;
-    pc.plan = pkv::plan_prefill(p, ci.kind, pkv::sm_count_current_device());
+    pc.plan = pkv::plan_prefill(p, pkv::sm_count_current_device());
     return PKV_OK;
 }
 

@@ -210,7 +210,7 @@ struct PrefillPlan {
     size_t workspace_bytes;
 };
 
-PrefillPlan plan_prefill(const PrefillParams &p, int cache_kind, int sm_count);
+PrefillPlan plan_prefill(const PrefillParams &p, int sm_count);
 cudaError_t launch_prefill(const PrefillParams &p, const PrefillPlan &plan, int cache_kind, void *ws, cudaStream_t s);
 
 // ---------------------------------------------------------------- pack3 / copy

@@ -92,7 +92,7 @@ size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
-PrefillPlan plan_prefill(const PrefillParams &p, int, int sm_count)
+PrefillPlan plan_prefill(const PrefillParams &p, int sm_count)
 {
     PrefillPlan pl{};
     const DecodeParams &d = p.d;

@@ -331,17 +331,21 @@ struct Smem {
     static_assert(kStages * kTile >= (kBins + 1) * 8, "bins lie in the ring");
     static_assert(kRaw <= 8, "info");
     static_assert(alloc <= 232448, "shared memory of a CTA");
+    static_assert(kColSlots >= kStages / 2 + 2, "see ColSlot");
     static_assert(sizeof(Start) <= 96, "misc");
 };
 
 // Column data of a key tile: scales of its 128 K and V rows and the V scales'
 // exponents, their range by producer warp, and which groups of 8 rows are there.
-// Tile T's is written once the ring has room for K of tile T.  With a ring of
-// R tiles of K that is when the scores of tile T - R are done; the tiles whose
-// softmax may still be under way then are fewer than 2 R + 2 (each subtile has
-// one, at most a tile's worth of the ring behind the other), and with three
-// (six) stages, where V of tile T - 2 (T - 4) is done too, fewer than 3 (5).
-// So 16-bit caches have 8 (head_dim 64: 16) slots, coded ones 4 (8).
+// Tile T's is written once the ring has room for K of tile T.
+//   K and V in rings of their own, R = stages / 2 tiles each: the scores of tile
+//   T - R are done, and (row tiles of one subtile) those of T - R - 1 by the other
+//   warpgroup; whoever issued them had finished the softmax of its tile before.
+//   So the softmax of T - R - 1 is the earliest that may be under way.
+//   One ring in the order K, V, K, V ...: V of tile T - 1 has had room (with three
+//   stages K of tile T itself), in the place of V of tile T - R - 1, so that tile's
+//   product with it is done, and its softmax before that.
+// In either case the column data of at most R + 2 tiles, T's included, is in use.
 struct ColSlot {
     float k[kKeyTile];
     float v[kKeyTile];
@@ -1027,7 +1031,7 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                         }
                         // exponents that keep both powers of two normal; the sign of the scale goes along
                         const int e = min(max(int(top >> 23), 16), 254);
-                        const float s = __uint_as_float(uint32_t(127 + 14 + 127 - e > 254 ? 254 : 268 - e) << 23);
+                        const float s = __uint_as_float(uint32_t(268 - e) << 23);
                         back = __uint_as_float(uint32_t(254 - (__float_as_uint(s) >> 23)) << 23);
                         const float sg = f.flip_q ? -s : s;
 #pragma unroll 4

@@ -26,52 +26,9 @@ __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols)
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-#define PKV_R32(r, o)                                                                                              \
-    "r"((r)[(o) + 0]), "r"((r)[(o) + 1]), "r"((r)[(o) + 2]), "r"((r)[(o) + 3]), "r"((r)[(o) + 4]),                 \
-        "r"((r)[(o) + 5]), "r"((r)[(o) + 6]), "r"((r)[(o) + 7]), "r"((r)[(o) + 8]), "r"((r)[(o) + 9]),             \
-        "r"((r)[(o) + 10]), "r"((r)[(o) + 11]), "r"((r)[(o) + 12]), "r"((r)[(o) + 13]), "r"((r)[(o) + 14]),        \
-        "r"((r)[(o) + 15]), "r"((r)[(o) + 16]), "r"((r)[(o) + 17]), "r"((r)[(o) + 18]), "r"((r)[(o) + 19]),        \
-        "r"((r)[(o) + 20]), "r"((r)[(o) + 21]), "r"((r)[(o) + 22]), "r"((r)[(o) + 23]), "r"((r)[(o) + 24]),        \
-        "r"((r)[(o) + 25]), "r"((r)[(o) + 26]), "r"((r)[(o) + 27]), "r"((r)[(o) + 28]), "r"((r)[(o) + 29]),        \
-        "r"((r)[(o) + 30]), "r"((r)[(o) + 31])
-#define PKV_W32(c, r, o)                                                                                           \
-    c((r)[(o) + 0]), c((r)[(o) + 1]), c((r)[(o) + 2]), c((r)[(o) + 3]), c((r)[(o) + 4]), c((r)[(o) + 5]),          \
-        c((r)[(o) + 6]), c((r)[(o) + 7]), c((r)[(o) + 8]), c((r)[(o) + 9]), c((r)[(o) + 10]), c((r)[(o) + 11]),    \
-        c((r)[(o) + 12]), c((r)[(o) + 13]), c((r)[(o) + 14]), c((r)[(o) + 15]), c((r)[(o) + 16]),                  \
-        c((r)[(o) + 17]), c((r)[(o) + 18]), c((r)[(o) + 19]), c((r)[(o) + 20]), c((r)[(o) + 21]),                  \
-        c((r)[(o) + 22]), c((r)[(o) + 23]), c((r)[(o) + 24]), c((r)[(o) + 25]), c((r)[(o) + 26]),                  \
-        c((r)[(o) + 27]), c((r)[(o) + 28]), c((r)[(o) + 29]), c((r)[(o) + 30]), c((r)[(o) + 31])
-
-// 32 columns of the warp's 32 lanes: thread = lane (row), register = column.
-// The registers hold the data only after tmem_ld_wait32 on them.
-template <int N>
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[N], int o)
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : PKV_W32("=r", r, o)
-        : "r"(addr));
-}
-
-// wait for this thread's tensor-memory loads; names the registers so that
-// nothing reads them before it
-template <int N>
-__device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[N], int o)
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;" : PKV_W32("+r", r, o)::"memory");
-}
-
-template <int N>
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[N], int o)
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
-        PKV_R32(r, o)
-        : "memory");
-}
-
+// Columns of the warp's 32 lanes: thread = lane (row), register = column.  The
+// registers hold the data only after tmem_ld_wait on them, which names them so
+// that nothing reads them before it.
 #define PKV_W16(c, r)                                                                                              \
     c((r)[0]), c((r)[1]), c((r)[2]), c((r)[3]), c((r)[4]), c((r)[5]), c((r)[6]), c((r)[7]), c((r)[8]), c((r)[9]),  \
         c((r)[10]), c((r)[11]), c((r)[12]), c((r)[13]), c((r)[14]), c((r)[15])
@@ -114,11 +71,8 @@ __device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8])
 }
 
 // by the array's length
-__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[32]) { tmem_ld32(addr, r, 0); }
 __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[16]) { tmem_ld16(addr, r); }
-__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) { tmem_ld_wait32(r, 0); }
 __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16]) { tmem_ld_wait16(r); }
-__device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[32]) { tmem_st32(addr, r, 0); }
 __device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[16]) { tmem_st16(addr, r); }
 __device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[8]) { tmem_st8(addr, r); }
 
