@@ -316,7 +316,8 @@ int pkv_kv_gather(const pkv_cache *cache, const pkv_tensor *slot_mapping, const 
  *   hold.  Supported: every cache dtype, layout and scale granularity;
  *   head_dim 64 or 128; block_size a power of two from 8 to 256; num_heads a
  *   multiple of num_kv_heads; num_tokens * (num_heads / num_kv_heads) <
- *   2^30; batch < 2^20.  The products take F16 / BF16 rows
+ *   2^30; batch < 2^20; at most 2^31 - 256 tokens to a block table's row.  The
+ *   products take F16 / BF16 rows
  *   as they are and codes exactly as F16; BF16 queries of a coded cache
  *   become F16 by a power of two per row (exactly but for elements below
  *   2^-31 of the row's largest, which are off by at most 2^-39 of it);

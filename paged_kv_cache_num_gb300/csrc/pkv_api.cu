@@ -748,8 +748,9 @@ int check_prefill_common(const pkv_tensor *q, const pkv_cache *cache, const pkv_
     if (T * (heads / ci.num_kv_heads) >= (int64_t(1) << 30))
         return fail(PKV_ERR_UNSUPPORTED, "num_tokens * group must be below 2^30");
     if (batch >= (1 << 20)) return fail(PKV_ERR_UNSUPPORTED, "batch must be below 2^20");
-    if (block_tables->shape[1] * ci.block_size >= (int64_t(1) << 31))
-        return fail(PKV_ERR_UNSUPPORTED, "block table rows must cover fewer than 2^31 tokens");
+    // token numbers, rounded up to whole key tiles, stay within 32 bits
+    if (block_tables->shape[1] * ci.block_size > (int64_t(1) << 31) - 256)
+        return fail(PKV_ERR_UNSUPPORTED, "block table rows must cover at most 2^31 - 256 tokens");
     pkv::PrefillParams &p = pc.p;
     p = pkv::PrefillParams{};
     pkv::DecodeParams &d = p.d;
