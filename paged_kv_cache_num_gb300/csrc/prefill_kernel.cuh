@@ -1283,7 +1283,12 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                         off = top;
                     }
                     float fac = 1.0f;
-                    if constexpr (is_q8(CK) && !GS) fac = d.v_scale[w.h];
+                    if constexpr (is_q8(CK) && !GS) {
+                        fac = d.v_scale[w.h];
+                        // a K scale that is NaN is seen by every row with a key; kept out of c, where
+                        // it would meet masked scores
+                        if (isnan(d.k_scale[w.h])) fac = d.k_scale[w.h];
+                    }
                     if (whole) fac = l == 0.0f ? 0.0f : fac / l;
                     w0 *= fac;
                     w1 *= fac;

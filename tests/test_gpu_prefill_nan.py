@@ -82,3 +82,21 @@ def test_a_part_of_no_weight(pkv, what, value, ctx):
         assert torch.isnan(attend(pkv, q, cache, bt, [1], [ctx])).all()
     else:                                    # a score of +infinity
         assert not torch.isfinite(attend(pkv, q, cache, bt, [1], [ctx])).any()
+
+
+@pytest.mark.parametrize("what", ["k_scale", "v_scale"])
+@pytest.mark.parametrize("kind", ["e4m3", "i8"])
+def test_a_nan_scale_of_a_head(pkv, kind, what):
+    """Rows of that head's q heads are NaN, but for those that see no key."""
+    H, G, D, BS, new, ctx = 2, 4, 128, 16, [40, 30, 150], [40, 5, 2000]
+    bt, P = R.tables(ctx, BS, seed=9)
+    cache, kv, vv = R.make_cache(pkv, kind, P, BS, H, D, seed=10)
+    q = torch.randn((sum(new), H * G, D), generator=torch.Generator().manual_seed(11)).bfloat16()
+    want = attend(pkv, q, cache, bt, new, ctx)
+    getattr(cache, what)[1] = float("nan")
+    out = attend(pkv, q, cache, bt, new, ctx)
+    blind = slice(40, 40 + 25)
+    assert torch.equal(out[:, :G], want[:, :G]) and (out[blind] == 0).all()
+    sees = torch.ones(sum(new), dtype=torch.bool)
+    sees[blind] = False
+    assert torch.isnan(out[sees][:, G:]).all()
