@@ -64,7 +64,8 @@ struct PrefillFast {
     int4 *desc;                 // [grid] (sequence, kv head, row tile, last CTA) of the row tile split at a CTA's end
     int *redo;                  // [grid] whether the CTA has written rows that are not finite
     Start *starts;              // [grid] ... and then its share
-    int later;                  // such rows are looked through by the join kernel (else at once)
+    int later;                  // the join kernel looks through them (else the CTA itself, at its end: there is no
+                                // join kernel where the table holds one key tile to a sequence)
     float *part_ml;             // [2 grid][2][256]
     float *part_acc;            // [2 grid][D / 4][256][4]
     int out32;                  // output rows at multiples of 32 bytes
@@ -916,6 +917,29 @@ __device__ __forceinline__ void convert_rows(const PrefillParams &p, const Start
     }
 }
 
+// ---------------------------------------------------------------- rows that are not finite
+// The whole row tiles of a CTA's share, warp `me` of `warps` in turn, `n` rows
+// (modulo `warps`) having been dealt before; returns that for the next share.  Out of
+// line: called where the output warps had written the row, it cost them
+// registers (packed prompts 165 -> 171 us).
+template <int QK, int CK, int D, int U>
+__device__ __noinline__ int redo_share(const PrefillParams &p, const Start &st, int n, int me, int warps)
+{
+    const DecodeParams &d = p.d;
+    Walk w = walk_from(p, st);
+    do {
+        if (w.k0 != 0 || w.k1 != w.units) continue;             // joined from several CTAs: see redo_rows
+        const int r0 = w.tile * 2 * p.sub_rows, rows = min(2 * p.sub_rows, w.s.rows - r0);
+        for (int i = (me - n + warps) % warps; i < rows; i += warps) {
+            const int r = r0 + i, tok = r / d.group;
+            redo_row<QK, CK, D, U>(d, d.block_tables + w.b * d.bt_b, int64_t(w.s.s0) + tok,
+                                   w.h * d.group + (r - tok * d.group), row_limit(p, w.s, r), w.reach());
+        }
+        n = (n + rows) % warps;
+    } while (w.next(p));
+    return n;
+}
+
 // ---------------------------------------------------------------- the kernel
 // Warps 0-7 softmax; 16-bit caches by TMA: 8 and 9 products, 10 K and Q, 11 V,
 // 12-15 output; the others: 8-11 producers, 12 and 13 products, 14 raw codes,
@@ -1363,20 +1387,9 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                         ptx::mbar_arrive(bars.e_empty(sub));
                         if (join) ptx::mbar_arrive(bars.e_empty(1));
                     }
-                    // not finite: weights of zero may have met values that are not; such a row is done
-                    // again by itself, here (with at most a key tile to a row) or by the join kernel
-                    unsigned redo = __ballot_sync(0xffffffffu, whole && live && bad != 0.0f);
-                    if (f.later) {
-                        if (redo && lane == 0) *not_finite = 1;
-                        redo = 0;
-                    }
-                    while (redo) {
-                        const int who = __ffs(redo) - 1;
-                        redo &= redo - 1;
-                        const int rr = __shfl_sync(0xffffffffu, r, who), tt = rr / d.group;
-                        redo_row<QK, CK, D, 1>(d, d.block_tables + w.b * d.bt_b, int64_t(w.s.s0) + tt,
-                                            w.h * d.group + (rr - tt * d.group), row_limit(p, w.s, rr), w.reach());
-                    }
+                    // not finite: weights of zero may have met values that are not.  Such rows are done
+                    // again later (see redo_row)
+                    if (__any_sync(0xffffffffu, whole && live && bad != 0.0f) && lane == 0) *not_finite = 1;
                 }
             } while (ok && w.next(p));
         }
@@ -1591,9 +1604,13 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
         }
     }
     __syncthreads();
-    if (f.later && threadIdx.x == 0) {
-        f.redo[blockIdx.x] = *not_finite;
-        if (*not_finite) f.starts[blockIdx.x] = *start;
+    if (f.later) {
+        if (threadIdx.x == 0) {
+            f.redo[blockIdx.x] = *not_finite;
+            if (*not_finite) f.starts[blockIdx.x] = *start;
+        }
+    } else if (*not_finite) {
+        redo_share<QK, CK, D, 1>(p, *start, 0, warp, prefill_threads<CK, FEED>() / 32);
     }
     if (*gone) {
         // copies and products under way end by themselves
@@ -1642,21 +1659,9 @@ __device__ __noinline__ void redo_rows(const PrefillParams &p, const PrefillFast
         }
     }
     const int warps = gridDim.x * gridDim.y * kJoinWarps, me = (blockIdx.y * gridDim.x + blockIdx.x) * kJoinWarps + warp;
-    int n = 0;                                      // rows of the tiles before, modulo `warps`
-    for (int c = 0; c < int(gridDim.x); ++c) {
-        if (!f.redo[c]) continue;
-        Walk w = walk_from(p, f.starts[c]);
-        do {
-            if (w.k0 != 0 || w.k1 != w.units) continue;         // joined: by its first CTA's blocks
-            const int r0 = w.tile * 2 * p.sub_rows, rows = min(2 * p.sub_rows, w.s.rows - r0);
-            for (int i = (me - n + warps) % warps; i < rows; i += warps) {
-                const int r = r0 + i, tok = r / d.group;
-                redo_row<QK, CK, D, 4>(d, d.block_tables + w.b * d.bt_b, int64_t(w.s.s0) + tok,
-                                    w.h * d.group + (r - tok * d.group), row_limit(p, w.s, r), w.reach());
-            }
-            n = (n + rows) % warps;
-        } while (w.next(p));
-    }
+    int n = 0;
+    for (int c = 0; c < int(gridDim.x); ++c)
+        if (f.redo[c]) n = redo_share<QK, CK, D, 4>(p, f.starts[c], n, me, warps);
 }
 
 // Joins the row tile that CTA blockIdx.x begins and a later one ends: with
