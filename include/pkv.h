@@ -378,7 +378,8 @@ int pkv_paged_prefill(const pkv_tensor *q, const pkv_cache *cache, const pkv_ten
  *   Grouped-query mapping: q head h reads kv head h / (num_heads /
  *   num_kv_heads).  Output = softmax(sm_scale * q . K^T) V over the first
  *   context_len tokens, with the dequantised K/V for E4M3 and U3 caches,
- *   accumulated in fp32 and rounded once to the output dtype.  Cache
+ *   accumulated in fp32 and rounded once to the output dtype (V scales per
+ *   block or token: from 2^-40 to 2^40; below 2^-40 bits are lost).  Cache
  *   contents beyond context_len (the tail of the last block) never affect
  *   the output, whatever they hold.
  *   Supported: head_dim in {64, 128}, block_size in {8, 16, 32, 64},

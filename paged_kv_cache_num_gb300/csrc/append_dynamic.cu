@@ -17,8 +17,8 @@
 // RN(x / s) through the correctly rounded reciprocal r = RN(1 / s): q = x r,
 // then q + (x - q s) r, the residual exact in one FMA (Markstein's
 // refinement).  For x and a of at most 11 significant bits and s = RN(a /
-// qmax), a and |x| <= a, that is the division's result for every pair of
-// significands and each qmax (all 108 million pairs down to 2^-34 a compared).
+// qmax), that is the division's result for every pair of significands and each
+// qmax (a test compares all of them; powers of two change nothing).
 // The residual must not underflow: s >= 2^-80 keeps it exact for every
 // quotient that a cast sees (2^-17 and above).  Rows below that, and rows with
 // infinities or NaN, take the division instruction.  The residual's sign is

@@ -1127,7 +1127,10 @@ decode_tma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             // is packed to f16, so the running max is that of score +
             // log2(scale), by the scale's exponent: P' is then at most about
             // one, whatever the scales, and its largest term keeps its bits.
-            // (The sums of weights have the same reference.)
+            // (The sums of weights have the same reference, and may be as small
+            // as 2^-40 and as large as 2^40 for a key.  A factor between two
+            // references that underflows, 2^-127, then leaves nothing that counts;
+            // with exponents clamped to more than 40 it could.)
             // one group of head columns: scores scg, running max mg / sums lg,
             // int8 offsets zsg / q1g, accumulators og; P^T as the B operand of
             // the PV product in pbg: each 8-token half of a tile (rows =
@@ -1142,7 +1145,7 @@ decode_tma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                     for (int t = 0; t < T::KT; ++t)
 #pragma unroll
                         for (int r = 0; r < 2; ++r)
-                            vexp[t][r] = scale_exp((__float_as_uint(row_vs(16 * t + gid + 8 * r)) >> 23) & 0xffu);
+                            vexp[t][r] = scale_exp<40>((__float_as_uint(row_vs(16 * t + gid + 8 * r)) >> 23) & 0xffu);
                 }
 #pragma unroll
                 for (int t = 0; t < T::KT; ++t) {

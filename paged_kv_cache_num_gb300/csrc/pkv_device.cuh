@@ -38,10 +38,10 @@ __device__ __forceinline__ float exp2_approx(float x)
     return y;
 }
 
-// log2 of a scale, at most 1 above it, from its biased exponent, within +-80:
-// what a softmax's reference takes of V scales whose products with the weights
-// are packed to 16 bits
-__device__ __forceinline__ float scale_exp(uint32_t e) { return float(min(max(int(e) - 126, -80), 80)); }
+// log2 of a scale, at most 1 above it, from its biased exponent, within +-K: what
+// a softmax's reference takes of V scales whose products with the weights are
+// packed to 16 bits
+template <int K> __device__ __forceinline__ float scale_exp(uint32_t e) { return float(min(max(int(e) - 126, -K), K)); }
 
 // 16-bit element <-> float
 template <int KIND> __device__ __forceinline__ float h2f(uint16_t v);

@@ -30,7 +30,7 @@
 // subtile's scores wait for its last P V (they share tensor memory), which
 // waits for its softmax, so that chain bounds the tile rate (about 3400 clocks
 // per pair of subtiles, whose products alone take 2048; 12001-token prompt, 32
-// q over 8 kv heads: 0.88 to 0.90 ms, 1310 to 1340 TFLOP/s, 0.69 of the
+// q over 8 kv heads: 0.86 to 0.91 ms, 1290 to 1370 TFLOP/s, 0.68 to 0.72 of the
 // measured cuBLAS rate).  A row tile of at most 128 rows has one subtile: then
 // the warpgroups take its key tiles in turn, with states of their own that are
 // joined at the end; few rows over long contexts run at HBM's rate that way.
@@ -88,24 +88,24 @@ template <int CK, int FEED> constexpr int prefill_threads()
 
 constexpr int kRowTile = 256;   // rows of a row tile, those between a subtile's whole tokens and 128 included
 // Beginning and ending a row tile costs as much as this many units.  (16 prompts
-// of 60 to 1500 tokens: 155, 156, 162, 167 us with 1, 2, 3, 4; few tokens over
-// long contexts: 70, 67, 66, 65 us.)
+// of 60 to 1500 tokens, times relative to that with 2: 0.99, 1, 1.04, 1.07 with 1, 2, 3,
+// 4; few tokens over long contexts: 1.04, 1, 0.99, 0.97.)
 constexpr int kTileCost = 2;
 constexpr int kKeyTile = 128;
 // P is handed to its product after this many keys and after all.  The early
 // hand-over gets the issuing warp past its waits for V and for the
 // accumulators while the other weights are made; the fewer keys go with it, the
 // less the two subtiles' products are cut up in the tensor core's queue (a
-// 12001-token prompt: 833 us with 16, 856 with 32, 921 with 64, 952 with 96,
-// 904 without; a third hand-over in between 914 to 947).
+// 12001-token prompt, times relative to that with 16: 1.03 with 32, 1.11 with 64, 1.14
+// with 96, 1.09 without; a third hand-over in between 1.10 to 1.14).
 constexpr int kFirst = 16;
 // In long segments the two subtiles' softmax take turns: run at the same time
 // they share the exponential unit and then leave it idle together while both
-// wait for products (12001-token prompt: 846 to 972 us without, depending on
-// how the two happen to fall, 845 to 861 us with; e4m3 chunks 667 to 629 us).
-// In short segments the order costs more than it brings (packed prompts 157
-// us without, 177 with), and so it does with scales per row, whose softmax is
-// long enough by itself (3-bit chunks 180 us without, 216 with).
+// wait for products (12001-token prompt: without 0.99 to 1.14 of the time with,
+// depending on how the two happen to fall; e4m3 chunks 1.06).  In short segments
+// the order costs more than it brings (packed prompts 1.13 of the time without),
+// and so it does with scales per row, whose softmax is long enough by itself
+// (3-bit chunks 1.2).
 constexpr int kTurnTiles = 16;
 // Scales per row: weights times V scales become the second product's operand, so
 // they are held relative to their own largest value, L = max of weight times
@@ -115,9 +115,12 @@ constexpr int kTurnTiles = 16;
 // of the warp sees all of it, the tile's maxima of score and scale bound L from above by at
 // most 2^(kScaleSpread + 1); else each row takes its maximum column by column
 // over the keys that it sees, with the scales' exponents, in a pass of its own.
-// Exponents are clamped (scale_exp): the sum of weights, relative to the same
-// reference, then stays below 2^(80 + 8 + 31).
+// Exponents are clamped to +-kScaleExp: the sum of weights l, relative to the same
+// reference, then stays below 2^(80 + 8 + 31).  It can be as small as 2^-80, so where
+// the reference moves l is scaled in two steps: a factor of 2^-130 is nothing to
+// O, but may leave l the larger part.
 constexpr int kScaleSpread = 4;
+constexpr int kScaleExp = 80;
 constexpr int kBins = 1024;
 // A wait gives up after this long and as much again for each key tile of the
 // table's rows: some waits last a whole segment (2^24 key tiles at the longest,
@@ -825,7 +828,7 @@ __device__ __forceinline__ void convert_rows(const PrefillParams &p, const Start
                     cs.k[row] = value(ks);
                     cs.v[row] = value(vs);
                     const uint32_t e = (__float_as_uint(value(vs)) >> 23) & 0xffu;
-                    cs.v_log2[row] = scale_exp(e);
+                    cs.v_log2[row] = scale_exp<kScaleExp>(e);
                     const uint32_t hi = __reduce_max_sync(0xffffffffu, e), lo = __reduce_min_sync(0xffffffffu, e);
                     if (lane == 0) cs.vexp[lw] = (hi << 16) | (255u - lo);
                 }
@@ -1196,17 +1199,23 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                             }
                             tc::tmem_st_wait();
                         } else {
-                            top = fmaf(top, c, scale_exp(ve >> 16));
+                            top = fmaf(top, c, scale_exp<kScaleExp>(ve >> 16));
                         }
                         tc::tmem_ld(ts, x[0]);
                     }
                     float grow = 1.0f;                          // what O and l shrink by
                     const float unit = GS ? 1.0f : c;
                     if (top > m && (m == ninf || (top - m) * unit > 8.0f)) {
-                        grow = m == ninf ? 0.0f : exp2_approx((m - top) * unit);
+                        if constexpr (GS) {                     // l in two steps: see kScaleSpread
+                            const float h = m == ninf ? 0.0f : exp2_approx(0.5f * (m - top));
+                            grow = h * h;
+                            l = l * h * h;
+                        } else {
+                            grow = m == ninf ? 0.0f : exp2_approx((m - top) * c);
+                            l *= grow;
+                        }
                         m = top;
                     }
-                    l *= grow;
                     if (j > j0 && __any_sync(0xffffffffu, grow != 1.0f)) {
                         // seldom: a rolled loop keeps its registers out of the way
 #pragma unroll 1
@@ -1303,7 +1312,13 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                         const float top = fmaxf(off, m1);
                         w0 = !use0 ? 0.0f : off == ninf ? l : exp2_approx(off - top);
                         w1 = !use1 ? 0.0f : m1 == ninf ? l1 : exp2_approx(m1 - top);
-                        l = fmaf(l, w0, l1 * w1);
+                        if constexpr (GS) {                     // in two steps, as everywhere
+                            const float h0 = !use0 || off == ninf ? w0 : exp2_approx(0.5f * (off - top));
+                            const float h1 = !use1 || m1 == ninf ? w1 : exp2_approx(0.5f * (m1 - top));
+                            l = fmaf(l * h0, h0, l1 * h1 * h1);
+                        } else {
+                            l = fmaf(l, w0, l1 * w1);
+                        }
                         off = top;
                     }
                     float fac = 1.0f;
@@ -1705,11 +1720,11 @@ __global__ void __launch_bounds__(kRowTile, 2) prefill_join_kernel(const __grid_
             for (int j = 0; j < 16; ++j) acc[j] = 0.0f;
             for (int i = first; i <= last; ++i) {
                 const float *ml = f.part_ml + slot(i) * 2 * kRowTile + row;
-                const float wgt = ml[0] == ninf ? 0.0f : exp2_approx(ml[0] - m);
+                const float half = ml[0] == ninf ? 0.0f : exp2_approx(0.5f * (ml[0] - m)), wgt = half * half;
                 const float li = ml[kRowTile];
                 // a part without keys (l = 0) has no O, whatever lies there
                 if (li == 0.0f) continue;
-                l = fmaf(li, wgt, l);
+                l = fmaf(li * half, half, l);       // in two steps: see kScaleSpread
                 const float4 *a = reinterpret_cast<const float4 *>(f.part_acc) + (slot(i) * (D / 4) + c0 / 4) * kRowTile + row;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {

@@ -86,3 +86,23 @@ def test_all_scales_small_or_large(pkv, kind, scales, bits):
     cache, kv, vv = S.coded_cache(pkv, kind, scales, ks, vs, D, seed=7)
     q = torch.randn((len(ctx), H * G, D), generator=torch.Generator().manual_seed(8)).bfloat16()
     compare(pkv, q, cache, kv, vv, vs, bt, ctx, kind, ks=float(ks.max()))
+
+
+@pytest.mark.parametrize("first", ["heavy", "large"])
+@pytest.mark.parametrize("c", [100, 3000])
+def test_weights_and_scales_at_opposite_ends(pkv, c, first):
+    """Half of the context has nearly all the weight and V scales of 2^-38, the
+    other half next to none and scales of 2^38."""
+    H, G, D, BS = 4, 4, 128, 16
+    bt, P = R.tables([c], BS, seed=9)
+    heavy = torch.arange(c) < c // 2 if first == "heavy" else torch.arange(c) >= c // 2
+    blk, off = bt[0].long()[torch.arange(c) // BS], torch.arange(c) % BS
+    ks, vs = torch.full((P, BS, H), 2.0 ** -20), torch.full((P, BS, H), 2.0 ** 38)
+    ks[blk[heavy], off[heavy]] = 2.0 ** -4
+    vs[blk[heavy], off[heavy]] = 2.0 ** -38
+    cache, kv, vv = S.coded_cache(pkv, "e4m3", "token", ks, vs, D, seed=10)
+    code = torch.full((), 4.0).to(torch.float8_e4m3fn).view(torch.uint8)
+    cache.k_cache.view(torch.uint8)[blk[heavy].to(DEV), off[heavy].to(DEV)] = int(code)
+    kv[blk[heavy], off[heavy]] = 4.0 * 2.0 ** -4
+    q = (torch.randn((1, H * G, D), generator=torch.Generator().manual_seed(11)).abs() * 2).bfloat16()
+    compare(pkv, q, cache, kv, vv, vs, bt, [c], "e4m3")

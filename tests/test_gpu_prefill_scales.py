@@ -201,3 +201,26 @@ def test_padded_pool_scales(pkv):
         q = queries(sum(new), H * G, D, torch.bfloat16, 24)
         st, out = attend(pkv, q, cache, bt, new, ctx)
         compare(out, q, kv, vv, vs, bt, st, ctx, kind, torch.bfloat16)
+
+
+@pytest.mark.parametrize("first", ["heavy", "large"])
+@pytest.mark.parametrize("n,c", [(1, 300), (40, 300), (300, 700), (2, 9000)])
+def test_weights_and_scales_at_opposite_ends(pkv, n, c, first):
+    """Half of the context has nearly all the weight and V scales of 2^-70, the
+    other half next to none and scales of 2^70: the sum of weights is the
+    first half's, though its products are nothing beside the other's."""
+    H, G, D, BS = 1, 4, 128, 16
+    bt, P = R.tables([c], BS, seed=25)
+    heavy = torch.arange(c) < c // 2 if first == "heavy" else torch.arange(c) >= c // 2
+    blk, off = bt[0].long()[torch.arange(c) // BS], torch.arange(c) % BS
+    ks, vs = torch.full((P, BS, H), 2.0 ** -20), torch.full((P, BS, H), 2.0 ** 70)
+    ks[blk[heavy], off[heavy]] = 2.0 ** -4
+    vs[blk[heavy], off[heavy]] = 2.0 ** -70
+    cache, kv, vv = S.coded_cache(pkv, "e4m3", "token", ks, vs, D, seed=26)
+    # the heavy keys' codes: 4 everywhere, against positive queries
+    code = torch.full((), 4.0).to(torch.float8_e4m3fn).view(torch.uint8)
+    cache.k_cache.view(torch.uint8)[blk[heavy].to(DEV), off[heavy].to(DEV)] = int(code)
+    kv[blk[heavy], off[heavy]] = 4.0 * 2.0 ** -4
+    q = queries(n, H * G, D, torch.bfloat16, 27).abs() * 2
+    st, out = attend(pkv, q, cache, bt, [n], [c])
+    compare(out, q, kv, vv, vs, bt, st, [c], "e4m3", torch.bfloat16)
