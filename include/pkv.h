@@ -325,7 +325,7 @@ int pkv_kv_gather(const pkv_cache *cache, const pkv_tensor *slot_mapping, const 
  *   product's type: by themselves, or, with scales per row or block, times the
  *   V scale, relative to the largest such product of the keys that the row
  *   sees (one far below it is off by at most 2^-20 of it).  Such V scales are
- *   zero or from 2^-80 to 2^80.
+ *   zero or from 2^-80 to 2^80, such K scales at most 2^90.
  *   Bad data never faults: a block id outside [0, num_blocks) is left out
  *   (PKV_DEVERR_BLOCK_RANGE); a context length below 0 counts as 0 and one
  *   above the table's capacity as that capacity

@@ -1083,7 +1083,9 @@ __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
                     c *= back;
                 }
                 ++item;
-                c = fmaxf(c, 1e-30f);                           // keeps 0 * -inf out: masked weights stay zero
+                // keeps 0 * -inf out, so that masked weights stay zero: the smallest number, which makes
+                // nothing of any score
+                c = fmaxf(c, __uint_as_float(1u));
                 const float ninf = -__int_as_float(0x7f800000);
                 float m = ninf, l = 0.0f;                       // m: of S, or (GS) of c S + log2(V scale)
                 const int step = split ? 2 : 1, j0 = split ? sub : 0;

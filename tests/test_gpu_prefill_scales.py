@@ -224,3 +224,48 @@ def test_weights_and_scales_at_opposite_ends(pkv, n, c, first):
     q = queries(n, H * G, D, torch.bfloat16, 27).abs() * 2
     st, out = attend(pkv, q, cache, bt, [n], [c])
     compare(out, q, kv, vv, vs, bt, st, [c], "e4m3", torch.bfloat16)
+
+
+@pytest.mark.parametrize("kind,scales", [("e4m3", "token"), ("i8", "block"), ("e4m3", "head"), ("bf16", "head")])
+@pytest.mark.parametrize("bits", [-85, 85])
+def test_queries_and_keys_at_opposite_ends(pkv, kind, scales, bits):
+    """Queries of 2^-bits and keys of 2^bits: ordinary scores."""
+    H, G, D, BS = 2, 4, 128, 16
+    new, ctx = [130, 2], [130, 900]
+    bt, P = R.tables(ctx, BS, seed=28)
+    if scales == "head":
+        cache, kv, vv = R.make_cache(pkv, kind, P, BS, H, D, seed=29)
+        vs = torch.ones((P, BS, H)) if kind == "bf16" else cache.v_scale.cpu().expand(P, BS, H)
+        if kind == "bf16":
+            cache.k_cache *= 2.0 ** bits
+        else:
+            cache.k_scale *= 2.0 ** bits
+        kv = kv * 2.0 ** bits
+    else:
+        ks, vs = S.flat_scale(kind, (P, BS, H), 2.0 ** bits), S.flat_scale(kind, (P, BS, H))
+        cache, kv, vv = S.coded_cache(pkv, kind, scales, ks, vs, D, seed=30)
+    q = queries(sum(new), H * G, D, torch.bfloat16, 31, 2.0 ** -bits)
+    st, out = attend(pkv, q, cache, bt, new, ctx)
+    S.CMAX.setdefault("bf16", 8.0)
+    compare(out, q, kv, vv, vs, bt, st, ctx, kind, torch.bfloat16)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("scale", [1e-34, -1e-34, 0.0])
+def test_a_tiny_softmax_scale(pkv, kind, scale):
+    """Queries and keys of 1e17, a scale of 1e-34: scores of a few units; and a
+    scale of zero, under which all weights are alike."""
+    H, G, D, BS, new, ctx = 2, 4, 128, 16, [130, 2], [130, 900]
+    bt, P = R.tables(ctx, BS, seed=32)
+    cache, kv, vv = R.make_cache(pkv, kind, P, BS, H, D, seed=33)
+    if kind == "bf16":
+        cache.k_cache *= 2.0 ** 56
+    else:
+        cache.k_scale *= 2.0 ** 56
+    kv = kv * 2.0 ** 56
+    q = queries(sum(new), H * G, D, torch.bfloat16, 34, 2.0 ** 54)
+    st = [0, 130, 132]
+    dev = [torch.tensor(x, dtype=torch.int32, device=DEV) for x in (st, ctx)]
+    out = pkv.paged_prefill(q.to(DEV), cache, bt.to(DEV), *dev, sm_scale=scale).cpu()
+    ref = R.prefill(q, kv, vv, bt, st, ctx, float(torch.tensor(scale)))
+    assert ((out.double() - ref[0]).abs() <= R.prefill_tolerance(*ref, 0.0, torch.bfloat16, D)).all()
