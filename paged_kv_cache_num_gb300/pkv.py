@@ -315,9 +315,28 @@ class KVCache:
         self.__dict__["_cstruct"] = (key, s)
         return s
 
+    def _check_types(self):
+        """The descriptors state the kind's own types: other tensors would be
+        read, and written, beyond their ends."""
+        width = 2 if self.kind in ("f16", "bf16") else 1
+        for name, t, size in (("k_cache", self.k_cache, width), ("v_cache", self.v_cache, width),
+                              ("k_qscale", self.k_qscale, 2), ("v_qscale", self.v_qscale, 2),
+                              ("k_qzero", self.k_qzero, 1), ("v_qzero", self.v_qzero, 1)):
+            if t is not None and t.element_size() != size:
+                raise ValueError("%s of a %s cache has elements of %d bytes, got %s" % (name, self.kind, size, t.dtype))
+        for name in ("k_scale", "v_scale", "k_scales", "v_scales"):
+            t = getattr(self, name)
+            if t is not None and t.dtype != torch.float32:
+                raise ValueError("%s must be float32, got %s" % (name, t.dtype))
+        for name in ("k_scale", "v_scale"):
+            t = getattr(self, name)
+            if t is not None and (t.numel() != self.num_kv_heads or not t.is_contiguous()):
+                raise ValueError("%s must be %d contiguous numbers, one for each kv head" % (name, self.num_kv_heads))
+
     def _build_struct(self) -> _Cache:
         s = _Cache()
         code = {"f16": F16, "bf16": BF16, "e4m3": E4M3, "e5m2": E5M2, "i8": I8, "u3": U3}[self.kind]
+        self._check_types()
         if self.layout == "xvec":
             # [P, Hkv, D/x, BS, x] described as [P, BS, Hkv, D] + the piece stride
             s.k_cache = _xvec_desc(self.k_cache, code)
