@@ -302,8 +302,8 @@ int pkv_kv_gather(const pkv_cache *cache, const pkv_tensor *slot_mapping, const 
  *   q_starts     : I32 [batch + 1], non-decreasing: sequence b owns rows
  *                  q_starts[b] .. q_starts[b + 1] - 1, n_b of them, which
  *                  are the last n_b of its context_lens[b] cached tokens.
- *   out          : as q's shape and dtype, head_dim contiguous.  Row i of
- *                  sequence b (i = 0 .. n_b - 1) is
+ *   out          : as q's shape and dtype, head_dim contiguous, apart from q
+ *                  in memory.  Row i of sequence b (i = 0 .. n_b - 1) is
  *                  softmax(sm_scale * q . K^T) V over the cached tokens
  *                  0 .. context_lens[b] - n_b + i, accumulated in fp32 and
  *                  rounded once; a row that sees no token (context_lens[b] <
