@@ -4,11 +4,12 @@
  * These operations make up the path:
  *   - kv_append: scatter new K/V rows into a paged block pool through a
  *     slot_mapping, optionally quantising them to fp8 e4m3 (per-kv-head
- *     fp32 scales) or to 3-bit affine codes packed 8 values per 3 bytes;
+ *     fp32 scales), to 3-bit affine codes packed 8 values per 3 bytes or to
+ *     4-bit ones packed 2 per byte;
  *   - paged_decode: one-query-token attention over that pool, indirected by
  *     block tables, with grouped-query heads, online softmax, a split over
- *     the context merged by log-sum-exp rescaling, and the fp8 / int8 /
- *     3-bit dequantisation done in registers;
+ *     the context merged by log-sum-exp rescaling, and the fp8 / int8 / 4-bit
+ *     / 3-bit dequantisation done in registers;
  *   - paged_prefill: causal attention of packed prompts, or chunks of them,
  *     over the same pool;
  *   - kv_gather: the read back of cached rows, dequantised;
@@ -56,7 +57,8 @@ enum {
     PKV_DTYPE_I64 = 7,
     PKV_DTYPE_F32 = 8,
     PKV_DTYPE_E5M2 = 9, /* OCP fp8 e5m2 (max 57344, with inf / NaN codes) */
-    PKV_DTYPE_I8 = 10   /* int8 codes (scaled, symmetric range +-127) */
+    PKV_DTYPE_I8 = 10,  /* int8 codes (scaled, symmetric range +-127) */
+    PKV_DTYPE_U4 = 11   /* 4-bit codes packed 2 per byte (see kv_append) */
 };
 
 /* Host-side status codes. */
@@ -88,7 +90,7 @@ typedef struct pkv_tensor {
     int32_t dtype;     /* PKV_DTYPE_* */
     int32_t ndim;
     int64_t shape[4];
-    int64_t stride[4]; /* in elements of dtype (bytes for U8/E4M3/U3) */
+    int64_t stride[4]; /* in elements of dtype (bytes for U8/E4M3/U3/U4) */
 } pkv_tensor;
 
 /*
@@ -102,16 +104,19 @@ typedef struct pkv_tensor {
  *                           head row is bits 3d..3d+2 of the row read as one
  *                           little-endian bit string, i.e. octet j holds
  *                           elements 8j..8j+7 in the layout of the
- *                           "triton-3bit-kv-cache-kernel" README, section 1.A.
+ *                           "triton-3bit-kv-cache-kernel" README, section 1.A;
+ *       U4                : row = head_dim / 2 bytes, head_dim 64 or 128; element
+ *                           d of a head row is bits 4d..4d+3 of the row read
+ *                           as one little-endian bit string.
  *     The last dimension must be contiguous (stride 1) and the base 16-byte
  *     aligned; the block stride must be a multiple of 16 bytes, and for
- *     F16/BF16/E4M3 also the slot and head strides.  K and V must have the
+ *     F16/BF16/E4M3/U4 also the slot and head strides.  K and V must have the
  *     same dtype, shape and strides.
  *   k_scale, v_scale : E4M3, E5M2 and I8 with scale_mode PER_HEAD, device
  *     fp32 [num_kv_heads], > 0.  A stored code c means fp8(c) * scale, or
  *     c * scale for I8, with the scale of the row's granularity (see
  *     PKV_SCALE_*).
- *   k_qscale, v_qscale (F16) and k_qzero, v_qzero (U8), U3 only:
+ *   k_qscale, v_qscale (F16) and k_qzero, v_qzero (U8), U3 and U4 only:
  *     [num_blocks, block_size, num_kv_heads]; a stored code u means
  *     (u - zero) * scale for its (slot, head) row.  Any strides are
  *     accepted (the two scale arrays alike, the two zero arrays alike).
@@ -218,6 +223,13 @@ int pkv_slot_mapping(const pkv_tensor *block_tables, const pkv_tensor *req,
  *                q_d = clamp(rint(x_d / s) + z, 0, 7), packed along head_dim;
  *                s == 0 stores z = 0 and all q = 0.  head_dim % 8 == 0.
  *                Rows must be finite.
+ *     U4       : the same with lo = min(0, min) and hi = max(0, max):
+ *                s = fp16_rn((hi - lo) / 15) (65504 if that overflows),
+ *                z = clamp(rint(-lo / s), 0, 15),
+ *                q_d = clamp(rint(x_d / s) + z, 0, 15), two to a byte;
+ *                s == 0 stores z = 0 and all q = 0.  Rows must be finite.
+ *                (Zero belongs to the range, so that a row without a sign
+ *                change keeps its largest elements.)
  *   block_size may be any positive number here (decode needs a power of two
  *   <= 256): a contiguous per-request cache [batch, num_kv_heads,
  *   max_seq_len, D] ("Write Triton Kv Cache Append Kernel", inputs item 1,
@@ -270,7 +282,7 @@ int pkv_kv_append_dynamic(const pkv_tensor *k_new, const pkv_tensor *v_new,
 /*
  * pkv_kv_gather -- read cached rows back: the inverse of the appends.
  *   cache        : every dtype, layout and scale granularity (pkv_cache),
- *                  head_dim a multiple of 8; U3 head_dim 64 or 128; any
+ *                  head_dim a multiple of 8; U3 and U4 head_dim 64 or 128; any
  *                  block size.
  *   slot_mapping : I64 [num_tokens], any stride; slot as in pkv_kv_append.
  *                  The same slot may appear more than once.
@@ -377,7 +389,7 @@ int pkv_paged_prefill(const pkv_tensor *q, const pkv_cache *cache, const pkv_ten
  *
  *   Grouped-query mapping: q head h reads kv head h / (num_heads /
  *   num_kv_heads).  Output = softmax(sm_scale * q . K^T) V over the first
- *   context_len tokens, with the dequantised K/V for E4M3 and U3 caches,
+ *   context_len tokens, with the dequantised K/V of coded caches,
  *   accumulated in fp32 and rounded once to the output dtype (V scales per
  *   block or token: from 2^-40 to 2^40; below 2^-40 bits are lost).  Cache
  *   contents beyond context_len (the tail of the last block) never affect

@@ -254,39 +254,6 @@ __global__ void __launch_bounds__(kAppendThreads) append_fp8_kernel(AppendParams
     }
 }
 
-// RN(x / s) for 16-bit float x and fp16 s > 0, through the correctly
-// rounded reciprocal rs = RN(1 / s): with y1 = RN(x rs) and the exact
-// residual e = x - y1 s (one FMA), RN(y1 + e rs) is within far less than
-// half an ulp of x / s (Markstein's refinement), so it equals x / s
-// wherever x / s is an fp32 value -- at every half-integer in particular.
-// Off the half-integers rint of it is rint(fl(x / s)) in the codes' range:
-// x and s have at most 11 significant bits, so an x / s with |x / s| < 2^10
-// that is not a half-integer lies at least 2^-13 away from one.
-__device__ __forceinline__ float u3_quotient(float x, float s, float rs)
-{
-    const float y1 = __fmul_rn(x, rs);
-    return __fmaf_rn(__fmaf_rn(-y1, s, x), rs, y1);
-}
-
-// min / max of two pairs of 16-bit floats (non-NaN operand wins, as fminf /
-// fmaxf); exact, the values being 16-bit floats
-template <int SRC>
-__device__ __forceinline__ uint32_t min2_16(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    if constexpr (SRC == kBF16) asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    else asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-template <int SRC>
-__device__ __forceinline__ uint32_t max2_16(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    if constexpr (SRC == kBF16) asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    else asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
 // 3-bit affine quantise + pack: LPR = 4 lanes per (token, head, K|V) row,
 // eight rows per warp.  Each lane holds EPL = head_dim / 4 consecutive
 // elements; a row's min / max are two-step shuffle reductions among its
@@ -365,7 +332,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_u3_kernel(AppendParams 
         // z = clamp(rint(fl(-min / s)), 0, 7); -min is one of the row's
         // 16-bit values, so u3_quotient gives the same rint
         float z = 0.0f;
-        if (s != 0.0f) z = fminf(fmaxf(rintf(u3_quotient(-mn, s, rs)), 0.0f), 7.0f);
+        if (s != 0.0f) z = fminf(fmaxf(rintf(row_quotient(-mn, s, rs)), 0.0f), 7.0f);
         // fields: codes q_j = clamp(rint(fl(x_j / s)) + z, 0, 7) at bits 3j
         // (small integers, exact in fp32).  A constant row (s = 0: every x_j
         // equal and finite) has rs = 0 and z = 0, so its quotients are 0 and
@@ -376,7 +343,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_u3_kernel(AppendParams 
             float fv = 0.0f;
 #pragma unroll
             for (int j = 7; j >= 0; --j) {
-                const float q = fminf(fmaxf(__fadd_rn(rintf(u3_quotient(x[8 * fi + j], s, rs)), z), 0.0f), 7.0f);
+                const float q = fminf(fmaxf(__fadd_rn(rintf(row_quotient(x[8 * fi + j], s, rs)), z), 0.0f), 7.0f);
                 fv = fmaf(fv, 8.0f, q);
             }
             f[fi] = uint32_t(fv);
@@ -478,6 +445,8 @@ cudaError_t launch_append(const AppendParams &p, int cache_kind, bool vec16, cud
         if (p.src_kind == kBF16)
             return vec16 ? go_u(BF{}, std::true_type{}) : go_u(BF{}, std::false_type{});
         return vec16 ? go_u(HF{}, std::true_type{}) : go_u(HF{}, std::false_type{});
+    } else if (cache_kind == kU4) {
+        return launch_append_u4(p, vec16, s);
     } else {  // kU3
         const int64_t rows = p.num_tokens * 2 * p.num_kv_heads;
         constexpr int LPR = 4;                      // lanes per row (two: slower)

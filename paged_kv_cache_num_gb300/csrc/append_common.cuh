@@ -1,5 +1,6 @@
 // append_common.cuh -- what the append kernels share: the slot of a token,
-// the walk over work items, and the one-byte casts.
+// the walk over work items, the one-byte casts and the quotient of the 3- and
+// 4-bit rows.
 #pragma once
 
 #include "pkv_device.cuh"
@@ -111,6 +112,79 @@ __device__ __forceinline__ uint32_t q8x2_encode(float2 x)
     } else {
         return __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, Q8 == kE4M3 ? __NV_E4M3 : __NV_E5M2);
     }
+}
+
+// RN(x / s) for 16-bit float x and fp16 s > 0, through the correctly
+// rounded reciprocal rs = RN(1 / s): with y1 = RN(x rs) and the exact
+// residual e = x - y1 s (one FMA), RN(y1 + e rs) is within far less than
+// half an ulp of x / s (Markstein's refinement), so it equals x / s
+// wherever x / s is an fp32 value -- at every half-integer in particular.
+// Off the half-integers rint of it is rint(fl(x / s)) in the codes' range:
+// x and s have at most 11 significant bits, so an x / s with |x / s| < 2^10
+// that is not a half-integer lies at least 2^-13 away from one.
+__device__ __forceinline__ float row_quotient(float x, float s, float rs)
+{
+    const float y1 = __fmul_rn(x, rs);
+    return __fmaf_rn(__fmaf_rn(-y1, s, x), rs, y1);
+}
+
+// min / max of two pairs of 16-bit floats (non-NaN operand wins, as fminf /
+// fmaxf); exact, the values being 16-bit floats
+template <int SRC>
+__device__ __forceinline__ uint32_t min2_16(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    if constexpr (SRC == kBF16) asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <int SRC>
+__device__ __forceinline__ uint32_t max2_16(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    if constexpr (SRC == kBF16) asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// A 4-bit row by LPR neighbouring lanes, each with 8 of its elements (e, pairs
+// in order): this lane's word of codes, and the row's scale and zero.  Every
+// lane of the warp calls it.
+struct RowU4 {
+    uint32_t codes;
+    uint16_t scale;
+    uint32_t zero;
+};
+template <int SRC, int LPR>
+__device__ __forceinline__ RowU4 row_u4(const uint32_t (&e)[4])
+{
+    uint32_t mn = min2_16<SRC>(min2_16<SRC>(e[0], e[1]), min2_16<SRC>(e[2], e[3]));
+    uint32_t mx = max2_16<SRC>(max2_16<SRC>(e[0], e[1]), max2_16<SRC>(e[2], e[3]));
+    mn = min2_16<SRC>(mn, __byte_perm(mn, 0u, 0x1032));         // both halves
+    mx = max2_16<SRC>(mx, __byte_perm(mx, 0u, 0x1032));
+    uint32_t both = min2_16<SRC>(__byte_perm(mn, mx ^ 0x80008000u, 0x5410), 0u);    // (min, -max), zero among them
+#pragma unroll
+    for (int o = 1; o < LPR; o <<= 1) both = min2_16<SRC>(both, __shfl_xor_sync(0xffffffffu, both, o));
+    const float lo = h2f<SRC>(uint16_t(both)), hi = -h2f<SRC>(uint16_t(both >> 16));
+    uint16_t sbits = __half_as_ushort(__float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f)));
+    if ((sbits & 0x7fff) == 0x7c00) sbits = 0x7bff;             // the largest finite fp16
+    const float s = __half2float(__ushort_as_half(sbits));
+    // s = 0: all quotients, z and the codes become 0
+    const float rs = s != 0.0f ? __frcp_rn(s) : 0.0f;
+    const float z = fminf(fmaxf(rintf(row_quotient(-lo, s, rs)), 0.0f), 15.0f);
+    float f[2];                                                 // four codes each, as a number below 2^16
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        f[j] = 0.0f;
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+            const uint32_t w = e[2 * j + (i >> 1)];
+            const float x = h2f<SRC>(uint16_t(i & 1 ? w >> 16 : w));
+            const float q = fminf(fmaxf(__fadd_rn(rintf(row_quotient(x, s, rs)), z), 0.0f), 15.0f);
+            f[j] = fmaf(f[j], 16.0f, q);
+        }
+    }
+    return {uint32_t(f[0]) | (uint32_t(f[1]) << 16), sbits, uint32_t(z)};
 }
 
 inline int grid_for(int64_t work, int threads)

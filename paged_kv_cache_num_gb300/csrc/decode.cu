@@ -61,6 +61,12 @@ __device__ __forceinline__ void load_row(const char *row, int e0, float scale, f
             const float2 a = fp8x2_to_float2<CK, 0>(uint32_t(*reinterpret_cast<const uint16_t *>(r)));
             x[0] = a.x * scale; x[1] = a.y * scale;
         }
+    } else if constexpr (CK == kU4) {  // element d at bits 4d..4d+3 of the little-endian row
+        static_assert(EPL == 2 || EPL == 4, "one or two bytes");
+        const char *r = row + e0 / 2;
+        const uint32_t w = EPL == 4 ? *reinterpret_cast<const uint16_t *>(r) : uint8_t(*r);
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) x[j] = (float((w >> (4 * j)) & 15u) - qzero) * qscale;
     } else {  // kU3: element d at bits 3d..3d+2 of the little-endian row
         const uint8_t *r = reinterpret_cast<const uint8_t *>(row);
         const int bit0 = 3 * e0;
@@ -127,12 +133,12 @@ __global__ void __launch_bounds__(kGenThreads) decode_general_kernel(DecodeParam
     const float ks = is_q8(CK) && p.scale_mode == 0 ? p.k_scale[kvh] : 1.0f;
     const float vs = is_q8(CK) && p.scale_mode == 0 ? p.v_scale[kvh] : 1.0f;
     const int bmask = (1 << p.block_shift) - 1;
-    // this lane's EPL elements: packed 3-bit rows are addressed by element;
+    // this lane's EPL elements: packed 3- and 4-bit rows are addressed by element;
     // the others lie inside one 16-byte piece of the row, the pieces being
     // c_chunk bytes apart (x-vectorised layout) or adjacent
     int64_t eoff = 0;
     int e0 = EPL * lane;
-    if constexpr (CK != kU3) {
+    if constexpr (!is_packed(CK)) {
         constexpr int ES = (CK == kF16 || CK == kBF16) ? 2 : 1;
         eoff = int64_t((EPL * lane * ES) >> 4) * p.c_chunk + ((EPL * lane * ES) & 15);
         e0 = 0;
@@ -181,7 +187,7 @@ __global__ void __launch_bounds__(kGenThreads) decode_general_kernel(DecodeParam
                 kst = p.k_gs[gi];
                 vst = p.v_gs[gi];
             }
-            if constexpr (CK == kU3) {
+            if constexpr (is_packed(CK)) {
                 kq = __half2float(__ushort_as_half(p.k_qs[pb * p.m_blk + off * p.m_slot + kvh * p.m_head]));
                 vq = __half2float(__ushort_as_half(p.v_qs[pb * p.m_blk + off * p.m_slot + kvh * p.m_head]));
                 kz = float(p.k_qz[pb * p.z_blk + off * p.z_slot + kvh * p.z_head]);
@@ -390,6 +396,7 @@ cudaError_t launch_decode(const DecodeParams &p, int cache_kind, int q_kind, cud
         case kE5M2: return launch_by_dim<kBF16, kE5M2>(p, s);
         case kI8: return launch_by_dim<kBF16, kI8>(p, s);
         case kU3: return launch_by_dim<kBF16, kU3>(p, s);
+        case kU4: return launch_by_dim<kBF16, kU4>(p, s);
         default: return cudaErrorInvalidValue;
         }
     }
@@ -399,6 +406,7 @@ cudaError_t launch_decode(const DecodeParams &p, int cache_kind, int q_kind, cud
     case kE5M2: return launch_by_dim<kF16, kE5M2>(p, s);
     case kI8: return launch_by_dim<kF16, kI8>(p, s);
     case kU3: return launch_by_dim<kF16, kU3>(p, s);
+    case kU4: return launch_by_dim<kF16, kU4>(p, s);
     default: return cudaErrorInvalidValue;
     }
 }

@@ -139,6 +139,8 @@ bool plan_fast(int batch, int num_heads, int num_kv_heads, int head_dim, int blo
     f.ncons = ncons;
     f.u3_tiles = u3_tiles;
     f.n_hg = n_hg;
+    f.unit_shift = 0;
+    while ((1 << f.unit_shift) < block_size) ++f.unit_shift;
     f.stages = stages;
     const int64_t slots = int64_t(sm_count) * ctas_per_sm;
     f.grid = int(max_units < slots ? (max_units > 0 ? max_units : 1) : slots);

@@ -1382,7 +1382,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(DecodeParams p,
         for (int b = lo; b < hi; ++b) {
             int ctx = p.context_lens[b * p.cl_stride];
             ctx = ctx < 0 ? 0 : (ctx > cap ? cap : ctx);
-            const int nb = (ctx + p.block_size - 1) >> p.block_shift;
+            const int nb = (ctx + (1 << f.unit_shift) - 1) >> f.unit_shift;
             sprefix[b] = nb;
             sum += nb;
         }

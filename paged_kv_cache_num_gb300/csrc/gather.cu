@@ -2,7 +2,7 @@
 //
 // A row (token, K|V, kv head) is read in pieces of EPP elements: 16 bytes of
 // a 16-bit cache (8) or a one-byte one (16; 8 where head_dim is no multiple
-// of 16), 12 bytes of a 3-bit one (32).  One warp takes parts of a
+// of 16), 16 or 12 bytes of a 4- or 3-bit one (32).  One warp takes parts of a
 // (token, K|V) row, its lanes over the (kv head, piece) pairs, as the appends
 // do, all of a lane's loads before its stores.  Bound by HBM.  A 3-bit row has
 // only eight values: a lane forms them once, (u - z) s rounded, and looks its
@@ -44,6 +44,28 @@ __device__ __forceinline__ void piece_out(const uint32_t (&w)[4], float s, float
     } else if constexpr (CK == kF16 || CK == kBF16) {
 #pragma unroll
         for (int j = 0; j < N; ++j) o[j] = pair_out<CK, OUT>(w[j], 1.0f);
+    } else if constexpr (CK == kU4) {
+        // u - z exactly as f16; times s: of an f16 output one rounding by itself (the
+        // product of 5 and 11 bits is exact in fp32 too, so both round alike)
+        const uint32_t zz = __half_as_ushort(__float2half_rn(-1024.0f - z)) * 0x10001u;
+        const __half2 ss = __float2half2_rn(s);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t p[4];
+            u4x8_to_f16(w[j], zz, p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __half2 x = *reinterpret_cast<const __half2 *>(&p[i]);
+                if constexpr (OUT == kF16) {
+                    const __half2 y = __hmul2(x, ss);
+                    o[4 * j + i] = *reinterpret_cast<const uint32_t *>(&y);
+                } else {
+                    const float2 y = __half22float2(x);
+                    const __nv_bfloat162 r = __floats2bfloat162_rn(y.x * s, y.y * s);
+                    o[4 * j + i] = *reinterpret_cast<const uint32_t *>(&r);
+                }
+            }
+        }
     } else if constexpr (CK == kU3) {
         uint32_t v[4], lo[2], hi[2];                // the row's eight values, two per word
 #pragma unroll
@@ -107,6 +129,10 @@ __global__ void __launch_bounds__(kAppendThreads) gather_kernel(GatherParams p)
             const char *src = src_row + h * c.c_head;
             sc[u] = 1.0f;
             ze[u] = 0.0f;
+            if constexpr (is_packed(CK)) {
+                sc[u] = __half2float(__ushort_as_half(__ldg((kv ? c.v_qs : c.k_qs) + blk * c.m_blk + off * c.m_slot + h * c.m_head)));
+                ze[u] = float(__ldg((kv ? c.v_qz : c.k_qz) + blk * c.z_blk + off * c.z_slot + h * c.z_head));
+            }
             if constexpr (CK == kU3) {
                 src += 12 * g;
                 if (p.word_rows) {
@@ -118,8 +144,6 @@ __global__ void __launch_bounds__(kAppendThreads) gather_kernel(GatherParams p)
                         e[u][j >> 2] = (j & 3 ? e[u][j >> 2] : 0u) |
                                        uint32_t(__ldg(reinterpret_cast<const uint8_t *>(src) + j)) << (8 * (j & 3));
                 }
-                sc[u] = __half2float(__ushort_as_half(__ldg((kv ? c.v_qs : c.k_qs) + blk * c.m_blk + off * c.m_slot + h * c.m_head)));
-                ze[u] = float(__ldg((kv ? c.v_qz : c.k_qz) + blk * c.z_blk + off * c.z_slot + h * c.z_head));
             } else if constexpr (EPP == 8 && is_q8(CK)) {
                 const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src + (g >> 1) * c.c_chunk + 8 * (g & 1)));
                 e[u][0] = v.x; e[u][1] = v.y;
@@ -188,6 +212,7 @@ cudaError_t launch_gather(const GatherParams &p, int cache_kind, int out_kind, c
     case kE4M3: return q8(std::integral_constant<int, kE4M3>{});
     case kE5M2: return q8(std::integral_constant<int, kE5M2>{});
     case kI8: return q8(std::integral_constant<int, kI8>{});
+    case kU4: return out(std::integral_constant<int, kU4>{}, std::integral_constant<int, 32>{});
     default: return out(std::integral_constant<int, kU3>{}, std::integral_constant<int, 32>{});
     }
 }

@@ -36,6 +36,7 @@ int elem_size(int dtype)
     case PKV_DTYPE_E5M2:
     case PKV_DTYPE_I8:
     case PKV_DTYPE_U3:
+    case PKV_DTYPE_U4:
     case PKV_DTYPE_U8: return 1;
     case PKV_DTYPE_I32:
     case PKV_DTYPE_F32: return 4;
@@ -95,15 +96,15 @@ int check_cache(const pkv_cache *c, CacheInfo &ci, bool any_block_size = false)
     const pkv_tensor &k = c->k_cache, &v = c->v_cache;
     if (k.dtype != v.dtype) return fail(PKV_ERR_DTYPE, "k_cache and v_cache dtypes differ");
     const int kind = k.dtype;
-    if (kind != PKV_DTYPE_F16 && kind != PKV_DTYPE_BF16 && !pkv::is_q8(kind) && kind != PKV_DTYPE_U3)
-        return fail(PKV_ERR_DTYPE, "cache dtype %d is not F16, BF16, E4M3, E5M2, I8 or U3", kind);
+    if (kind != PKV_DTYPE_F16 && kind != PKV_DTYPE_BF16 && !pkv::is_q8(kind) && !pkv::is_packed(kind))
+        return fail(PKV_ERR_DTYPE, "cache dtype %d is not F16, BF16, E4M3, E5M2, I8, U4 or U3", kind);
     for (int i = 0; i < 4; ++i) {
         if (k.shape[i] != v.shape[i]) return fail(PKV_ERR_SHAPE, "k_cache and v_cache shapes differ");
         if (k.stride[i] != v.stride[i]) return fail(PKV_ERR_LAYOUT, "k_cache and v_cache strides differ");
     }
     if (k.stride[3] != 1) return fail(PKV_ERR_LAYOUT, "cache rows must be contiguous (last stride 1)");
     const int es = elem_size(kind);
-    // 16-bit and e4m3 rows are whole 16-byte units; packed 3-bit rows
+    // 16-bit, one-byte and 4-bit rows are whole 16-byte units; packed 3-bit rows
     // (3*head_dim/8 bytes) only need 16-byte aligned blocks
     for (int i = 0; i < (kind == PKV_DTYPE_U3 ? 1 : 3); ++i)
         if ((k.stride[i] * es) % 16 != 0)
@@ -112,8 +113,8 @@ int check_cache(const pkv_cache *c, CacheInfo &ci, bool any_block_size = false)
         return fail(PKV_ERR_LAYOUT, "cache base pointers must be 16-byte aligned");
     ci.c_chunk = 16;
     if (c->chunk_stride != 0) {     // x-vectorised rows: pieces of 16 bytes
-        if (kind == PKV_DTYPE_U3)
-            return fail(PKV_ERR_UNSUPPORTED, "chunk_stride does not apply to U3 caches");
+        if (pkv::is_packed(kind))
+            return fail(PKV_ERR_UNSUPPORTED, "chunk_stride does not apply to U3 and U4 caches");
         if (c->chunk_stride < 0 || (c->chunk_stride * es) % 16 != 0)
             return fail(PKV_ERR_LAYOUT, "chunk_stride must be a positive multiple of 16 bytes");
         if ((k.shape[3] * es) % 16 != 0)
@@ -124,7 +125,7 @@ int check_cache(const pkv_cache *c, CacheInfo &ci, bool any_block_size = false)
     ci.num_blocks = k.shape[0];
     ci.block_size = k.shape[1];
     ci.num_kv_heads = k.shape[2];
-    ci.head_dim = kind == PKV_DTYPE_U3 ? k.shape[3] * 8 / 3 : k.shape[3];
+    ci.head_dim = kind == PKV_DTYPE_U3 ? k.shape[3] * 8 / 3 : kind == PKV_DTYPE_U4 ? k.shape[3] * 2 : k.shape[3];
     if (kind == PKV_DTYPE_U3 && k.shape[3] * 8 != ci.head_dim * 3)
         return fail(PKV_ERR_SHAPE, "U3 cache row of %lld bytes is not 3*head_dim/8", (long long)k.shape[3]);
     if (any_block_size ? ci.block_size < 1 : (!is_pow2(ci.block_size) || ci.block_size > 256))
@@ -159,20 +160,20 @@ int check_cache(const pkv_cache *c, CacheInfo &ci, bool any_block_size = false)
         ci.gs_slot = blk ? 0 : c->k_scales.stride[1];
         ci.gs_head = c->k_scales.stride[blk ? 1 : 2];
     }
-    if (kind == PKV_DTYPE_U3) {
+    if (pkv::is_packed(kind)) {
         TRY(check_tensor(&c->k_qscale, "k_qscale", 3));
         TRY(check_tensor(&c->k_qzero, "k_qzero", 3));
         TRY(check_tensor(&c->v_qscale, "v_qscale", 3));
         TRY(check_tensor(&c->v_qzero, "v_qzero", 3));
         if (c->k_qscale.dtype != PKV_DTYPE_F16 || c->v_qscale.dtype != PKV_DTYPE_F16)
-            return fail(PKV_ERR_DTYPE, "U3 scales must be F16");
+            return fail(PKV_ERR_DTYPE, "U3 / U4 scales must be F16");
         if (c->k_qzero.dtype != PKV_DTYPE_U8 || c->v_qzero.dtype != PKV_DTYPE_U8)
-            return fail(PKV_ERR_DTYPE, "U3 zeros must be U8");
+            return fail(PKV_ERR_DTYPE, "U3 / U4 zeros must be U8");
         for (int i = 0; i < 3; ++i) {
             const int64_t want = k.shape[i];
             if (c->k_qscale.shape[i] != want || c->v_qscale.shape[i] != want ||
                 c->k_qzero.shape[i] != want || c->v_qzero.shape[i] != want)
-                return fail(PKV_ERR_SHAPE, "U3 metadata must be [num_blocks, block_size, num_kv_heads]");
+                return fail(PKV_ERR_SHAPE, "U3 / U4 metadata must be [num_blocks, block_size, num_kv_heads]");
             if (c->k_qscale.stride[i] != c->v_qscale.stride[i] || c->k_qzero.stride[i] != c->v_qzero.stride[i])
                 return fail(PKV_ERR_LAYOUT, "K and V metadata strides differ");
         }
@@ -285,8 +286,8 @@ static int prep_kv_append(const pkv_tensor *k_new, const pkv_tensor *v_new, cons
         return fail(PKV_ERR_DTYPE, "16-bit cache dtype must equal the source dtype");
     if (pkv::is_q8(ci.kind) && ci.head_dim % 8 != 0)
         return fail(PKV_ERR_UNSUPPORTED, "fp8 / int8 append needs head_dim % 8 == 0");
-    if (ci.kind == PKV_DTYPE_U3 && ci.head_dim != 64 && ci.head_dim != 128)
-        return fail(PKV_ERR_UNSUPPORTED, "U3 append supports head_dim 64 and 128");
+    if (pkv::is_packed(ci.kind) && ci.head_dim != 64 && ci.head_dim != 128)
+        return fail(PKV_ERR_UNSUPPORTED, "U3 / U4 append supports head_dim 64 and 128");
     const int64_t es = 2;
     vec16 = aligned(k_new->data, 16) && aligned(v_new->data, 16) &&
                        (k_new->stride[0] * es) % 16 == 0 && (k_new->stride[1] * es) % 16 == 0 &&
@@ -339,7 +340,7 @@ static int prep_kv_append(const pkv_tensor *k_new, const pkv_tensor *v_new, cons
     } else if (k_new_scale || v_new_scale) {
         return fail(PKV_ERR_VALUE, "new-token scales given for a cache without per-token scales");
     }
-    if (ci.kind == PKV_DTYPE_U3) {
+    if (pkv::is_packed(ci.kind)) {
         p.k_qs = static_cast<uint16_t *>(cache->k_qscale.data);
         p.v_qs = static_cast<uint16_t *>(cache->v_qscale.data);
         p.k_qz = static_cast<uint8_t *>(cache->k_qzero.data);
@@ -409,7 +410,7 @@ void fill_cache_params(const pkv_cache *cache, const CacheInfo &ci, pkv::DecodeP
         p.gs_slot = ci.gs_slot;
         p.gs_head = ci.gs_head;
     }
-    if (ci.kind == PKV_DTYPE_U3) {
+    if (pkv::is_packed(ci.kind)) {
         p.k_qs = static_cast<const uint16_t *>(cache->k_qscale.data);
         p.v_qs = static_cast<const uint16_t *>(cache->v_qscale.data);
         p.k_qz = static_cast<const uint8_t *>(cache->k_qzero.data);
@@ -499,7 +500,24 @@ int check_decode_common(const pkv_tensor *q, const pkv_cache *cache, const pkv_t
         gs_ok = gs_ok && aligned(p.k_gs, 16) && aligned(p.v_gs, 16);
     // x-vectorised caches: the persistent kernel with per-head scales
     if (ci.c_chunk != 16 && ci.scale_mode != PKV_SCALE_PER_HEAD) gs_ok = false;
-    if (num_splits == 0 && gs_ok &&
+    if (num_splits == 0 && ci.kind == PKV_DTYPE_U4) {
+        // the persistent kernel takes 16-byte aligned q rows and 16-byte aligned
+        // runs of scales and zeros, head by head or slot by slot
+        const bool hmaj = p.m_slot == 1 && p.m_head == ci.block_size && p.z_slot == 1 && p.z_head == ci.block_size;
+        const bool smaj = p.m_head == 1 && p.m_slot == ci.num_kv_heads && p.z_head == 1 && p.z_slot == ci.num_kv_heads;
+        const bool ok = (hmaj || smaj) && (p.m_blk * 2) % 16 == 0 && p.z_blk % 16 == 0 && aligned(p.k_qs, 16) &&
+                        aligned(p.v_qs, 16) && aligned(p.k_qz, 16) && aligned(p.v_qz, 16) && aligned(q->data, 16) &&
+                        p.q_b % 16 == 0 && p.q_h % 16 == 0;
+        pkv::FastParams f{};
+        size_t ws = 0;
+        if (ok && pkv::plan_decode_u4(p, hmaj, sm, f, ws)) {
+            dc.plan.kernel = 1;
+            dc.plan.fast = f;
+            dc.plan.workspace_bytes = ws;
+            dc.plan.num_splits = 0;
+            return PKV_OK;
+        }
+    } else if (num_splits == 0 && gs_ok &&
         pkv::fast_decode_supported(ci.kind, p.head_dim, p.block_size, p.group, p.batch)) {
         // q rows are read 16 (3-bit), 8 (fp8) or 4 (16-bit) bytes at a time
         const size_t qa = ci.kind == PKV_DTYPE_U3 ? 16 : (pkv::is_q8(ci.kind) ? 8 : 4);
@@ -612,6 +630,8 @@ static int prep_paged_decode(const pkv_tensor *q, const pkv_cache *cache, const 
 static int launch_paged_decode(const DecodeCheck &dc, int q_dtype, void *workspace, size_t workspace_bytes,
                                void *stream)
 {
+    if (dc.plan.kernel == 1 && dc.ci.kind == PKV_DTYPE_U4)
+        return launch_status(pkv::launch_decode_u4(dc.p, dc.plan.fast, workspace, as_stream(stream)), "paged_decode kernels");
     if (dc.plan.kernel == 1)
         return launch_status(pkv::launch_decode_fast(dc.p, dc.plan.fast, dc.ci.kind, workspace, workspace_bytes,
                                                      as_stream(stream)),
@@ -693,8 +713,8 @@ int pkv_kv_gather(const pkv_cache *cache, const pkv_tensor *slot_mapping, const 
     if (k_out->stride[2] != 1 || v_out->stride[2] != 1)
         return fail(PKV_ERR_LAYOUT, "head_dim of k_out / v_out must be contiguous");
     if (ci.head_dim % 8 != 0) return fail(PKV_ERR_UNSUPPORTED, "gather needs head_dim % 8 == 0");
-    if (ci.kind == PKV_DTYPE_U3 && ci.head_dim != 64 && ci.head_dim != 128)
-        return fail(PKV_ERR_UNSUPPORTED, "U3 gather supports head_dim 64 and 128");
+    if (pkv::is_packed(ci.kind) && ci.head_dim != 64 && ci.head_dim != 128)
+        return fail(PKV_ERR_UNSUPPORTED, "U3 / U4 gather supports head_dim 64 and 128");
     pkv::GatherParams p{};
     fill_cache_params(cache, ci, p.c);
     p.num_slots = ci.num_blocks * ci.block_size;

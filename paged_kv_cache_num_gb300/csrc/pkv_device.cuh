@@ -64,6 +64,21 @@ template <> __device__ __forceinline__ uint16_t f2h<kBF16>(float v)
     return __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
+// Eight 4-bit codes (element j at bits 4j .. 4j+3) minus their zero point z, as
+// pairs of f16 numbers in order, exactly: under 0x6400 a byte with code u is
+// 1024 + u; nz holds -1024 - z twice.
+__device__ __forceinline__ void u4x8_to_f16(uint32_t w, uint32_t nz, uint32_t (&o)[4])
+{
+    const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
+    const uint32_t lo = __byte_perm(even, odd, 0x5140), hi = __byte_perm(even, odd, 0x7362);
+    o[0] = __byte_perm(lo, 0x64646464u, 0x4140);
+    o[1] = __byte_perm(lo, 0x64646464u, 0x4342);
+    o[2] = __byte_perm(hi, 0x64646464u, 0x4140);
+    o[3] = __byte_perm(hi, 0x64646464u, 0x4342);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("add.rn.f16x2 %0, %0, %1;" : "+r"(o[i]) : "r"(nz));
+}
+
 // Two fp8 codes of cache kind FP8 (kE4M3 / kE5M2), bytes 2HI and 2HI+1 of w
 // (low byte first) -> two floats, exactly: cvt.rn.f16x2 on the 16-bit half
 // of the register, then the f16 -> f32 widening.

@@ -9,10 +9,13 @@
 
 namespace pkv {
 
-enum CacheKind : int { kF16 = 1, kBF16 = 2, kE4M3 = 3, kU3 = 4, kE5M2 = 9, kI8 = 10 };
+enum CacheKind : int { kF16 = 1, kBF16 = 2, kE4M3 = 3, kU3 = 4, kE5M2 = 9, kI8 = 10, kU4 = 11 };
 
 // one-byte codes with a per-kv-head fp32 scale: fp8 e4m3 / e5m2 and int8
 constexpr bool is_q8(int ck) { return ck == kE4M3 || ck == kE5M2 || ck == kI8; }
+// affine codes of 3 or 4 bits, with an fp16 scale and a uint8 zero per row
+constexpr bool is_packed(int ck) { return ck == kU3 || ck == kU4; }
+constexpr int packed_row_bytes(int ck, int head_dim) { return (ck == kU3 ? 3 : 4) * head_dim / 8; }
 
 // ---------------------------------------------------------------- append
 struct SlotMapParams {
@@ -50,7 +53,7 @@ struct AppendParams {
     const float *k_ns;          // per-token mode: the new tokens' scales
     const float *v_ns;
     int64_t ns_tok, ns_head;
-    // 3-bit metadata (element strides, same for the four arrays)
+    // 3- and 4-bit metadata (element strides, same for the four arrays)
     uint16_t *k_qs;
     uint8_t *k_qz;
     uint16_t *v_qs;
@@ -73,6 +76,8 @@ struct AppendParams {
 };
 
 cudaError_t launch_append(const AppendParams &p, int cache_kind, bool vec16, cudaStream_t s);
+
+cudaError_t launch_append_u4(const AppendParams &p, bool vec16, cudaStream_t s);
 
 cudaError_t launch_slot_mapping(const SlotMapParams &p, cudaStream_t s);
 
@@ -138,6 +143,7 @@ struct FastParams {
     int hpw;                    // 3-bit multi-head caches: kv heads per consumer warp
                                 // (1, 2 or 4); 1 otherwise
     int ncons;                  // consumer warps per CTA
+    int unit_shift;             // log2 of the tokens that a unit of work has (block_size; 4-bit: 32)
     int u3_tiles;               // 3-bit K / V tiles ([head][slot][row] in shared
                                 // memory): 0 by 4-D tensor copies; 1 by one bulk
                                 // copy per tile (heads stored [block][head][slot][row])
@@ -168,6 +174,10 @@ cudaError_t launch_decode_fast_q8_d64(const DecodeParams &p, const FastParams &f
                                       const void *tmk, const void *tmv, cudaStream_t s);
 cudaError_t launch_decode_fast_xv(const DecodeParams &p, const FastParams &f, int cache_kind,
                                   const void *tmk, const void *tmv, cudaStream_t s);
+
+// 4-bit caches (decode_u4.cu)
+bool plan_decode_u4(const DecodeParams &p, bool meta_head_major, int sm_count, FastParams &f, size_t &workspace);
+cudaError_t launch_decode_u4(const DecodeParams &p, FastParams f, void *ws, cudaStream_t s);
 
 cudaError_t launch_decode(const DecodeParams &p, int cache_kind, int q_kind, cudaStream_t s);
 cudaError_t launch_decode_fast(const DecodeParams &p, FastParams f, int cache_kind, void *ws,

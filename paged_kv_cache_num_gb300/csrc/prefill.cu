@@ -41,7 +41,7 @@ bool cache_map(CUtensorMap *m, const char *base, const DecodeParams &d, int kind
     auto enc = encoder();
     if (!enc || d.num_blocks == 0) return false;
     const bool coded = kind != kF16 && kind != kBF16;
-    const int row = kind == kU3 ? 3 * d.head_dim / 8 : d.head_dim;
+    const int row = is_packed(kind) ? packed_row_bytes(kind, d.head_dim) : d.head_dim;
     const cuuint32_t slots = cuuint32_t(std::min(d.block_size, 128));
     const cuuint64_t n_slots = cuuint64_t(d.block_size), heads = cuuint64_t(d.num_kv_heads), blocks = cuuint64_t(d.num_blocks);
     const cuuint64_t slot = cuuint64_t(d.c_slot), head = cuuint64_t(d.c_head), block = cuuint64_t(d.c_blk);
@@ -146,6 +146,7 @@ cudaError_t launch_prefill(const PrefillParams &p, const PrefillPlan &pl, int ca
     case kE4M3: return launch_prefill_e4m3(a);
     case kE5M2: return launch_prefill_e5m2(a);
     case kI8: return launch_prefill_i8(a);
+    case kU4: return launch_prefill_u4(a);
     default: return launch_prefill_u3(a);
     }
 }

@@ -78,8 +78,8 @@ struct PrefillFast {
 namespace {
 
 enum Feed : int { kFeedTma, kFeedCopy, kFeedCodes };
-// warps that convert codes: 3-bit ones take the most work and have room
-template <int CK> constexpr int conv_warps() { return CK == kU3 ? 8 : 4; }
+// warps that convert codes: 3- and 4-bit ones take the most work and have room
+template <int CK> constexpr int conv_warps() { return is_packed(CK) ? 8 : 4; }
 
 template <int CK, int FEED> constexpr int prefill_threads()
 {
@@ -309,7 +309,7 @@ __device__ __forceinline__ void find_start(const PrefillParams &p, int64_t *bins
 
 // ---------------------------------------------------------------- shared memory
 template <int CK> constexpr bool is_coded() { return CK != kF16 && CK != kBF16; }
-template <int CK, int D> constexpr int raw_row() { return CK == kU3 ? 3 * D / 8 : D; }
+template <int CK, int D> constexpr int raw_row() { return is_packed(CK) ? packed_row_bytes(CK, D) : D; }
 
 template <int CK, int D>
 struct Smem {
@@ -317,7 +317,7 @@ struct Smem {
     static constexpr int kTile = 128 * D * 2;                   // bytes of 128 operand rows
     // stages of operands and of raw codes: what fits.  One-byte codes have three
     // operand stages, the others four
-    static constexpr int kStages = (kCoded && CK != kU3 ? 3 : 4) * (D == 128 ? 1 : 2);
+    static constexpr int kStages = (kCoded && !is_packed(CK) ? 3 : 4) * (D == 128 ? 1 : 2);
     static constexpr int kRaw = kCoded ? 3 * (D == 128 ? 1 : 2) : 0;
     static constexpr int kRawTile = kCoded ? 128 * raw_row<CK, D>() : 0;
     static constexpr int kColSlots = (kCoded ? 4 : 8) * (D == 128 ? 1 : 2);      // see ColSlot
@@ -703,7 +703,7 @@ __device__ __forceinline__ void raw_codes(const PrefillParams &p, const PrefillF
                 __syncwarp();
                 if (in) {
                     const CUtensorMap *m = kv ? tmv : tmk;
-                    if (d.c_chunk == 16 || CK == kU3)
+                    if (d.c_chunk == 16 || is_packed(CK))
                         ptx::tma_load_4d(dst + lane * rows * RB, m, bars.raw_full(s), 0, slot0, h, now);
                     else
                         ptx::tma_load_5d(dst + lane * rows * RB, m, bars.raw_full(s), 0, slot0, 0, h, now);
@@ -714,7 +714,7 @@ __device__ __forceinline__ void raw_codes(const PrefillParams &p, const PrefillF
                 // with the softmax (unrolled: e4m3 chunks that never come here
                 // 615 -> 702 us).
                 const char *cache = kv ? d.v_cache : d.k_cache;
-                const bool xv = d.c_chunk != 16 && CK != kU3;
+                const bool xv = d.c_chunk != 16 && !is_packed(CK);
 #pragma unroll 1
                 for (int i = lane; i < kKeyTile; i += 32) {
                     const int in_blk = i & (rows - 1);
@@ -763,15 +763,15 @@ __device__ __forceinline__ void convert_rows(const PrefillParams &p, const Start
 {
     using L = Smem<CK, D>;
     constexpr int ST = L::kStages, RB = raw_row<CK, D>();
-    constexpr int kPieces = CK == kU3 ? D / 32 : D / 16;        // per row and per lane: 16 one-byte codes, or 32
-                                                                // 3-bit ones (12 bytes)
+    constexpr int kPieces = is_packed(CK) ? D / 32 : D / 16;    // per row: 16 one-byte codes, or 32 of 3 or 4 bits
+                                                                // (12 or 16 bytes)
     const DecodeParams &d = p.d;
     const uint32_t *info = reinterpret_cast<const uint32_t *>(sm + L::info);
     ColSlot *cols = reinterpret_cast<ColSlot *>(sm + L::cols);
     constexpr int NR = kKeyTile / conv_warps<CK>();             // rows of this warp: 32 or 16
     const int row0 = NR * lw, row = row0 + lane % NR;
     const int shift = min(d.block_shift, 7), rows = 1 << shift;
-    const bool xv = d.c_chunk != 16 && CK != kU3;
+    const bool xv = d.c_chunk != 16 && !is_packed(CK);
     TileWalk tw{walk_from(p, st), 0};
     tw.k = tw.w.k0;
     uint32_t pos = 0, tile_n = 0;
@@ -789,7 +789,7 @@ __device__ __forceinline__ void convert_rows(const PrefillParams &p, const Start
         ks = vs = kz = vz = 0;
         if (entry < 0 || entry >= d.num_blocks) return;
         const int64_t slot = (x.k * kKeyTile + row) & (d.block_size - 1);
-        if constexpr (CK == kU3) {
+        if constexpr (is_packed(CK)) {
             const int64_t m = entry * d.m_blk + slot * d.m_slot + x.w.h * d.m_head;
             const int64_t z = entry * d.z_blk + slot * d.z_slot + x.w.h * d.z_head;
             ks = __ldg(d.k_qs + m);
@@ -825,7 +825,7 @@ __device__ __forceinline__ void convert_rows(const PrefillParams &p, const Start
                 ColSlot &cs = cols[tile_n % L::kColSlots];
                 if constexpr (GS) {
                     auto value = [](uint32_t x) {
-                        return CK == kU3 ? __half2float(__ushort_as_half(uint16_t(x))) : __uint_as_float(x);
+                        return is_packed(CK) ? __half2float(__ushort_as_half(uint16_t(x))) : __uint_as_float(x);
                     };
                     cs.k[row] = value(ks);
                     cs.v[row] = value(vs);
@@ -853,7 +853,35 @@ __device__ __forceinline__ void convert_rows(const PrefillParams &p, const Start
             const bool all = ok == 0xffffffffu;
             // lane -> (row, piece) so that the 8 lanes of a load or store phase hit
             // different banks; four pieces' loads before their conversion
-            if constexpr (CK == kU3) {
+            if constexpr (CK == kU4) {
+                // 32 / kPieces rows at a time.  A lane's four stores go to pieces 4c + j of its
+                // row; at head_dim 128 the lanes of pieces 2 and 3, whose stores lie in the other
+                // chunk at the same banks, take j in the order 2 3 0 1
+                constexpr int RPP = 32 / kPieces;
+                const int r = lane / kPieces, c = lane % kPieces, turn = kPieces == 4 ? c & 2 : 0;
+                const float z_of = float(kv ? vz_now : kz_now);
+                uint4 v[NR / RPP];
+#pragma unroll
+                for (int i = 0; i < NR / RPP; ++i) {
+                    v[i] = *reinterpret_cast<const uint4 *>(from + (row0 + r + i * RPP) * RB + 16 * c);
+                    // a row that is not wanted becomes zero: code 0 with zero point 0
+                    if (!((ok >> (r + i * RPP)) & 1u)) v[i] = make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int i = 0; i < NR / RPP; ++i) {
+                    const int rr = row0 + r + i * RPP;
+                    float z = __shfl_sync(0xffffffffu, z_of, r + i * RPP);
+                    if (!((ok >> (r + i * RPP)) & 1u)) z = 0.0f;
+                    const uint32_t nz = tc::pack16<kF16>(-1024.0f - z, -1024.0f - z);
+                    const uint32_t w[4] = {turn ? v[i].z : v[i].x, turn ? v[i].w : v[i].y, turn ? v[i].x : v[i].z, turn ? v[i].y : v[i].w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t o[4];
+                        u4x8_to_f16(w[j], nz, o);
+                        tc::st_shared16(dst + piece_at(rr, 4 * c + (j ^ turn)), make_uint4(o[0], o[1], o[2], o[3]));
+                    }
+                }
+            } else if constexpr (CK == kU3) {
                 const int r = lane >> 1, rr = row0 + r, h = lane & 1;
                 const float z = float(__shfl_sync(0xffffffffu, kv ? vz_now : kz_now, r));
                 const bool there = (ok >> r) & 1u;
@@ -948,7 +976,7 @@ __device__ __noinline__ int redo_share(const PrefillParams &p, const Start &st, 
 // ---------------------------------------------------------------- the kernel
 // Warps 0-7 softmax; 16-bit caches by TMA: 8 and 9 products, 10 K and Q, 11 V,
 // 12-15 output; the others: 8-11 producers, 12 and 13 products, 14 raw codes,
-// 15 Q, 16-19 output, and for 3-bit codes 20-23 producers.
+// 15 Q, 16-19 output, and for 3- and 4-bit codes 20-23 producers.
 template <int QK, int CK, int D, int FEED, bool GS>
 __global__ void __launch_bounds__(prefill_threads<CK, FEED>(), 1)
     prefill_kernel(PrefillParams p, PrefillFast f, const __grid_constant__ CUtensorMap tmk,

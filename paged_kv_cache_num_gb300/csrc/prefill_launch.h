@@ -33,5 +33,6 @@ cudaError_t launch_prefill_e4m3(const PrefillLaunch &a);
 cudaError_t launch_prefill_e5m2(const PrefillLaunch &a);
 cudaError_t launch_prefill_i8(const PrefillLaunch &a);
 cudaError_t launch_prefill_u3(const PrefillLaunch &a);
+cudaError_t launch_prefill_u4(const PrefillLaunch &a);
 
 }  // namespace pkv

@@ -14,11 +14,15 @@ __device__ __forceinline__ void cached_elems(const DecodeParams &p, bool v, int6
                                              float (&x)[EPL])
 {
     const char *row = (v ? p.v_cache : p.k_cache) + blk * p.c_blk + off * p.c_slot + h * p.c_head;
-    if constexpr (CK == kU3) {
+    if constexpr (is_packed(CK)) {
         const float s = __half2float(__ushort_as_half((v ? p.v_qs : p.k_qs)[blk * p.m_blk + off * p.m_slot + h * p.m_head]));
         const float z = float((v ? p.v_qz : p.k_qz)[blk * p.z_blk + off * p.z_slot + h * p.z_head]);
 #pragma unroll
         for (int e = 0; e < EPL; ++e) {
+            if constexpr (CK == kU4) {
+                x[e] = (float((uint8_t(row[(e0 + e) >> 1]) >> (4 * ((e0 + e) & 1))) & 15u) - z) * s;
+                continue;
+            }
             const int bit = 3 * (e0 + e);
             uint32_t w = uint8_t(row[bit >> 3]);
             if ((bit & 7) > 5) w |= uint32_t(uint8_t(row[(bit >> 3) + 1])) << 8;

@@ -19,7 +19,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libpkv.so")
 
 # dtype codes (pkv.h)
-F16, BF16, E4M3, U3, U8, I32, I64, F32, E5M2, I8 = 1, 2, 3, 4, 5, 6, 7, 8, 9, 10
+F16, BF16, E4M3, U3, U8, I32, I64, F32, E5M2, I8, U4 = 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11
 # device error bits
 DEVERR_SLOT_RANGE, DEVERR_BLOCK_RANGE, DEVERR_CONTEXT_RANGE, DEVERR_POS_RANGE, DEVERR_TIMEOUT = (
     1, 2, 4, 8, 16)
@@ -194,9 +194,9 @@ def _elsewhere(dev: int, stream):
 @dataclass
 class KVCache:
     """A paged KV cache [num_blocks, block_size, num_kv_heads, row] in device
-    memory.  kind: "f16", "bf16", "e4m3" / "e5m2" / "i8" (+ per-kv-head fp32 scales) or "u3"
-    (3-bit codes, row = 3*head_dim/8 bytes, + fp16 scale / uint8 zero per
-    (slot, head)).  layout "xvec" (16-bit and one-byte kinds): k_cache /
+    memory.  kind: "f16", "bf16", "e4m3" / "e5m2" / "i8" (+ per-kv-head fp32 scales), or "u3" /
+    "u4" (3- or 4-bit codes, row = 3*head_dim/8 or head_dim/2 bytes, + fp16
+    scale / uint8 zero per (slot, head)).  layout "xvec" (16-bit and one-byte kinds): k_cache /
     v_cache are stored [num_blocks, num_kv_heads, head_dim // x, block_size,
     x] with x = 16 bytes / element size."""
     kind: str
@@ -233,7 +233,7 @@ class KVCache:
         if self.layout == "xvec":
             return self.k_cache.shape[2] * self.k_cache.shape[4]
         r = self.k_cache.shape[3]
-        return r * 8 // 3 if self.kind == "u3" else r
+        return r * 8 // 3 if self.kind == "u3" else r * 2 if self.kind == "u4" else r
 
     @staticmethod
     def allocate(kind: str, num_blocks: int, block_size: int, num_kv_heads: int, head_dim: int,
@@ -287,8 +287,8 @@ class KVCache:
                 hm = (num_blocks, num_kv_heads, block_size)
                 c.k_scales = torch.ones(hm, dtype=torch.float32, device=device).permute(0, 2, 1)
                 c.v_scales = torch.ones(hm, dtype=torch.float32, device=device).permute(0, 2, 1)
-        elif kind == "u3":
-            k = torch.empty(shape + (3 * head_dim // 8,), dtype=torch.uint8, device=device)
+        elif kind in ("u3", "u4"):
+            k = torch.empty(shape + (int(kind[1]) * head_dim // 8,), dtype=torch.uint8, device=device)
             v = torch.empty_like(k)
             # scale / zero stored head-major ([num_blocks, num_kv_heads,
             # block_size]) and seen through a [num_blocks, block_size,
@@ -302,7 +302,7 @@ class KVCache:
         else:
             raise ValueError(kind)
         if fill is not None:
-            for t in [c.k_cache, c.v_cache] + (phys if kind == "u3" else []):
+            for t in [c.k_cache, c.v_cache] + (phys if kind in ("u3", "u4") else []):
                 t.view(torch.uint8).fill_(fill)
         return c
 
@@ -335,7 +335,7 @@ class KVCache:
 
     def _build_struct(self) -> _Cache:
         s = _Cache()
-        code = {"f16": F16, "bf16": BF16, "e4m3": E4M3, "e5m2": E5M2, "i8": I8, "u3": U3}[self.kind]
+        code = {"f16": F16, "bf16": BF16, "e4m3": E4M3, "e5m2": E5M2, "i8": I8, "u3": U3, "u4": U4}[self.kind]
         self._check_types()
         if self.layout == "xvec":
             # [P, Hkv, D/x, BS, x] described as [P, BS, Hkv, D] + the piece stride
@@ -350,7 +350,7 @@ class KVCache:
                 raise ValueError("fp8 / int8 cache needs k_scale / v_scale")
             s.k_scale = self.k_scale.data_ptr()
             s.v_scale = self.v_scale.data_ptr()
-        if self.kind == "u3":
+        if self.kind in ("u3", "u4"):
             s.k_qscale = _desc(self.k_qscale, F16)
             s.k_qzero = _desc(self.k_qzero, U8)
             s.v_qscale = _desc(self.v_qscale, F16)
