@@ -13,6 +13,10 @@
  *   - paged_prefill: causal attention of packed prompts, or chunks of them,
  *     over the same pool;
  *   - kv_gather: the read back of cached rows, dequantised;
+ *   - norm_rope, norm_rope_append: the norm of each query and key head and its
+ *     rotation by position, with the keys' and values' append in the same pass;
+ *   - extend_tables, trim_tables: block tables, slots and row numbers of a step
+ *     made from request lengths, and blocks given back;
  *   - pack3 / unpack3: the bit-exact 3-bit packing on its own.
  *
  * Conventions shared by every call
@@ -81,7 +85,8 @@ enum {
     PKV_DEVERR_CONTEXT_RANGE = 4, /* decode: context_len < 0 or > table capacity */
     PKV_DEVERR_POS_RANGE = 8,     /* slot_mapping: position outside the table */
     PKV_DEVERR_TIMEOUT = 16,      /* a bounded in-kernel wait gave up */
-    PKV_DEVERR_QSTART_RANGE = 32  /* prefill: q_starts decreasing or outside [0, num_tokens] */
+    PKV_DEVERR_QSTART_RANGE = 32, /* prefill: q_starts decreasing or outside [0, num_tokens] */
+    PKV_DEVERR_POOL_RANGE = 64    /* extend / trim_tables: too few free blocks or rows, or a bad free count */
 };
 
 /* A strided view of device memory (up to 4 dimensions). */
@@ -300,6 +305,113 @@ int pkv_kv_append_dynamic(const pkv_tensor *k_new, const pkv_tensor *v_new,
  */
 int pkv_kv_gather(const pkv_cache *cache, const pkv_tensor *slot_mapping, const pkv_tensor *k_out,
                   const pkv_tensor *v_out, int32_t *err_flag, void *stream);
+
+/*
+ * pkv_norm_rope -- the norm of each query and key head and its rotation by
+ * position.  Per (token, head) row x of q and of k, in fp32, rounded once to
+ * the row's type:
+ *   y_d = x_d / sqrt(mean of x^2 + eps) * weight_d  (weight given; else y = x)
+ *   for i < rot / 2, with c = cos[pos][i], s = sin[pos][i]:
+ *     (y_a, y_b) -> (y_a c - y_b s, y_b c + y_a s),
+ *     (a, b) = (i, i + rot / 2), or (2i, 2i + 1) where `interleaved` is not 0;
+ *   elements from rot on are not rotated.  The rows' sums of squares have to be
+ *   finite in fp32.
+ *   q            : F16 or BF16 [num_tokens, num_heads, head_dim], head_dim 64 or
+ *                  128, contiguous, any token and head strides.
+ *   k            : as q's type, [num_tokens, num_kv_heads, head_dim], likewise.
+ *   q_weight, k_weight : F32 or q's type (both the same), [head_dim] contiguous;
+ *                  NULL: rows are rotated without a norm.
+ *   eps          : finite, >= 0.
+ *   cos_sin      : F32 [max_pos, rot], rows contiguous, of 16-byte alignment: rot /
+ *                  2 cosines, then as many sines.  rot is a multiple of 16, from
+ *                  16 to head_dim.
+ *   pos          : I32 [num_tokens], any stride: row of cos_sin.  pos < 0 is a
+ *                  padding token: its rows are neither read nor written.  One
+ *                  >= max_pos is left out too and raises PKV_DEVERR_POS_RANGE.
+ *   q_out, k_out : as q and k, head_dim contiguous, any token and head strides;
+ *                  may be q and k themselves, and must not overlap them
+ *                  otherwise.
+ * An addition of this library.
+ */
+int pkv_norm_rope(const pkv_tensor *q, const pkv_tensor *k, const pkv_tensor *q_weight,
+                  const pkv_tensor *k_weight, float eps, const pkv_tensor *cos_sin, const pkv_tensor *pos,
+                  int interleaved, const pkv_tensor *q_out, const pkv_tensor *k_out, int32_t *err_flag,
+                  void *stream);
+
+/*
+ * pkv_norm_rope_append -- pkv_norm_rope whose keys go into the cache, and the
+ * values with them: byte for byte what pkv_norm_rope followed by pkv_kv_append
+ * (pkv_kv_append_dynamic for caches with per-token scales) of its k_out and of
+ * v_new stores.  Every dtype, layout and scale granularity of pkv_cache (16-bit
+ * caches of q's dtype), head_dim 64 or 128, any block size.
+ *   k_new, v_new, slot_mapping, cache : as pkv_kv_append.  A token with slot < 0
+ *                  stores no keys and values; its queries are still written
+ *                  unless pos < 0, which leaves the token out altogether.
+ * An addition of this library.
+ */
+int pkv_norm_rope_append(const pkv_tensor *q, const pkv_tensor *k_new, const pkv_tensor *v_new,
+                         const pkv_tensor *q_weight, const pkv_tensor *k_weight, float eps,
+                         const pkv_tensor *cos_sin, const pkv_tensor *pos, int interleaved,
+                         const pkv_tensor *slot_mapping, const pkv_cache *cache, const pkv_tensor *q_out,
+                         int32_t *err_flag, void *stream);
+
+/*
+ * pkv_extend_tables -- a step's block tables, context lengths, row numbers and
+ * slots, from the requests' lengths, on the device.  Request b has
+ * cached_lens[b] tokens and gets new_lens[b] more; blocks that it needs come
+ * from the top of a stack of free ones, those of a request below those of the
+ * requests before it.
+ *   block_tables : I32 [batch, max_blocks_per_seq], any strides; entries of the
+ *                  new blocks are written, the others stay.
+ *   cached_lens, new_lens : I32 [batch], any strides.
+ *   free_blocks  : I32 [pool] contiguous: the stack, of which the first
+ *                  free_count entries count.  Not written.
+ *   free_count, free_left : I32 [1]: free blocks before and after; may be the
+ *                  same memory.
+ *   context_lens : I32 [batch] output, any stride: cached + new; may be
+ *                  cached_lens itself.
+ *   q_starts     : I32 [batch + 1] output, contiguous: row numbers of the step,
+ *                  as pkv_paged_prefill takes them.
+ *   req, pos     : I32 [num_rows], slot_mapping : I64 [num_rows], outputs,
+ *                  contiguous: each row's request, position and slot; -1 in the
+ *                  rows behind the last request's, for any num_rows.
+ *   block_size   : a power of two.
+ *   A cached length below 0 or above the table's capacity counts as 0 or as the
+ *   capacity, and new tokens below 0 or beyond the capacity as none
+ *   (PKV_DEVERR_CONTEXT_RANGE).  Requests are served in order; from the first one
+ *   on that finds too few free blocks or rows none gets new tokens, and
+ *   their context_lens are their cached ones (PKV_DEVERR_POOL_RANGE).  A free
+ *   count outside [0, pool] is brought into it and raises that too.
+ *   batch <= 16384, a table's capacity and num_rows below 2^31.  Outputs that are
+ *   not said to share memory must not.  An addition of this library.
+ */
+int pkv_extend_tables(const pkv_tensor *block_tables, const pkv_tensor *cached_lens,
+                      const pkv_tensor *new_lens, const pkv_tensor *free_blocks,
+                      const pkv_tensor *free_count, int block_size, const pkv_tensor *context_lens,
+                      const pkv_tensor *q_starts, const pkv_tensor *req, const pkv_tensor *pos,
+                      const pkv_tensor *slot_mapping, const pkv_tensor *free_left, int32_t *err_flag,
+                      void *stream);
+
+/*
+ * pkv_trim_tables -- the inverse: request b keeps the first keep_lens[b] of its
+ * context_lens[b] tokens (0: the request ends; fewer than it had: rejected
+ * drafts), and the blocks that hold none of them are pushed on the stack, in
+ * the order of requests and of their tables.
+ *   block_tables : as pkv_extend_tables; only read (entries of dropped blocks
+ *                  stay as they were).
+ *   context_lens, keep_lens : I32 [batch], any strides.  A length to keep above
+ *                  the context's drops nothing, one below 0 counts as 0.
+ *   free_blocks  : I32 [pool]; entries free_count .. free_left - 1 are written.
+ *   kept_lens    : I32 [batch] output, any stride: min(keep, context); may be
+ *                  context_lens or keep_lens.
+ *   free_count, free_left, block_size, limits and errors as pkv_extend_tables; from
+ *   the first request on whose blocks the stack has no room for none drops any
+ *   (PKV_DEVERR_POOL_RANGE).  An addition of this library.
+ */
+int pkv_trim_tables(const pkv_tensor *block_tables, const pkv_tensor *context_lens,
+                    const pkv_tensor *keep_lens, const pkv_tensor *free_blocks,
+                    const pkv_tensor *free_count, int block_size, const pkv_tensor *kept_lens,
+                    const pkv_tensor *free_left, int32_t *err_flag, void *stream);
 
 /*
  * pkv_paged_prefill -- causal attention of packed new tokens over the paged

@@ -738,6 +738,205 @@ int pkv_kv_gather(const pkv_cache *cache, const pkv_tensor *slot_mapping, const 
 
 namespace {
 
+// What both forms of the norm and rotation share: queries, weights, the table,
+// positions.  `head_dim`, `T`, `src` come from the keys.
+int prep_norm_rope(const pkv_tensor *q, const pkv_tensor *q_weight, const pkv_tensor *k_weight, float eps,
+                   const pkv_tensor *cos_sin, const pkv_tensor *pos, int interleaved, const pkv_tensor *q_out,
+                   pkv::NormRopeParams &p)
+{
+    const int64_t T = p.a.num_tokens, D = p.a.head_dim;
+    const int src = p.a.src_kind;
+    TRY(check_tensor(q, "q", 3));
+    TRY(check_tensor(q_out, "q_out", 3));
+    TRY(check_tensor(cos_sin, "cos_sin", 2));
+    TRY(check_tensor(pos, "pos", 1));
+    if (q->dtype != src || q_out->dtype != src) return fail(PKV_ERR_DTYPE, "q, q_out and the keys must have one dtype");
+    if (q->shape[0] != T || q->shape[2] != D) return fail(PKV_ERR_SHAPE, "q and the keys differ in tokens or head_dim");
+    if (D != 64 && D != 128) return fail(PKV_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+    for (int i = 0; i < 3; ++i)
+        if (q_out->shape[i] != q->shape[i]) return fail(PKV_ERR_SHAPE, "q_out shape must equal q shape");
+    if (q->stride[2] != 1 || q_out->stride[2] != 1) return fail(PKV_ERR_LAYOUT, "head_dim of q and q_out must be contiguous");
+    if (q->shape[1] > (1 << 24) || p.a.num_kv_heads > (1 << 24)) return fail(PKV_ERR_UNSUPPORTED, "more than 2^24 heads");
+    p.weight_kind = src;
+    const pkv_tensor *weights[2] = {q_weight, k_weight};
+    for (const pkv_tensor *w : weights) {
+        if (!w) continue;
+        TRY(check_tensor(w, "weight", 1));
+        if (w->dtype != src && w->dtype != PKV_DTYPE_F32) return fail(PKV_ERR_DTYPE, "weights must be F32 or of q's dtype");
+        if (w->shape[0] != D) return fail(PKV_ERR_SHAPE, "weights must be [head_dim]");
+        if (w->stride[0] != 1) return fail(PKV_ERR_LAYOUT, "weights must be contiguous");
+        p.weight_kind = w->dtype;
+    }
+    if (q_weight && k_weight && q_weight->dtype != k_weight->dtype) return fail(PKV_ERR_DTYPE, "q_weight and k_weight dtypes differ");
+    if (!std::isfinite(eps) || eps < 0.0f) return fail(PKV_ERR_VALUE, "eps must be finite and not negative");
+    if (cos_sin->dtype != PKV_DTYPE_F32) return fail(PKV_ERR_DTYPE, "cos_sin must be F32");
+    if (pos->dtype != PKV_DTYPE_I32) return fail(PKV_ERR_DTYPE, "pos must be I32");
+    if (pos->shape[0] != T) return fail(PKV_ERR_SHAPE, "pos has %lld entries, q %lld tokens", (long long)pos->shape[0], (long long)T);
+    const int64_t rot = cos_sin->shape[1];
+    if (rot < 16 || rot > D || rot % 16 != 0) return fail(PKV_ERR_UNSUPPORTED, "cos_sin rows must be a multiple of 16, at most head_dim");
+    if (cos_sin->stride[1] != 1 || cos_sin->stride[0] % 4 != 0 || !aligned(cos_sin->data, 16))
+        return fail(PKV_ERR_LAYOUT, "cos_sin rows must be contiguous and 16-byte aligned");
+    p.q = static_cast<const char *>(q->data);
+    p.q_tok = q->stride[0] * 2;
+    p.q_head = q->stride[1] * 2;
+    p.q_out = static_cast<char *>(q_out->data);
+    p.qo_tok = q_out->stride[0] * 2;
+    p.qo_head = q_out->stride[1] * 2;
+    p.num_heads = int(q->shape[1]);
+    p.q_weight = q_weight ? q_weight->data : nullptr;
+    p.k_weight = k_weight ? k_weight->data : nullptr;
+    p.eps = eps;
+    p.cos_sin = static_cast<const float *>(cos_sin->data);
+    p.cs_row = cos_sin->stride[0];
+    p.max_pos = cos_sin->shape[0];
+    p.rot = int(rot);
+    p.interleaved = interleaved != 0;
+    p.pos = static_cast<const int32_t *>(pos->data);
+    p.pos_stride = pos->stride[0];
+    return PKV_OK;
+}
+
+bool rows16(const void *data, int64_t tok, int64_t head) { return aligned(data, 16) && tok % 16 == 0 && head % 16 == 0; }
+
+}  // namespace
+
+int pkv_norm_rope(const pkv_tensor *q, const pkv_tensor *k, const pkv_tensor *q_weight, const pkv_tensor *k_weight,
+                  float eps, const pkv_tensor *cos_sin, const pkv_tensor *pos, int interleaved, const pkv_tensor *q_out,
+                  const pkv_tensor *k_out, int32_t *err_flag, void *stream)
+{
+    TRY(check_tensor(k, "k", 3));
+    TRY(check_tensor(k_out, "k_out", 3));
+    if (k->dtype != PKV_DTYPE_F16 && k->dtype != PKV_DTYPE_BF16) return fail(PKV_ERR_DTYPE, "k must be F16 or BF16");
+    if (k_out->dtype != k->dtype) return fail(PKV_ERR_DTYPE, "k_out dtype must equal k dtype");
+    for (int i = 0; i < 3; ++i)
+        if (k_out->shape[i] != k->shape[i]) return fail(PKV_ERR_SHAPE, "k_out shape must equal k shape");
+    if (k->stride[2] != 1 || k_out->stride[2] != 1) return fail(PKV_ERR_LAYOUT, "head_dim of k and k_out must be contiguous");
+    if (k->shape[2] > 128) return fail(PKV_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+    pkv::NormRopeParams p{};
+    p.a.k_new = static_cast<const char *>(k->data);
+    p.a.k_src_tok = k->stride[0] * 2;
+    p.a.k_src_head = k->stride[1] * 2;
+    p.a.num_tokens = k->shape[0];
+    p.a.num_kv_heads = int(k->shape[1] > (1 << 24) ? (1 << 24) + 1 : k->shape[1]);
+    p.a.head_dim = int(k->shape[2]);
+    p.a.src_kind = k->dtype;
+    p.a.err_flag = err_flag;
+    TRY(prep_norm_rope(q, q_weight, k_weight, eps, cos_sin, pos, interleaved, q_out, p));
+    p.k_out = static_cast<char *>(k_out->data);
+    p.ko_tok = k_out->stride[0] * 2;
+    p.ko_head = k_out->stride[1] * 2;
+    p.vec = rows16(p.q, p.q_tok, p.q_head) && rows16(p.a.k_new, p.a.k_src_tok, p.a.k_src_head);
+    p.out_vec = rows16(p.q_out, p.qo_tok, p.qo_head) && rows16(p.k_out, p.ko_tok, p.ko_head);
+    return launch_status(pkv::launch_norm_rope(p, 0, as_stream(stream)), "norm_rope kernel");
+}
+
+int pkv_norm_rope_append(const pkv_tensor *q, const pkv_tensor *k_new, const pkv_tensor *v_new,
+                         const pkv_tensor *q_weight, const pkv_tensor *k_weight, float eps, const pkv_tensor *cos_sin,
+                         const pkv_tensor *pos, int interleaved, const pkv_tensor *slot_mapping, const pkv_cache *cache,
+                         const pkv_tensor *q_out, int32_t *err_flag, void *stream)
+{
+    if (!cache) return fail(PKV_ERR_NULL, "cache: descriptor is NULL");
+    pkv::NormRopeParams p{};
+    int kind = 0;
+    bool vec16 = false;
+    TRY(prep_kv_append(k_new, v_new, slot_mapping, cache, err_flag, p.a, kind, vec16, nullptr, nullptr,
+                       cache->scale_mode == PKV_SCALE_PER_TOKEN));
+    TRY(prep_norm_rope(q, q_weight, k_weight, eps, cos_sin, pos, interleaved, q_out, p));
+    p.vec = vec16 && rows16(p.q, p.q_tok, p.q_head);
+    p.out_vec = rows16(p.q_out, p.qo_tok, p.qo_head);
+    return launch_status(pkv::launch_norm_rope(p, kind, as_stream(stream)), "norm_rope_append kernel");
+}
+
+namespace {
+
+// What extend_tables and trim_tables share.
+int prep_tables(const pkv_tensor *block_tables, const pkv_tensor *first, const pkv_tensor *second,
+                const pkv_tensor *lens_out, const pkv_tensor *free_blocks, const pkv_tensor *free_count,
+                const pkv_tensor *free_left, int block_size, int32_t *err_flag, pkv::TableParams &p)
+{
+    TRY(check_tensor(block_tables, "block_tables", 2));
+    TRY(check_tensor(first, "lengths", 1));
+    TRY(check_tensor(second, "lengths", 1));
+    TRY(check_tensor(lens_out, "lengths", 1));
+    TRY(check_tensor(free_blocks, "free_blocks", 1));
+    TRY(check_tensor(free_count, "free_count", 1));
+    TRY(check_tensor(free_left, "free_left", 1));
+    const pkv_tensor *all[] = {block_tables, first, second, lens_out, free_blocks, free_count, free_left};
+    for (const pkv_tensor *t : all)
+        if (t->dtype != PKV_DTYPE_I32) return fail(PKV_ERR_DTYPE, "block tables, lengths, free blocks and counts must be I32");
+    const int64_t batch = block_tables->shape[0];
+    if (first->shape[0] != batch || second->shape[0] != batch || lens_out->shape[0] != batch)
+        return fail(PKV_ERR_SHAPE, "lengths and block_tables rows differ in number");
+    if (free_count->shape[0] != 1 || free_left->shape[0] != 1) return fail(PKV_ERR_SHAPE, "free_count and free_left are one number each");
+    if (free_blocks->stride[0] != 1 && free_blocks->shape[0] > 1) return fail(PKV_ERR_LAYOUT, "free_blocks must be contiguous");
+    if (!is_pow2(block_size)) return fail(PKV_ERR_VALUE, "block_size must be a power of two");
+    if (batch > pkv::kTableMaxBatch) return fail(PKV_ERR_UNSUPPORTED, "more than %d requests", pkv::kTableMaxBatch);
+    if (block_tables->shape[1] > INT32_MAX / block_size) return fail(PKV_ERR_UNSUPPORTED, "block table rows must cover less than 2^31 tokens");
+    if (free_blocks->shape[0] > INT32_MAX) return fail(PKV_ERR_UNSUPPORTED, "free_blocks of 2^31 entries or more");
+    p = pkv::TableParams{};
+    p.bt = static_cast<int32_t *>(block_tables->data);
+    p.bt_b = block_tables->stride[0];
+    p.bt_j = block_tables->stride[1];
+    p.batch = int(batch);
+    p.max_blocks = int(block_tables->shape[1]);
+    p.block_shift = log2i(block_size);
+    p.first = static_cast<const int32_t *>(first->data);
+    p.first_stride = first->stride[0];
+    p.second = static_cast<const int32_t *>(second->data);
+    p.second_stride = second->stride[0];
+    p.lens_out = static_cast<int32_t *>(lens_out->data);
+    p.lens_stride = lens_out->stride[0];
+    p.free_blocks = static_cast<int32_t *>(free_blocks->data);
+    p.pool = free_blocks->shape[0];
+    p.free_count = static_cast<const int32_t *>(free_count->data);
+    p.free_left = static_cast<int32_t *>(free_left->data);
+    p.err_flag = err_flag;
+    return PKV_OK;
+}
+
+}  // namespace
+
+int pkv_extend_tables(const pkv_tensor *block_tables, const pkv_tensor *cached_lens, const pkv_tensor *new_lens,
+                      const pkv_tensor *free_blocks, const pkv_tensor *free_count, int block_size,
+                      const pkv_tensor *context_lens, const pkv_tensor *q_starts, const pkv_tensor *req,
+                      const pkv_tensor *pos, const pkv_tensor *slot_mapping, const pkv_tensor *free_left,
+                      int32_t *err_flag, void *stream)
+{
+    pkv::TableParams p;
+    TRY(prep_tables(block_tables, cached_lens, new_lens, context_lens, free_blocks, free_count, free_left, block_size, err_flag, p));
+    TRY(check_tensor(q_starts, "q_starts", 1));
+    TRY(check_tensor(req, "req", 1));
+    TRY(check_tensor(pos, "pos", 1));
+    TRY(check_tensor(slot_mapping, "slot_mapping", 1));
+    if (q_starts->dtype != PKV_DTYPE_I32 || req->dtype != PKV_DTYPE_I32 || pos->dtype != PKV_DTYPE_I32)
+        return fail(PKV_ERR_DTYPE, "q_starts, req and pos must be I32");
+    if (slot_mapping->dtype != PKV_DTYPE_I64) return fail(PKV_ERR_DTYPE, "slot_mapping must be I64");
+    if (q_starts->shape[0] != int64_t(p.batch) + 1) return fail(PKV_ERR_SHAPE, "q_starts must have batch + 1 entries");
+    const int64_t n = req->shape[0];
+    if (pos->shape[0] != n || slot_mapping->shape[0] != n) return fail(PKV_ERR_SHAPE, "req, pos and slot_mapping lengths differ");
+    if (n > INT32_MAX - (1 << 20)) return fail(PKV_ERR_UNSUPPORTED, "2^31 rows or more");
+    const pkv_tensor *rows[] = {q_starts, req, pos, slot_mapping};
+    for (const pkv_tensor *t : rows)
+        if (t->stride[0] != 1 && t->shape[0] > 1) return fail(PKV_ERR_LAYOUT, "q_starts, req, pos and slot_mapping must be contiguous");
+    p.q_starts = static_cast<int32_t *>(q_starts->data);
+    p.req = static_cast<int32_t *>(req->data);
+    p.pos = static_cast<int32_t *>(pos->data);
+    p.slot_mapping = static_cast<int64_t *>(slot_mapping->data);
+    p.num_rows = n;
+    return launch_status(pkv::launch_tables(p, false, as_stream(stream)), "extend_tables kernel");
+}
+
+int pkv_trim_tables(const pkv_tensor *block_tables, const pkv_tensor *context_lens, const pkv_tensor *keep_lens,
+                    const pkv_tensor *free_blocks, const pkv_tensor *free_count, int block_size,
+                    const pkv_tensor *kept_lens, const pkv_tensor *free_left, int32_t *err_flag, void *stream)
+{
+    pkv::TableParams p;
+    TRY(prep_tables(block_tables, context_lens, keep_lens, kept_lens, free_blocks, free_count, free_left, block_size, err_flag, p));
+    return launch_status(pkv::launch_tables(p, true, as_stream(stream)), "trim_tables kernel");
+}
+
+namespace {
+
 struct PrefillCheck {
     CacheInfo ci;
     pkv::PrefillParams p;      // every field known before q_starts / context_lens / out / workspace

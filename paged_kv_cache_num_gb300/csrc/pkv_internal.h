@@ -203,6 +203,62 @@ struct GatherParams {
 
 cudaError_t launch_gather(const GatherParams &p, int cache_kind, int out_kind, cudaStream_t s);
 
+// ---------------------------------------------------------------- norm and rotation
+struct NormRopeParams {
+    AppendParams a;             // keys and values: k_new, v_new, num_tokens, num_kv_heads, head_dim, src_kind, and,
+                                // with a cache, where they go
+    const char *q;
+    int64_t q_tok, q_head;      // byte strides
+    char *q_out;
+    int64_t qo_tok, qo_head;
+    char *k_out;                // without a cache
+    int64_t ko_tok, ko_head;
+    int num_heads;
+    const void *q_weight;       // [head_dim], or none: no norm
+    const void *k_weight;
+    int weight_kind;            // kF16, kBF16 or PKV_DTYPE_F32
+    float eps;
+    const float *cos_sin;       // [max_pos][rot]: cos, then sin
+    int64_t cs_row;             // elements
+    int64_t max_pos;
+    int rot;
+    int interleaved;
+    const int32_t *pos;
+    int64_t pos_stride;
+    int vec;                    // source rows at multiples of 16 bytes
+    int out_vec;                // output rows likewise
+};
+
+// cache_kind 0: keys to k_out
+cudaError_t launch_norm_rope(const NormRopeParams &p, int cache_kind, cudaStream_t s);
+
+// ---------------------------------------------------------------- block tables
+constexpr int kTableMaxBatch = 16384;   // three 32-bit numbers each in shared memory
+
+struct TableParams {
+    int32_t *bt;
+    int64_t bt_b, bt_j;
+    int batch, max_blocks, block_shift;
+    const int32_t *first;       // cached tokens
+    int64_t first_stride;
+    const int32_t *second;      // new tokens, or (trim) tokens to keep
+    int64_t second_stride;
+    int32_t *lens_out;
+    int64_t lens_stride;
+    int32_t *free_blocks;
+    int64_t pool;               // entries of free_blocks
+    const int32_t *free_count;
+    int32_t *free_left;
+    int32_t *q_starts;          // extend: [batch + 1]
+    int32_t *req;               // extend: [num_rows]
+    int32_t *pos;
+    int64_t *slot_mapping;
+    int64_t num_rows;
+    int32_t *err_flag;
+};
+
+cudaError_t launch_tables(const TableParams &p, bool trim, cudaStream_t s);
+
 // ---------------------------------------------------------------- prefill
 struct PrefillParams {
     DecodeParams d;             // q / out: [num_tokens, num_heads, head_dim], q_b / o_b the token strides

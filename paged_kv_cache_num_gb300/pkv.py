@@ -24,6 +24,7 @@ F16, BF16, E4M3, U3, U8, I32, I64, F32, E5M2, I8, U4 = 1, 2, 3, 4, 5, 6, 7, 8, 9
 DEVERR_SLOT_RANGE, DEVERR_BLOCK_RANGE, DEVERR_CONTEXT_RANGE, DEVERR_POS_RANGE, DEVERR_TIMEOUT = (
     1, 2, 4, 8, 16)
 DEVERR_QSTART_RANGE = 32
+DEVERR_POOL_RANGE = 64
 
 _TORCH_CODES = {torch.float16: F16, torch.bfloat16: BF16, torch.float8_e4m3fn: E4M3,
                 torch.float8_e5m2: E5M2, torch.int8: I8,
@@ -94,6 +95,10 @@ def lib():
             L.pkv_paged_prefill_workspace.argtypes = [P, P, P, P]
             L.pkv_paged_prefill_launches.argtypes = [P, P, P, P]
             L.pkv_paged_prefill.argtypes = [P, P, P, P, P, ctypes.c_float, P, P, ctypes.c_size_t, P, P]
+            L.pkv_norm_rope.argtypes = [P, P, P, P, ctypes.c_float, P, P, ctypes.c_int, P, P, P, P]
+            L.pkv_norm_rope_append.argtypes = [P, P, P, P, P, ctypes.c_float, P, P, ctypes.c_int, P, P, P, P, P]
+            L.pkv_extend_tables.argtypes = [P, P, P, P, P, ctypes.c_int, P, P, P, P, P, P, P, P]
+            L.pkv_trim_tables.argtypes = [P, P, P, P, P, ctypes.c_int, P, P, P, P]
             L.pkv_noalloc_scratch_bytes.restype = ctypes.c_size_t
             L.pkv_pack3.argtypes = [P, P, ctypes.c_int64, P]
             L.pkv_unpack3.argtypes = [P, P, ctypes.c_int64, P]
@@ -103,7 +108,8 @@ def lib():
                        "pkv_paged_decode_workspace", "pkv_paged_decode_launches",
                        "pkv_paged_decode", "pkv_paged_decode_noalloc", "pkv_decode_step", "pkv_pack3",
                        "pkv_kv_append_dynamic", "pkv_kv_gather", "pkv_paged_prefill_workspace",
-                       "pkv_paged_prefill_launches", "pkv_paged_prefill", "pkv_unpack3", "pkv_unpack3_words", "pkv_copy_peak"):
+                       "pkv_paged_prefill_launches", "pkv_paged_prefill", "pkv_norm_rope", "pkv_norm_rope_append",
+                       "pkv_extend_tables", "pkv_trim_tables", "pkv_unpack3", "pkv_unpack3_words", "pkv_copy_peak"):
                 getattr(L, fn).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -447,6 +453,111 @@ def kv_gather(cache: KVCache, slot_mapping, dtype: Optional[torch.dtype] = None,
     _check(lib().pkv_kv_gather(ctypes.byref(cache._struct()), _packed(slot_mapping), _packed(k_out), _packed(v_out),
                                None if err_flag is None else err_flag.data_ptr(), _raw_stream(dev)))
     return k_out, v_out
+
+
+def _flag(err_flag):
+    return None if err_flag is None else err_flag.data_ptr()
+
+
+def norm_rope(q, k, cos_sin, pos, q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False,
+              q_out=None, k_out=None, err_flag=None, stream=None):
+    """Each head row of q [T, Hq, D] and k [T, Hkv, D] normed by its own mean
+    square (where a weight [D] is given) and rotated by its token's position:
+    row pos[t] of cos_sin [max_pos, rot] fp32, cosines then sines.  Returns
+    (q_out, k_out), allocated, with zeros where pos < 0, unless given; they
+    may be q and k themselves."""
+    dev = _one_device(q, k, cos_sin, pos, q_weight, k_weight, q_out, k_out, err_flag)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return norm_rope(q, k, cos_sin, pos, q_weight, k_weight, eps, interleaved, q_out, k_out, err_flag)
+    if q_out is None:
+        q_out = torch.zeros_like(q, memory_format=torch.contiguous_format)
+    if k_out is None:
+        k_out = torch.zeros_like(k, memory_format=torch.contiguous_format)
+    _check(lib().pkv_norm_rope(_packed(q), _packed(k), None if q_weight is None else _packed(q_weight),
+                               None if k_weight is None else _packed(k_weight), eps, _packed(cos_sin), _packed(pos),
+                               int(interleaved), _packed(q_out), _packed(k_out), _flag(err_flag), _raw_stream(dev)))
+    return q_out, k_out
+
+
+def norm_rope_append(q, k_new, v_new, cos_sin, pos, slot_mapping, cache: KVCache, q_weight=None, k_weight=None,
+                     eps: float = 1e-6, interleaved: bool = False, q_out=None, err_flag=None, stream=None):
+    """norm_rope whose keys go into the cache at slot_mapping, with the values,
+    in the same pass: what norm_rope and then kv_append (kv_append_dynamic for
+    per-token scales) store.  Returns q_out, allocated, with zeros where pos <
+    0, unless given; it may be q itself."""
+    dev = _one_device(q, k_new, v_new, cos_sin, pos, slot_mapping, q_weight, k_weight, q_out, err_flag, *cache.tensors())
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return norm_rope_append(q, k_new, v_new, cos_sin, pos, slot_mapping, cache, q_weight, k_weight, eps,
+                                    interleaved, q_out, err_flag)
+    if q_out is None:
+        q_out = torch.zeros_like(q, memory_format=torch.contiguous_format)
+    _check(lib().pkv_norm_rope_append(_packed(q), _packed(k_new), _packed(v_new),
+                                      None if q_weight is None else _packed(q_weight),
+                                      None if k_weight is None else _packed(k_weight), eps, _packed(cos_sin),
+                                      _packed(pos), int(interleaved), _packed(slot_mapping),
+                                      ctypes.byref(cache._struct()), _packed(q_out), _flag(err_flag), _raw_stream(dev)))
+    return q_out
+
+
+def extend_tables(block_tables, cached_lens, new_lens, free_blocks, free_count, block_size: int,
+                  num_rows: Optional[int] = None, context_lens=None, q_starts=None, req=None, pos=None,
+                  slot_mapping=None, free_left=None, err_flag=None, stream=None):
+    """Gives request b new_lens[b] tokens behind its cached_lens[b]: blocks from
+    the top of the stack free_blocks[:free_count] into block_tables (in
+    place), and the step's rows.  Returns (context_lens, q_starts, req, pos,
+    slot_mapping, free_left), allocated unless given; context_lens may be
+    cached_lens, free_left free_count.  The rows' outputs have num_rows
+    entries, -1 behind the last request's rows."""
+    dev = _one_device(block_tables, cached_lens, new_lens, free_blocks, free_count, context_lens, q_starts, req, pos,
+                      slot_mapping, free_left, err_flag)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return extend_tables(block_tables, cached_lens, new_lens, free_blocks, free_count, block_size, num_rows,
+                                 context_lens, q_starts, req, pos, slot_mapping, free_left, err_flag)
+    if num_rows is None:
+        given = next((t for t in (req, pos, slot_mapping) if t is not None), None)
+        if given is None:
+            raise ValueError("num_rows, or one of req, pos and slot_mapping, says how many rows there are")
+        num_rows = given.shape[0]
+
+    def out(t, n, dtype=torch.int32):
+        return torch.empty(n, dtype=dtype, device=block_tables.device) if t is None else t
+
+    batch = block_tables.shape[0]
+    context_lens, q_starts, free_left = out(context_lens, batch), out(q_starts, batch + 1), out(free_left, 1)
+    req, pos, slot_mapping = out(req, num_rows), out(pos, num_rows), out(slot_mapping, num_rows, torch.int64)
+    _check(lib().pkv_extend_tables(_packed(block_tables), _packed(cached_lens), _packed(new_lens), _packed(free_blocks),
+                                   _packed(free_count), int(block_size), _packed(context_lens), _packed(q_starts),
+                                   _packed(req), _packed(pos), _packed(slot_mapping), _packed(free_left),
+                                   _flag(err_flag), _raw_stream(dev)))
+    return context_lens, q_starts, req, pos, slot_mapping, free_left
+
+
+def trim_tables(block_tables, context_lens, keep_lens, free_blocks, free_count, block_size: int, kept_lens=None,
+                free_left=None, err_flag=None, stream=None):
+    """Request b keeps the first keep_lens[b] of its context_lens[b] tokens; the
+    blocks that hold none of them go back on the stack free_blocks (in
+    place).  Returns (kept_lens, free_left), allocated unless given; kept_lens
+    may be context_lens or keep_lens, free_left free_count."""
+    dev = _one_device(block_tables, context_lens, keep_lens, free_blocks, free_count, kept_lens, free_left, err_flag)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return trim_tables(block_tables, context_lens, keep_lens, free_blocks, free_count, block_size, kept_lens,
+                               free_left, err_flag)
+    if kept_lens is None:
+        kept_lens = torch.empty(block_tables.shape[0], dtype=torch.int32, device=block_tables.device)
+    if free_left is None:
+        free_left = torch.empty(1, dtype=torch.int32, device=block_tables.device)
+    _check(lib().pkv_trim_tables(_packed(block_tables), _packed(context_lens), _packed(keep_lens), _packed(free_blocks),
+                                 _packed(free_count), int(block_size), _packed(kept_lens), _packed(free_left),
+                                 _flag(err_flag), _raw_stream(dev)))
+    return kept_lens, free_left
 
 
 def prefill_workspace_bytes(q, cache: KVCache, block_tables) -> int:
