@@ -6,19 +6,21 @@
 //   k_t = sk_t (u_t - zk_t), v_t = sv_t (w_t - zv_t), codes u, w in 0 .. 15.
 // With that, per query head
 //   c q . k_t = c sk_t (q . u_t - zk_t sum q),
-//   sum_t p_t v_t = sum_t P_t (w_t - zv_t),  P_t = p_t sv_t,
-// so K's zero points cost one operation per score, and V's leave the operand as
-// it is made.
+//   sum_t p_t v_t = sum_t P_t w_t - sum_t P_t zv_t,  P_t = p_t sv_t,
+// so both products are of 16-bit numbers and bare codes.  K's zero points cost one
+// operation per score, V's one more row of the product.
 //
-// Codes as operands.  K: a 4-bit code at bit 4 of an otherwise zero 16-bit half
-// is the f16 subnormal u 2^-20, exact; an AND makes a pair, 7 operations for 8
-// codes.  The tensor core aligns products by their exponents as stored, 2^-14 for
-// a subnormal, so up to 2^-16 of |q|'s largest element times sk is cut off in a
-// k-step (codes at bit 0 would make that 2^-12).  V: under 0x6400 a code at bit 0
-// is 1024 + w, at bit 4 1024 + 16 w, of which one f16 addition or FMA (in another
-// pipe than the ANDs) makes w - zv, exactly.  The sums over the keys then hold what
-// they are to hold, without a part that is taken off at the end.  Pairs of V are two
-// tokens' codes, brought together by byte permutes of two rows.
+// Codes as operands.  A 4-bit code at bit 2 of an otherwise zero 16-bit half is
+// the f16 subnormal u 2^-22, at bit 6 u 2^-18, exact: two shifts and four ANDs make
+// four pairs of a word's eight codes.  The 2^4 between the two goes into q (times
+// 1/16 for the codes at bit 6) and into the output.  The tensor core aligns
+// products by their exponents as stored, 2^-14 for a subnormal, and cuts off what is
+// 2^23 below: of a score at most 2^-14 of |q|'s largest element times sk per k-step,
+// of the sums over the keys 2^-15 of a step of the code per 16 keys whose largest
+// weight is one.  (Codes at bits 0 and 4, a shift less: 2^-12 and 2^-13.  Codes made
+// normal numbers, (1024 + w) - (1024 + zv): exact, but a third more instructions,
+// which bound this kernel.)  Pairs of V are two tokens' codes: a transposed 8 x 8 load
+// of 16-bit pieces brings four codes of each.
 //
 // Work.  A unit is 32 tokens of a group of nh kv heads (two blocks of 16
 // slots, one of 32, or a part of a larger one).  All (head group, sequence,
@@ -28,10 +30,9 @@
 //
 // A CTA is nh consumer warps, one per kv head, and a producer warp that keeps
 // a ring of stages full: K and V tiles [block][nh][slots][row] by tensor copies
-// and the rows' scales and zeros by bulk copies.  Rows are 64 bytes (swizzled by
-// 64) or 32; the token that is row r of a 16-token product is chosen (row_token)
-// so that the loads of K rows (4 lanes a row) and of V rows (8 lanes a row) meet no
-// bank twice.
+// and the rows' scales and zeros by bulk copies.  Rows are 64 or 32 bytes, swizzled
+// by as much, so that neither the loads of K rows (4 lanes a row) nor the transposed
+// ones of V meet a bank twice.
 // Every wait is bounded (about 2 s) and raises PKV_DEVERR_TIMEOUT.
 #include "decode_tma_kernel.cuh"
 
@@ -45,30 +46,11 @@ constexpr int kUnitShift = 5;
 template <int NG> constexpr int kHeadsU4 = 4;
 template <int NG> constexpr int kCtasU4 = NG == 1 ? 3 : 2;
 
-// Token (of 8) that is row r of a product's tile.  head_dim 128, rows of 64
-// bytes swizzled by 64 (16-byte piece c of row i at piece c ^ (i >> 1 & 3)): lanes
-// of K take rows in pairs, which have to differ in parity; lanes of V rows 0 2 4
-// 6 or 1 3 5 7, of which those of one parity have to differ in bit 2.  head_dim 64,
-// rows of 32 bytes: K takes rows 0 - 3 and 4 - 7, V the even and the odd ones, each
-// different modulo 4.
-template <int D> __host__ __device__ constexpr int row_token(int r)
-{
-    return D == 128 ? r ^ ((r >> 1) & 1) : int((0x57463120u >> (4 * r)) & 7u);
-}
-// its inverse
-template <int D> __host__ __device__ constexpr int token_row(int t)
-{
-    return D == 128 ? t ^ ((t >> 1) & 1) : int((0x64753120u >> (4 * t)) & 7u);
-}
-constexpr bool rows_match(int (*f)(int), int (*g)(int))
-{
-    for (int r = 0; r < 8; ++r)
-        if (g(f(r)) != r) return false;
-    return true;
-}
-static_assert(rows_match(row_token<128>, token_row<128>) && rows_match(row_token<64>, token_row<64>), "inverse");
-
-constexpr int kConvBytes = kUnit * (16 + 2);        // per consumer warp: see unit()
+constexpr uint32_t kAt2 = 0x003c003cu, kAt6 = 0x03c003c0u;       // codes at bits 2 and 6 of both halves
+constexpr int kConvBytes = kUnit * (16 + 4 + 2);    // per consumer warp: see unit()
+// The maximum is raised when a score passes it by more than this (log2 units): P
+// then is at most 2^6, far within f16's range, and few units rescale.
+constexpr float kRaise = 6.0f;
 
 struct U4Smem {
     int tile, meta, stage, conv, bars, mask, prefix, ctx, total;
@@ -167,29 +149,39 @@ __global__ void __launch_bounds__(32 * (kHeadsU4<NG> + 1), (kCtasU4<NG>))
         const int sub = p.block_shift - kUnitShift;             // units of a block, log2 (NB == 1)
         const uint32_t part = uint32_t(slots) * ROW * nh;       // bytes of a block's part of the K tile
         const uint32_t block_tx = 2 * part + 6u * uint32_t(slots) * MH;
-        // the copies of scales and zeros: by array and block, or by array and head where a
-        // unit is part of a block and the arrays are head-major
+        // the copies of scales and zeros, one by a lane: by array and block, or by array and head
+        // where a unit is part of a block and the arrays are head-major
         const bool by_head = f.meta_hmaj && p.block_size > kUnit;
-        const int n_meta = 4 * (by_head ? nh : NB);
-        bool aborted = false;
+        const int arr = lane & 3, nth = lane >> 2;              // K scales, V scales, K zeros, V zeros; block or head
+        const bool copies = nth < (by_head ? nh : NB);
+        const int es = arr < 2 ? 2 : 1, my_blk = by_head ? 0 : nth & (NB - 1);
+        const uint32_t bytes = uint32_t((by_head ? slots : slots * MH) * es);
+        const uint32_t meta_to = 2 * L.tile + (arr < 2 ? 2 * arr : 2 + arr) * kUnit * MH + nth * bytes;
+        const char *meta_src = (arr == 0   ? reinterpret_cast<const char *>(p.k_qs)
+                                : arr == 1 ? reinterpret_cast<const char *>(p.v_qs)
+                                : arr == 2 ? reinterpret_cast<const char *>(p.k_qz)
+                                           : reinterpret_cast<const char *>(p.v_qz)) +
+                               (by_head ? nth * p.block_size * es : 0);
+        const int64_t meta_blk = arr < 2 ? 2 * p.m_blk : p.z_blk;
+        const int meta_hg = f.meta_hmaj ? nh * p.block_size * es : 0, meta_slot = (f.meta_hmaj ? 1 : MH) * es;
         int64_t issued = 0;
-        int ps = 0;
-        uint32_t pphase = 0;
+        int s = 0;
+        uint32_t phase = 0;
+        bool aborted = false;
         for (int64_t base = lo; base < hi && !aborted; base += 32 / NB) {
             // lane -> (unit, block of it)
             const int64_t x = base + lane / NB;
-            int pb = -1, hg = 0, slot0 = 0;
+            int pb = -1, at = 0;                                // block; head group and first slot
             if (x < hi) {
-                hg = int(x / NU);
-                const int r = int(x - int64_t(hg) * NU);
-                const int b = find_seq(prefix, B, r);
-                const int j = r - prefix[b];
+                const int hg = int(x / NU), r = int(x - int64_t(hg) * NU);
+                const int b = find_seq(prefix, B, r), j = r - prefix[b];
                 int64_t lb;                                     // logical block
                 if constexpr (NB == 2) {
                     lb = 2 * int64_t(j) + lane % NB;
+                    at = hg;
                 } else {
                     lb = j >> sub;
-                    slot0 = (j & ((1 << sub) - 1)) << kUnitShift;
+                    at = hg | ((j & ((1 << sub) - 1)) << 16);   // (hg < 2^15, see plan_decode_u4)
                 }
                 if ((lb << p.block_shift) < ctxs[b]) {          // entries behind the context are not read
                     pb = p.block_tables[b * p.bt_b + lb * p.bt_j];
@@ -199,21 +191,17 @@ __global__ void __launch_bounds__(32 * (kHeadsU4<NG> + 1), (kCtasU4<NG>))
                     }
                 }
             }
+            const uint32_t in = __ballot_sync(0xffffffffu, pb >= 0);
             const int n = int(hi - base < 32 / NB ? hi - base : 32 / NB);
             for (int k = 0; k < n; ++k) {
-                const int hgk = __shfl_sync(0xffffffffu, hg, k * NB);
-                const int s0k = __shfl_sync(0xffffffffu, slot0, k * NB);
-                int pbk[NB];
-                uint32_t there = 0;
-#pragma unroll
-                for (int i = 0; i < NB; ++i) {
-                    pbk[i] = __shfl_sync(0xffffffffu, pb, k * NB + i);
-                    there |= (pbk[i] >= 0 ? 1u : 0u) << i;
-                }
-                const int s = ps;
+                const int atk = __shfl_sync(0xffffffffu, at, k * NB);
+                const int tile_blk = __shfl_sync(0xffffffffu, pb, k * NB + (lane & (NB - 1)));
+                const int meta_b = NB == 1 ? tile_blk : __shfl_sync(0xffffffffu, pb, k * NB + my_blk);
+                const int hgk = NB == 2 ? atk : atk & 0xffff, s0k = NB == 2 ? 0 : (atk >> 16) << kUnitShift;
+                const uint32_t there = (in >> (k * NB)) & ((1u << NB) - 1);
                 const uint32_t fb = bar_full + 8 * s;
                 if (lane == 0) {
-                    if (issued >= stages && !ptx::mbar_wait_bounded(bar_empty + 8 * s, pphase ^ 1u, kTimeoutNs)) {
+                    if (issued >= stages && !ptx::mbar_wait_bounded(bar_empty + 8 * s, phase ^ 1u, kTimeoutNs)) {
                         raise_err(p.err_flag, PKV_DEVERR_TIMEOUT);
                         aborted = true;
                     } else {
@@ -221,39 +209,21 @@ __global__ void __launch_bounds__(32 * (kHeadsU4<NG> + 1), (kCtasU4<NG>))
                         ptx::mbar_arrive_expect_tx(fb, uint32_t(__popc(there)) * block_tx);
                     }
                 }
-                aborted = __shfl_sync(0xffffffffu, aborted, 0);
+                aborted = __any_sync(0xffffffffu, aborted);
                 if (aborted) break;
-                if (++ps == stages) {
-                    ps = 0;
-                    pphase ^= 1u;
+                const uint32_t dst = sbase + s * L.stage;
+                if (lane < NB && tile_blk >= 0) {
+                    ptx::tma_load_4d_hint(dst + lane * part, &tmk, fb, 0, s0k, hgk * nh, tile_blk, once);
+                    ptx::tma_load_4d_hint(dst + L.tile + lane * part, &tmv, fb, 0, s0k, hgk * nh, tile_blk, once);
                 }
-                ++issued;
-                const uint32_t kdst = sbase + s * L.stage, md = kdst + 2 * L.tile;
-                if (lane < NB) {
-                    const int blk = NB == 2 && lane == 1 ? pbk[NB - 1] : pbk[0];
-                    if (blk >= 0) {
-                        ptx::tma_load_4d_hint(kdst + lane * part, &tmk, fb, 0, s0k, hgk * nh, blk, once);
-                        ptx::tma_load_4d_hint(kdst + L.tile + lane * part, &tmv, fb, 0, s0k, hgk * nh, blk, once);
-                    }
-                }
-                if (lane < n_meta) {
-                    const int a = lane & 3, i = lane >> 2;      // array; block or head
-                    const int blk = NB == 2 && i == 1 ? pbk[NB - 1] : pbk[0];
-                    if (blk >= 0) {
-                        const int h0 = f.meta_hmaj ? hgk * nh : 0;
-                        const int es = a < 2 ? 2 : 1;
-                        // entries of one copy, the first one's place in the block and in the stage
-                        const int cnt = by_head ? slots : slots * MH;
-                        const int64_t at = f.meta_hmaj ? int64_t(h0 + (by_head ? i : 0)) * p.block_size + s0k : int64_t(s0k) * MH;
-                        const char *src = a == 0   ? reinterpret_cast<const char *>(p.k_qs + int64_t(blk) * p.m_blk + at)
-                                          : a == 1 ? reinterpret_cast<const char *>(p.v_qs + int64_t(blk) * p.m_blk + at)
-                                          : a == 2 ? reinterpret_cast<const char *>(p.k_qz + int64_t(blk) * p.z_blk + at)
-                                                   : reinterpret_cast<const char *>(p.v_qz + int64_t(blk) * p.z_blk + at);
-                        const uint32_t to = md + (a < 2 ? 2 * a : 2 + a) * kUnit * MH + i * cnt * es;
-                        ptx::bulk_load(to, src, uint32_t(cnt * es), fb);
-                    }
-                }
+                if (copies && meta_b >= 0)
+                    ptx::bulk_load(dst + meta_to, meta_src + meta_b * meta_blk + (hgk * meta_hg + s0k * meta_slot), bytes, fb);
                 __syncwarp();
+                ++issued;
+                if (++s == stages) {
+                    s = 0;
+                    phase ^= 1u;
+                }
             }
         }
         // the copies in flight land before this warp retires
@@ -270,41 +240,43 @@ __global__ void __launch_bounds__(32 * (kHeadsU4<NG> + 1), (kCtasU4<NG>))
     // A lane (gid, tig) of the results holds heads 2 tig, 2 tig + 1 of rows gid, gid + 8.
     const int kvl = warp, gid = lane >> 2, tig = lane & 3;
     const int GW = min(8 * NG, G);
-    int64_t x = lo;
-    int hg = int(x / NU), b, j;
+    int hg = int(lo / NU), b, j;
     {
-        const int r = int(x - int64_t(hg) * NU);
+        const int r = int(lo - int64_t(hg) * NU);
         b = find_seq(prefix, B, r);
         j = r - prefix[b];
     }
     int64_t seg_start = lo;
-    const int ktok = row_token<D>(gid);             // token of this lane's score rows (and + 8, of each tile)
-    const int vtok[2] = {row_token<D>((2 * tig) & 7), row_token<D>((2 * tig + 1) & 7)};
-    // byte offsets of this lane's words within a tile's rows
-    const uint32_t koff = D == 128 ? ktok * ROW + (((tig ^ (ktok >> 1)) & 3) << 4) : ktok * ROW + 8 * tig;
-    uint32_t voff[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        voff[i] = D == 128 ? vtok[i] * ROW + ((((gid >> 1) ^ (vtok[i] >> 1)) & 3) << 4) + 8 * (gid & 1) : vtok[i] * ROW + 4 * gid;
-    // of the unit's tokens (sk, zk, sv, log2 sv), and zv as f16 by their rows in the products
-    float4 *conv = reinterpret_cast<float4 *>(smem + L.conv + warp * kConvBytes);
-    __half *conv_z = reinterpret_cast<__half *>(conv + kUnit);
+    // byte offsets within a tile's 16 rows: this lane's words of K row gid, and the 16-byte piece
+    // of a V row whose address it gives to a transposed load (matrices: tokens 0 - 7 and 8 - 15
+    // of one piece, then of the next)
+    const int vrow = lane & 15;
+    const uint32_t koff = D == 128 ? gid * ROW + (((tig ^ (gid >> 1)) & 3) << 4) : gid * ROW + ((((tig >> 1) ^ (gid >> 2)) & 1) << 4) + 8 * (tig & 1);
+    const uint32_t voff = D == 128 ? vrow * ROW + ((((lane >> 4) ^ (vrow >> 1)) & 3) << 4) : vrow * ROW + ((((lane >> 4) ^ (vrow >> 2)) & 1) << 4);
+    // what the products take of the unit's tokens: (sk in log2 units, zk, e, sv
+    // 2^-e) with e about log2 sv, 2^-e, and zv as f16
+    const uint32_t conv = sbase + L.conv + warp * kConvBytes, conv_e = conv + kUnit * 16, conv_z = conv_e + kUnit * 4;
+    // places of this lane's token's scales and zeros among the unit's
+    const int meta_k = (NB == 2 ? lane >> 4 : 0) * slots * MH +
+                       (f.meta_hmaj ? kvl * slots + (lane & (slots - 1)) : (lane & (slots - 1)) * MH + kvl);
 
     uint32_t qb[NG][QK][2];                         // q as the B operand
     float o[NG][OT][4];
     float m[NG][2], l[NG][2];                       // maximum and sum of p, of heads 2 tig, 2 tig + 1
-    float q1[NG][2], mult[NG][2];                   // sum of q 2^-20 as in qb; what makes q . u log2 units
+    float zs[NG][4];                                // sum of P zv, of lanes 0 - 3 (row 0)
+    float q1[NG][2];                                // sum of q 2^-22 as in qb
+    float mult = 0.0f;                              // what makes q . u log2 units
     int ctx_b = 0;
 
     auto start_segment = [&]() {
         ctx_b = ctxs[b];
+        // column gid of group g: q head 8 g + gid; this lane's elements are those of its words
+        // of K, 8 w .. 8 w + 7 from d0 on, in pairs (n, n + 4)
+        float v[NG][8 * WK], top = 0.0f;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            // column gid: q head 8 g + gid; this lane's elements are those of its words of K:
-            // words w of codes d0 + 8 w .. + 7, pairs (n, n + 4)
             const int head = 8 * g + gid;
             const uint16_t *qr = reinterpret_cast<const uint16_t *>(p.q + b * p.q_b + ((hg * nh + kvl) * G + head) * p.q_h) + 8 * WK * tig;
-            float v[8 * WK], top = 0.0f;
 #pragma unroll
             for (int c = 0; c < WK; ++c) {
                 uint4 u = make_uint4(0, 0, 0, 0);
@@ -315,43 +287,45 @@ __global__ void __launch_bounds__(32 * (kHeadsU4<NG> + 1), (kCtasU4<NG>))
                     float2 t;
                     if (p.q_is_bf16) t = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
                     else t = __half22float2(*reinterpret_cast<const __half2 *>(&w[e]));
-                    v[8 * c + 2 * e] = t.x;
-                    v[8 * c + 2 * e + 1] = t.y;
+                    v[g][8 * c + 2 * e] = t.x;
+                    v[g][8 * c + 2 * e + 1] = t.y;
                     top = fmaxf(top, fmaxf(fabsf(t.x), fabsf(t.y)));
                 }
             }
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // times the power of two that brings the row's largest element to 2^13 .. 2^14: what
-            // falls below f16's normal range then is off by at most 2^-38 of the largest
-            const int e = min(max(int(__float_as_uint(top) >> 23), 13), 253);
-            const float qs = __uint_as_float(uint32_t(267 - e) << 23);         // 2^(140 - e)
+        }
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+        // times the power of two that brings the group's largest element to 2^13 .. 2^14: an
+        // element is then off by at most 2^-34 of the largest
+        const int e = min(max(int(__float_as_uint(top) >> 23), 13), 253);
+        const float qs = __uint_as_float(uint32_t(267 - e) << 23);             // 2^(140 - e)
+        mult = p.scale_log2 * __uint_as_float(uint32_t(min(max(e + 9, 1), 254)) << 23);    // c 2^22 / qs
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
             float sum = 0.0f;
 #pragma unroll
             for (int k = 0; k < QK; ++k) {
                 const int n = 8 * (k >> 1) + 2 * (k & 1);
                 float a0, a1, b0, b1;
-                qb[g][k][0] = pack_f16(v[n] * qs, v[n + 4] * qs, a0, a1);
-                qb[g][k][1] = pack_f16(v[n + 1] * qs, v[n + 5] * qs, b0, b1);
-                sum += (a0 + a1) + (b0 + b1);
+                qb[g][k][0] = pack_f16(v[g][n] * qs, v[g][n + 4] * qs, a0, a1);
+                qb[g][k][1] = pack_f16(v[g][n + 1] * (0.0625f * qs), v[g][n + 5] * (0.0625f * qs), b0, b1);
+                sum += (a0 + a1) + 16.0f * (b0 + b1);
             }
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            // c 2^20 / qs
-            const float mu = p.scale_log2 * __uint_as_float(uint32_t(min(max(e - 120 + 127, 1), 254)) << 23);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                q1[g][c] = 0x1p-20f * __shfl_sync(0xffffffffu, sum, 4 * (2 * tig + c));
-                mult[g][c] = __shfl_sync(0xffffffffu, mu, 4 * (2 * tig + c));
+                q1[g][c] = 0x1p-22f * __shfl_sync(0xffffffffu, sum, 4 * (2 * tig + c));
                 m[g][c] = NEG_INF;
                 l[g][c] = 0.0f;
             }
 #pragma unroll
             for (int t = 0; t < OT; ++t) o[g][t][0] = o[g][t][1] = o[g][t][2] = o[g][t][3] = 0.0f;
+            zs[g][0] = zs[g][1] = zs[g][2] = zs[g][3] = 0.0f;
         }
     };
 
-    // lane gid holds elements d = (D / 8) gid + 2 t + r of the output (tile t, row half r)
+    // tile 2 i + h, row half r of lane gid: element 32 i + 4 gid + 2 h + r of the output
     auto finish_segment = [&](int64_t seg_end) {
         const int64_t first = int64_t(hg) * NU + prefix[b];
         const bool whole = seg_start == first && seg_end == int64_t(hg) * NU + prefix[b + 1] - 1;
@@ -363,58 +337,62 @@ __global__ void __launch_bounds__(32 * (kHeadsU4<NG> + 1), (kCtasU4<NG>))
                 float lt = l[g][c];
 #pragma unroll
                 for (int s = 4; s < 32; s <<= 1) lt += __shfl_xor_sync(0xffffffffu, lt, s);
+                const float zt = __shfl_sync(0xffffffffu, zs[g][c], tig);
                 const int head = 8 * g + 2 * tig + c;
                 if (head >= GW) continue;
                 const int local = kvl * G + head;
                 const float inv = whole ? (lt > 0.0f ? 1.0f / lt : 0.0f) : 1.0f;
-                float v[D / 8];
-#pragma unroll
-                for (int t = 0; t < OT; ++t) {
-                    v[2 * t] = o[g][t][c] * inv;
-                    v[2 * t + 1] = o[g][t][2 + c] * inv;
+                uint16_t *to = reinterpret_cast<uint16_t *>(p.out + b * p.o_b + int64_t(hg * nh * G + local) * p.o_h) + 4 * gid;
+                const int64_t row = key * (int64_t(nh) * G) + local;
+                if (!whole && gid == 0) {
+                    f.part_ml[2 * row] = m[g][c];
+                    f.part_ml[2 * row + 1] = lt;
                 }
-                if (whole) {
-                    uint16_t *to = reinterpret_cast<uint16_t *>(p.out + b * p.o_b + int64_t(hg * nh * G + local) * p.o_h) + D / 8 * gid;
-                    uint32_t w[D / 16];
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        float r0, r1;
-                        w[i] = p.q_is_bf16 ? pack_bf16(v[2 * i], v[2 * i + 1], r0, r1) : pack_f16(v[2 * i], v[2 * i + 1], r0, r1);
+                for (int i = 0; i < D / 32; ++i) {
+                    const float v[4] = {(o[g][2 * i][c] * 0x1p22f - zt) * inv, (o[g][2 * i][2 + c] * 0x1p18f - zt) * inv,
+                                        (o[g][2 * i + 1][c] * 0x1p22f - zt) * inv, (o[g][2 * i + 1][2 + c] * 0x1p18f - zt) * inv};
+                    if (!whole) {
+                        *reinterpret_cast<float4 *>(f.part_acc + row * D + 32 * i + 4 * gid) = make_float4(v[0], v[1], v[2], v[3]);
+                        continue;
                     }
+                    float r0, r1;
+                    const uint32_t w0 = p.q_is_bf16 ? pack_bf16(v[0], v[1], r0, r1) : pack_f16(v[0], v[1], r0, r1);
+                    const uint32_t w1 = p.q_is_bf16 ? pack_bf16(v[2], v[3], r0, r1) : pack_f16(v[2], v[3], r0, r1);
                     if (p.out_vec_ok) {
-#pragma unroll
-                        for (int i = 0; i < D / 16; i += 4) *reinterpret_cast<uint4 *>(to + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+                        *reinterpret_cast<uint2 *>(to + 32 * i) = make_uint2(w0, w1);
                     } else {
-#pragma unroll
-                        for (int i = 0; i < D / 8; ++i) to[i] = uint16_t(w[i >> 1] >> (16 * (i & 1)));
+                        to[32 * i] = uint16_t(w0);
+                        to[32 * i + 1] = uint16_t(w0 >> 16);
+                        to[32 * i + 2] = uint16_t(w1);
+                        to[32 * i + 3] = uint16_t(w1 >> 16);
                     }
-                } else {
-                    const int64_t row = key * (int64_t(nh) * G) + local;
-                    float *acc = f.part_acc + row * D + D / 8 * gid;
-                    if (gid == 0) {
-                        f.part_ml[2 * row] = m[g][c];
-                        f.part_ml[2 * row + 1] = lt;
-                    }
-#pragma unroll
-                    for (int i = 0; i < D / 8; i += 4) *reinterpret_cast<float4 *>(acc + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                 }
             }
     };
 
-    // one unit in stage s; bit i of `live`: token i counts
-    auto unit = [&](int s, uint32_t live) {
-        const bool all = live == 0xffffffffu;
+    // one unit in stage s; bit i of `live`: token i counts (all of them do where ALL)
+    auto unit = [&](auto all_c, int s, uint32_t live) {
+        constexpr bool ALL = decltype(all_c)::value;
         // ---- scales and zeros of a token by its lane, for all lanes
         {
-            const unsigned char *raw = smem + (s * L.stage + 2 * L.tile);
-            const int i = NB == 2 ? lane >> 4 : 0, slot = NB == 2 ? lane & 15 : lane;
-            const int k = i * slots * MH + (f.meta_hmaj ? kvl * slots + slot : slot * MH + hg * nh + kvl);
-            const __half *qs = reinterpret_cast<const __half *>(raw);
-            const unsigned char *qz = raw + 4 * kUnit * MH;
-            const float sv = __half2float(qs[kUnit * MH + k]);
+            const uint32_t raw = sbase + s * L.stage + 2 * L.tile + meta_k + (f.meta_hmaj ? 0 : hg * nh), sc = raw + meta_k + (f.meta_hmaj ? 0 : hg * nh);
+            uint32_t ks, vs, kz, vz;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=r"(ks) : "r"(sc));
+            asm volatile("ld.shared.u16 %0, [%1];" : "=r"(vs) : "r"(sc + 2 * kUnit * MH));
+            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(kz) : "r"(raw + 4 * kUnit * MH));
+            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(vz) : "r"(raw + 5 * kUnit * MH));
+            const float sv = __half2float(__ushort_as_half(uint16_t(vs)));
+            // e: the exponent of an fp16 number as fp32, within +-40 (zero: -40)
+            const int e = min(max(int((__float_as_uint(sv) >> 23) & 0xffu) - 126, -40), 40);
+            const float down = __uint_as_float(uint32_t(127 - e) << 23);
+            const bool on = ALL || ((live >> lane) & 1u);       // a scale behind the context may be anything
             __syncwarp();                           // the unit before is done with the place
-            conv[lane] = make_float4(__half2float(qs[k]), float(qz[k]), sv, scale_exp<40>((__float_as_uint(sv) >> 23) & 0xffu));
-            conv_z[(lane & 24) | token_row<D>(lane & 7)] = __float2half_rn(float(qz[kUnit * MH + k]));
+            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(conv + 16 * lane),
+                         "f"(mult * __half2float(__ushort_as_half(uint16_t(ks)))), "f"(float(kz)), "f"(float(e)), "f"(on ? sv * down : 0.0f)
+                         : "memory");
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(conv_e + 4 * lane), "f"(down) : "memory");
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(conv_z + 2 * lane), "h"(__half_as_ushort(__float2half_rn(float(vz)))) : "memory");
             __syncwarp();
         }
         // first row of tile t's rows 8 r .. 8 r + 7
@@ -441,10 +419,8 @@ __global__ void __launch_bounds__(32 * (kHeadsU4<NG> + 1), (kCtasU4<NG>))
             }
 #pragma unroll
             for (int k = 0; k < QK; ++k) {
-                const uint32_t xa = xw[k >> 1], ya = yw[k >> 1];
-                constexpr uint32_t kAt4 = 0x00f000f0u;
-                const uint32_t a[4] = {(k & 1 ? xa >> 4 : xa << 4) & kAt4, (k & 1 ? ya >> 4 : ya << 4) & kAt4,
-                                       (k & 1 ? xa >> 8 : xa) & kAt4, (k & 1 ? ya >> 8 : ya) & kAt4};
+                const uint32_t xa = k & 1 ? xw[k >> 1] >> 6 : xw[k >> 1] << 2, ya = k & 1 ? yw[k >> 1] >> 6 : yw[k >> 1] << 2;
+                const uint32_t a[4] = {xa & kAt2, ya & kAt2, xa & kAt6, ya & kAt6};
 #pragma unroll
                 for (int g = 0; g < NG; ++g) ptx::mma16816<false>((k & 1) ? odd[g] : sc[g][t], a, qb[g][k][0], qb[g][k][1]);
             }
@@ -454,15 +430,20 @@ __global__ void __launch_bounds__(32 * (kHeadsU4<NG> + 1), (kCtasU4<NG>))
                 for (int e = 0; e < 4; ++e) sc[g][t][e] += odd[g][e];
         }
         // ---- online softmax per head column, log2 units.  P = p sv is packed to f16,
-        // so the maximum is that of score + log2(sv), by sv's exponent: the largest P is
-        // about one and keeps its bits, whatever the scales (an fp16 scale's exponent
-        // lies within the bounds of scale_exp)
+        // so the maximum is that of score + e, e about log2(sv): the largest P is about
+        // one and keeps its bits, whatever the scales.  With x = 2^(score + e - max), P = x
+        // (sv 2^-e) and p = x 2^-e.
         uint32_t pb[NG][KT][2];
         float4 mt[KT][2];
+        float dn[KT][2];
 #pragma unroll
         for (int t = 0; t < KT; ++t)
 #pragma unroll
-            for (int r = 0; r < 2; ++r) mt[t][r] = conv[16 * t + 8 * r + ktok];
+            for (int r = 0; r < 2; ++r) {
+                const int row = 16 * t + 8 * r + gid;
+                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(mt[t][r].x), "=f"(mt[t][r].y), "=f"(mt[t][r].z), "=f"(mt[t][r].w) : "r"(conv + 16 * row));
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(dn[t][r]) : "r"(conv_e + 4 * row));
+            }
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             float mx[2] = {NEG_INF, NEG_INF};
@@ -470,19 +451,17 @@ __global__ void __launch_bounds__(32 * (kHeadsU4<NG> + 1), (kCtasU4<NG>))
             for (int t = 0; t < KT; ++t)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const bool ok = all || ((live >> (16 * t + 8 * r + ktok)) & 1u);
+                    const bool ok = ALL || ((live >> (16 * t + 8 * r + gid)) & 1u);
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        float v = fmaf(-mt[t][r].y, q1[g][c], sc[g][t][2 * r + c]) * (mt[t][r].x * mult[g][c]);
-                        if (!ok) v = NEG_INF;
-                        sc[g][t][2 * r + c] = v;
-                        mx[c] = fmaxf(mx[c], v + mt[t][r].w);
+                        const float v = fmaf(fmaf(-mt[t][r].y, q1[g][c], sc[g][t][2 * r + c]), mt[t][r].x, mt[t][r].z);
+                        sc[g][t][2 * r + c] = ok ? v : NEG_INF;
+                        mx[c] = fmaxf(mx[c], sc[g][t][2 * r + c]);
                     }
                 }
-            // a unit that raises no maximum skips the reductions and the rescale
-            float alpha[2] = {1.0f, 1.0f};
-            const bool raise = __any_sync(0xffffffffu, mx[0] > m[g][0] || mx[1] > m[g][1]);
-            if (raise) {
+            // a unit that passes no maximum by much skips the reductions and the rescale
+            if (__any_sync(0xffffffffu, mx[0] > m[g][0] + kRaise || mx[1] > m[g][1] + kRaise)) {
+                float alpha[2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], 4));
@@ -493,21 +472,6 @@ __global__ void __launch_bounds__(32 * (kHeadsU4<NG> + 1), (kCtasU4<NG>))
                     m[g][c] = mn;
                     l[g][c] *= alpha[c];
                 }
-            }
-#pragma unroll
-            for (int t = 0; t < KT; ++t)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float p0 = exp2_approx(sc[g][t][2 * r] - m[g][0]), p1 = exp2_approx(sc[g][t][2 * r + 1] - m[g][1]);
-                    l[g][0] += p0;
-                    l[g][1] += p1;
-                    // (a scale behind the context may be anything)
-                    const float sv = all || ((live >> (16 * t + 8 * r + ktok)) & 1u) ? mt[t][r].z : 0.0f;
-                    float q0, qq;
-                    const uint32_t w = pack_f16(p0 * sv, p1 * sv, q0, qq);
-                    pb[g][t][r] = ptx::movmatrix_trans(w);
-                }
-            if (raise && __any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
 #pragma unroll
                 for (int t = 0; t < OT; ++t) {
                     o[g][t][0] *= alpha[0];
@@ -515,59 +479,57 @@ __global__ void __launch_bounds__(32 * (kHeadsU4<NG> + 1), (kCtasU4<NG>))
                     o[g][t][2] *= alpha[0];
                     o[g][t][3] *= alpha[1];
                 }
+                zs[g][0] *= alpha[0];
+                zs[g][1] *= alpha[1];
             }
+#pragma unroll
+            for (int t = 0; t < KT; ++t)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float x0 = exp2_approx(sc[g][t][2 * r] - m[g][0]), x1 = exp2_approx(sc[g][t][2 * r + 1] - m[g][1]);
+                    l[g][0] = fmaf(x0, dn[t][r], l[g][0]);
+                    l[g][1] = fmaf(x1, dn[t][r], l[g][1]);
+                    float r0, r1;
+                    pb[g][t][r] = ptx::movmatrix_trans(pack_f16(x0 * mt[t][r].w, x1 * mt[t][r].w, r0, r1));
+                }
         }
-        // ---- O^T += V^T P^T: a lane takes codes (D / 8) gid .. of four tokens, tile
-        // 4 w + i holding codes 8 w + 2 i (row gid, at bit 0) and + 1 (row gid + 8, at bit 4)
+        // ---- O^T += V^T P^T: piece i of the rows holds elements 32 i ..; a lane gets those
+        // from 32 i + 4 gid on, of tokens 2 tig and 2 tig + 1 (and + 8), tile 2 i + h taking
+        // two of the four
 #pragma unroll
         for (int t = 0; t < KT; ++t) {
-            const uint32_t at = rows_at(t) + L.tile;
-            uint32_t v[4][WV];
-            // -1024 - zv and -64 - zv of rows 2 tig, 2 tig + 1 and of those + 8
-            __half2 nz0[2], nz4[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const __half2 z = *reinterpret_cast<const __half2 *>(conv_z + 16 * t + 8 * i + 2 * tig);
-                nz0[i] = __hsub2(__float2half2_rn(-1024.0f), z);
-                nz4[i] = __hsub2(__float2half2_rn(-64.0f), z);
-            }
-            auto at0 = [](uint32_t x, __half2 nz) -> uint32_t {
-                const uint32_t u = (x & 0x000f000fu) | 0x64006400u;
-                const __half2 y = __hadd2(*reinterpret_cast<const __half2 *>(&u), nz);
-                return *reinterpret_cast<const uint32_t *>(&y);
-            };
-            auto at4 = [](uint32_t x, __half2 nz) -> uint32_t {
-                const uint32_t u = (x & 0x00f000f0u) | 0x64006400u;
-                const __half2 y = __hfma2(*reinterpret_cast<const __half2 *>(&u), __float2half2_rn(0.0625f), nz);
-                return *reinterpret_cast<const uint32_t *>(&y);
-            };
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t a = at + voff[i & 1] + (i >> 1) * 8 * ROW;
-                if constexpr (D == 128) asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[i][0]), "=r"(v[i][1]) : "r"(a));
-                else v[i][0] = ld_shared_u32(a);
-            }
-#pragma unroll
-            for (int w = 0; w < WV; ++w)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t x01 = ptx::prmt(v[0][w], v[1][w], h ? 0x7632u : 0x5410u);
-                    const uint32_t x23 = ptx::prmt(v[2][w], v[3][w], h ? 0x7632u : 0x5410u);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t xa = x01 >> (8 * i), ya = x23 >> (8 * i);
-                        const uint32_t a[4] = {at0(xa, nz0[0]), at4(xa, nz4[0]), at0(ya, nz0[1]), at4(ya, nz4[1])};
-#pragma unroll
-                        for (int g = 0; g < NG; ++g) ptx::mma16816<false>(o[g][4 * w + 2 * h + i], a, pb[g][t][0], pb[g][t][1]);
-                    }
+            const uint32_t at = rows_at(t) + L.tile + voff;
+            {                                       // zv as row 0 of another tile
+                uint32_t z[4] = {0, 0, 0, 0};
+                if (gid == 0) {
+                    z[0] = ld_shared_u32(conv_z + 2 * (16 * t + 2 * tig));
+                    z[2] = ld_shared_u32(conv_z + 2 * (16 * t + 8 + 2 * tig));
                 }
+#pragma unroll
+                for (int g = 0; g < NG; ++g) ptx::mma16816<false>(zs[g], z, pb[g][t][0], pb[g][t][1]);
+            }
+#pragma unroll
+            for (int i2 = 0; i2 < D / 64; ++i2) {
+                uint32_t v[4];
+                ptx::ldmatrix_x4_trans(at ^ (32 * i2), v[0], v[1], v[2], v[3]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t xa = h ? v[2 * i] >> 6 : v[2 * i] << 2, ya = h ? v[2 * i + 1] >> 6 : v[2 * i + 1] << 2;
+                        const uint32_t a[4] = {xa & kAt2, xa & kAt6, ya & kAt2, ya & kAt6};
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) ptx::mma16816<false>(o[g][4 * i2 + 2 * i + h], a, pb[g][t][0], pb[g][t][1]);
+                    }
+            }
         }
     };
 
     start_segment();
     int cs = 0;
     uint32_t cphase = 0;
-    for (; x < hi; ++x) {
+    int valid = ctx_b - j * kUnit;                  // tokens from this unit on, at least 1
+    for (int left = int(hi - lo); left > 0; --left, valid -= kUnit) {
         const int s = cs;
         if (!ptx::mbar_wait_bounded(bar_full + 8 * s, cphase, kTimeoutNs)) {
             raise_err(p.err_flag, PKV_DEVERR_TIMEOUT);
@@ -577,31 +539,27 @@ __global__ void __launch_bounds__(32 * (kHeadsU4<NG> + 1), (kCtasU4<NG>))
             cs = 0;
             cphase ^= 1u;
         }
-        const int valid = ctx_b - j * kUnit;        // at least 1
         uint32_t live = valid >= kUnit ? 0xffffffffu : (1u << valid) - 1u;
         const uint32_t there = stage_mask[s];
         if (NB == 2) live &= ((there & 1u) ? 0xffffu : 0u) | ((there & 2u) ? 0xffff0000u : 0u);
         else if (there == 0) live = 0;
-        if (live != 0) unit(s, live);
+        if (live == 0xffffffffu) unit(std::true_type{}, s, live);
+        else if (live != 0) unit(std::false_type{}, s, live);
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar_empty + 8 * s);
-        if (x + 1 < hi) {
-            ++j;
-            if (prefix[b] + j == prefix[b + 1]) {   // the sequence's last unit
-                finish_segment(x);
-                j = 0;
-                do {
-                    if (++b == B) {
-                        b = 0;
-                        ++hg;
-                    }
-                } while (prefix[b] == prefix[b + 1]);
-                seg_start = x + 1;
-                start_segment();
+        if (valid > kUnit && left > 1) continue;    // the sequence goes on here
+        const int64_t x = hi - left;
+        finish_segment(x);
+        if (left == 1) break;
+        do {
+            if (++b == B) {
+                b = 0;
+                ++hg;
             }
-        } else {
-            finish_segment(x);
-        }
+        } while (prefix[b] == prefix[b + 1]);
+        seg_start = x + 1;
+        start_segment();
+        valid = ctx_b + kUnit;                      // (less a unit by the loop)
     }
 }
 
@@ -631,7 +589,7 @@ bool u4_map(CUtensorMap *m, const char *base, const DecodeParams &p, int nh)
     const cuuint32_t box[4] = {row, cuuint32_t(p.block_size < kUnit ? p.block_size : kUnit), cuuint32_t(nh), 1};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<char *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -669,6 +627,7 @@ bool plan_decode_u4(const DecodeParams &p, bool meta_head_major, int sm_count, F
 {
     if (p.block_size < 16 || p.batch < 1 || p.batch > 4096 || p.group < 1) return false;
     if (int64_t(p.max_blocks) * p.block_size > (int64_t(1) << 31) - 64) return false;      // token numbers in 32 bits
+    if (p.num_kv_heads >= 1 << 15) return false;                                            // head groups in 15
     const int row = p.head_dim / 2, ng = p.group > 8 ? 2 : 1;
     const int most = ng == 1 ? kHeadsU4<1> : kHeadsU4<2>, per_sm = ng == 1 ? kCtasU4<1> : kCtasU4<2>;
     int nh = most;

@@ -57,16 +57,16 @@ def make_cache(pkv, P, BS, H, D, seed=0, hmaj=True, device="cuda", dual=False, a
 
 def prefill_parts(q, vals, tops, bt, starts, ctx, sm_scale):
     """The definition in float64 and what its tolerance is made of: R.prefill's
-    (out, mean |v|, error of a score, keys), the third being (D + 8) roundings of a
-    step of 2^-23 (a tensor core's sums may cut instead of round) of the largest sum
-    |q| (u + z) s, and, of kernels that take codes as f16 subnormals of 2^-20, whose
-    products are aligned as if they were 2^-14: a step of 2^-23 of |q|'s largest element,
-    brought to at least 2^13, over 2^13 2^-20 for each of D / 16 + 1 sums of 16, that is
-    2^-16 of it times s."""
+    (out, mean |v|, error of a score, keys, mean (u + z) s of v).  The third is (D + 8)
+    roundings of a step of 2^-23 (a tensor core's sums may cut instead of round) of the
+    largest sum |q| (u + z) s, and, of kernels that take codes as f16 subnormals of
+    2^-22, whose products are aligned as if they were 2^-14: a step of 2^-23 of |q|'s
+    largest element, brought to at least 2^13, over 2^13 2^-22 for each of D / 16 + 1 sums
+    of 16, that is 2^-14 of it times s."""
     out, mean, _, keys = R.prefill(q, vals[0], vals[1], bt, starts, ctx, sm_scale)
     T, Hq, D = q.shape
     H = vals[0].shape[2]
-    top = torch.zeros((T, Hq), dtype=torch.float64)
+    top, wide = torch.zeros((T, Hq), dtype=torch.float64), torch.zeros_like(out)
     BS = vals[0].shape[1]
     for b in range(len(ctx)):
         s0, s1, c = int(starts[b]), int(starts[b + 1]), int(ctx[b])
@@ -75,14 +75,16 @@ def prefill_parts(q, vals, tops, bt, starts, ctx, sm_scale):
         n = s1 - s0
         pos = torch.arange(c)
         ids = bt[b].long()[pos // BS]
-        kt = tops[0][ids, pos % BS]
+        k, kt, vt = vals[0][ids, pos % BS], tops[0][ids, pos % BS], tops[1][ids, pos % BS]
         qb = q[s0:s1].double().view(n, H, Hq // H, D)
         seen = pos[None, :] <= (c - n + torch.arange(n))[:, None]
+        s = (torch.einsum("nhgd,chd->hgnc", qb, k) * sm_scale).masked_fill(~seen, -math.inf)
+        wide[s0:s1] = torch.einsum("hgnc,chd->nhgd", torch.nan_to_num(torch.softmax(s, -1)), vt).reshape(n, Hq, D)
         a = torch.einsum("nhgd,chd->hgnc", qb.abs(), kt) * abs(sm_scale)
         top[s0:s1] = (a * seen).amax(-1).permute(2, 0, 1).reshape(n, Hq)
     # a row of codes up to 15 has s = its largest (u + z) s over 15 at most
     cut = q.double().abs().amax(-1) * abs(sm_scale) * float(tops[0].max()) / 15
-    return out, mean, (D + 8) * 2.0 ** -23 * top + (D / 16 + 1) * 2.0 ** -16 * cut, keys
+    return out, mean, (D + 8) * 2.0 ** -23 * top + (D / 16 + 1) * 2.0 ** -14 * cut, keys, wide
 
 
 def tolerance(parts, vmax, dtype, D):
@@ -92,14 +94,17 @@ def tolerance(parts, vmax, dtype, D):
       - the weights' rounding, half an f16 step each (2^-11 of the mean |v|);
       - the weights' error from the scores', in the weight and in the maximum, and exp2
         to 2^-21;
-      - the sums over the keys of P (u - z), a step of 2^-23 a key of the mean |v|;
+      - the sums over the keys of P u and P z, a step of 2^-23 a key of the mean (u + z) s,
+        and, of codes taken as subnormals of 2^-22, a step of 2^-23 2^-14 over 2^-22, that is
+        2^-15, of s = vmax / 15 and of the weights' largest of each 16 keys, together at most
+        the weights' sum;
       - products P below f16's normal range, off by 2^-25 each where the largest is at
-        least 2^-2: with |u - z| up to 15, and 15 s = vmax at most, 2^-23 vmax a key."""
-    out, mean, score, keys = parts
+        least 2^-2: with u up to 15, and 15 s = vmax at most, 2^-23 vmax a key."""
+    out, mean, score, keys, wide = parts
     h = R.half_step(dtype)
     keys = keys[:, None, None]
-    tol = h * out.abs() * (1 + h) + mean * (2.0 ** -11 * (1 + h) + 2.0 ** -21 + 2 * score[..., None] + (keys + 8) * 2.0 ** -23)
-    tol = tol + keys * 2.0 ** -23 * vmax
+    tol = h * out.abs() * (1 + h) + mean * (2.0 ** -11 * (1 + h) + 2.0 ** -21 + 2 * score[..., None])
+    tol = tol + wide * (keys + 8) * 2.0 ** -23 + (2.0 ** -15 / 15 + keys * 2.0 ** -23) * vmax
     if dtype == torch.float16:
         tol = tol + 2.0 ** -25
     return tol + 1e-30
@@ -112,7 +117,7 @@ def decode_parts(q, vals, tops, bt, ctx, sm_scale):
     parts = prefill_parts(q, vals, tops, bt, starts, [max(c, 1) for c in ctx], sm_scale)
     for b, c in enumerate(ctx):
         if c == 0:
-            for t in parts[:4]:
+            for t in parts:
                 t[b] = 0
     return parts
 
