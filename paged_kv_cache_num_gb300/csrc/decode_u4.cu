@@ -403,11 +403,10 @@ __global__ void __launch_bounds__(32 * (kHeadsU4<NG> + 1), (kCtasU4<NG>))
         float sc[NG][KT][4];
 #pragma unroll
         for (int t = 0; t < KT; ++t) {
-            float odd[NG][4];                       // a second chain
 #pragma unroll
             for (int g = 0; g < NG; ++g)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sc[g][t][e] = odd[g][e] = 0.0f;
+                for (int e = 0; e < 4; ++e) sc[g][t][e] = 0.0f;
             const uint32_t at = rows_at(t) + koff;
             uint32_t xw[WK], yw[WK];
             if constexpr (D == 128) {
@@ -422,12 +421,8 @@ __global__ void __launch_bounds__(32 * (kHeadsU4<NG> + 1), (kCtasU4<NG>))
                 const uint32_t xa = k & 1 ? xw[k >> 1] >> 6 : xw[k >> 1] << 2, ya = k & 1 ? yw[k >> 1] >> 6 : yw[k >> 1] << 2;
                 const uint32_t a[4] = {xa & kAt2, ya & kAt2, xa & kAt6, ya & kAt6};
 #pragma unroll
-                for (int g = 0; g < NG; ++g) ptx::mma16816<false>((k & 1) ? odd[g] : sc[g][t], a, qb[g][k][0], qb[g][k][1]);
+                for (int g = 0; g < NG; ++g) ptx::mma16816<false>(sc[g][t], a, qb[g][k][0], qb[g][k][1]);
             }
-#pragma unroll
-            for (int g = 0; g < NG; ++g)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sc[g][t][e] += odd[g][e];
         }
         // ---- online softmax per head column, log2 units.  P = p sv is packed to f16,
         // so the maximum is that of score + e, e about log2(sv): the largest P is about
