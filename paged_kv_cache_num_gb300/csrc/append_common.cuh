@@ -147,44 +147,62 @@ __device__ __forceinline__ uint32_t max2_16(uint32_t a, uint32_t b)
     return r;
 }
 
-// A 4-bit row by LPR neighbouring lanes, each with 8 of its elements (e, pairs
-// in order): this lane's word of codes, and the row's scale and zero.  Every
+// A 4-bit row by LPR neighbouring lanes, each with 8 W of its elements (e, pairs
+// in order): this lane's W words of codes, and the row's scale and zero.  Every
 // lane of the warp calls it.
+//   lo = min(0, min), hi = max(0, max), s = fp16((hi - lo) / 15), z = clamp(rint(-lo / s), 0, 15),
+//   code = clamp(rint(x / s) + z, 0, 15)
+// The quotient by 15 is the division's, by Markstein's refinement (row_quotient;
+// below 2^-100, where its residual underflows, s is 0 in any case).  A quotient is
+// cut to -z .. 15 - z before it is rounded, by adding 1.5 2^23: the sum's bits are a
+// constant plus the integer, and a word is the sum of 16^i times them.
+template <int W>
 struct RowU4 {
-    uint32_t codes;
+    uint32_t codes[W];
     uint16_t scale;
     uint32_t zero;
 };
-template <int SRC, int LPR>
-__device__ __forceinline__ RowU4 row_u4(const uint32_t (&e)[4])
+template <int SRC, int LPR, int W>
+__device__ __forceinline__ RowU4<W> row_u4(const uint32_t (&e)[4 * W])
 {
-    uint32_t mn = min2_16<SRC>(min2_16<SRC>(e[0], e[1]), min2_16<SRC>(e[2], e[3]));
-    uint32_t mx = max2_16<SRC>(max2_16<SRC>(e[0], e[1]), max2_16<SRC>(e[2], e[3]));
+    uint32_t mn = e[0], mx = e[0];
+#pragma unroll
+    for (int j = 1; j < 4 * W; ++j) {
+        mn = min2_16<SRC>(mn, e[j]);
+        mx = max2_16<SRC>(mx, e[j]);
+    }
     mn = min2_16<SRC>(mn, __byte_perm(mn, 0u, 0x1032));         // both halves
     mx = max2_16<SRC>(mx, __byte_perm(mx, 0u, 0x1032));
     uint32_t both = min2_16<SRC>(__byte_perm(mn, mx ^ 0x80008000u, 0x5410), 0u);    // (min, -max), zero among them
 #pragma unroll
     for (int o = 1; o < LPR; o <<= 1) both = min2_16<SRC>(both, __shfl_xor_sync(0xffffffffu, both, o));
     const float lo = h2f<SRC>(uint16_t(both)), hi = -h2f<SRC>(uint16_t(both >> 16));
-    uint16_t sbits = __half_as_ushort(__float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f)));
+    const float range = fminf(__fsub_rn(hi, lo), 3.0e38f);      // (bf16 rows may overflow: s is 65504 then)
+    uint16_t sbits = __half_as_ushort(__float2half_rn(row_quotient(range, 15.0f, 1.0f / 15.0f)));
     if ((sbits & 0x7fff) == 0x7c00) sbits = 0x7bff;             // the largest finite fp16
     const float s = __half2float(__ushort_as_half(sbits));
     // s = 0: all quotients, z and the codes become 0
     const float rs = s != 0.0f ? __frcp_rn(s) : 0.0f;
-    const float z = fminf(fmaxf(rintf(row_quotient(-lo, s, rs)), 0.0f), 15.0f);
-    float f[2];                                                 // four codes each, as a number below 2^16
+    constexpr float kMagic = 12582912.0f;
+    const float z = __fsub_rn(__fadd_rn(fminf(fmaxf(row_quotient(-lo, s, rs), 0.0f), 15.0f), kMagic), kMagic);
+    const uint32_t zi = uint32_t(z);
+    const float least = -z, most = 15.0f - z;
+    RowU4<W> r;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        f[j] = 0.0f;
+    for (int w = 0; w < W; ++w) {
+        uint32_t sum = 0;
 #pragma unroll
-        for (int i = 3; i >= 0; --i) {
-            const uint32_t w = e[2 * j + (i >> 1)];
-            const float x = h2f<SRC>(uint16_t(i & 1 ? w >> 16 : w));
-            const float q = fminf(fmaxf(__fadd_rn(rintf(row_quotient(x, s, rs)), z), 0.0f), 15.0f);
-            f[j] = fmaf(f[j], 16.0f, q);
+        for (int i = 7; i >= 0; --i) {
+            const uint32_t p = e[4 * w + (i >> 1)];
+            const float x = h2f<SRC>(uint16_t(i & 1 ? p >> 16 : p));
+            const float q = fminf(fmaxf(row_quotient(x, s, rs), least), most);
+            sum = sum * 16u + __float_as_uint(__fadd_rn(q, kMagic));
         }
+        r.codes[w] = sum + (zi - 0x4b400000u) * 0x11111111u;
     }
-    return {uint32_t(f[0]) | (uint32_t(f[1]) << 16), sbits, uint32_t(z)};
+    r.scale = sbits;
+    r.zero = zi;
+    return r;
 }
 
 inline int grid_for(int64_t work, int threads)

@@ -5,11 +5,11 @@
 // The range takes zero in, so z is never cut off and a row of equal numbers
 // keeps its value.
 //
-// A lane takes 8 elements (16 source bytes -> one word of codes), so a row is
-// 16 lanes at head_dim 128 and 8 at 64; one warp takes parts of a (token, K|V)
-// row, its lanes over the (kv head, 8 elements) pieces, as the one-byte
-// appends do.  The extremes of a row go through its lanes as one word, (min,
-// -max) in 16 bits each: exact, the elements being 16-bit numbers.  Bound by HBM.
+// A lane takes 16 elements (32 source bytes -> two words of codes), so a row is 8
+// lanes at head_dim 128 and 4 at 64; one warp takes parts of a (token, K|V) row,
+// its lanes over the (kv head, 16 elements) pieces, as the one-byte appends do.
+// The extremes of a row go through its lanes as one word, (min, -max) in 16 bits
+// each: exact, the elements being 16-bit numbers.
 #include <type_traits>
 
 #include "append_common.cuh"
@@ -24,7 +24,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_u4_kernel(AppendParams 
 {
     griddep_wait();
     griddep_launch_dependents();
-    constexpr int LPR = D / 8;                      // lanes of a row
+    constexpr int LPR = D / 16;                     // lanes of a row
     const int lane = threadIdx.x & 31;
     const int per = p.num_kv_heads * LPR;           // pieces per (token, K|V)
     const int parts = (per + 32 * U - 1) / (32 * U);
@@ -41,27 +41,29 @@ __global__ void __launch_bounds__(kAppendThreads) append_u4_kernel(AppendParams 
         uint16_t *qs = (kv ? p.v_qs : p.k_qs) + blk * p.m_blk + off * p.m_slot;
         uint8_t *qz = (kv ? p.v_qz : p.k_qz) + blk * p.z_blk + off * p.z_slot;
         const int i0 = w.minor * 32 * U + lane;
-        uint32_t e[U][4];
+        uint32_t e[U][8];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int i = i0 + 32 * u, h = i / LPR, c = i % LPR;
-            e[u][0] = e[u][1] = e[u][2] = e[u][3] = 0u;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) e[u][j] = 0u;
             if (i >= per) continue;
-            const uint16_t *src = reinterpret_cast<const uint16_t *>(src_row + h * src_head) + 8 * c;
+            const uint16_t *src = reinterpret_cast<const uint16_t *>(src_row + h * src_head) + 16 * c;
             if constexpr (VEC) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src));
-                e[u][0] = v.x; e[u][1] = v.y; e[u][2] = v.z; e[u][3] = v.w;
+                const uint4 a = __ldg(reinterpret_cast<const uint4 *>(src)), b = __ldg(reinterpret_cast<const uint4 *>(src) + 1);
+                e[u][0] = a.x; e[u][1] = a.y; e[u][2] = a.z; e[u][3] = a.w;
+                e[u][4] = b.x; e[u][5] = b.y; e[u][6] = b.z; e[u][7] = b.w;
             } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) e[u][j] = uint32_t(src[2 * j]) | (uint32_t(src[2 * j + 1]) << 16);
+                for (int j = 0; j < 8; ++j) e[u][j] = uint32_t(src[2 * j]) | (uint32_t(src[2 * j + 1]) << 16);
             }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int i = i0 + 32 * u, h = i / LPR, c = i % LPR;
-            const RowU4 r = row_u4<SRC, LPR>(e[u]);
+            const RowU4<2> r = row_u4<SRC, LPR, 2>(e[u]);
             if (i >= per) continue;
-            *(reinterpret_cast<uint32_t *>(dst_row + h * p.c_head) + c) = r.codes;
+            *(reinterpret_cast<uint2 *>(dst_row + h * p.c_head) + c) = make_uint2(r.codes[0], r.codes[1]);
             if (c == 0) {
                 qs[h * p.m_head] = r.scale;
                 qz[h * p.z_head] = uint8_t(r.zero);
@@ -74,21 +76,21 @@ __global__ void __launch_bounds__(kAppendThreads) append_u4_kernel(AppendParams 
 
 cudaError_t launch_append_u4(const AppendParams &p, bool vec16, cudaStream_t s)
 {
-    const int per = p.num_kv_heads * (p.head_dim / 8);
+    const int per = p.num_kv_heads * (p.head_dim / 16);
     if (p.num_tokens == 0 || per == 0) return cudaSuccess;
-    // four pieces per lane where a (token, K|V) row has them and every SM still gets
+    // two pieces per lane where a (token, K|V) row has them and every SM still gets
     // several warps, else one (more, shorter warps)
     auto warps = [&](int U) { return p.num_tokens * 2 * ((per + 32 * U - 1) / (32 * U)); };
-    const bool one = per <= 32 || warps(4) < int64_t(sm_count_current_device()) * 8;
-    const int g = grid_for(warps(one ? 1 : 4) * 32, kAppendThreads);
+    const bool one = per <= 32 || warps(2) < int64_t(sm_count_current_device()) * 8;
+    const int g = grid_for(warps(one ? 1 : 2) * 32, kAppendThreads);
     auto go = [&](auto src_c, auto vec_c) -> cudaError_t {
         constexpr int S = decltype(src_c)::value;
         constexpr bool V = decltype(vec_c)::value;
         if (p.head_dim == 128)
             return one ? launch_pdl(append_u4_kernel<S, V, 128, 1>, g, kAppendThreads, 0, s, p)
-                       : launch_pdl(append_u4_kernel<S, V, 128, 4>, g, kAppendThreads, 0, s, p);
+                       : launch_pdl(append_u4_kernel<S, V, 128, 2>, g, kAppendThreads, 0, s, p);
         return one ? launch_pdl(append_u4_kernel<S, V, 64, 1>, g, kAppendThreads, 0, s, p)
-                   : launch_pdl(append_u4_kernel<S, V, 64, 4>, g, kAppendThreads, 0, s, p);
+                   : launch_pdl(append_u4_kernel<S, V, 64, 2>, g, kAppendThreads, 0, s, p);
     };
     using BF = std::integral_constant<int, kBF16>;
     using HF = std::integral_constant<int, kF16>;

@@ -8,9 +8,9 @@
 // with j = i + rot / 2, or (interleaved) the pair 2i, 2i + 1; elements from rot
 // on stay.  cos and sin are the row of a table that the token's position names.
 //
-// One warp takes a part of a token's query, key or value rows, 8 elements (16
-// bytes) a lane, U row groups at a time, all loads before the arithmetic: the
-// table's row and the weights are loaded once for them.  A row is 16 or 8
+// One warp takes a token, or a part of its query, key or value rows, 8 elements (16
+// bytes) a lane, U row groups at a time, their loads before the arithmetic: the
+// products of the weights and the table's row are made once for all of them.  A row is 16 or 8
 // neighbouring lanes: its sum of squares is log2 of that in shuffles, the other
 // half of a rotated pair four more (of the 16-bit source, normed again here).
 // Bound by HBM, or for a decode step's few tokens by the launch.
@@ -23,7 +23,7 @@ namespace {
 
 // 3-bit row of LPR lanes with 8 elements each: this lane's 24 bits of codes
 template <int SRC, int LPR>
-__device__ __forceinline__ RowU4 row_u3(const uint32_t (&e)[4])
+__device__ __forceinline__ RowU4<1> row_u3(const uint32_t (&e)[4])
 {
     uint32_t mn = min2_16<SRC>(min2_16<SRC>(e[0], e[1]), min2_16<SRC>(e[2], e[3]));
     uint32_t mx = max2_16<SRC>(max2_16<SRC>(e[0], e[1]), max2_16<SRC>(e[2], e[3]));
@@ -45,7 +45,7 @@ __device__ __forceinline__ RowU4 row_u3(const uint32_t (&e)[4])
         const float x = h2f<SRC>(uint16_t(i & 1 ? e[i >> 1] >> 16 : e[i >> 1]));
         f = fmaf(f, 8.0f, fminf(fmaxf(__fadd_rn(rintf(row_quotient(x, s, rs)), z), 0.0f), 7.0f));
     }
-    return {uint32_t(f), sbits, uint32_t(z)};
+    return {{uint32_t(f)}, sbits, uint32_t(z)};
 }
 
 // the scale that kv_append_dynamic computes for a row of LPR lanes
@@ -65,14 +65,22 @@ __device__ __forceinline__ float dynamic_scale(const uint32_t (&e)[4])
     return fmaxf(__fdiv_rn(h2f<SRC>(uint16_t(top)), qmax), 1.17549435e-38f);
 }
 
-// 8 elements (pairs in order) of piece c of head h's row, to the token's place in the cache.
-// Every lane calls it; `on` lanes store.
-template <int SRC, int CK, int LPR>
-__device__ __forceinline__ void store_piece(const AppendParams &p, bool v, int64_t blk, int64_t off, int h, int c, bool on, const uint32_t (&e)[4])
+// where a lane's 8 elements lie in a cached row (piece c of head_dim / 8)
+template <int CK>
+__device__ __forceinline__ int64_t piece_offset(const AppendParams &p, int c)
 {
-    char *row = (v ? p.v_cache : p.k_cache) + blk * p.c_blk + off * p.c_slot + h * p.c_head;
+    if constexpr (CK == kF16 || CK == kBF16) return c * p.c_chunk;
+    else if constexpr (is_q8(CK)) return (c >> 1) * p.c_chunk + 8 * (c & 1);
+    else return CK == kU4 ? 4 * c : 3 * c;
+}
+
+// 8 elements (pairs in order) of piece c of head h's row, to their place `to` in the cache, the
+// token's being (blk, off).  Every lane calls it; `on` lanes store.
+template <int SRC, int CK, int LPR>
+__device__ __forceinline__ void store_piece(const AppendParams &p, char *to, bool v, int64_t blk, int64_t off, int h, int c, bool on, const uint32_t (&e)[4])
+{
     if constexpr (CK == kF16 || CK == kBF16) {
-        if (on) *reinterpret_cast<uint4 *>(row + c * p.c_chunk) = make_uint4(e[0], e[1], e[2], e[3]);
+        if (on) *reinterpret_cast<uint4 *>(to) = make_uint4(e[0], e[1], e[2], e[3]);
     } else if constexpr (is_q8(CK)) {
         float scale = 1.0f;
         if (p.scale_mode == 2) {
@@ -90,17 +98,17 @@ __device__ __forceinline__ void store_piece(const AppendParams &p, bool v, int64
             const uint32_t two = q8x2_encode<CK>(x);
             w[j >> 1] = j & 1 ? w[j >> 1] | (two << 16) : two;
         }
-        if (on) *reinterpret_cast<uint2 *>(row + (c >> 1) * p.c_chunk + 8 * (c & 1)) = make_uint2(w[0], w[1]);
+        if (on) *reinterpret_cast<uint2 *>(to) = make_uint2(w[0], w[1]);
     } else {
-        RowU4 r;
-        if constexpr (CK == kU4) r = row_u4<SRC, LPR>(e);
+        RowU4<1> r;
+        if constexpr (CK == kU4) r = row_u4<SRC, LPR, 1>(e);
         else r = row_u3<SRC, LPR>(e);
         if (!on) return;
         if constexpr (CK == kU4) {
-            *(reinterpret_cast<uint32_t *>(row) + c) = r.codes;
+            *reinterpret_cast<uint32_t *>(to) = r.codes[0];
         } else {
 #pragma unroll
-            for (int j = 0; j < 3; ++j) row[3 * c + j] = char(r.codes >> (8 * j));
+            for (int j = 0; j < 3; ++j) to[j] = char(r.codes[0] >> (8 * j));
         }
         if (c == 0) {
             (v ? p.v_qs : p.k_qs)[blk * p.m_blk + off * p.m_slot + h * p.m_head] = r.scale;
@@ -115,6 +123,14 @@ __device__ __forceinline__ void load_weights(const NormRopeParams &p, const void
     if (p.weight_kind == PKV_DTYPE_F32) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] = __ldg(static_cast<const float *>(w) + d + i);
+    } else if (p.weight_vec) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(w) + d));
+        const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint16_t v = uint16_t(x[i >> 1] >> (16 * (i & 1)));
+            o[i] = p.weight_kind == kBF16 ? h2f<kBF16>(v) : h2f<kF16>(v);
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -126,7 +142,7 @@ __device__ __forceinline__ void load_weights(const NormRopeParams &p, const void
 
 // CK: the cache's kind; 0: keys to k_out, and no values
 template <int SRC, int CK, int D, int U>
-__global__ void __launch_bounds__(kAppendThreads) norm_rope_kernel(NormRopeParams p)
+__global__ void __launch_bounds__(kAppendThreads, 3) norm_rope_kernel(NormRopeParams p)
 {
     griddep_wait();
     griddep_launch_dependents();
@@ -142,119 +158,158 @@ __global__ void __launch_bounds__(kAppendThreads) norm_rope_kernel(NormRopeParam
     const int other = p.interleaved || !turned ? lane : 8 * sub < half ? lane + half / 8 : lane - half / 8;
     const float sign = 8 * sub < half ? -1.0f : 1.0f;
     const int64_t wstep = (int64_t(gridDim.x) * blockDim.x) >> 5;
-    for (Walk2 w((blockIdx.x * int64_t(blockDim.x) + threadIdx.x) >> 5, wstep, parts_q + (CK ? 2 : 1) * parts_k);
-         w.major < p.a.num_tokens; w.next()) {
-        const int64_t t = w.major;
-        const int32_t pos = p.pos[t * p.pos_stride];
+    // an item is a token, or, of few tokens, a part of one
+    const int parts = parts_q + (CK ? 2 : 1) * parts_k;
+    Walk2 w((blockIdx.x * int64_t(blockDim.x) + threadIdx.x) >> 5, wstep, p.whole ? 1 : parts);
+    // the position and slot of an item are loaded while the one before is worked on
+    int32_t pos_next = -1;
+    int64_t slot_next = -1;
+    auto fetch = [&]() {
+        if (w.major >= p.a.num_tokens) return;
+        pos_next = p.pos[w.major * p.pos_stride];
+        if (CK && (p.whole || w.minor >= parts_q)) slot_next = p.a.slot_mapping[w.major * p.a.slot_stride];
+    };
+    fetch();
+    while (w.major < p.a.num_tokens) {
+        const int64_t t = w.major, slot = slot_next;
+        const int minor = w.minor;
+        const int32_t pos = pos_next;
+        w.next();
+        fetch();
         if (pos < 0) continue;                      // a padding token
         if (pos >= p.max_pos) {
             if (lane == 0) raise_err(p.a.err_flag, PKV_DEVERR_POS_RANGE);
             continue;
         }
-        const int what = w.minor < parts_q ? 0 : w.minor < parts_q + parts_k ? 1 : 2;       // queries, keys, values
-        const int heads = what == 0 ? p.num_heads : hk;
-        const int h0 = (w.minor - (what == 0 ? 0 : what == 1 ? parts_q : parts_q + parts_k)) * per_part + lane / LPR;
+        int part = p.whole ? 0 : minor, end = p.whole ? parts : minor + 1;
         int64_t blk = 0, off = 0;
-        if (CK && what > 0 && !place_slot(p.a, p.a.slot_mapping[t * p.a.slot_stride], blk, off)) continue;
-        const char *src = what == 0 ? p.q + t * p.q_tok : what == 1 ? p.a.k_new + t * p.a.k_src_tok : p.a.v_new + t * p.a.v_src_tok;
-        const int64_t src_head = what == 0 ? p.q_head : what == 1 ? p.a.k_src_head : p.a.v_src_head;
-        uint32_t e[U][4];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = h0 + u * (32 / LPR);
-            e[u][0] = e[u][1] = e[u][2] = e[u][3] = 0u;
-            if (h >= heads) continue;
-            const uint16_t *s = reinterpret_cast<const uint16_t *>(src + h * src_head) + 8 * sub;
-            if (p.vec) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(s);        // (the output may be the same memory)
-                e[u][0] = x.x; e[u][1] = x.y; e[u][2] = x.z; e[u][3] = x.w;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) e[u][j] = uint32_t(s[2 * j]) | (uint32_t(s[2 * j + 1]) << 16);
-            }
-        }
-        if (what < 2) {
-            const void *weight = what == 0 ? p.q_weight : p.k_weight;
-            const bool norm = weight != nullptr;
-            float w1[8], w2[8], cs[8], sn[8];
-            if (norm) {
-                load_weights(p, weight, 8 * sub, w1);
-                load_weights(p, weight, 8 * (sub + other - lane), w2);
-            }
-            if (turned) {                           // pairs 4 sub .. + 3 of 8 sub .. + 7, or those of 8 sub modulo rot / 2
-                const float *row = p.cos_sin + int64_t(pos) * p.cs_row + (p.interleaved ? 4 * sub : 8 * sub < half ? 8 * sub : 8 * sub - half);
-                const float4 c0 = __ldg(reinterpret_cast<const float4 *>(row)), s0 = __ldg(reinterpret_cast<const float4 *>(row + half));
-                if (p.interleaved) {
-                    const float c4[4] = {c0.x, c0.y, c0.z, c0.w}, s4[4] = {s0.x, s0.y, s0.z, s0.w};
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        cs[i] = c4[i >> 1];
-                        sn[i] = i & 1 ? s4[i >> 1] : -s4[i >> 1];
-                    }
-                } else {
-                    const float4 c1 = __ldg(reinterpret_cast<const float4 *>(row) + 1), s1 = __ldg(reinterpret_cast<const float4 *>(row + half) + 1);
-                    const float c8[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w}, s8[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        cs[i] = c8[i];
-                        sn[i] = sign * s8[i];
-                    }
-                }
-            }
+        if (CK && end > parts_q && !place_slot(p.a, slot, blk, off)) end = min(end, parts_q);      // queries alone
+        // a row's element becomes r (x a + y b): x itself, y the other of its pair, a and b
+        // weights times cosine and signed sine, r what the norm divides by
+        float a[8], b[8];
+        for (bool first = true; part < end; ++part, first = false) {
+            const int what = part < parts_q ? 0 : part < parts_q + parts_k ? 1 : 2;             // queries, keys, values
+            const int heads = what == 0 ? p.num_heads : hk;
+            const int h0 = (part - (what == 0 ? 0 : what == 1 ? parts_q : parts_q + parts_k)) * per_part + lane / LPR;
+            // this lane's place in the first row group, and how far the next one's is
+            const int64_t src_head = what == 0 ? p.q_head : what == 1 ? p.a.k_src_head : p.a.v_src_head;
+            const char *src = (what == 0 ? p.q + t * p.q_tok : what == 1 ? p.a.k_new + t * p.a.k_src_tok : p.a.v_new + t * p.a.v_src_tok) +
+                              h0 * src_head + 16 * sub;
+            const int64_t src_step = 32 / LPR * src_head;
+            uint32_t e[U][4];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                float x[8], r = 1.0f;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    x[2 * j] = h2f<SRC>(uint16_t(e[u][j]));
-                    x[2 * j + 1] = h2f<SRC>(uint16_t(e[u][j] >> 16));
-                }
-                if (norm) {
-                    float ss = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-                    for (int o = 1; o < LPR; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                    r = __frsqrt_rn(fmaf(ss, 1.0f / D, p.eps));
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w1[i];
-                }
-                float y[8];
-                if (p.interleaved) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) y[i] = x[i ^ 1];
+                const int h = h0 + u * (32 / LPR);
+                e[u][0] = e[u][1] = e[u][2] = e[u][3] = 0u;
+                const uint16_t *s = reinterpret_cast<const uint16_t *>(src);
+                src += src_step;
+                if (h >= heads) continue;
+                if (p.vec) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(s);        // (the output may be the same memory)
+                    e[u][0] = x.x; e[u][1] = x.y; e[u][2] = x.z; e[u][3] = x.w;
                 } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) e[u][j] = uint32_t(s[2 * j]) | (uint32_t(s[2 * j + 1]) << 16);
+                }
+            }
+            if (what < 2) {
+                const void *weight = what == 0 ? p.q_weight : p.k_weight;
+                const bool norm = weight != nullptr;
+                if (first || part == parts_q) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        a[i] = 1.0f;
+                        b[i] = 0.0f;
+                    }
+                    if (turned) {                           // pairs 4 sub .. + 3 of 8 sub .. + 7, or those of 8 sub modulo rot / 2
+                        const float *row = p.cos_sin + int64_t(pos) * p.cs_row + (p.interleaved ? 4 * sub : 8 * sub < half ? 8 * sub : 8 * sub - half);
+                        const float4 c0 = __ldg(reinterpret_cast<const float4 *>(row)), s0 = __ldg(reinterpret_cast<const float4 *>(row + half));
+                        if (p.interleaved) {
+                            const float c4[4] = {c0.x, c0.y, c0.z, c0.w}, s4[4] = {s0.x, s0.y, s0.z, s0.w};
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                a[i] = c4[i >> 1];
+                                b[i] = i & 1 ? s4[i >> 1] : -s4[i >> 1];
+                            }
+                        } else {
+                            const float4 c1 = __ldg(reinterpret_cast<const float4 *>(row) + 1), s1 = __ldg(reinterpret_cast<const float4 *>(row + half) + 1);
+                            const float c8[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w}, s8[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                a[i] = c8[i];
+                                b[i] = sign * s8[i];
+                            }
+                        }
+                    }
+                    if (norm) {
+                        float w[8];
+                        load_weights(p, weight, 8 * sub, w);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) a[i] *= w[i];
+                        if (!p.interleaved) load_weights(p, weight, 8 * (sub + other - lane), w);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) b[i] *= p.interleaved ? w[i ^ 1] : w[i];
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float x[8], y[8], r = 1.0f;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const uint32_t o = __shfl_sync(0xffffffffu, e[u][j], other);
-                        y[2 * j] = h2f<SRC>(uint16_t(o));
-                        y[2 * j + 1] = h2f<SRC>(uint16_t(o >> 16));
+                        x[2 * j] = h2f<SRC>(uint16_t(e[u][j]));
+                        x[2 * j + 1] = h2f<SRC>(uint16_t(e[u][j] >> 16));
                     }
-                    if (norm)
+                    if (norm) {
+                        float ss = 0.0f;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) y[i] = y[i] * r * w2[i];
+                        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+                        for (int o = 1; o < LPR; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                        r = rsqrtf(fmaf(ss, 1.0f / D, p.eps));
+                    }
+                    if (p.interleaved) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) y[i] = x[i ^ 1];
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t o = __shfl_sync(0xffffffffu, e[u][j], other);
+                            y[2 * j] = h2f<SRC>(uint16_t(o));
+                            y[2 * j + 1] = h2f<SRC>(uint16_t(o >> 16));
+                        }
+                    }
+                    if (turned) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i], a[i], y[i] * b[i]);
+                    } else if (norm) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] *= a[i];
+                    }
+                    if (norm || turned)                 // (else the source's bits)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) e[u][j] = uint32_t(f2h<SRC>(r * x[2 * j])) | (uint32_t(f2h<SRC>(r * x[2 * j + 1])) << 16);
                 }
-                if (turned) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i], cs[i], y[i] * sn[i]);
-                }
-                if (norm || turned)                 // (else the source's bits)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) e[u][j] = uint32_t(f2h<SRC>(x[2 * j])) | (uint32_t(f2h<SRC>(x[2 * j + 1])) << 16);
             }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = h0 + u * (32 / LPR);
             if (CK && what > 0) {
-                store_piece<SRC, CK, LPR>(p.a, what == 2, blk, off, h, sub, h < heads, e[u]);
-            } else if (h < heads) {
-                uint16_t *o = reinterpret_cast<uint16_t *>(what == 0 ? p.q_out + t * p.qo_tok + h * p.qo_head : p.k_out + t * p.ko_tok + h * p.ko_head) + 8 * sub;
-                if (p.out_vec) {
-                    *reinterpret_cast<uint4 *>(o) = make_uint4(e[u][0], e[u][1], e[u][2], e[u][3]);
-                } else {
+                char *to = (what == 2 ? p.a.v_cache : p.a.k_cache) + blk * p.a.c_blk + off * p.a.c_slot + h0 * p.a.c_head + piece_offset<CK>(p.a, sub);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) o[j] = uint16_t(e[u][j >> 1] >> (16 * (j & 1)));
+                for (int u = 0; u < U; ++u, to += 32 / LPR * p.a.c_head) {
+                    const int h = h0 + u * (32 / LPR);
+                    store_piece<SRC, CK, LPR>(p.a, to, what == 2, blk, off, h, sub, h < heads, e[u]);
+                }
+            } else {
+                const int64_t head = what == 0 ? p.qo_head : p.ko_head;
+                char *to = (what == 0 ? p.q_out + t * p.qo_tok : p.k_out + t * p.ko_tok) + h0 * head + 16 * sub;
+#pragma unroll
+                for (int u = 0; u < U; ++u, to += 32 / LPR * head) {
+                    if (h0 + u * (32 / LPR) >= heads) continue;
+                    uint16_t *o = reinterpret_cast<uint16_t *>(to);
+                    if (p.out_vec) {
+                        *reinterpret_cast<uint4 *>(o) = make_uint4(e[u][0], e[u][1], e[u][2], e[u][3]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) o[j] = uint16_t(e[u][j >> 1] >> (16 * (j & 1)));
+                    }
                 }
             }
         }
@@ -263,7 +318,7 @@ __global__ void __launch_bounds__(kAppendThreads) norm_rope_kernel(NormRopeParam
 
 }  // namespace
 
-cudaError_t launch_norm_rope(const NormRopeParams &p, int cache_kind, cudaStream_t s)
+cudaError_t launch_norm_rope(NormRopeParams p, int cache_kind, cudaStream_t s)
 {
     if (p.a.num_tokens == 0) return cudaSuccess;
     const int lpr = p.a.head_dim / 8;
@@ -271,10 +326,14 @@ cudaError_t launch_norm_rope(const NormRopeParams &p, int cache_kind, cudaStream
         const int rows = 32 * U / lpr;
         return (p.num_heads + rows - 1) / rows + (cache_kind ? 2 : 1) * ((p.a.num_kv_heads + rows - 1) / rows);
     };
-    // four row groups per warp where that still gives every SM several warps, else one
-    const bool one = p.a.num_tokens * parts(4) < int64_t(sm_count_current_device()) * 8;
-    const int n = parts(one ? 1 : 4);
+    // four row groups at a time where that still gives every SM several warps, else one; and
+    // whole tokens, one after another, where every SM gets its fill of them
+    const int64_t sms = sm_count_current_device();
+    const bool one = p.a.num_tokens * parts(4) < sms * 8;
+    int n = parts(one ? 1 : 4);
     if (n == 0) return cudaSuccess;
+    p.whole = p.a.num_tokens >= sms * 32;
+    if (p.whole) n = 1;
     const int g = grid_for(p.a.num_tokens * n * 32, kAppendThreads);
     auto go = [&](auto src_c, auto ck_c, auto d_c) -> cudaError_t {
         constexpr int S = decltype(src_c)::value, CK = decltype(ck_c)::value, D = decltype(d_c)::value;

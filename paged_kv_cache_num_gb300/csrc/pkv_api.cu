@@ -758,6 +758,7 @@ int prep_norm_rope(const pkv_tensor *q, const pkv_tensor *q_weight, const pkv_te
     if (q->stride[2] != 1 || q_out->stride[2] != 1) return fail(PKV_ERR_LAYOUT, "head_dim of q and q_out must be contiguous");
     if (q->shape[1] > (1 << 24) || p.a.num_kv_heads > (1 << 24)) return fail(PKV_ERR_UNSUPPORTED, "more than 2^24 heads");
     p.weight_kind = src;
+    p.weight_vec = 1;
     const pkv_tensor *weights[2] = {q_weight, k_weight};
     for (const pkv_tensor *w : weights) {
         if (!w) continue;
@@ -766,6 +767,7 @@ int prep_norm_rope(const pkv_tensor *q, const pkv_tensor *q_weight, const pkv_te
         if (w->shape[0] != D) return fail(PKV_ERR_SHAPE, "weights must be [head_dim]");
         if (w->stride[0] != 1) return fail(PKV_ERR_LAYOUT, "weights must be contiguous");
         p.weight_kind = w->dtype;
+        p.weight_vec = p.weight_vec && aligned(w->data, 16);
     }
     if (q_weight && k_weight && q_weight->dtype != k_weight->dtype) return fail(PKV_ERR_DTYPE, "q_weight and k_weight dtypes differ");
     if (!std::isfinite(eps) || eps < 0.0f) return fail(PKV_ERR_VALUE, "eps must be finite and not negative");

@@ -217,6 +217,7 @@ struct NormRopeParams {
     const void *q_weight;       // [head_dim], or none: no norm
     const void *k_weight;
     int weight_kind;            // kF16, kBF16 or PKV_DTYPE_F32
+    int weight_vec;             // 16-bit weights at multiples of 16 bytes
     float eps;
     const float *cos_sin;       // [max_pos][rot]: cos, then sin
     int64_t cs_row;             // elements
@@ -227,10 +228,11 @@ struct NormRopeParams {
     int64_t pos_stride;
     int vec;                    // source rows at multiples of 16 bytes
     int out_vec;                // output rows likewise
+    int whole;                  // a warp takes whole tokens (launch_norm_rope)
 };
 
 // cache_kind 0: keys to k_out
-cudaError_t launch_norm_rope(const NormRopeParams &p, int cache_kind, cudaStream_t s);
+cudaError_t launch_norm_rope(NormRopeParams p, int cache_kind, cudaStream_t s);
 
 // ---------------------------------------------------------------- block tables
 constexpr int kTableMaxBatch = 16384;   // three 32-bit numbers each in shared memory

@@ -22,7 +22,7 @@
 namespace pkv {
 namespace {
 
-constexpr int kTableThreads = 512;
+constexpr int kTableThreads = 1024;                 // at most
 constexpr int kTableMaxDevices = 64;
 
 // Inclusive sums of two numbers over the threads of the CTA.
@@ -42,9 +42,19 @@ __device__ __forceinline__ void cta_scan(int64_t &a, int64_t &b, int64_t (*sums)
         sums[warp][1] = b;
     }
     __syncthreads();
-    for (int w = 0; w < warp; ++w) {
-        a += sums[w][0];
-        b += sums[w][1];
+    int64_t x = lane < (blockDim.x >> 5) ? sums[lane][0] : 0, y = lane < (blockDim.x >> 5) ? sums[lane][1] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) {
+            x += u;
+            y += v;
+        }
+    }
+    const int64_t u = __shfl_sync(0xffffffffu, x, (warp + 31) & 31), v = __shfl_sync(0xffffffffu, y, (warp + 31) & 31);
+    if (warp > 0) {
+        a += u;
+        b += v;
     }
     __syncthreads();
 }
@@ -79,7 +89,8 @@ __global__ void __launch_bounds__(kTableThreads) tables_kernel(TableParams p)
     // what a stack can give, or take
     const int64_t room = TRIM ? p.pool - count : count;
     if (tid < 2) totals[tid] = 0;
-    const int per = (B + kTableThreads - 1) / kTableThreads;
+    const int threads = blockDim.x;
+    const int per = (B + threads - 1) / threads;
     const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
     // rows and blocks of request b
     bool bad_len = false;
@@ -116,13 +127,14 @@ __global__ void __launch_bounds__(kTableThreads) tables_kernel(TableParams p)
     // Served is who fits together with all before him; the others, as the sums only
     // grow, are those from some request on, and count as without new rows.  Their
     // starts are corrected below: every start is at most the total.
+    int most_rows = 0, most_blocks = 0;
     for (int b = b0; b < b1; ++b) {
         int64_t cached, rows, blocks;
         request(b, cached, rows, blocks);
         const bool fits = (TRIM || r + rows <= p.num_rows) && k + blocks <= room;
         if (fits) {
-            if (!TRIM) atomicMax(&totals[0], int(r + rows));
-            atomicMax(&totals[1], int(k + blocks));
+            if (!TRIM) most_rows = int(r + rows);
+            most_blocks = int(k + blocks);
         } else if (rows > 0 || blocks > 0) {
             bad_pool = true;
         }
@@ -132,20 +144,26 @@ __global__ void __launch_bounds__(kTableThreads) tables_kernel(TableParams p)
         r += rows;
         k += blocks;
     }
+    most_rows = __reduce_max_sync(0xffffffffu, most_rows);
+    most_blocks = __reduce_max_sync(0xffffffffu, most_blocks);
+    if ((tid & 31) == 0 && (most_rows | most_blocks) != 0) {
+        atomicMax(&totals[0], most_rows);
+        atomicMax(&totals[1], most_blocks);
+    }
     if (blockIdx.x == 0) {
         if (bad_len) raise_err(p.err_flag, PKV_DEVERR_CONTEXT_RANGE);
         if (bad_pool) raise_err(p.err_flag, PKV_DEVERR_POOL_RANGE);
     }
     __syncthreads();
     const int total_rows = totals[0], total_blocks = totals[1];
-    for (int b = tid; b < B; b += kTableThreads) {
+    for (int b = tid; b < B; b += threads) {
         if (!TRIM) row0[b] = min(row0[b], total_rows);
         blk0[b] = min(blk0[b], total_blocks);
     }
     // all CTAs have read the lengths and counts that are written below
     cooperative_groups::this_cluster().sync();
 
-    const int at = blockIdx.x * kTableThreads + tid, step = gridDim.x * kTableThreads;
+    const int at = blockIdx.x * threads + tid, step = gridDim.x * threads;
     for (int b = at; b < B; b += step) {
         if (TRIM) {
             p.lens_out[b * p.lens_stride] = row0[b];
@@ -170,25 +188,51 @@ __global__ void __launch_bounds__(kTableThreads) tables_kernel(TableParams p)
         }
     }
     if (TRIM) return;
-    for (int i = at; i < p.num_rows; i += step) {
-        int b = -1, pos = -1;
-        int64_t slot = -1;
-        if (i < total_rows) {
-            b = find(row0, B, i);
-            pos = len[b] + (i - row0[b]);
-            const int64_t j = pos >> p.block_shift, have = (int64_t(len[b]) + round) >> p.block_shift;
-            // the request's own last block, or one of those handed out now (which are not read back)
-            const int64_t blk = j < have ? p.bt[b * p.bt_b + j * p.bt_j] : p.free_blocks[count - 1 - (blk0[b] + (j - have))];
-            slot = (blk << p.block_shift) + (pos & round);
+    // four neighbouring rows a thread: one bisection for those of a request, and their loads together
+    const bool quads = ((reinterpret_cast<uintptr_t>(p.req) | reinterpret_cast<uintptr_t>(p.pos) |
+                         reinterpret_cast<uintptr_t>(p.slot_mapping)) & 15) == 0;
+    const int num_rows = int(p.num_rows);
+    for (int64_t i0 = 4 * int64_t(at); i0 < num_rows; i0 += 4 * int64_t(step)) {
+        int b[4], pos[4];
+        int64_t slot[4];
+        int cur = i0 < total_rows ? find(row0, B, int(i0)) : 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = int(i0) + u;
+            b[u] = pos[u] = -1;
+            slot[u] = -1;
+            if (i < total_rows) {
+                if (cur + 1 < B && row0[cur + 1] <= i) cur = find(row0, B, i);
+                b[u] = cur;
+                pos[u] = len[cur] + (i - row0[cur]);
+                const int64_t j = pos[u] >> p.block_shift, have = (int64_t(len[cur]) + round) >> p.block_shift;
+                // the request's own last block, or one of those handed out now (which are not read back)
+                const int32_t *entry = j < have ? p.bt + cur * p.bt_b + j * p.bt_j : p.free_blocks + (count - 1 - (blk0[cur] + (j - have)));
+                slot[u] = *entry;
+            }
         }
-        p.req[i] = b;
-        p.pos[i] = pos;
-        p.slot_mapping[i] = slot;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (pos[u] >= 0) slot[u] = (slot[u] << p.block_shift) + (pos[u] & round);
+        if (quads && i0 + 4 <= num_rows) {
+            *reinterpret_cast<int4 *>(p.req + i0) = make_int4(b[0], b[1], b[2], b[3]);
+            *reinterpret_cast<int4 *>(p.pos + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+            *reinterpret_cast<longlong2 *>(p.slot_mapping + i0) = make_longlong2(slot[0], slot[1]);
+            *reinterpret_cast<longlong2 *>(p.slot_mapping + i0 + 2) = make_longlong2(slot[2], slot[3]);
+        } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (i0 + u < num_rows) {
+                    p.req[i0 + u] = b[u];
+                    p.pos[i0 + u] = pos[u];
+                    p.slot_mapping[i0 + u] = slot[u];
+                }
+        }
     }
 }
 
 template <bool TRIM>
-cudaError_t launch_tables_t(const TableParams &p, int ctas, cudaStream_t s)
+cudaError_t launch_tables_t(const TableParams &p, int ctas, int threads, cudaStream_t s)
 {
     const size_t smem = size_t(p.batch) * 12;
     static std::atomic<int> configured[kTableMaxDevices];
@@ -201,9 +245,19 @@ cudaError_t launch_tables_t(const TableParams &p, int ctas, cudaStream_t s)
         if (e != cudaSuccess) return e;
         configured[dev].store(kTableMaxBatch * 12, std::memory_order_relaxed);
     }
+    if (ctas > 8) {                                 // beyond the portable size, if this GPU has room for it
+        static std::atomic<int> wide[kTableMaxDevices];         // 0: not asked yet, else 8 or 16
+        int w = wide[dev].load(std::memory_order_relaxed);
+        if (w == 0) {
+            w = cudaFuncSetAttribute(tables_kernel<TRIM>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess ? 16 : 8;
+            if (w == 8) cudaGetLastError();
+            wide[dev].store(w, std::memory_order_relaxed);
+        }
+        ctas = w;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kTableThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -214,6 +268,14 @@ cudaError_t launch_tables_t(const TableParams &p, int ctas, cudaStream_t s)
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
+    if (ctas > 8) {
+        int clusters = 0;
+        if (cudaOccupancyMaxActiveClusters(&clusters, tables_kernel<TRIM>, &cfg) != cudaSuccess || clusters < 1) {
+            cudaGetLastError();
+            cfg.gridDim = dim3(8);
+            attr[1].val.clusterDim.x = 8;
+        }
+    }
     return cudaLaunchKernelEx(&cfg, tables_kernel<TRIM>, p);
 }
 
@@ -221,11 +283,13 @@ cudaError_t launch_tables_t(const TableParams &p, int ctas, cudaStream_t s)
 
 cudaError_t launch_tables(const TableParams &p, bool trim, cudaStream_t s)
 {
-    // one CTA, or the eight of a portable cluster where there are many rows, or many
-    // requests that may drop blocks
+    // one CTA, or the eight of a portable cluster, or sixteen, where there are many rows,
+    // or many requests that may drop blocks
     const int64_t work = trim ? int64_t(p.batch) * p.max_blocks / 8 : p.num_rows;
-    const int ctas = work > 4 * kTableThreads ? 8 : 1;
-    return trim ? launch_tables_t<true>(p, ctas, s) : launch_tables_t<false>(p, ctas, s);
+    const int ctas = work > 16 * kTableThreads ? 16 : work > 4 * kTableThreads ? 8 : 1;
+    // a decode step's few requests and rows: fewer warps to bring together
+    const int threads = p.batch <= 256 && work <= 1024 ? 256 : kTableThreads;
+    return trim ? launch_tables_t<true>(p, ctas, threads, s) : launch_tables_t<false>(p, ctas, threads, s);
 }
 
 }  // namespace pkv

@@ -76,20 +76,18 @@ def lib():
             L.pkv_version.restype = ctypes.c_char_p
             L.pkv_last_error.restype = ctypes.c_char_p
             L.pkv_abi_version.restype = ctypes.c_int
-            L.pkv_slot_mapping.argtypes = [TP, TP, TP, ctypes.c_int, TP, P, P]
-            L.pkv_kv_append.argtypes = [TP, TP, TP, CP, P, P]
+            # descriptors of most calls are packed bytes (_packed)
+            L.pkv_slot_mapping.argtypes = [P, P, P, ctypes.c_int, P, P, P]
+            L.pkv_kv_append.argtypes = [P, P, P, P, P, P]
             L.pkv_kv_append_scaled.argtypes = [TP, TP, TP, TP, TP, CP, P, P]
-            L.pkv_paged_decode_workspace.argtypes = [TP, CP, TP, ctypes.c_int,
-                                                     ctypes.POINTER(ctypes.c_size_t)]
+            L.pkv_paged_decode_workspace.argtypes = [P, P, P, ctypes.c_int, P]
             L.pkv_paged_decode_launches.argtypes = [TP, CP, TP, ctypes.c_int,
                                                     ctypes.POINTER(ctypes.c_int32)]
-            L.pkv_paged_decode.argtypes = [TP, CP, TP, TP, ctypes.c_float, TP, ctypes.c_int, P,
-                                           ctypes.c_size_t, P, P]
+            L.pkv_paged_decode.argtypes = [P, P, P, P, ctypes.c_float, P, ctypes.c_int, P, ctypes.c_size_t, P, P]
             L.pkv_paged_decode_noalloc.argtypes = [TP, CP, TP, TP, ctypes.c_float, TP,
                                                    ctypes.c_int, P, P]
-            L.pkv_decode_step.argtypes = [TP, TP, TP, TP, TP, TP, CP, TP, TP, ctypes.c_float, TP,
-                                          ctypes.c_int, P, ctypes.c_size_t, P, P]
-            # descriptors of these as packed bytes (_packed)
+            L.pkv_decode_step.argtypes = [P, P, P, P, P, P, P, P, P, ctypes.c_float, P, ctypes.c_int, P,
+                                          ctypes.c_size_t, P, P]
             L.pkv_kv_append_dynamic.argtypes = [P, P, P, P, P, P]
             L.pkv_kv_gather.argtypes = [P, P, P, P, P, P]
             L.pkv_paged_prefill_workspace.argtypes = [P, P, P, P]
@@ -153,13 +151,17 @@ def _xvec_desc(t: torch.Tensor, code: int) -> _Tensor:
     return d
 
 
+def _flag(err_flag):
+    return None if err_flag is None else err_flag.data_ptr()
+
+
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -313,7 +315,9 @@ class KVCache:
         return c
 
     def _struct(self) -> _Cache:
-        key = tuple((t.data_ptr(), t.dtype, t.shape, t.stride()) for t in self.tensors())
+        key = [x for t in (self.k_cache, self.v_cache, self.k_scale, self.v_scale, self.k_qscale, self.k_qzero,
+                           self.v_qscale, self.v_qzero, self.k_scales, self.v_scales) if t is not None
+               for x in (t.data_ptr(), t.dtype, t.shape, t.stride())]
         cached = self.__dict__.get("_cstruct")
         if cached is not None and cached[0] == key:
             return cached[1]
@@ -382,9 +386,8 @@ def slot_mapping(block_tables, req, pos, block_size: int, out=None, err_flag=Non
     _need_cuda(block_tables, req, pos)
     if out is None:
         out = torch.empty(req.shape[0], dtype=torch.int64, device=req.device)
-    _check(lib().pkv_slot_mapping(ctypes.byref(_desc(block_tables)), ctypes.byref(_desc(req)),
-                                  ctypes.byref(_desc(pos)), int(block_size),
-                                  ctypes.byref(_desc(out)), _ptr(err_flag), _stream(stream)))
+    _check(lib().pkv_slot_mapping(_packed(block_tables), _packed(req), _packed(pos), int(block_size), _packed(out),
+                                  _flag(err_flag), _stream(stream)))
     return out
 
 
@@ -392,9 +395,8 @@ def kv_append(k_new, v_new, slot_mapping, cache: KVCache, err_flag=None, stream=
     """Scatter new K/V rows [T, Hkv, D] into the cache through slot_mapping."""
     _need_cuda(k_new, v_new, slot_mapping, *cache.tensors())
     cs = cache._struct()
-    _check(lib().pkv_kv_append(ctypes.byref(_desc(k_new)), ctypes.byref(_desc(v_new)),
-                               ctypes.byref(_desc(slot_mapping)), ctypes.byref(cs),
-                               _ptr(err_flag), _stream(stream)))
+    _check(lib().pkv_kv_append(_packed(k_new), _packed(v_new), _packed(slot_mapping), ctypes.byref(cs),
+                               _flag(err_flag), _stream(stream)))
 
 
 def kv_append_scaled(k_new, v_new, k_new_scale, v_new_scale, slot_mapping, cache: KVCache,
@@ -453,10 +455,6 @@ def kv_gather(cache: KVCache, slot_mapping, dtype: Optional[torch.dtype] = None,
     _check(lib().pkv_kv_gather(ctypes.byref(cache._struct()), _packed(slot_mapping), _packed(k_out), _packed(v_out),
                                None if err_flag is None else err_flag.data_ptr(), _raw_stream(dev)))
     return k_out, v_out
-
-
-def _flag(err_flag):
-    return None if err_flag is None else err_flag.data_ptr()
 
 
 def norm_rope(q, k, cos_sin, pos, q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False,
@@ -602,8 +600,7 @@ def paged_prefill(q, cache: KVCache, block_tables, q_starts, context_lens,
 def decode_workspace_bytes(q, cache: KVCache, block_tables, num_splits: int = 0) -> int:
     n = ctypes.c_size_t(0)
     cs = cache._struct()
-    _check(lib().pkv_paged_decode_workspace(ctypes.byref(_desc(q)), ctypes.byref(cs),
-                                            ctypes.byref(_desc(block_tables)), int(num_splits),
+    _check(lib().pkv_paged_decode_workspace(_packed(q), ctypes.byref(cs), _packed(block_tables), int(num_splits),
                                             ctypes.byref(n)))
     return int(n.value)
 
@@ -630,13 +627,11 @@ def paged_decode(q, cache: KVCache, block_tables, context_lens, sm_scale: Option
         need = decode_workspace_bytes(q, cache, block_tables, num_splits)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    ws_ptr = None if workspace is None else ctypes.c_void_p(workspace.data_ptr())
+    ws_ptr = None if workspace is None else workspace.data_ptr()
     ws_n = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().pkv_paged_decode(ctypes.byref(_desc(q)), ctypes.byref(cs),
-                                  ctypes.byref(_desc(block_tables)),
-                                  ctypes.byref(_desc(context_lens)), float(sm_scale),
-                                  ctypes.byref(_desc(out)), int(num_splits), ws_ptr, ws_n,
-                                  _ptr(err_flag), _stream(stream)))
+    _check(lib().pkv_paged_decode(_packed(q), ctypes.byref(cs), _packed(block_tables), _packed(context_lens),
+                                  float(sm_scale), _packed(out), int(num_splits), ws_ptr, ws_n, _flag(err_flag),
+                                  _stream(stream)))
     return out
 
 
@@ -658,14 +653,11 @@ def decode_step(k_new, v_new, req, pos, q, cache: KVCache, block_tables, context
         need = decode_workspace_bytes(q, cache, block_tables, num_splits)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    ws_ptr = None if workspace is None else ctypes.c_void_p(workspace.data_ptr())
+    ws_ptr = None if workspace is None else workspace.data_ptr()
     ws_n = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().pkv_decode_step(ctypes.byref(_desc(k_new)), ctypes.byref(_desc(v_new)),
-                                 ctypes.byref(_desc(req)), ctypes.byref(_desc(pos)),
-                                 ctypes.byref(_desc(slots)), ctypes.byref(_desc(q)), ctypes.byref(cs),
-                                 ctypes.byref(_desc(block_tables)), ctypes.byref(_desc(context_lens)),
-                                 float(sm_scale), ctypes.byref(_desc(out)), int(num_splits), ws_ptr,
-                                 ws_n, _ptr(err_flag), _stream(stream)))
+    _check(lib().pkv_decode_step(_packed(k_new), _packed(v_new), _packed(req), _packed(pos), _packed(slots), _packed(q),
+                                 ctypes.byref(cs), _packed(block_tables), _packed(context_lens), float(sm_scale),
+                                 _packed(out), int(num_splits), ws_ptr, ws_n, _flag(err_flag), _stream(stream)))
     return out
 
 
