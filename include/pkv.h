@@ -123,7 +123,8 @@ typedef struct pkv_tensor {
  *     PKV_SCALE_*).
  *   k_qscale, v_qscale (F16) and k_qzero, v_qzero (U8), U3 and U4 only:
  *     [num_blocks, block_size, num_kv_heads]; a stored code u means
- *     (u - zero) * scale for its (slot, head) row.  Any strides are
+ *     (u - zero) * scale for its (slot, head) row (finite scales, as the appends
+ *     store).  Any strides are
  *     accepted (the two scale arrays alike, the two zero arrays alike).
  *     Decode reads them fastest head-major (slot stride 1, head stride
  *     block_size: a [num_blocks, num_kv_heads, block_size] array seen through

@@ -34,6 +34,17 @@
 // by as much, so that neither the loads of K rows (4 lanes a row) nor the transposed
 // ones of V meet a bank twice.
 // Every wait is bounded (about 2 s) and raises PKV_DEVERR_TIMEOUT.
+//
+// What bounds it.  16 sequences of 16K to 32K tokens, 64 q over 8 kv heads of 128
+// (421 MB): 81 us for this kernel, 86 us a call (0.72 of the copy bandwidth); the
+// copies alone, without any arithmetic, take 68 to 70 us (6.1 TB/s with start and
+// end).  32 sequences of 1K to 8K, 32 heads (677 MB): 132 us a call (0.75), copies
+// alone 104 to 108.  The rest is the instructions: about 480 a warp for 32 tokens of
+// a kv head (QK and softmax 186, PV 148, scales and zeros 54, ring and walk 95 with the
+// producer's), of which an SM sub-partition issues 0.5 a cycle; the logic pipe is
+// 60 % busy in bursts.  Tried: four CTAs an SM (96 registers, spills: 98 us), units of
+// 64 tokens (83), eight heads a CTA (88), shifts in the multiplier (102 as before),
+// two or three stages (84, 83).
 #include "decode_tma_kernel.cuh"
 
 namespace pkv {
@@ -42,7 +53,10 @@ namespace {
 constexpr int kUnit = 32;                           // tokens of a unit
 constexpr int kUnitShift = 5;
 
-// kv heads of a CTA at most, and CTAs that an SM is to hold: see plan_decode_u4
+// kv heads of a CTA at most, and CTAs that an SM is to hold.  Three CTAs of five warps
+// leave each SM sub-partition at most four warps of 128 registers; with 16 head
+// columns (twice the accumulators) it is three of 168, two CTAs (128 q over 8 kv heads
+// on the long contexts: 135 us; four CTAs of two heads 140, three of four heads 207).
 template <int NG> constexpr int kHeadsU4 = 4;
 template <int NG> constexpr int kCtasU4 = NG == 1 ? 3 : 2;
 
@@ -621,7 +635,9 @@ cudaError_t launch_u4(const DecodeParams &p, const FastParams &f, const CUtensor
 bool plan_decode_u4(const DecodeParams &p, bool meta_head_major, int sm_count, FastParams &f, size_t &workspace)
 {
     if (p.block_size < 16 || p.batch < 1 || p.batch > 4096 || p.group < 1) return false;
-    if (int64_t(p.max_blocks) * p.block_size > (int64_t(1) << 31) - 64) return false;      // token numbers in 32 bits
+    // token numbers, and units of all sequences, in 32 bits
+    const int64_t tokens = int64_t(p.max_blocks) * p.block_size;
+    if (tokens > (int64_t(1) << 31) - 64 || p.batch * ((tokens + kUnit - 1) / kUnit) >= (int64_t(1) << 31)) return false;
     if (p.num_kv_heads >= 1 << 15) return false;                                            // head groups in 15
     const int row = p.head_dim / 2, ng = p.group > 8 ? 2 : 1;
     const int most = ng == 1 ? kHeadsU4<1> : kHeadsU4<2>, per_sm = ng == 1 ? kCtasU4<1> : kCtasU4<2>;
@@ -646,7 +662,7 @@ bool plan_decode_u4(const DecodeParams &p, bool meta_head_major, int sm_count, F
     f.meta_heads = meta_heads;
     f.meta_hmaj = meta_head_major ? 1 : 0;
     f.smem_bytes = L.total;
-    const int64_t units = int64_t(f.n_hg) * p.batch * ((int64_t(p.max_blocks) * p.block_size + kUnit - 1) / kUnit);
+    const int64_t units = int64_t(f.n_hg) * p.batch * ((tokens + kUnit - 1) / kUnit);
     const int64_t room = int64_t(sm_count) * ctas;
     f.grid = int(units < room ? (units > 0 ? units : 1) : room);
     const int64_t rows = partial_rows(p, f);

@@ -12,7 +12,9 @@
 // itself (reads of a few bytes per request), then takes its share of the blocks and
 // rows, finding their request by bisection in shared memory.  The cluster's
 // barrier parts the reads of lengths and counts from the writes, which may be to
-// the same memory.  Bound by latency: a launch and three trips to memory.
+// the same memory.  Bound by latency, a launch and three trips to memory: 64 requests
+// of 1 to 8 new tokens 5 us on the device, 601 prompts' 150000 rows 14 us with sixteen
+// CTAs (eight: 20; a row at a time: 32).
 #include <cooperative_groups.h>
 
 #include <atomic>

@@ -383,20 +383,28 @@ def version() -> str:
 
 def slot_mapping(block_tables, req, pos, block_size: int, out=None, err_flag=None, stream=None):
     """slot = block_tables[req][pos // bs] * bs + pos % bs (pos < 0 -> -1), on the GPU."""
-    _need_cuda(block_tables, req, pos)
+    dev = _one_device(block_tables, req, pos)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return slot_mapping(block_tables, req, pos, block_size, out, err_flag)
     if out is None:
         out = torch.empty(req.shape[0], dtype=torch.int64, device=req.device)
     _check(lib().pkv_slot_mapping(_packed(block_tables), _packed(req), _packed(pos), int(block_size), _packed(out),
-                                  _flag(err_flag), _stream(stream)))
+                                  _flag(err_flag), _raw_stream(dev)))
     return out
 
 
 def kv_append(k_new, v_new, slot_mapping, cache: KVCache, err_flag=None, stream=None):
     """Scatter new K/V rows [T, Hkv, D] into the cache through slot_mapping."""
-    _need_cuda(k_new, v_new, slot_mapping, *cache.tensors())
+    dev = _one_device(k_new, v_new, slot_mapping, *cache.tensors())
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return kv_append(k_new, v_new, slot_mapping, cache, err_flag)
     cs = cache._struct()
     _check(lib().pkv_kv_append(_packed(k_new), _packed(v_new), _packed(slot_mapping), ctypes.byref(cs),
-                               _flag(err_flag), _stream(stream)))
+                               _flag(err_flag), _raw_stream(dev)))
 
 
 def kv_append_scaled(k_new, v_new, k_new_scale, v_new_scale, slot_mapping, cache: KVCache,
@@ -617,7 +625,11 @@ def decode_launches(q, cache: KVCache, block_tables, num_splits: int = 0) -> int
 def paged_decode(q, cache: KVCache, block_tables, context_lens, sm_scale: Optional[float] = None,
                  out=None, num_splits: int = 0, workspace=None, err_flag=None, stream=None):
     """softmax(sm_scale * q . K^T) V over each sequence's paged context."""
-    _need_cuda(q, block_tables, context_lens, *cache.tensors())
+    dev = _one_device(q, block_tables, context_lens, *cache.tensors())
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return paged_decode(q, cache, block_tables, context_lens, sm_scale, out, num_splits, workspace, err_flag)
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(q.shape[-1])
     if out is None:
@@ -631,7 +643,7 @@ def paged_decode(q, cache: KVCache, block_tables, context_lens, sm_scale: Option
     ws_n = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().pkv_paged_decode(_packed(q), ctypes.byref(cs), _packed(block_tables), _packed(context_lens),
                                   float(sm_scale), _packed(out), int(num_splits), ws_ptr, ws_n, _flag(err_flag),
-                                  _stream(stream)))
+                                  _raw_stream(dev)))
     return out
 
 
@@ -641,7 +653,12 @@ def decode_step(k_new, v_new, req, pos, q, cache: KVCache, block_tables, context
     """slot_mapping + kv_append + paged_decode in one library call (see
     pkv_decode_step in pkv.h); returns out.  `slots` (int64 [num_tokens])
     receives the slot mapping."""
-    _need_cuda(k_new, v_new, req, pos, q, block_tables, context_lens, *cache.tensors())
+    dev = _one_device(k_new, v_new, req, pos, q, block_tables, context_lens, *cache.tensors())
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return decode_step(k_new, v_new, req, pos, q, cache, block_tables, context_lens, sm_scale, out, slots,
+                               num_splits, workspace, err_flag)
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(q.shape[-1])
     if out is None:
@@ -657,7 +674,7 @@ def decode_step(k_new, v_new, req, pos, q, cache: KVCache, block_tables, context
     ws_n = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().pkv_decode_step(_packed(k_new), _packed(v_new), _packed(req), _packed(pos), _packed(slots), _packed(q),
                                  ctypes.byref(cs), _packed(block_tables), _packed(context_lens), float(sm_scale),
-                                 _packed(out), int(num_splits), ws_ptr, ws_n, _flag(err_flag), _stream(stream)))
+                                 _packed(out), int(num_splits), ws_ptr, ws_n, _flag(err_flag), _raw_stream(dev)))
     return out
 
 
