@@ -192,11 +192,12 @@ __device__ __forceinline__ RowU4<W> row_u4(const uint32_t (&e)[4 * W])
     for (int w = 0; w < W; ++w) {
         uint32_t sum = 0;
 #pragma unroll
-        for (int i = 7; i >= 0; --i) {
-            const uint32_t p = e[4 * w + (i >> 1)];
-            const float x = h2f<SRC>(uint16_t(i & 1 ? p >> 16 : p));
-            const float q = fminf(fmaxf(row_quotient(x, s, rs), least), most);
-            sum = sum * 16u + __float_as_uint(__fadd_rn(q, kMagic));
+        for (int i = 3; i >= 0; --i) {
+            const float2 x = h2f2<SRC>(e[4 * w + i]);
+            const float q1 = fminf(fmaxf(row_quotient(x.y, s, rs), least), most);
+            const float q0 = fminf(fmaxf(row_quotient(x.x, s, rs), least), most);
+            sum = sum * 16u + __float_as_uint(__fadd_rn(q1, kMagic));
+            sum = sum * 16u + __float_as_uint(__fadd_rn(q0, kMagic));
         }
         r.codes[w] = sum + (zi - 0x4b400000u) * 0x11111111u;
     }

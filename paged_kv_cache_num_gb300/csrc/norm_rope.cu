@@ -259,8 +259,9 @@ __global__ void __launch_bounds__(kAppendThreads, 3) norm_rope_kernel(NormRopePa
                     float x[8], y[8], r = 1.0f;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        x[2 * j] = h2f<SRC>(uint16_t(e[u][j]));
-                        x[2 * j + 1] = h2f<SRC>(uint16_t(e[u][j] >> 16));
+                        const float2 v = h2f2<SRC>(e[u][j]);
+                        x[2 * j] = v.x;
+                        x[2 * j + 1] = v.y;
                     }
                     if (norm) {
                         float ss = 0.0f;
@@ -276,9 +277,9 @@ __global__ void __launch_bounds__(kAppendThreads, 3) norm_rope_kernel(NormRopePa
                     } else {
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const uint32_t o = __shfl_sync(0xffffffffu, e[u][j], other);
-                            y[2 * j] = h2f<SRC>(uint16_t(o));
-                            y[2 * j + 1] = h2f<SRC>(uint16_t(o >> 16));
+                            const float2 v = h2f2<SRC>(__shfl_sync(0xffffffffu, e[u][j], other));
+                            y[2 * j] = v.x;
+                            y[2 * j + 1] = v.y;
                         }
                     }
                     if (turned) {
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(kAppendThreads, 3) norm_rope_kernel(NormRopePa
                     }
                     if (norm || turned)                 // (else the source's bits)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) e[u][j] = uint32_t(f2h<SRC>(r * x[2 * j])) | (uint32_t(f2h<SRC>(r * x[2 * j + 1])) << 16);
+                        for (int j = 0; j < 4; ++j) e[u][j] = f2h2<SRC>(r * x[2 * j], r * x[2 * j + 1]);
                 }
             }
             if (CK && what > 0) {

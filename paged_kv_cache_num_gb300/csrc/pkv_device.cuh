@@ -64,6 +64,25 @@ template <> __device__ __forceinline__ uint16_t f2h<kBF16>(float v)
     return __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
+// two 16-bit elements -> two floats, without a shift for the upper one
+template <int KIND> __device__ __forceinline__ float2 h2f2(uint32_t w)
+{
+    if constexpr (KIND == kF16) return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    else return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+// two floats -> two 16-bit elements, rounded to nearest even
+template <int KIND> __device__ __forceinline__ uint32_t f2h2(float x, float y)
+{
+    if constexpr (KIND == kF16) {
+        const __half2 v = __floats2half2_rn(x, y);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    } else {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+}
+
 // Eight 4-bit codes (element j at bits 4j .. 4j+3) minus their zero point z, as
 // pairs of f16 numbers in order, exactly: under 0x6400 a byte with code u is
 // 1024 + u; nz holds -1024 - z twice.
