@@ -41,8 +41,8 @@
 // end).  32 sequences of 1K to 8K, 32 heads (677 MB): 132 us a call (0.75), copies
 // alone 104 to 108.  The rest is the instructions: about 480 a warp for 32 tokens of
 // a kv head (QK and softmax 186, PV 148, scales and zeros 54, ring and walk 95 with the
-// producer's), of which an SM sub-partition issues 0.5 a cycle; the logic pipe is
-// 60 % busy in bursts.  Tried: four CTAs an SM (96 registers, spills: 98 us), units of
+// producer's), of which an SM sub-partition issues 0.53 a cycle; the logic pipe is
+// 57 % busy, in bursts.  Tried: four CTAs an SM (96 registers, spills: 98 us), units of
 // 64 tokens (83), eight heads a CTA (88), shifts in the multiplier (102 as before),
 // two or three stages (84, 83).
 #include "decode_tma_kernel.cuh"
