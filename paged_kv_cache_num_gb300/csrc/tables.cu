@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kTableThreads) tables_kernel(TableParams p)
     const int B = p.batch, tid = threadIdx.x;
     int *row0 = sm, *blk0 = sm + B, *len = sm + 2 * B;          // first row, first block, cached tokens (TRIM: kept blocks in row0)
     const int64_t cap = int64_t(p.max_blocks) << p.block_shift;
-    const int64_t round = (int64_t(1) << p.block_shift) - 1;
+    const int64_t low = (int64_t(1) << p.block_shift) - 1;      // the slot within a block of a position
     int64_t count = p.free_count[0];
     bool bad_pool = count < 0 || count > p.pool;
     count = count < 0 ? 0 : count > p.pool ? p.pool : count;
@@ -106,14 +106,14 @@ __global__ void __launch_bounds__(kTableThreads) tables_kernel(TableParams p)
         if (TRIM) {
             n = n < 0 ? 0 : n > cached ? cached : n;            // tokens kept
             rows = n;
-            blocks = ((cached + round) >> p.block_shift) - ((n + round) >> p.block_shift);
+            blocks = ((cached + low) >> p.block_shift) - ((n + low) >> p.block_shift);
         } else {
             if (n < 0 || cached + n > cap) {
                 bad_len = true;
                 n = 0;
             }
             rows = n;
-            blocks = ((cached + n + round) >> p.block_shift) - ((cached + round) >> p.block_shift);
+            blocks = ((cached + n + low) >> p.block_shift) - ((cached + low) >> p.block_shift);
         }
     };
     int64_t ra = 0, bl = 0;
@@ -182,10 +182,10 @@ __global__ void __launch_bounds__(kTableThreads) tables_kernel(TableParams p)
     for (int i = at; i < total_blocks; i += step) {
         const int b = find(blk0, B, i);
         if (TRIM) {
-            const int64_t j = ((int64_t(row0[b]) + round) >> p.block_shift) + (i - blk0[b]);
+            const int64_t j = ((int64_t(row0[b]) + low) >> p.block_shift) + (i - blk0[b]);
             p.free_blocks[count + i] = p.bt[b * p.bt_b + j * p.bt_j];
         } else {
-            const int64_t j = ((int64_t(len[b]) + round) >> p.block_shift) + (i - blk0[b]);
+            const int64_t j = ((int64_t(len[b]) + low) >> p.block_shift) + (i - blk0[b]);
             p.bt[b * p.bt_b + j * p.bt_j] = p.free_blocks[count - 1 - i];
         }
     }
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kTableThreads) tables_kernel(TableParams p)
                 if (cur + 1 < B && row0[cur + 1] <= i) cur = find(row0, B, i);
                 b[u] = cur;
                 pos[u] = len[cur] + (i - row0[cur]);
-                const int64_t j = pos[u] >> p.block_shift, have = (int64_t(len[cur]) + round) >> p.block_shift;
+                const int64_t j = pos[u] >> p.block_shift, have = (int64_t(len[cur]) + low) >> p.block_shift;
                 // the request's own last block, or one of those handed out now (which are not read back)
                 const int32_t *entry = j < have ? p.bt + cur * p.bt_b + j * p.bt_j : p.free_blocks + (count - 1 - (blk0[cur] + (j - have)));
                 slot[u] = *entry;
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kTableThreads) tables_kernel(TableParams p)
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-            if (pos[u] >= 0) slot[u] = (slot[u] << p.block_shift) + (pos[u] & round);
+            if (pos[u] >= 0) slot[u] = (slot[u] << p.block_shift) + (pos[u] & low);
         if (quads && i0 + 4 <= num_rows) {
             *reinterpret_cast<int4 *>(p.req + i0) = make_int4(b[0], b[1], b[2], b[3]);
             *reinterpret_cast<int4 *>(p.pos + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
