@@ -36,15 +36,15 @@
 // Every wait is bounded (about 2 s) and raises PKV_DEVERR_TIMEOUT.
 //
 // What bounds it.  16 sequences of 16K to 32K tokens, 64 q over 8 kv heads of 128
-// (421 MB): 81 us for this kernel, 86 us a call (0.72 of the copy bandwidth); the
+// (421 MB): 80 us for this kernel, 84 us a call (0.74 of the copy bandwidth); the
 // copies alone, without any arithmetic, take 68 to 70 us (6.1 TB/s with start and
-// end).  32 sequences of 1K to 8K, 32 heads (677 MB): 132 us a call (0.75), copies
+// end).  32 sequences of 1K to 8K, 32 heads (677 MB): 128 us a call (0.78), copies
 // alone 104 to 108.  The rest is the instructions: about 480 a warp for 32 tokens of
 // a kv head (QK and softmax 186, PV 148, scales and zeros 54, ring and walk 95 with the
 // producer's), of which an SM sub-partition issues 0.53 a cycle; the logic pipe is
 // 57 % busy, in bursts.  Tried: four CTAs an SM (96 registers, spills: 98 us), units of
-// 64 tokens (83), eight heads a CTA (88), shifts in the multiplier (102 as before),
-// two or three stages (84, 83).
+// 64 tokens (83), eight heads a CTA (88), shifts to the right as products' upper
+// halves (no gain), two or three stages (84, 83).
 #include "decode_tma_kernel.cuh"
 
 namespace pkv {
@@ -261,6 +261,9 @@ __global__ void __launch_bounds__(32 * (kHeadsU4<NG> + 1), (kCtasU4<NG>))
         j = r - prefix[b];
     }
     int64_t seg_start = lo;
+    // shifts to the left by 2 are products with a number that the compiler does not know: they go
+    // to the multiplier's pipe, the ANDs have the logic one (1 to 2 %)
+    const uint32_t four = f.four;
     // byte offsets within a tile's 16 rows: this lane's words of K row gid, and the 16-byte piece
     // of a V row whose address it gives to a transposed load (matrices: tokens 0 - 7 and 8 - 15
     // of one piece, then of the next)
@@ -432,7 +435,7 @@ __global__ void __launch_bounds__(32 * (kHeadsU4<NG> + 1), (kCtasU4<NG>))
             }
 #pragma unroll
             for (int k = 0; k < QK; ++k) {
-                const uint32_t xa = k & 1 ? xw[k >> 1] >> 6 : xw[k >> 1] << 2, ya = k & 1 ? yw[k >> 1] >> 6 : yw[k >> 1] << 2;
+                const uint32_t xa = k & 1 ? xw[k >> 1] >> 6 : xw[k >> 1] * four, ya = k & 1 ? yw[k >> 1] >> 6 : yw[k >> 1] * four;
                 const uint32_t a[4] = {xa & kAt2, ya & kAt2, xa & kAt6, ya & kAt6};
 #pragma unroll
                 for (int g = 0; g < NG; ++g) ptx::mma16816<false>(sc[g][t], a, qb[g][k][0], qb[g][k][1]);
@@ -525,7 +528,7 @@ __global__ void __launch_bounds__(32 * (kHeadsU4<NG> + 1), (kCtasU4<NG>))
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint32_t xa = h ? v[2 * i] >> 6 : v[2 * i] << 2, ya = h ? v[2 * i + 1] >> 6 : v[2 * i + 1] << 2;
+                        const uint32_t xa = h ? v[2 * i] >> 6 : v[2 * i] * four, ya = h ? v[2 * i + 1] >> 6 : v[2 * i + 1] * four;
                         const uint32_t a[4] = {xa & kAt2, xa & kAt6, ya & kAt2, ya & kAt6};
 #pragma unroll
                         for (int g = 0; g < NG; ++g) ptx::mma16816<false>(o[g][4 * i2 + 2 * i + h], a, pb[g][t][0], pb[g][t][1]);
@@ -659,6 +662,7 @@ bool plan_decode_u4(const DecodeParams &p, bool meta_head_major, int sm_count, F
     f.n_hg = p.num_kv_heads / nh;
     f.stages = stages;
     f.unit_shift = kUnitShift;
+    f.four = 4;
     f.meta_heads = meta_heads;
     f.meta_hmaj = meta_head_major ? 1 : 0;
     f.smem_bytes = L.total;

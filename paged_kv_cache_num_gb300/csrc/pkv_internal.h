@@ -144,6 +144,7 @@ struct FastParams {
                                 // (1, 2 or 4); 1 otherwise
     int ncons;                  // consumer warps per CTA
     int unit_shift;             // log2 of the tokens that a unit of work has (block_size; 4-bit: 32)
+    uint32_t four;              // 4-bit: 4
     int u3_tiles;               // 3-bit K / V tiles ([head][slot][row] in shared
                                 // memory): 0 by 4-D tensor copies; 1 by one bulk
                                 // copy per tile (heads stored [block][head][slot][row])
