@@ -61,7 +61,7 @@ template <int NG> constexpr int kHeadsU4 = 4;
 template <int NG> constexpr int kCtasU4 = NG == 1 ? 3 : 2;
 
 constexpr uint32_t kAt2 = 0x003c003cu, kAt6 = 0x03c003c0u;       // codes at bits 2 and 6 of both halves
-constexpr int kConvBytes = kUnit * (16 + 4 + 2);    // per consumer warp: see unit()
+constexpr int kConvBytes = kUnit * (16 + 4 + 2) + 64;        // per consumer warp: see unit(), and a number a head
 // The maximum is raised when a score passes it by more than this (log2 units): P
 // then is at most 2^6, far within f16's range, and few units rescale.
 constexpr float kRaise = 6.0f;
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(32 * (kHeadsU4<NG> + 1), (kCtasU4<NG>))
     const uint32_t voff = D == 128 ? vrow * ROW + ((((lane >> 4) ^ (vrow >> 1)) & 3) << 4) : vrow * ROW + ((((lane >> 4) ^ (vrow >> 2)) & 1) << 4);
     // what the products take of the unit's tokens: (sk in log2 units, zk, e, sv
     // 2^-e) with e about log2 sv, 2^-e, and zv as f16
-    const uint32_t conv = sbase + L.conv + warp * kConvBytes, conv_e = conv + kUnit * 16, conv_z = conv_e + kUnit * 4;
+    const uint32_t conv = sbase + L.conv + warp * kConvBytes, conv_e = conv + kUnit * 16, conv_z = conv_e + kUnit * 4, conv_up = conv_z + kUnit * 2;
     // places of this lane's token's scales and zeros among the unit's
     const int meta_k = (NB == 2 ? lane >> 4 : 0) * slots * MH +
                        (f.meta_hmaj ? kvl * slots + (lane & (slots - 1)) : (lane & (slots - 1)) * MH + kvl);
@@ -281,18 +281,21 @@ __global__ void __launch_bounds__(32 * (kHeadsU4<NG> + 1), (kCtasU4<NG>))
     float o[NG][OT][4];
     float m[NG][2], l[NG][2];                       // maximum and sum of p, of heads 2 tig, 2 tig + 1
     float zs[NG][4];                                // sum of P zv, of lanes 0 - 3 (row 0)
-    float q1[NG][2];                                // sum of q 2^-22 as in qb
-    float mult = 0.0f;                              // what makes q . u log2 units
+    float q1[NG][2];                                // sum of q 2^-22 as in qb, times the head's own factor
+    uint32_t keep = 0;                              // all ones: the heads' factors differ (theirs are at
+                                                    // conv_up); else all ones less one
+    float mult = 0.0f;                              // what makes q . u (times theirs) log2 units
     int ctx_b = 0;
 
     auto start_segment = [&]() {
         ctx_b = ctxs[b];
         // column gid of group g: q head 8 g + gid; this lane's elements are those of its words
         // of K, 8 w .. 8 w + 7 from d0 on, in pairs (n, n + 4)
-        float v[NG][8 * WK], top = 0.0f;
+        float v[NG][8 * WK], top[NG];
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             const int head = 8 * g + gid;
+            top[g] = 0.0f;
             const uint16_t *qr = reinterpret_cast<const uint16_t *>(p.q + b * p.q_b + ((hg * nh + kvl) * G + head) * p.q_h) + 8 * WK * tig;
 #pragma unroll
             for (int c = 0; c < WK; ++c) {
@@ -306,19 +309,39 @@ __global__ void __launch_bounds__(32 * (kHeadsU4<NG> + 1), (kCtasU4<NG>))
                     else t = __half22float2(*reinterpret_cast<const __half2 *>(&w[e]));
                     v[g][8 * c + 2 * e] = t.x;
                     v[g][8 * c + 2 * e + 1] = t.y;
-                    top = fmaxf(top, fmaxf(fabsf(t.x), fabsf(t.y)));
+                    top[g] = fmaxf(top[g], fmaxf(fabsf(t.x), fabsf(t.y)));
                 }
             }
         }
-#pragma unroll
-        for (int s = 1; s < 32; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-        // times the power of two that brings the group's largest element to 2^13 .. 2^14: an
-        // element is then off by at most 2^-34 of the largest
-        const int e = min(max(int(__float_as_uint(top) >> 23), 13), 253);
-        const float qs = __uint_as_float(uint32_t(267 - e) << 23);             // 2^(140 - e)
-        mult = p.scale_log2 * __uint_as_float(uint32_t(min(max(e + 9, 1), 254)) << 23);    // c 2^22 / qs
+        // Times the power of two that brings the largest element to 2^13 .. 2^14: that of all heads,
+        // which are then off by at most 2^-24 of their own largest; where one is smaller than another
+        // by 2^10 or more, each head's own, and a product more per score.  (That product in every
+        // unit: 84 -> 86 us on the long contexts.)  What is not finite counts for no factor: it
+        // is no matter of the other heads.
+        float all = 0.0f;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
+            top[g] = fmaxf(top[g], __shfl_xor_sync(0xffffffffu, top[g], 1));
+            top[g] = fmaxf(top[g], __shfl_xor_sync(0xffffffffu, top[g], 2));
+            all = fmaxf(all, top[g] <= 3.4e38f ? top[g] : 0.0f);
+        }
+#pragma unroll
+        for (int s = 4; s < 32; s <<= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, s));
+        auto exponent = [](float x) { return min(max(int(__float_as_uint(x) >> 23), 13), 253); };
+        bool far = all > 0x1p73f;                   // (up to there mult is finite)
+#pragma unroll
+        for (int g = 0; g < NG; ++g) far = far || (top[g] > 0.0f && top[g] < all * 0x1p-10f);
+        const bool apart = __any_sync(0xffffffffu, far);
+        keep = apart ? 0xffffffffu : 0xfffffffeu;
+        // c 2^22 / qs is mult times 2^(e - 135), at most 2^118: nothing overflows that is not a score
+        // beyond fp32
+        const int most = exponent(all);
+        mult = p.scale_log2 * 0x1p17f * (apart ? 1.0f : __uint_as_float(uint32_t(most - 8) << 23));
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            const int e = apart && top[g] > 0.0f && top[g] <= 3.4e38f ? exponent(top[g]) : most;
+            const float qs = __uint_as_float(uint32_t(267 - e) << 23);         // 2^(140 - e)
+            const float back = apart ? __uint_as_float(uint32_t(e - 8) << 23) : 1.0f;
             float sum = 0.0f;
 #pragma unroll
             for (int k = 0; k < QK; ++k) {
@@ -328,11 +351,15 @@ __global__ void __launch_bounds__(32 * (kHeadsU4<NG> + 1), (kCtasU4<NG>))
                 qb[g][k][1] = pack_f16(v[g][n + 1] * (0.0625f * qs), v[g][n + 5] * (0.0625f * qs), b0, b1);
                 sum += (a0 + a1) + 16.0f * (b0 + b1);
             }
+            __syncwarp();                           // (the segment before is done with the place)
+            if (tig == 0)
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(conv_up + 4 * (8 * g + gid)), "f"(back) : "memory");
+            __syncwarp();
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                q1[g][c] = 0x1p-22f * __shfl_sync(0xffffffffu, sum, 4 * (2 * tig + c));
+                q1[g][c] = __shfl_sync(0xffffffffu, 0x1p-22f * sum * back, 4 * (2 * tig + c));
                 m[g][c] = NEG_INF;
                 l[g][c] = 0.0f;
             }
@@ -388,7 +415,8 @@ __global__ void __launch_bounds__(32 * (kHeadsU4<NG> + 1), (kCtasU4<NG>))
             }
     };
 
-    // one unit in stage s; bit i of `live`: token i counts (all of them do where ALL)
+    // one unit in stage s; bit i of `live`: token i counts (all of them do where ALL, and the heads
+    // have one factor)
     auto unit = [&](auto all_c, int s, uint32_t live) {
         constexpr bool ALL = decltype(all_c)::value;
         // ---- scales and zeros of a token by its lane, for all lanes
@@ -439,6 +467,17 @@ __global__ void __launch_bounds__(32 * (kHeadsU4<NG> + 1), (kCtasU4<NG>))
                 const uint32_t a[4] = {xa & kAt2, ya & kAt2, xa & kAt6, ya & kAt6};
 #pragma unroll
                 for (int g = 0; g < NG; ++g) ptx::mma16816<false>(sc[g][t], a, qb[g][k][0], qb[g][k][1]);
+            }
+        }
+        if (!ALL && keep == 0xffffffffu) {          // the heads' own factors
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                float up[2];
+                asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(up[0]), "=f"(up[1]) : "r"(conv_up + 4 * (8 * g + 2 * tig)));
+#pragma unroll
+                for (int t = 0; t < KT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[g][t][e] *= up[e & 1];       // (exact)
             }
         }
         // ---- online softmax per head column, log2 units.  P = p sv is packed to f16,
@@ -555,7 +594,7 @@ __global__ void __launch_bounds__(32 * (kHeadsU4<NG> + 1), (kCtasU4<NG>))
         const uint32_t there = stage_mask[s];
         if (NB == 2) live &= ((there & 1u) ? 0xffffu : 0u) | ((there & 2u) ? 0xffff0000u : 0u);
         else if (there == 0) live = 0;
-        if (live == 0xffffffffu) unit(std::true_type{}, s, live);
+        if (live > keep) unit(std::true_type{}, s, live);
         else if (live != 0) unit(std::false_type{}, s, live);
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar_empty + 8 * s);
