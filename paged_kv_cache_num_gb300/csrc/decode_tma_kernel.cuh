@@ -125,7 +125,7 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi, float &rlo, flo
 // is the high byte of the f16 of the same value, subnormals, infinities and
 // NaN included); int8 c as 1152 + c (a byte permute puts c next to the
 // exponent of 1024 and an XOR of the byte's top bit adds 128), the 1152
-// offset being removed in fp32 after the MMA.
+// offset being removed in fp32 after the MMA (K; V: v_from_q8).
 template <int CK, int HI>
 __device__ __forceinline__ uint32_t f16x2_from_q8(uint32_t w)
 {
@@ -144,6 +144,23 @@ __device__ __forceinline__ uint32_t f16x2_from_q8(uint32_t w)
 }
 
 constexpr float kI8Bias = 1152.0f;
+
+// The same for V, of int8 without the offset: the sums over the keys would hold 1152 sum(P)
+// beside what they are to hold, and the tensor core cuts off up to 2^-23 of a sum per 16 keys (4K
+// keys of nearly equal weight in one CTA: 6 % of the row, 32K: all of it).  w has the bytes' top bits
+// turned, one operation for four codes, so that this takes no more than the offset's sums did
+// (64 q over 8 kv heads on 16K to 32K tokens as before, 128 q heads 153 -> 145 us).
+template <int CK, int HI>
+__device__ __forceinline__ uint32_t v_from_q8(uint32_t w)
+{
+    if constexpr (CK == kI8) {
+        uint32_t r = ptx::prmt(w, 0x64646464u, HI ? 0x4342u : 0x4140u);
+        asm("add.rn.f16x2 %0, %0, %1;" : "+r"(r) : "r"(0xe480e480u));
+        return r;
+    } else {
+        return f16x2_from_q8<CK, HI>(w);
+    }
+}
 
 __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t a)
 {
@@ -530,8 +547,8 @@ decode_tma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
     float mult = 1.0f, vmul = 1.0f;
     int ctx_b = 0;
     // per head column: 3-bit, sum(q' 2^(x-24)) of the QK operand and the
-    // running sum of P' * zero of the PV operand; int8, 1152 sum(q') and the
-    // running sum of P' (the operands' 1152 offsets)
+    // running sum of P' * zero of the PV operand; int8, 1152 sum(q') (the K
+    // operand's offset)
     float q1h[2] = {0.0f, 0.0f}, zs[2] = {0.0f, 0.0f};
     // the same for the second group of head columns (NG = 2)
     constexpr int NG1 = NG > 1 ? 1 : 0;
@@ -730,21 +747,19 @@ decode_tma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             lt[c] = v;
         }
         float zt[2] = {0.0f, 0.0f};
-        if constexpr (T::kIsU3 || CK == kI8) {
+        if constexpr (T::kIsU3) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 float z = zsg[c];
 #pragma unroll
                 for (int o2 = 4; o2 < 32; o2 <<= 1) z += __shfl_xor_sync(0xffffffffu, z, o2);
-                zt[c] = CK == kI8 ? kI8Bias * z : z;
+                zt[c] = z;
             }
         }
         // accumulator entry (t, r, c) -> value of the segment's unnormalised output
         auto oval = [&](int t, int r, int c) -> float {
             if constexpr (T::kIsU3) {
                 return og[t][2 * r + c] * float(1 << (24 - u3v_x(2 * t + r))) - zt[c];
-            } else if constexpr (CK == kI8) {
-                return og[t][2 * r + c] - zt[c];
             } else {
                 return og[t][2 * r + c];
             }
@@ -780,6 +795,23 @@ decode_tma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
 #pragma unroll
                     for (int r = 0; r < 2; ++r) acc[d_of(t, r)] = oval(t, r, c) * vmul;
             }
+        }
+    };
+    // 3-bit: what the zero points have summed up to, off the sums of codes.  Every 256 tokens: both
+    // grow with the keys, each cut by the tensor core at every step, and what counts is their
+    // difference (32K keys of equal weight in one CTA: 5 % of the row where they are taken off at
+    // its end alone).  Costs 0.5 to 2 %.
+    auto take_zeros = [&](float (*og)[4], float *zsg) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            float z = zsg[c];
+#pragma unroll
+            for (int o2 = 4; o2 < 32; o2 <<= 1) z += __shfl_xor_sync(0xffffffffu, z, o2);
+            zsg[c] = 0.0f;
+#pragma unroll
+            for (int t = 0; t < T::DT / 2; ++t)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) og[t][2 * r + c] = fmaf(-1.0f / float(1 << (24 - u3v_x(2 * t + r))), z, og[t][2 * r + c]);
         }
     };
     auto finish_segment = [&](int64_t seg_end) {
@@ -1178,7 +1210,6 @@ decode_tma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                         alpha[c] = mn == NEG_INF ? 1.0f : exp2_approx(mg[c] - mn);
                         mg[c] = mn;
                         lg[c] *= alpha[c];
-                        if constexpr (CK == kI8) zsg[c] *= alpha[c];
                     }
                 }
 #pragma unroll
@@ -1198,10 +1229,6 @@ decode_tma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                         }
                         float q0, q1;
                         const uint32_t w = T::kBF ? pack_bf16(p0, p1, q0, q1) : pack_f16(p0 * vsr, p1 * vsr, q0, q1);
-                        if constexpr (CK == kI8) {   // the PV operand's offset: sum of P' as rounded
-                            zsg[0] += q0;
-                            zsg[1] += q1;
-                        }
                         pbg[t][r] = ptx::movmatrix_trans(w);
                     }
                 }
@@ -1271,6 +1298,7 @@ decode_tma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                         for (int i = 0; i < 4; ++i) {
                             w[i] = ld_shared_u32(XV ? vb[i] + q4 * 2 * BS * 16 : vb[i] + vswz[i & 1][q4 & 3]);
                             if (partial && rows[i] >= valid) w[i] = 0u;
+                            if constexpr (CK == kI8) w[i] ^= 0x80808080u;
                         }
 #pragma unroll
                         for (int hb = 0; hb < 2; ++hb) {
@@ -1279,10 +1307,10 @@ decode_tma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                             const uint32_t x01 = ptx::prmt(w[0], w[1], sel);
                             const uint32_t x23 = ptx::prmt(w[2], w[3], sel);
                             uint32_t a[4];
-                            a[0] = f16x2_from_q8<CK, 0>(x01);
-                            a[1] = f16x2_from_q8<CK, 1>(x01);
-                            a[2] = f16x2_from_q8<CK, 0>(x23);
-                            a[3] = f16x2_from_q8<CK, 1>(x23);
+                            a[0] = v_from_q8<CK, 0>(x01);
+                            a[1] = v_from_q8<CK, 1>(x01);
+                            a[2] = v_from_q8<CK, 0>(x23);
+                            a[3] = v_from_q8<CK, 1>(x23);
                             ptx::mma16816<false>(o[2 * q4 + hb], a, pb[kt][0], pb[kt][1]);
                             if constexpr (NG1) ptx::mma16816<false>(o1[2 * q4 + hb], a, pb1[kt][0], pb1[kt][1]);
                         }
@@ -1339,6 +1367,11 @@ decode_tma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 } while (nblk[b] == 0);
                 seg_start = x + 1;
                 start_segment();
+            } else if constexpr (T::kIsU3) {        // (blocks of 16 tokens go by twos, from any first one)
+                if ((j & (256 / BS - 1)) < (BS == 16 && HPW == 1 && NG == 1 ? 2 : 1)) {
+                    take_zeros(o, zs);
+                    if constexpr (NG1) take_zeros(o1, zs1);
+                }
             }
         } else {
             finish_segment(x);
