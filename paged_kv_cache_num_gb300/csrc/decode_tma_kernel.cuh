@@ -544,7 +544,8 @@ decode_tma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
     uint32_t qb[T::QK][2];        // B fragments of Q^T per k-step
     float o[T::DT / 2][4];        // O^T accumulators: 16-d tiles x (heads 2tig, 2tig+1)
     float m[2], l[2];             // running max / partial sum for heads 2tig, 2tig+1
-    float mult = 1.0f, vmul = 1.0f;
+    float vmul = 1.0f;
+    float mult[2] = {1.0f, 1.0f}, mult1[2] = {1.0f, 1.0f};      // of the head columns 2tig, 2tig+1 of both groups
     int ctx_b = 0;
     // per head column: 3-bit, sum(q' 2^(x-24)) of the QK operand and the
     // running sum of P' * zero of the PV operand; int8, 1152 sum(q') (the K
@@ -557,6 +558,16 @@ decode_tma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
     float m1[2], l1[2];
     float q1h1[2] = {0.0f, 0.0f}, zs1[2] = {0.0f, 0.0f};
 
+    // The power of two that brings a head's q into f16's range, from the largest element that this
+    // lane holds, one of the head's four.  Each head has its own, so that one that is not finite, or
+    // far larger than the others, is no matter of theirs (3-bit: 1 to 2 % more time, the others none).
+    auto q_factor = [&](float amax) -> float {
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        float qs = 1.0f;
+        while (amax * qs > 16384.0f && qs > 0x1p-126f) qs *= 0.5f;
+        return qs;
+    };
     auto start_segment = [&]() {
         const int kvh = hg * nh + kvl;
         {
@@ -574,8 +585,7 @@ decode_tma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             // q' = q qs 2^(1-x) (f16, exact) in the pair order of the K
             // fragments: k-step kk, lane tig holds pair 2kk (k = 2tig, 2tig+1)
             // and pair 2kk+1 (k = 2tig+8, 2tig+9) of 96-bit group tig, so that
-            // q' k' = qs 2^-23 q v for every code.  One power-of-two qs
-            // serves all the warp's head columns (both groups).
+            // q' k' = qs 2^-23 q v for every code.
             auto load_q = [&](const uint16_t *qrow, bool has, float (&qv)[32]) -> float {
                 float amax = 0.0f;
 #pragma unroll
@@ -602,18 +612,10 @@ decode_tma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 return amax;
             };
             float qv[32];
-            float amax = load_q(qr, hv, qv);
-            if constexpr (NG1) {
-                float qv1[32];
-                amax = fmaxf(amax, load_q(qr1, hv1, qv1));
-            }
-#pragma unroll
-            for (int o2 = 16; o2 > 0; o2 >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o2));
-            float qs = 1.0f;
-            while (amax * qs > 16384.0f) qs *= 0.5f;
+            const float qs = q_factor(load_q(qr, hv, qv));
             // the fragments of one group and, per head column 2tig + c, the
             // sum of q' 2^(x-24) over head_dim
-            auto convert_q = [&](const float (&qv)[32], uint32_t (*qbg)[2], float *q1g) {
+            auto convert_q = [&](const float (&qv)[32], float qs, uint32_t (*qbg)[2], float *q1g, float *multg) {
                 float q1 = 0.0f;
 #pragma unroll
                 for (int pp = 0; pp < 16; ++pp) {
@@ -627,17 +629,20 @@ decode_tma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 q1 += __shfl_xor_sync(0xffffffffu, q1, 1);
                 q1 += __shfl_xor_sync(0xffffffffu, q1, 2);
 #pragma unroll
-                for (int c = 0; c < 2; ++c) q1g[c] = __shfl_sync(0xffffffffu, q1, 4 * (2 * tig + c));
+                for (int c = 0; c < 2; ++c) {
+                    q1g[c] = __shfl_sync(0xffffffffu, q1, 4 * (2 * tig + c));
+                    // (cut off below infinity: scores of that size pick one key either way)
+                    multg[c] = fmaxf(fminf(log2e_scale * 0x1p23f / __shfl_sync(0xffffffffu, qs, 4 * (2 * tig + c)), 3.0e38f), -3.0e38f);
+                }
             };
-            convert_q(qv, qb, q1h);
+            convert_q(qv, qs, qb, q1h, mult);
             zs[0] = zs[1] = 0.0f;
             if constexpr (NG1) {
                 float qv1[32];
-                load_q(qr1, hv1, qv1);     // (read again: fewer live registers)
-                convert_q(qv1, qb1, q1h1);
+                const float qs1 = q_factor(load_q(qr1, hv1, qv1));
+                convert_q(qv1, qs1, qb1, q1h1, mult1);
                 zs1[0] = zs1[1] = 0.0f;
             }
-            mult = log2e_scale * 0x1p23f / qs;
             vmul = 1.0f;
         } else if constexpr (!T::kFp8) {
 #pragma unroll
@@ -650,7 +655,7 @@ decode_tma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                     qb1[kk][1] = hv1 ? *reinterpret_cast<const uint32_t *>(qr1 + d + 8) : 0u;
                 }
             }
-            mult = log2e_scale;
+            mult[0] = mult[1] = mult1[0] = mult1[1] = log2e_scale;
             vmul = 1.0f;
         } else {
             // q (16-bit) -> f16 operands in the element order of the fp8 K
@@ -658,9 +663,10 @@ decode_tma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             // (k = 2tig, 2tig+1) and + {2,3} (k = 2tig+8, 2tig+9).  A
             // power-of-two pre-scale keeps every element inside f16 range.
             float f[NG][T::QK][4];
-            float amax = 0.0f;
+            float qs[NG];
 #pragma unroll
-            for (int g = 0; g < NG; ++g)
+            for (int g = 0; g < NG; ++g) {
+                float amax = 0.0f;
 #pragma unroll
                 for (int kk = 0; kk < T::QK; ++kk) {
                     uint2 u = make_uint2(0, 0);
@@ -679,18 +685,16 @@ decode_tma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                         amax = fmaxf(amax, fmaxf(fabsf(f[g][kk][2 * e]), fabsf(f[g][kk][2 * e + 1])));
                     }
                 }
-#pragma unroll
-            for (int o2 = 16; o2 > 0; o2 >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o2));
-            float qs = 1.0f;
-            while (amax * qs > 16384.0f) qs *= 0.5f;
+                qs[g] = q_factor(amax);
+            }
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 float d0, d1, d2, d3, c0 = 0.0f;
                 uint32_t (*qg)[2] = g == 0 ? qb : qb1;
 #pragma unroll
                 for (int kk = 0; kk < T::QK; ++kk) {
-                    qg[kk][0] = pack_f16(f[g][kk][0] * qs, f[g][kk][1] * qs, d0, d1);
-                    qg[kk][1] = pack_f16(f[g][kk][2] * qs, f[g][kk][3] * qs, d2, d3);
+                    qg[kk][0] = pack_f16(f[g][kk][0] * qs[g], f[g][kk][1] * qs[g], d0, d1);
+                    qg[kk][1] = pack_f16(f[g][kk][2] * qs[g], f[g][kk][3] * qs[g], d2, d3);
                     c0 += (d0 + d1) + (d2 + d3);
                 }
                 if constexpr (CK == kI8) {     // sum of q' over head_dim, per q head gid
@@ -704,7 +708,12 @@ decode_tma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 }
             }
             // per-block / per-token scales are applied per row (scores and P')
-            mult = log2e_scale * (gscale ? 1.0f : p.k_scale[kvh]) / qs;
+            const float ks = log2e_scale * (gscale ? 1.0f : p.k_scale[kvh]);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                mult[c] = ks / __shfl_sync(0xffffffffu, qs[0], 4 * (2 * tig + c));
+                if constexpr (NG1) mult1[c] = ks / __shfl_sync(0xffffffffu, qs[NG1], 4 * (2 * tig + c));
+            }
             vmul = gscale ? 1.0f : p.v_scale[kvh];
         }
 #pragma unroll
@@ -951,7 +960,7 @@ decode_tma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         // in ptg: pt[t][r] gives lane (gid, tig) the P' of tokens 8r + 2tig,
         // +1 of tile t in head column gid
         auto u3_softmax = [&](float (*scg)[4], float *mg, float *lg, float *zsg, const float *q1g,
-                              uint32_t (*ptg)[2], float (*og)[4]) {
+                              const float *multg, uint32_t (*ptg)[2], float (*og)[4]) {
             float mx[2] = {NEG_INF, NEG_INF};
 #pragma unroll
             for (int t = 0; t < KTT; ++t)
@@ -960,7 +969,7 @@ decode_tma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                     const int r = e >> 1, c = e & 1;
                     if (c >= NC) continue;
                     const float2 kz = *reinterpret_cast<const float2 *>(meta_of(t, r, c));   // (sk, zk)
-                    float v = mult * kz.x * (scg[t][e] - kz.y * q1g[c]);
+                    float v = kz.x * (scg[t][e] - kz.y * q1g[c]) * multg[c];
                     if (partial) v = (16 * t + gid + 8 * r) < valid ? v : NEG_INF;
                     scg[t][e] = v;
                     mx[c] = fmaxf(mx[c], v);
@@ -1014,8 +1023,8 @@ decode_tma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         };
         uint32_t pt[KTT][2];
         [[maybe_unused]] uint32_t pt1[NG1 ? KTT : 1][2];
-        u3_softmax(sc, m, l, zs, q1h, pt, o);
-        if constexpr (NG1) u3_softmax(sc1, m1, l1, zs1, q1h1, pt1, o1);
+        u3_softmax(sc, m, l, zs, q1h, mult, pt, o);
+        if constexpr (NG1) u3_softmax(sc1, m1, l1, zs1, q1h1, mult1, pt1, o1);
         // ---- O^T += V'^T P'^T with V converted straight into A fragments:
         // lane (gid, tig) owns codes 16gid .. 16gid+15 (row bytes 6gid ..
         // 6gid+5) of two token rows ra0, ra0+1 of head ha (k = 2tig, 2tig+1)
@@ -1169,7 +1178,7 @@ decode_tma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             // tokens, cols = heads) packed and transposed in registers, giving
             // lane (gid, tig) tokens 2tig, 2tig+1 of head gid
             auto softmax_group = [&](float (*scg)[4], float *mg, float *lg, float *zsg, const float *q1g,
-                                     uint32_t (*pbg)[2], float (*og)[4]) {
+                                     const float *multg, uint32_t (*pbg)[2], float (*og)[4]) {
                 float mx[2] = {NEG_INF, NEG_INF};
                 [[maybe_unused]] float vexp[T::KT][2];
                 if constexpr (T::kFp8 && gscale) {
@@ -1183,7 +1192,7 @@ decode_tma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 for (int t = 0; t < T::KT; ++t) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float v = (CK == kI8 ? scg[t][e] - q1g[e & 1] : scg[t][e]) * mult;
+                        float v = (CK == kI8 ? scg[t][e] - q1g[e & 1] : scg[t][e]) * multg[e & 1];
                         if (T::kFp8 && gscale) v *= row_ks(16 * t + gid + 8 * (e >> 1));
                         if (partial) {
                             const int tok = 16 * t + gid + 8 * (e >> 1);
@@ -1243,8 +1252,8 @@ decode_tma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 }
             };
             uint32_t pb[T::KT][2], pb1[NG1 ? T::KT : 1][2];
-            softmax_group(sc, m, l, zs, q1h, pb, o);
-            if constexpr (NG1) softmax_group(sc1, m1, l1, zs1, q1h1, pb1, o1);
+            softmax_group(sc, m, l, zs, q1h, mult, pb, o);
+            if constexpr (NG1) softmax_group(sc1, m1, l1, zs1, q1h1, mult1, pb1, o1);
             // ---------------- O^T += V^T P^T
 #pragma unroll
             for (int kt = 0; kt < T::KT; ++kt) {
