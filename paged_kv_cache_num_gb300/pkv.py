@@ -159,18 +159,6 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:
-        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
-    return ctypes.c_void_p(stream.cuda_stream)
-
-
-def _need_cuda(*ts):
-    for t in ts:
-        if t is not None and not t.is_cuda:
-            raise ValueError("all tensors must be CUDA tensors")
-
-
 def _one_device(*ts) -> int:
     """The CUDA device that every tensor is on."""
     dev = None
@@ -383,7 +371,7 @@ def version() -> str:
 
 def slot_mapping(block_tables, req, pos, block_size: int, out=None, err_flag=None, stream=None):
     """slot = block_tables[req][pos // bs] * bs + pos % bs (pos < 0 -> -1), on the GPU."""
-    dev = _one_device(block_tables, req, pos)
+    dev = _one_device(block_tables, req, pos, out, err_flag)
     there = _elsewhere(dev, stream)
     if there is not None:
         with there:
@@ -397,7 +385,7 @@ def slot_mapping(block_tables, req, pos, block_size: int, out=None, err_flag=Non
 
 def kv_append(k_new, v_new, slot_mapping, cache: KVCache, err_flag=None, stream=None):
     """Scatter new K/V rows [T, Hkv, D] into the cache through slot_mapping."""
-    dev = _one_device(k_new, v_new, slot_mapping, *cache.tensors())
+    dev = _one_device(k_new, v_new, slot_mapping, err_flag, *cache.tensors())
     there = _elsewhere(dev, stream)
     if there is not None:
         with there:
@@ -411,11 +399,15 @@ def kv_append_scaled(k_new, v_new, k_new_scale, v_new_scale, slot_mapping, cache
                      err_flag=None, stream=None):
     """kv_append for a cache with per-token scales: k_new_scale / v_new_scale
     fp32 [num_tokens, Hkv] are divided out and stored at the tokens' slots."""
-    _need_cuda(k_new, v_new, k_new_scale, v_new_scale, slot_mapping, *cache.tensors())
+    dev = _one_device(k_new, v_new, k_new_scale, v_new_scale, slot_mapping, err_flag, *cache.tensors())
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return kv_append_scaled(k_new, v_new, k_new_scale, v_new_scale, slot_mapping, cache, err_flag)
     _check(lib().pkv_kv_append_scaled(ctypes.byref(_desc(k_new)), ctypes.byref(_desc(v_new)),
                                       ctypes.byref(_desc(k_new_scale)), ctypes.byref(_desc(v_new_scale)),
                                       ctypes.byref(_desc(slot_mapping)), ctypes.byref(cache._struct()),
-                                      _ptr(err_flag), _stream(stream)))
+                                      _flag(err_flag), _raw_stream(dev)))
 
 
 def _raw_stream(dev: int) -> int:
@@ -625,7 +617,7 @@ def decode_launches(q, cache: KVCache, block_tables, num_splits: int = 0) -> int
 def paged_decode(q, cache: KVCache, block_tables, context_lens, sm_scale: Optional[float] = None,
                  out=None, num_splits: int = 0, workspace=None, err_flag=None, stream=None):
     """softmax(sm_scale * q . K^T) V over each sequence's paged context."""
-    dev = _one_device(q, block_tables, context_lens, *cache.tensors())
+    dev = _one_device(q, block_tables, context_lens, out, workspace, err_flag, *cache.tensors())
     there = _elsewhere(dev, stream)
     if there is not None:
         with there:
@@ -653,7 +645,7 @@ def decode_step(k_new, v_new, req, pos, q, cache: KVCache, block_tables, context
     """slot_mapping + kv_append + paged_decode in one library call (see
     pkv_decode_step in pkv.h); returns out.  `slots` (int64 [num_tokens])
     receives the slot mapping."""
-    dev = _one_device(k_new, v_new, req, pos, q, block_tables, context_lens, *cache.tensors())
+    dev = _one_device(k_new, v_new, req, pos, q, block_tables, context_lens, out, slots, workspace, err_flag, *cache.tensors())
     there = _elsewhere(dev, stream)
     if there is not None:
         with there:
@@ -683,7 +675,11 @@ def paged_decode_noalloc(q, cache: KVCache, block_tables, context_lens,
                          err_flag=None, stream=None):
     """paged_decode without a caller workspace: the split-K scratch is the
     library's fixed device array (see pkv_paged_decode_noalloc in pkv.h)."""
-    _need_cuda(q, block_tables, context_lens, *cache.tensors())
+    dev = _one_device(q, block_tables, context_lens, out, err_flag, *cache.tensors())
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return paged_decode_noalloc(q, cache, block_tables, context_lens, sm_scale, out, num_splits, err_flag)
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(q.shape[-1])
     if out is None:
@@ -693,42 +689,58 @@ def paged_decode_noalloc(q, cache: KVCache, block_tables, context_lens,
                                           ctypes.byref(_desc(block_tables)),
                                           ctypes.byref(_desc(context_lens)), float(sm_scale),
                                           ctypes.byref(_desc(out)), int(num_splits),
-                                          _ptr(err_flag), _stream(stream)))
+                                          _flag(err_flag), _raw_stream(dev)))
     return out
 
 
 def pack3(values, packed=None, stream=None):
     """uint8 [n*8] codes -> uint8 [n*3] packed bytes."""
-    _need_cuda(values)
+    dev = _one_device(values, packed)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return pack3(values, packed)
     n = values.numel() // 8
     if packed is None:
         packed = torch.empty(n * 3, dtype=torch.uint8, device=values.device)
-    _check(lib().pkv_pack3(_ptr(values), _ptr(packed), n, _stream(stream)))
+    _check(lib().pkv_pack3(_ptr(values), _ptr(packed), n, _raw_stream(dev)))
     return packed
 
 
 def unpack3(packed, values=None, stream=None):
     """uint8 [n*3] packed bytes -> uint8 [n*8] codes."""
-    _need_cuda(packed)
+    dev = _one_device(packed, values)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return unpack3(packed, values)
     n = packed.numel() // 3
     if values is None:
         values = torch.empty(n * 8, dtype=torch.uint8, device=packed.device)
-    _check(lib().pkv_unpack3(_ptr(packed), _ptr(values), n, _stream(stream)))
+    _check(lib().pkv_unpack3(_ptr(packed), _ptr(values), n, _raw_stream(dev)))
     return values
 
 
 def unpack3_words(words, values=None, stream=None):
     """int32/uint32 words [m*3] (same bytes as packed octets) -> uint8 [m*32]."""
-    _need_cuda(words)
+    dev = _one_device(words, values)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return unpack3_words(words, values)
     m = words.numel() // 3
     if values is None:
         values = torch.empty(m * 32, dtype=torch.uint8, device=words.device)
-    _check(lib().pkv_unpack3_words(_ptr(words), _ptr(values), m, _stream(stream)))
+    _check(lib().pkv_unpack3_words(_ptr(words), _ptr(values), m, _raw_stream(dev)))
     return values
 
 
 def copy_peak(src, dst, stream=None):
     """16-byte vectorised copy of src's bytes into dst (bandwidth yardstick)."""
-    _need_cuda(src, dst)
+    dev = _one_device(src, dst)
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return copy_peak(src, dst)
     nbytes = src.numel() * src.element_size()
-    _check(lib().pkv_copy_peak(_ptr(src), _ptr(dst), nbytes, _stream(stream)))
+    _check(lib().pkv_copy_peak(_ptr(src), _ptr(dst), nbytes, _raw_stream(dev)))
