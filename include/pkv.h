@@ -316,7 +316,9 @@ int pkv_kv_gather(const pkv_cache *cache, const pkv_tensor *slot_mapping, const 
  *     (y_a, y_b) -> (y_a c - y_b s, y_b c + y_a s),
  *     (a, b) = (i, i + rot / 2), or (2i, 2i + 1) where `interleaved` is not 0;
  *   elements from rot on are not rotated.  The rows' sums of squares have to be
- *   finite in fp32.
+ *   finite in fp32, and, where eps is below 2^-100, their mean squares normal fp32
+ *   numbers (2^-126 or more): with eps = 0 a row of zeros is NaN, one of bf16
+ *   elements below 2^-63 not finite.
  *   q            : F16 or BF16 [num_tokens, num_heads, head_dim], head_dim 64 or
  *                  128, contiguous, any token and head strides.
  *   k            : as q's type, [num_tokens, num_kv_heads, head_dim], likewise.
