@@ -508,8 +508,29 @@ int pkv_paged_prefill(const pkv_tensor *q, const pkv_cache *cache, const pkv_ten
  *   accumulated in fp32 and rounded once to the output dtype (V scales per
  *   block or token: from 2^-40 to 2^40; below 2^-40 bits are lost).  Cache
  *   contents beyond context_len (the tail of the last block) never affect
- *   the output, whatever they hold.
- *   Supported: head_dim in {64, 128}, block_size in {8, 16, 32, 64},
+ *   the output, whatever they hold; nor do other query heads, not finite ones
+ *   either.
+ *   Arithmetic: an explicit num_splits computes in fp32 throughout.  With
+ *   num_splits 0 the products are of 16-bit operands, where the shapes and
+ *   layouts allow it, with sums in fp32 that the tensor core may cut by
+ *   2^-23 of themselves per 16 summands:
+ *     - weights are rounded once to the cache's type, of coded caches to F16,
+ *       there times the V scale if that is per block, token or row: for U4 and
+ *       one-byte codes relative to the largest such product so far (one below
+ *       2^-13 of it is off by at most 2^-25), for U3 as it is (products below
+ *       2^-14 lose bits);
+ *     - queries of coded caches become F16 by a power of two per head (U4: one
+ *       for all heads of a kv head that are within 2^10 of each other), off by at
+ *       most 2^-24 of the head's largest element where that is more than F16's
+ *       own rounding; one-byte and U3: elements below 2^-14 lose bits;
+ *     - codes are exact.  U4 and U3 codes are operands below F16's normal range,
+ *       whose products the tensor core cuts earlier: per 16 elements a score by
+ *       2^-14 (U3: 2^-13) of the head's largest |q| times the row's K scale
+ *       times sm_scale, and per 16 keys a sum by 2^-15 (U3: 2^-13) of the V
+ *       scale times the largest weight there.  I8 codes are code + 1152 in the
+ *       scores' products alone.
+ *   Supported: head_dim in {64, 128}, block_size a power of two up to 256 (the
+ *   16-bit products: 16, 32 and 64, U4 also 128 and 256),
  *   num_heads % num_kv_heads == 0 with a group of at most 16 q heads.
  *   Bad table data never faults: a block id outside [0, num_blocks) is
  *   skipped (its tokens are left out) and raises PKV_DEVERR_BLOCK_RANGE; a
