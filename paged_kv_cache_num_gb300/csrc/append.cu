@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_u3_kernel(AppendParams 
         const float s = __half2float(__ushort_as_half(sbits));
         const float rs = s != 0.0f ? __frcp_rn(s) : 0.0f;
         // z = clamp(rint(fl(-min / s)), 0, 7); -min is one of the row's
-        // 16-bit values, so u3_quotient gives the same rint
+        // 16-bit values, so row_quotient gives the same rint
         float z = 0.0f;
         if (s != 0.0f) z = fminf(fmaxf(rintf(row_quotient(-mn, s, rs)), 0.0f), 7.0f);
         // fields: codes q_j = clamp(rint(fl(x_j / s)) + z, 0, 7) at bits 3j

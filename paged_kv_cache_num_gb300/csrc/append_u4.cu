@@ -21,7 +21,7 @@ namespace pkv {
 namespace {
 
 // Whole rows per warp and step: the lanes of a row stay together (head_dim /
-// 8 divides 32 and a part begins at a multiple of 32 pieces).
+// 16 divides 32 and a part begins at a multiple of 32 pieces).
 template <int SRC, bool VEC, int D, int U>
 __global__ void __launch_bounds__(kAppendThreads) append_u4_kernel(AppendParams p)
 {

@@ -12,7 +12,8 @@
 // bytes) a lane, U row groups at a time, their loads before the arithmetic: the
 // products of the weights and the table's row are made once for all of them.  A row is 16 or 8
 // neighbouring lanes: its sum of squares is log2 of that in shuffles, the other
-// half of a rotated pair four more (of the 16-bit source, normed again here).
+// half of a rotated pair four more (of the 16-bit source; the norm's factor is the
+// row's, and the other's weight is in the table's products).
 // 20011 tokens, 32 q and 8 kv heads of 128, bf16 (497 MB): 98 us, 0.75 of the copy
 // bandwidth (the products made for every four row groups 117, at 101 registers 149);
 // what is left is latency: 24 warps an SM with 2 KB each on the way.  A decode step's 64
