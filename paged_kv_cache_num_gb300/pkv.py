@@ -152,11 +152,21 @@ def _xvec_desc(t: torch.Tensor, code: int) -> _Tensor:
 
 
 def _flag(err_flag):
-    return None if err_flag is None else err_flag.data_ptr()
+    if err_flag is None:
+        return None
+    if err_flag.dtype is not torch.int32 or err_flag.numel() < 1:
+        raise ValueError("err_flag must be an int32")
+    return err_flag.data_ptr()
 
 
-def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+def _room(t, name: str, nbytes: int = 0):
+    """(address, bytes) of a buffer that is taken as one run of bytes."""
+    if t is None:
+        return None, 0
+    n = t.numel() * t.element_size()
+    if not t.is_contiguous() or n < nbytes:
+        raise ValueError("%s must be contiguous, of %d bytes or more" % (name, nbytes))
+    return t.data_ptr(), n
 
 
 def _one_device(*ts) -> int:
@@ -428,7 +438,7 @@ def kv_append_dynamic(k_new, v_new, slot_mapping, cache: KVCache, err_flag=None,
             return kv_append_dynamic(k_new, v_new, slot_mapping, cache, err_flag)
     _check(lib().pkv_kv_append_dynamic(_packed(k_new), _packed(v_new), _packed(slot_mapping),
                                        ctypes.byref(cache._struct()),
-                                       None if err_flag is None else err_flag.data_ptr(), _raw_stream(dev)))
+                                       _flag(err_flag), _raw_stream(dev)))
 
 
 def kv_gather(cache: KVCache, slot_mapping, dtype: Optional[torch.dtype] = None, k_out=None, v_out=None,
@@ -453,7 +463,7 @@ def kv_gather(cache: KVCache, slot_mapping, dtype: Optional[torch.dtype] = None,
         if v_out is None:
             v_out = torch.zeros(shape, dtype=dtype, device=slot_mapping.device)
     _check(lib().pkv_kv_gather(ctypes.byref(cache._struct()), _packed(slot_mapping), _packed(k_out), _packed(v_out),
-                               None if err_flag is None else err_flag.data_ptr(), _raw_stream(dev)))
+                               _flag(err_flag), _raw_stream(dev)))
     return k_out, v_out
 
 
@@ -592,8 +602,8 @@ def paged_prefill(q, cache: KVCache, block_tables, q_starts, context_lens,
         workspace = torch.empty(prefill_workspace_bytes(q, cache, block_tables), dtype=torch.uint8, device=q.device)
     _check(lib().pkv_paged_prefill(_packed(q), ctypes.byref(cache._struct()), _packed(block_tables),
                                    _packed(q_starts), _packed(context_lens), sm_scale, _packed(out),
-                                   workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                   None if err_flag is None else err_flag.data_ptr(), _raw_stream(dev)))
+                                   *_room(workspace, "workspace"),
+                                   _flag(err_flag), _raw_stream(dev)))
     return out
 
 
@@ -631,8 +641,7 @@ def paged_decode(q, cache: KVCache, block_tables, context_lens, sm_scale: Option
         need = decode_workspace_bytes(q, cache, block_tables, num_splits)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    ws_ptr = None if workspace is None else workspace.data_ptr()
-    ws_n = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_ptr, ws_n = _room(workspace, "workspace")
     _check(lib().pkv_paged_decode(_packed(q), ctypes.byref(cs), _packed(block_tables), _packed(context_lens),
                                   float(sm_scale), _packed(out), int(num_splits), ws_ptr, ws_n, _flag(err_flag),
                                   _raw_stream(dev)))
@@ -662,8 +671,7 @@ def decode_step(k_new, v_new, req, pos, q, cache: KVCache, block_tables, context
         need = decode_workspace_bytes(q, cache, block_tables, num_splits)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    ws_ptr = None if workspace is None else workspace.data_ptr()
-    ws_n = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_ptr, ws_n = _room(workspace, "workspace")
     _check(lib().pkv_decode_step(_packed(k_new), _packed(v_new), _packed(req), _packed(pos), _packed(slots), _packed(q),
                                  ctypes.byref(cs), _packed(block_tables), _packed(context_lens), float(sm_scale),
                                  _packed(out), int(num_splits), ws_ptr, ws_n, _flag(err_flag), _raw_stream(dev)))
@@ -703,7 +711,7 @@ def pack3(values, packed=None, stream=None):
     n = values.numel() // 8
     if packed is None:
         packed = torch.empty(n * 3, dtype=torch.uint8, device=values.device)
-    _check(lib().pkv_pack3(_ptr(values), _ptr(packed), n, _raw_stream(dev)))
+    _check(lib().pkv_pack3(_room(values, "values")[0], _room(packed, "packed", 3 * n)[0], n, _raw_stream(dev)))
     return packed
 
 
@@ -717,7 +725,7 @@ def unpack3(packed, values=None, stream=None):
     n = packed.numel() // 3
     if values is None:
         values = torch.empty(n * 8, dtype=torch.uint8, device=packed.device)
-    _check(lib().pkv_unpack3(_ptr(packed), _ptr(values), n, _raw_stream(dev)))
+    _check(lib().pkv_unpack3(_room(packed, "packed")[0], _room(values, "values", 8 * n)[0], n, _raw_stream(dev)))
     return values
 
 
@@ -731,7 +739,7 @@ def unpack3_words(words, values=None, stream=None):
     m = words.numel() // 3
     if values is None:
         values = torch.empty(m * 32, dtype=torch.uint8, device=words.device)
-    _check(lib().pkv_unpack3_words(_ptr(words), _ptr(values), m, _raw_stream(dev)))
+    _check(lib().pkv_unpack3_words(_room(words, "words", 12 * m)[0], _room(values, "values", 32 * m)[0], m, _raw_stream(dev)))
     return values
 
 
@@ -742,5 +750,5 @@ def copy_peak(src, dst, stream=None):
     if there is not None:
         with there:
             return copy_peak(src, dst)
-    nbytes = src.numel() * src.element_size()
-    _check(lib().pkv_copy_peak(_ptr(src), _ptr(dst), nbytes, _raw_stream(dev)))
+    at, nbytes = _room(src, "src")
+    _check(lib().pkv_copy_peak(at, _room(dst, "dst", nbytes)[0], nbytes, _raw_stream(dev)))
