@@ -8,7 +8,7 @@
 //   c q . k_t = c sk_t (q . u_t - zk_t sum q),
 //   sum_t p_t v_t = sum_t P_t w_t - sum_t P_t zv_t,  P_t = p_t sv_t,
 // so both products are of 16-bit numbers and bare codes.  K's zero points cost one
-// operation per score, V's one more row of the product.
+// operation per score, V's one more row of the product, taken off every 256 tokens.
 //
 // Codes as operands.  A 4-bit code at bit 2 of an otherwise zero 16-bit half is
 // the f16 subnormal u 2^-22, at bit 6 u 2^-18, exact: two shifts and four ANDs make
@@ -36,15 +36,16 @@
 // Every wait is bounded (about 2 s) and raises PKV_DEVERR_TIMEOUT.
 //
 // What bounds it.  16 sequences of 16K to 32K tokens, 64 q over 8 kv heads of 128
-// (421 MB): 80 us for this kernel, 84 us a call (0.74 of the copy bandwidth); the
+// (421 MB): 81 us for this kernel, 85 us a call (0.73 of the copy bandwidth); the
 // copies alone, without any arithmetic, take 68 to 70 us (6.1 TB/s with start and
-// end).  32 sequences of 1K to 8K, 32 heads (677 MB): 128 us a call (0.78), copies
-// alone 104 to 108.  The rest is the instructions: about 480 a warp for 32 tokens of
-// a kv head (QK and softmax 186, PV 148, scales and zeros 54, ring and walk 95 with the
-// producer's), of which an SM sub-partition issues 0.53 a cycle; the logic pipe is
-// 57 % busy, in bursts.  Tried: four CTAs an SM (96 registers, spills: 98 us), units of
-// 64 tokens (83), eight heads a CTA (88), shifts to the right as products' upper
-// halves (no gain), two or three stages (84, 83).
+// end).  32 sequences of 1K to 8K, 32 heads (677 MB): 130 us a call (0.77), copies
+// alone 104 to 108.  The rest is the instructions: about 490 a warp for 32 tokens of
+// a kv head (QK and softmax 186, PV 148, scales and zeros 54, ring, walk and the zeros'
+// sums 100 with the producer's), of which an SM sub-partition issues 0.55 a cycle; the
+// logic pipe is 55 % busy, in bursts.  Tried, against a kernel of 81 us: four CTAs an SM
+// (96 registers, spills: 98 us), units of 64 tokens (83), eight heads a CTA (88), shifts
+// to the right as products' upper halves (no gain), two or three stages (84, 83); scores'
+// operations two heads at a time (fma.rn.f32x2: 6 us more).
 #include "decode_tma_kernel.cuh"
 
 namespace pkv {
@@ -56,7 +57,7 @@ constexpr int kUnitShift = 5;
 // kv heads of a CTA at most, and CTAs that an SM is to hold.  Three CTAs of five warps
 // leave each SM sub-partition at most four warps of 128 registers; with 16 head
 // columns (twice the accumulators) it is three of 168, two CTAs (128 q over 8 kv heads
-// on the long contexts: 135 us; four CTAs of two heads 140, three of four heads 207).
+// on the long contexts: 132 us; before that, against 135, four CTAs of two heads 140, three of four heads 207).
 template <int NG> constexpr int kHeadsU4 = 4;
 template <int NG> constexpr int kCtasU4 = NG == 1 ? 3 : 2;
 
